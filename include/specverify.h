@@ -459,6 +459,161 @@ sv_status sv_mirror_reuse(const int32_t *branches, const int32_t *accept_len,
                           uint8_t *reuse, sv_stream_t stream);
 
 /* ----------------------------------------------------------------------------------------
+ * The target's side of a verification step (no counterpart on the pages, which take the logits as
+ * given): rotary positions, a paged key/value cache, attention of the drafted block over it, and
+ * the commit of what was accepted.
+ *
+ * A block is the rows that one step scores for a sequence: row 0 holds the last committed token,
+ * rows 1.. the drafted ones.  As a chain, row i follows row i - 1.  As a tree, row i (1..N) is node i of
+ * sv_tree_verify and follows row parents[b][i-1]; rows see their ancestors, themselves and every
+ * cached token.
+ *
+ * Cache.  Keys and values of one layer lie in n_pages pages of page_size slots.  Slot s of sequence b is
+ * place s % page_size of page page_table[b * table_pitch + s / page_size].  Head h of it starts
+ * page * page_stride + place * slot_stride + h * head_stride elements after k (after v).  Bases
+ * must be 16-byte aligned and the strides and head_dim multiples of 16 bytes.  Any order of the axes works, and
+ * keys and values may be interleaved in one allocation as long as they share the strides.
+ *
+ * Batch.  Rows of q, k, v and out are [row][head][element] with caller-given strides.  Without
+ * row_start, sequence b has rows b*n..b*n+n-1; with it, rows row_start[b]..row_start[b+1]-1 (at most n
+ * of them, none is allowed) and parents must be NULL.  context_len[b] tokens of sequence b are
+ * cached before the call; its block takes the slots after them.
+ *
+ * Device-side checks, reported to stats as SV_ERR_INVALID_ARG with the sequence (row) index: a context_len that
+ * is negative or whose block passes max_pages * page_size; a row_start that falls, exceeds `rows` or
+ * gives a sequence more than n rows; a page id outside [0, n_pages); a parent outside [0, i-1].  Nothing is read or
+ * written out of range for them; the outputs of the sequences concerned are unspecified.
+ * -------------------------------------------------------------------------------------- */
+#define SV_KV_MAX_HEAD_DIM 256
+
+typedef struct sv_kv_cache {
+    void *k, *v;                                     /* dev */
+    int64_t page_stride, slot_stride, head_stride;   /* elements */
+    int32_t n_pages, page_size, kv_heads, head_dim;
+    int32_t dtype;                                   /* sv_dtype */
+} sv_kv_cache;
+
+typedef struct sv_kv_batch {
+    const int32_t *context_len;   /* dev [B] */
+    const int32_t *page_table;    /* dev [B][table_pitch], max_pages used */
+    const int32_t *row_start;     /* dev [B+1] or NULL */
+    const int32_t *parents;       /* dev [B][n-1] or NULL (chain); n - 1 <= SV_MAX_TREE */
+    int64_t table_pitch;
+    int32_t max_pages;
+    int32_t B, n;                 /* sequences; rows of each (the most, with row_start) */
+    int32_t rows;                 /* rows in all (B * n without row_start) */
+} sv_kv_batch;
+
+/* How a head's first rotary_dim elements pair up: (x[i], x[i + rotary_dim/2]) or (x[2i], x[2i+1]). */
+typedef enum sv_rope_style { SV_ROPE_HALF = 0, SV_ROPE_INTERLEAVED = 1 } sv_rope_style;
+
+/* Frequencies for contexts longer than a model was trained on, from f_i = base^(-2i/rotary_dim):
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   BASE    (base * factor^(r/(r-2)))^(-2i/r), r = rotary_dim > 2
+ *   TURNS   f_i (g + (1-g)/factor), g = clamp((original_len f_i / 2pi - low) / (high - low), 0, 1)
+ *   DIMS    f_i (1-h + h/factor), h = clamp((i - d(high)) / (d(low) - d(high)), 0, 1),
+ *           d(n) = r ln(original_len / (2pi n)) / (2 ln base), d(high) rounded down and d(low) up and both
+ *           kept in [0, r - 1] (0.001 apart at least); magnitude 1 + 0.1 ln(factor) */
+typedef enum sv_rope_scaling {
+    SV_ROPE_SCALE_NONE = 0, SV_ROPE_SCALE_LINEAR = 1, SV_ROPE_SCALE_BASE = 2, SV_ROPE_SCALE_TURNS = 3,
+    SV_ROPE_SCALE_DIMS = 4
+} sv_rope_scaling;
+
+/* ----------------------------------------------------------------------------------------
+ * sv_rope_frequencies — inv_freq host float [rotary_dim/2] and the magnitude of sv_rope; host only
+ * (no counterpart on the pages).  factor >= 1 (ignored by NONE); TURNS and DIMS use low < high (number
+ * of turns within original_len tokens; low > 0 for DIMS) and original_len >= 1.
+ * Returns SV_ERR_INVALID_ARG for an odd rotary_dim, one outside 2..SV_KV_MAX_HEAD_DIM, base <= 1, a bad
+ * scaling or null outputs.
+ * -------------------------------------------------------------------------------------- */
+sv_status sv_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double low, double high,
+                              int64_t original_len, float *inv_freq, float *magnitude);
+
+/* ----------------------------------------------------------------------------------------
+ * sv_rope — rotary positions of [rows][heads][head_dim] (no counterpart on the pages).
+ * Pair i of a row at position t turns by the angle t * inv_freq[i] (formed to 2e-6 + 1.5e-14 |t| rad, not
+ * rounded to float32 first) and is scaled by `magnitude`; elements from rotary_dim on are
+ * copied.  backward != 0 applies the transpose: it takes the gradient of the output to the input's.
+ *
+ *  x, out      dev, any strides and alignment (16-byte vectors are used where they allow it); out may be x with
+ *              the same strides, otherwise they must not overlap.
+ *  positions   dev int32 [rows]; inv_freq dev float [rotary_dim/2].
+ * Returns SV_ERR_INVALID_ARG for rows < 0, heads or head_dim < 1, an odd rotary_dim, one above head_dim or
+ * above SV_KV_MAX_HEAD_DIM, a bad style or dtype, or a null pointer.  rows = 0 does nothing.
+ * -------------------------------------------------------------------------------------- */
+sv_status sv_rope(const void *x, int64_t x_row_stride, int64_t x_head_stride, void *out, int64_t out_row_stride,
+                  int64_t out_head_stride, sv_dtype dtype, int64_t rows, int heads, int head_dim,
+                  const int32_t *positions, const float *inv_freq, int rotary_dim, int style, float magnitude,
+                  int backward, sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * sv_kv_append — write a block's keys and values to the cache, rotating keys (and queries) on the
+ * way (no counterpart on the pages).
+ * Row i of sequence b goes to slot context_len[b] + i; its position is context_len[b] plus its depth (i in a
+ * chain).  Rounding to the cache's type happens once, after the rotation.
+ *
+ *  q, q_out    dev or both NULL: the rows' queries, q_heads heads, rotated to q_out (may be q with the same strides).
+ *  k, v        dev, cache->kv_heads heads a row; each with its row and head stride in elements.
+ *  inv_freq    dev float [rotary_dim/2], or NULL with rotary_dim 0: no rotation.
+ * q, k, v, q_out and their strides are 16-byte aligned.
+ * Returns SV_ERR_INVALID_ARG for null required pointers, sizes below 1, head_dim above SV_KV_MAX_HEAD_DIM,
+ * misaligned bases or strides, parents with row_start, or n - 1 > SV_MAX_TREE with parents.
+ * -------------------------------------------------------------------------------------- */
+sv_status sv_kv_append(const sv_kv_cache *cache, const sv_kv_batch *batch, const void *q, int64_t q_row_stride,
+                       int64_t q_head_stride, void *q_out, int64_t q_out_row_stride, int64_t q_out_head_stride,
+                       int q_heads, const void *k, int64_t k_row_stride, int64_t k_head_stride, const void *v,
+                       int64_t v_row_stride, int64_t v_head_stride, const float *inv_freq, int rotary_dim, int style,
+                       float magnitude, sv_stats *stats, sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * sv_kv_attend — attention of the block's rows over the cache, the block's own tokens included
+ * (they have been appended) (no counterpart on the pages).
+ *   out[row][h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j), over the tokens j that the row sees
+ *   lse[row][h] = log sum_j w_j               (a row that sees none: out 0, lse -inf)
+ * Query head h reads key/value head h / (q_heads / kv_heads).
+ *
+ * Shared prefixes.  Sequences group_start[g]..group_start[g+1]-1 declare that their first prefix_len[g] cached
+ * tokens are the same.  These are read once for the whole group, through the page table of its first
+ * sequence; the result is that of reading them once a sequence.  group_start rises from 0 to B,
+ * and prefix_len[g] is at most the context_len of each of its sequences.
+ *
+ * Tokens that a row does not see cannot reach it, whatever their keys and values hold (infinities and NaN
+ * included); slots past the block are not read.
+ *
+ *  q, out       dev, strides in elements, 16-byte aligned; out must not overlap q.
+ *  group_start  dev int32 [n_groups + 1], prefix_len dev int32 [n_groups]; NULL with n_groups 0.
+ *  lse          dev float [rows][q_heads] or NULL.
+ *  workspace    dev, >= sv_kv_attend_workspace_size(rows, q_heads, head_dim, B, n_groups) bytes, 256-byte aligned.
+ * Results do not change from run to run: partial sums are joined in a fixed order.
+ * Returns SV_ERR_INVALID_ARG as sv_kv_append, and for a q_heads that kv_heads does not divide, a scale that is not
+ * finite, or n_groups > B.
+ * -------------------------------------------------------------------------------------- */
+size_t sv_kv_attend_workspace_size(int64_t rows, int q_heads, int head_dim, int B, int n_groups);
+
+sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *batch, const void *q, int64_t q_row_stride,
+                       int64_t q_head_stride, int q_heads, float scale, const int32_t *group_start,
+                       const int32_t *prefix_len, int n_groups, void *out, int64_t out_row_stride,
+                       int64_t out_head_stride, float *lse, sv_stats *stats, void *workspace,
+                       size_t workspace_bytes, sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * sv_kv_commit — after verification, keep the accepted path: for j < accept_len[b] the keys and values of slot
+ * context_len[b] + path[b][j] move to slot context_len[b] + 1 + j, in every layer (no counterpart on the
+ * pages; Mirror-SD notes §3.2 reuse the accepted branch, whose cache this keeps).
+ * path and accept_len are sv_tree_verify's; row 0's slot stays.
+ *
+ *  n_layers, layer_stride   layer l of the cache starts l * layer_stride elements after k (after v).
+ *  accept_len   dev int32 [B]; path dev int32 [B][n-1], rising node ids in 1..n-1.
+ *  context_out  dev int32 [B] or NULL (not context_len itself): context_len[b] + 1 + accept_len[b].
+ * batch->row_start and batch->parents are not used.  An accept_len outside [0, n-1] or a path that does not rise is
+ * reported in stats; that sequence is left as it is, with context_out = context_len.
+ * -------------------------------------------------------------------------------------- */
+sv_status sv_kv_commit(const sv_kv_cache *cache, const sv_kv_batch *batch, int n_layers, int64_t layer_stride,
+                       const int32_t *accept_len, const int32_t *path, int32_t *context_out, sv_stats *stats,
+                       sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
  * sv_set_profile_events — measurement hook (no counterpart on the pages).  begin and end are
  * cudaEvent_t handles (or NULL to disable).  While set, every call made from this host thread
  * records `begin` on its stream just before its statistics pass (the one streaming read of the

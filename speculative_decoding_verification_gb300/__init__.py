@@ -17,7 +17,8 @@ from ._abi import (DBG, SV_BF16, SV_F32, SV_MAX_K, STATS_BYTES, STATS_FIELDS, Sv
                    load, status_string)
 
 __all__ = ["sv_verify", "sv_saguaro_sample", "sv_fanout", "sv_cache_keys", "sv_cache_lookup", "sv_topk_rows",
-           "sv_mirror_reuse", "sv_selftest_timeout", "sv_selftest_exp2", "read_stats", "load", "status_string",
+           "sv_mirror_reuse", "sv_rope_frequencies", "sv_rope", "sv_kv_append", "sv_kv_attend", "sv_kv_commit",
+           "sv_selftest_timeout", "sv_selftest_exp2", "read_stats", "load", "status_string",
            "SvError", "Workspace"]
 
 
@@ -486,6 +487,233 @@ def sv_mirror_reuse(branches, accept_len, out_tokens, reuse=None, stream=None):
                                _stream(stream, dev))
     _abi.check("sv_mirror_reuse", code)
     return reuse
+
+
+def _style(style):
+    code = _abi.SV_ROPE_STYLES.get(style)
+    if code is None:
+        raise ValueError(f"style must be one of {sorted(_abi.SV_ROPE_STYLES)}, got {style!r}")
+    return code
+
+
+def _heads(t, name, like=None):
+    """(row stride, head stride) in elements of a [rows, heads, dim] or [B, n, heads, dim] tensor whose
+    rows lie one stride apart."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name}: expected [rows, heads, dim] or [B, n, heads, dim]")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+        raise ValueError(f"{name}: rows of a sequence must be consecutive rows of one stride")
+    row = t.stride(1) if t.dim() == 4 and t.shape[1] > 1 else t.stride(0)
+    if like is not None:
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    return row, t.stride(-2)
+
+
+def sv_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                        low: float = 1.0, high: float = 32.0, original_len: int = 0):
+    """Host-only: the frequencies of sv_rope (list of rotary_dim/2 floats) and their magnitude.  scaling: "none",
+    "linear", "base", "turns" or "dims" (formulas in specverify.h)."""
+    if scaling not in _abi.SV_ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_abi.SV_ROPE_SCALINGS)}, got {scaling!r}")
+    lib = load()
+    f = (ctypes.c_float * max(1, rotary_dim // 2))()
+    mag = ctypes.c_float(0.0)
+    code = lib.sv_rope_frequencies(int(rotary_dim), float(base), _abi.SV_ROPE_SCALINGS[scaling], float(factor), float(low),
+                                   float(high), int(original_len), ctypes.addressof(f), ctypes.addressof(mag))
+    _abi.check("sv_rope_frequencies", code)
+    return list(f), mag.value
+
+
+def sv_rope(x, positions, inv_freq, style="half", magnitude=1.0, backward=False, out=None, stream=None):
+    """sv_rope: rotary positions of x [rows, heads, dim] or [B, n, heads, dim] (float32 or bfloat16).
+
+    positions int32 [rows]; inv_freq float32 [rotary_dim/2] on the device; style "half" or "interleaved".
+    backward=True takes the gradient of the output to the input's.  out may be x.  Returns out."""
+    lib = load()
+    dev = _cuda(x, "x")
+    row, head = _heads(x, "x")
+    rows, heads, dim = x.shape[:-2].numel(), x.shape[-2], x.shape[-1]
+    _arr(positions, "positions", torch.int32, rows, dev)
+    _arr(inv_freq, "inv_freq", torch.float32, 1, dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape:
+        raise ValueError(f"out must have shape {tuple(x.shape)}")
+    o_row, o_head = _heads(out, "out", x)
+    code = _on(dev, lib.sv_rope, x.data_ptr(), row, head, out.data_ptr(), o_row, o_head, _dtype_code(x), rows, heads, dim,
+               positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), _style(style), float(magnitude),
+               int(bool(backward)), _stream(stream, dev))
+    _abi.check("sv_rope", code)
+    return out
+
+
+def _kv_cache(k_cache, v_cache, dims):
+    """The sv_kv_cache of paged tensors [pages, page_size, kv_heads, dim] (with a leading layer axis where
+    dims is 5): one shape, dtype, device and set of strides for keys and values."""
+    dev = _cuda(k_cache, "k_cache")
+    if k_cache.dim() != dims:
+        raise ValueError(f"k_cache: expected {dims} axes, [{'layers, ' if dims == 5 else ''}pages, page_size, kv_heads, dim]")
+    strides = k_cache.stride()
+    if v_cache.shape != k_cache.shape or v_cache.stride() != strides:
+        raise ValueError("k_cache and v_cache must share their shape and strides")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must share a dtype")
+    if v_cache.device != dev:
+        raise ValueError("k_cache and v_cache must be on one device")
+    shape = k_cache.shape
+    if shape[-1] > 1 and strides[-1] != 1:
+        raise ValueError("k_cache: the last axis must be contiguous")
+    return dev, _abi.SvKvCache(k_cache.data_ptr(), v_cache.data_ptr(), strides[-4], strides[-3], strides[-2], shape[-4],
+                               shape[-3], shape[-2], shape[-1], _dtype_code(k_cache))
+
+
+def _kv_batch(dev, context_len, page_table, rows_of, row_start, parents, max_rows):
+    """The sv_kv_batch of a call whose rows are those of the tensor `rows_of`."""
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != dev or page_table.stride(1) != 1:
+        raise ValueError(f"page_table must be an int32 [B, pages] tensor on {dev} with contiguous rows")
+    B = page_table.shape[0]
+    _arr(context_len, "context_len", torch.int32, B, dev)
+    if row_start is None:
+        if rows_of.dim() != 4 or rows_of.shape[0] != B:
+            raise ValueError(f"without row_start the block's tensors are [B, n, heads, dim] with B = {B}")
+        n = rows_of.shape[1]
+        rows = B * n
+        if parents is not None:
+            _arr(parents, "parents", torch.int32, B * (n - 1), dev)
+    else:
+        if rows_of.dim() != 3:
+            raise ValueError("with row_start the block's tensors are [rows, heads, dim]")
+        if parents is not None:
+            raise ValueError("parents needs blocks of one size (no row_start)")
+        _arr(row_start, "row_start", torch.int32, B + 1, dev)
+        rows = rows_of.shape[0]
+        n = rows if max_rows is None else int(max_rows)
+    return _abi.SvKvBatch(context_len.data_ptr(), page_table.data_ptr(), row_start.data_ptr() if row_start is not None else 0,
+                          parents.data_ptr() if parents is not None else 0, page_table.stride(0), page_table.shape[1], B,
+                          max(n, 1), rows)
+
+
+def sv_kv_append(k, v, k_cache, v_cache, context_len, page_table, q=None, q_out=None, inv_freq=None, style="half",
+                 magnitude=1.0, parents=None, row_start=None, max_rows=None, stats=None, stream=None):
+    """sv_kv_append: write the block's keys and values to the paged cache, rotating keys and queries.
+
+    k, v [B, n, kv_heads, dim], q [B, n, heads, dim] or None (views of one projection are fine); k_cache, v_cache
+    [pages, page_size, kv_heads, dim]; context_len int32 [B]; page_table int32 [B, pages].  inv_freq float32
+    [rotary_dim/2] or None (no rotation).  parents int32 [B, n-1]: the block is a tree (as sv_tree_verify's).
+    row_start int32 [B+1]: ragged blocks, with k, v, q [rows, heads, dim] and at most max_rows rows a sequence.
+    Returns the rotated queries (q_out, which may be q), or None without q.  Device-side errors are written to
+    stats where one is passed (new_stats)."""
+    lib = load()
+    dev, cache = _kv_cache(k_cache, v_cache, 4)
+    k_row, k_head = _heads(k, "k", k_cache)
+    v_row, v_head = _heads(v, "v", k_cache)
+    if k.shape != v.shape or tuple(k.shape[-2:]) != tuple(k_cache.shape[-2:]):
+        raise ValueError("k and v must share a shape that ends in the cache's [kv_heads, dim]")
+    batch = _kv_batch(dev, context_len, page_table, k, row_start, parents, max_rows)
+    if inv_freq is not None:
+        _arr(inv_freq, "inv_freq", torch.float32, 1, dev)
+    q_row = q_head = o_row = o_head = heads = 0
+    if q is not None:
+        q_row, q_head = _heads(q, "q", k_cache)
+        heads = q.shape[-2]
+        if q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+            raise ValueError("q must have the rows and head width of k")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        elif q_out.shape != q.shape:
+            raise ValueError(f"q_out must have shape {tuple(q.shape)}")
+        o_row, o_head = _heads(q_out, "q_out", k_cache)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if stats is not None:
+        _stats(stats, dev)
+    if batch.rows == 0:
+        return q_out
+    code = _on(dev, lib.sv_kv_append, cache, batch, q.data_ptr() if q is not None else 0, q_row, q_head,
+               q_out.data_ptr() if q is not None else 0, o_row, o_head, heads, k.data_ptr(), k_row, k_head, v.data_ptr(),
+               v_row, v_head, inv_freq.data_ptr() if inv_freq is not None else 0,
+               2 * inv_freq.numel() if inv_freq is not None else 0, _style(style), float(magnitude),
+               stats.data_ptr() if stats is not None else 0, _stream(stream, dev))
+    _abi.check("sv_kv_append", code)
+    return q_out
+
+
+def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, parents=None, row_start=None, max_rows=None,
+                 group_start=None, prefix_len=None, out=None, lse=False, stats=None, workspace=None, stream=None):
+    """sv_kv_attend: attention of the block's rows over the paged cache, their own tokens included.
+
+    q [B, n, heads, dim] (or [rows, heads, dim] with row_start); the other arguments as sv_kv_append's.  scale defaults to
+    dim ** -0.5.  group_start int32 [G+1] and prefix_len int32 [G]: the sequences of a group share their first
+    prefix_len tokens, which are read once for all of them.  lse: True, or a float32 tensor of q's shape without
+    the last axis.  Returns (out, lse or None)."""
+    lib = load()
+    dev, cache = _kv_cache(k_cache, v_cache, 4)
+    q_row, q_head = _heads(q, "q", k_cache)
+    heads, dim = q.shape[-2], q.shape[-1]
+    if dim != k_cache.shape[-1]:
+        raise ValueError("q must have the cache's head width")
+    batch = _kv_batch(dev, context_len, page_table, q, row_start, parents, max_rows)
+    groups = 0
+    if (group_start is None) != (prefix_len is None):
+        raise ValueError("group_start and prefix_len come together")
+    if prefix_len is not None:
+        groups = prefix_len.numel()
+        _arr(prefix_len, "prefix_len", torch.int32, 1, dev)
+        _arr(group_start, "group_start", torch.int32, groups + 1, dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must have shape {tuple(q.shape)}")
+    o_row, o_head = _heads(out, "out", k_cache)
+    if lse is True:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    _opt(lse, "lse", torch.float32, batch.rows * heads, dev)
+    if stats is not None:
+        _stats(stats, dev)
+    if batch.rows == 0:
+        return out, lse
+    ws = (workspace or _default_ws).get(lib.sv_kv_attend_workspace_size(batch.rows, heads, dim, batch.B, groups), dev)
+    code = _on(dev, lib.sv_kv_attend, cache, batch, q.data_ptr(), q_row, q_head, heads,
+               float(dim ** -0.5 if scale is None else scale), group_start.data_ptr() if groups else 0,
+               prefix_len.data_ptr() if groups else 0, groups, out.data_ptr(), o_row, o_head,
+               lse.data_ptr() if lse is not None else 0, stats.data_ptr() if stats is not None else 0, ws.data_ptr(),
+               ws.numel(), _stream(stream, dev))
+    _abi.check("sv_kv_attend", code)
+    return out, lse
+
+
+def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, context_out=None, stats=None, stream=None):
+    """sv_kv_commit: after sv_tree_verify, move the accepted path's keys and values to consecutive slots in every
+    layer.  k_cache, v_cache [layers, pages, page_size, kv_heads, dim]; accept_len int32 [B] and path int32 [B, N]
+    as sv_tree_verify gives them.  Returns context_out int32 [B]: context_len + 1 + accept_len."""
+    lib = load()
+    dev, cache = _kv_cache(k_cache, v_cache, 5)
+    B, N = path.shape
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32 or page_table.device != dev or \
+            page_table.stride(1) != 1:
+        raise ValueError(f"page_table must be an int32 [{B}, pages] tensor on {dev} with contiguous rows")
+    _arr(context_len, "context_len", torch.int32, B, dev)
+    _arr(accept_len, "accept_len", torch.int32, B, dev)
+    _arr(path, "path", torch.int32, B * N, dev)
+    if context_out is not None and context_out.data_ptr() == context_len.data_ptr():
+        raise ValueError("context_out must not be context_len")
+    context_out = _out(context_out, "context_out", torch.int32, (B,), dev)
+    if stats is not None:
+        _stats(stats, dev)
+    batch = _abi.SvKvBatch(context_len.data_ptr(), page_table.data_ptr(), 0, 0, page_table.stride(0), page_table.shape[1], B,
+                           N + 1, B * (N + 1))
+    code = _on(dev, lib.sv_kv_commit, cache, batch, k_cache.shape[0], k_cache.stride(0), accept_len.data_ptr(),
+               path.data_ptr() if N else 0, context_out.data_ptr(), stats.data_ptr() if stats is not None else 0,
+               _stream(stream, dev))
+    _abi.check("sv_kv_commit", code)
+    return context_out
 
 
 def sv_selftest_timeout(limit_cycles: int, stats=None, stream=None):

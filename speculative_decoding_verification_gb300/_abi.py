@@ -19,6 +19,10 @@ SV_DEBUG_FIELDS = 8
 SV_MAX_K = 32
 SV_STATIC_SCRATCH_BYTES = 32 << 20
 SV_ACCEPT_DIVERGENCE, SV_ACCEPT_ASSISTED = 0, 1   # sv_accept_mode   # scratch array behind sv_verify_static
+SV_MAX_TREE = 128
+SV_KV_MAX_HEAD_DIM = 256
+SV_ROPE_STYLES = {"half": 0, "interleaved": 1}   # sv_rope_style
+SV_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "turns": 3, "dims": 4}   # sv_rope_scaling
 DBG = dict(lse_q=0, lse_p=1, q_s=2, p_s=3, ratio=4, mass_q=5, mass_p=6, R=7)
 
 
@@ -28,8 +32,23 @@ class SvStats(ctypes.Structure):
                 ("near_boundary", ctypes.c_int64), ("unresolved", ctypes.c_int64)]
 
 
+class SvKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class SvKvBatch(ctypes.Structure):
+    _fields_ = [("context_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("row_start", ctypes.c_void_p),
+                ("parents", ctypes.c_void_p), ("table_pitch", ctypes.c_int64), ("max_pages", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("n", ctypes.c_int32), ("rows", ctypes.c_int32)]
+
+
 STATS_FIELDS = [f for f, _ in SvStats._fields_]
 STATS_BYTES = ctypes.sizeof(SvStats)
+
+c_kv, c_bt = ctypes.POINTER(SvKvCache), ctypes.POINTER(SvKvBatch)
 
 # name -> (restype, argtypes); the order follows the header.
 SIGNATURES = {
@@ -63,6 +82,15 @@ SIGNATURES = {
     "sv_topk_rows_workspace_size": (c_size, [c_int, c_int]),
     "sv_topk_rows": (c_int, [c_vp, c_i64, c_int, c_int, c_int, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
     "sv_mirror_reuse": (c_int, [c_vp, c_vp, c_vp, c_int, c_int, c_int, c_vp, c_vp]),
+    "sv_rope_frequencies": (c_int, [c_int, c_f64, c_int, c_f64, c_f64, c_f64, c_i64, c_vp, c_vp]),
+    "sv_rope": (c_int, [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_int, c_i64, c_int, c_int, c_vp, c_vp, c_int, c_int,
+                        c_f32, c_int, c_vp]),
+    "sv_kv_append": (c_int, [c_kv, c_bt, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_int, c_vp, c_i64, c_i64, c_vp,
+                             c_i64, c_i64, c_vp, c_int, c_int, c_f32, c_vp, c_vp]),
+    "sv_kv_attend_workspace_size": (c_size, [c_i64, c_int, c_int, c_int, c_int]),
+    "sv_kv_attend": (c_int, [c_kv, c_bt, c_vp, c_i64, c_i64, c_int, c_f32, c_vp, c_vp, c_int, c_vp, c_i64, c_i64, c_vp,
+                             c_vp, c_vp, c_size, c_vp]),
+    "sv_kv_commit": (c_int, [c_kv, c_bt, c_int, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "sv_set_profile_events": (None, [c_vp, c_vp]),
     "sv_selftest_timeout": (c_int, [c_i64, c_vp, c_vp]),
     "sv_selftest_exp2": (c_int, [c_f64, c_f64, c_i64, c_vp, c_vp]),

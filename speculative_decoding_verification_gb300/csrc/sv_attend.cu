@@ -1,0 +1,467 @@
+// sv_attend.cu — sv_kv_attend: the float32-arithmetic kernel, the join of partial results, the entry point.
+#include <math.h>
+#include <type_traits>
+
+#include "sv_attend.cuh"
+
+namespace sv {
+
+constexpr int kAttThreads = 256;
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four consecutive elements in shared memory, as float32.
+template <int ES>
+__device__ __forceinline__ float4 lds4(const char *p) {
+    if constexpr (ES == 4) {
+        return *reinterpret_cast<const float4 *>(p);
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+    }
+}
+
+template <int ES, int DP, int TM>
+struct F32Shape {
+    static constexpr int TK = DP == 256 ? 32 : 64;
+    static constexpr int RG = TM / 4;                       // groups of four rows
+    static constexpr int TPR = kAttThreads / RG;            // threads of a row group
+    static constexpr int NK = TK >= TPR ? TK / TPR : 1;     // keys a thread scores
+    static constexpr int CG = DP / 4;                       // groups of four columns
+    static constexpr int KS = TPR > CG ? TPR / CG : 1;      // keys split over threads in the weighted sum
+    static constexpr int NC = TPR > CG ? 1 : CG / TPR;      // column groups of a thread
+    static constexpr int ROW = DP * ES + 16;                // bytes of a key row, padded off the banks
+    static constexpr int SP = TK + 4;                       // floats of a score row
+    static constexpr int ANC = (SV_MAX_TREE + 32) / 32;
+    static constexpr size_t OFF_K = (size_t)TM * DP * 4;
+    static constexpr size_t OFF_V = OFF_K + 2 * (size_t)TK * ROW;
+    static constexpr size_t OFF_S = OFF_V + 2 * (size_t)TK * ROW;
+    static constexpr size_t OFF_M = OFF_S + (size_t)TM * SP * 4;
+    static constexpr size_t BYTES = OFF_M + (size_t)TM * 4 * (4 + ANC) + 64;
+};
+
+// Scores, softmax and weighted sum in float32 FMA, a tile of TM packed rows by TK keys at a time.  Threads hold
+// 4 rows by NK keys of the scores and 4 rows by 4 NC columns of the output; keys and values are
+// double buffered with asynchronous copies.
+template <int ES, int DP, int TM>
+__global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) {
+    using S = F32Shape<ES, DP, TM>;
+    constexpr int TK = S::TK;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ Walk s_walk;
+    float *sq = reinterpret_cast<float *>(smem);
+    char *sk = smem + S::OFF_K, *sv_ = smem + S::OFF_V;
+    float *ss = reinterpret_cast<float *>(smem + S::OFF_S);
+    float *row_m = reinterpret_cast<float *>(smem + S::OFF_M), *row_l = row_m + TM, *row_a = row_l + TM;
+    int *row_lim = reinterpret_cast<int *>(row_a + TM);
+    uint32_t *row_anc = reinterpret_cast<uint32_t *>(row_lim + TM);
+
+    walk_start<kAttThreads>(a, &s_walk);
+    Walk w = s_walk;
+    const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+    const int D = a.c.head_dim, D4 = D / 4, chunks = D * ES / 16;
+    const int rg = tid / S::TPR, tx = tid % S::TPR;
+    const int cx = tx % S::CG, ks = S::KS > 1 ? tx / S::CG : 0;
+    Piece p;
+    while (w.next(a, p)) {
+        const int m0 = p.t * TM, h = p.h;
+        const int32_t *table = a.bt.page_table + p.g.table * a.bt.table_pitch;
+        auto load_tile = [&](int k, int buf) {
+            const int first = p.g.key0 + k * TK + wp * (TK / 8);
+            int64_t off = -1;
+            if (lane < TK / 8 && first + lane < p.end) {
+                off = slot_offset(a.c, table, first + lane);
+                if (off < 0) report_error(a.stats, SV_ERR_INVALID_ARG, p.g.table);
+            }
+#pragma unroll
+            for (int r = 0; r < TK / 8; ++r) {
+                const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+                const size_t dst = (size_t)(buf * TK + wp * (TK / 8) + r) * S::ROW;
+                for (int c = lane; c < chunks; c += 32) {
+                    const int64_t src = o < 0 ? 0 : o + h * a.c.head_b + c * 16;
+                    cp_async16(sk + dst + c * 16, a.c.k + src, o >= 0);
+                    cp_async16(sv_ + dst + c * 16, a.c.v + src, o >= 0);
+                }
+            }
+            cp_async_commit();
+        };
+        load_tile(p.k0, 0);
+        for (int i = tid; i < TM * D4; i += kAttThreads) {
+            const int m = i / D4, d = i - m * D4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (m < p.vr) {
+                const int r = (m0 + m) / a.G, g = m0 + m - r * a.G;
+                const char *src = a.q + (int64_t)(p.g.r0 + r) * a.q_row + (int64_t)(h * a.G + g) * a.q_head + d * 4 * ES;
+                x = lds4<ES>(src);
+            }
+            *reinterpret_cast<float4 *>(sq + m * DP + d * 4) = x;
+        }
+        const bool tree = !p.g.chain && p.seg >= a.n_groups;
+        if (tid < TM) {
+            const int i = (m0 + tid) / a.G;
+            row_m[tid] = -INFINITY;
+            row_l[tid] = 0.0f;
+            row_lim[tid] = tid >= p.vr ? 0 : p.g.chain ? min(p.g.ctx + i + 1, p.end) : tree ? p.g.ctx : p.end;
+            if (tree) {
+                uint32_t anc[S::ANC] = {};
+                if (tid < p.vr) ancestor_words(a.bt.parents + (int64_t)p.g.table * (a.bt.n - 1), i, a.bt.n, anc, a.stats, p.g.table);
+#pragma unroll
+                for (int j = 0; j < S::ANC; ++j) row_anc[tid * S::ANC + j] = anc[j];
+            }
+        }
+        float4 acc[4][S::NC];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < S::NC; ++c) acc[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+
+        for (int k = p.k0; k < p.k1; ++k) {
+            const int buf = (k - p.k0) & 1;
+            if (k + 1 < p.k1) {
+                load_tile(k + 1, buf ^ 1);
+                cp_async_wait<1>();
+            } else {
+                cp_async_wait<0>();
+            }
+            __syncthreads();
+            const char *tk = sk + (size_t)buf * TK * S::ROW, *tv = sv_ + (size_t)buf * TK * S::ROW;
+            const int first = p.g.key0 + k * TK;
+            if (tx < TK) {
+                float s[4][S::NK] = {};
+                for (int d = 0; d < D4; ++d) {
+                    float4 qv[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) qv[r] = *reinterpret_cast<const float4 *>(sq + (rg * 4 + r) * DP + d * 4);
+#pragma unroll
+                    for (int j = 0; j < S::NK; ++j) {
+                        const float4 kv = lds4<ES>(tk + (size_t)(tx + j * S::TPR) * S::ROW + d * 4 * ES);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            s[r][j] = fmaf(qv[r].x, kv.x, fmaf(qv[r].y, kv.y, fmaf(qv[r].z, kv.z, fmaf(qv[r].w, kv.w, s[r][j]))));
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int j = 0; j < S::NK; ++j) ss[(rg * 4 + r) * S::SP + tx + j * S::TPR] = s[r][j] * a.scale_log2;
+            }
+            __syncthreads();
+            // softmax: a warp takes rows wp, wp + 8, ...
+            for (int m = wp; m < TM; m += 8) {
+                const int lim = row_lim[m];
+                float x[TK / 32], top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < TK / 32; ++j) {
+                    const int key = first + lane + j * 32;
+                    bool sees = key < lim;
+                    if (tree && m < p.vr && key >= p.g.ctx && key < p.end) {
+                        const int rel = key - p.g.ctx;
+                        sees = (row_anc[m * S::ANC + (rel >> 5)] >> (rel & 31)) & 1u;
+                    }
+                    x[j] = sees ? ss[m * S::SP + lane + j * 32] : -INFINITY;
+                    top = fmaxf(top, x[j]);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                const float m_old = row_m[m], m_new = fmaxf(m_old, top);
+                const float base = m_new == -INFINITY ? 0.0f : m_new;
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < TK / 32; ++j) {
+                    const float e = exp2f(x[j] - base);
+                    ss[m * S::SP + lane + j * 32] = e;
+                    sum += e;
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                __syncwarp();
+                if (lane == 0) {
+                    const float alpha = exp2f(m_old - base);
+                    row_a[m] = alpha;
+                    row_m[m] = m_new;
+                    row_l[m] = row_l[m] * alpha + sum;
+                }
+            }
+            __syncthreads();
+            // A tile in which some row does not see some key multiplies only where the weight is not zero: 0 * inf
+            // of a token that is not seen must not reach the sum.
+            const bool masked = first + TK > p.end || (p.seg >= a.n_groups && first + TK > p.g.ctx);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float al = row_a[rg * 4 + r];
+#pragma unroll
+                for (int c = 0; c < S::NC; ++c) {
+                    acc[r][c].x *= al;
+                    acc[r][c].y *= al;
+                    acc[r][c].z *= al;
+                    acc[r][c].w *= al;
+                }
+            }
+            auto weigh = [&](auto guard) {
+                for (int k4 = ks * 4; k4 < TK; k4 += 4 * S::KS) {
+                    float4 pw[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) pw[r] = *reinterpret_cast<const float4 *>(ss + (rg * 4 + r) * S::SP + k4);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                        for (int c = 0; c < S::NC; ++c) {
+                            const float4 v = lds4<ES>(tv + (size_t)(k4 + u) * S::ROW + (cx + c * S::TPR) * 4 * ES);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float e = u == 0 ? pw[r].x : u == 1 ? pw[r].y : u == 2 ? pw[r].z : pw[r].w;
+                                if (!guard.value || e != 0.0f) {
+                                    acc[r][c].x = fmaf(e, v.x, acc[r][c].x);
+                                    acc[r][c].y = fmaf(e, v.y, acc[r][c].y);
+                                    acc[r][c].z = fmaf(e, v.z, acc[r][c].z);
+                                    acc[r][c].w = fmaf(e, v.w, acc[r][c].w);
+                                }
+                            }
+                        }
+                    }
+                }
+            };
+            if (masked) weigh(std::true_type{});
+            else weigh(std::false_type{});
+            __syncthreads();
+        }
+        // join the threads that split the keys
+        if constexpr (S::KS > 1) {
+            float *red = reinterpret_cast<float *>(smem + S::OFF_K);   // [KS - 1][TM][DP]: the key buffers are free
+            static_assert((size_t)(S::KS - 1) * TM * DP * 4 <= S::OFF_S - S::OFF_K, "fits the key and value buffers");
+            if (ks > 0) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<float4 *>(red + ((size_t)(ks - 1) * TM + rg * 4 + r) * DP + cx * 4) = acc[r][0];
+            }
+            __syncthreads();
+            if (ks == 0) {
+#pragma unroll
+                for (int j = 0; j < S::KS - 1; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float4 o = *reinterpret_cast<const float4 *>(red + ((size_t)j * TM + rg * 4 + r) * DP + cx * 4);
+                        acc[r][0].x += o.x;
+                        acc[r][0].y += o.y;
+                        acc[r][0].z += o.z;
+                        acc[r][0].w += o.w;
+                    }
+            }
+        }
+        const bool whole = p.k0 == 0 && p.k1 == p.kt && p.seg >= a.n_groups && seg_alone(p.g);
+        const size_t slot = unit_slot(a, p.g, p.seg < a.n_groups, h, p.t) + (size_t)blockIdx.x * TM;
+        if (ks == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int m = rg * 4 + r;
+                if (m >= p.vr) continue;
+                const float l = row_l[m], inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                const int i = (m0 + m) / a.G, g = m0 + m - i * a.G;
+                char *dst = a.out + (int64_t)(p.g.r0 + i) * a.o_row + (int64_t)(h * a.G + g) * a.o_head;
+#pragma unroll
+                for (int c = 0; c < S::NC; ++c) {
+                    const int col = cx + c * S::TPR;
+                    if (col >= D4) continue;
+                    float4 o = acc[r][c];
+                    if (!whole) {
+                        *reinterpret_cast<float4 *>(a.part + (slot + m) * D + col * 4) = o;
+                    } else if constexpr (ES == 4) {
+                        *reinterpret_cast<float4 *>(dst + col * 16) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                    } else {
+                        const float f[8] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv, 0.f, 0.f, 0.f, 0.f};
+                        const uint4 wv = pack16<2>(f);
+                        *reinterpret_cast<uint2 *>(dst + col * 8) = make_uint2(wv.x, wv.y);
+                    }
+                }
+            }
+        }
+        if (tid < p.vr) {
+            if (!whole) {
+                a.part_ml[slot + tid] = make_float2(row_m[tid], row_l[tid]);
+            } else if (a.lse) {
+                const int i = (m0 + tid) / a.G, g = m0 + tid - i * a.G;
+                const float l = row_l[tid];
+                a.lse[(size_t)(p.g.r0 + i) * a.q_heads + h * a.G + g] = l == 0.0f ? -INFINITY : (row_m[tid] + log2f(l)) / kLog2e;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Adds the pieces of a row's units: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  One warp a (row, query
+// head), prefix pieces first, then own ones, each in the order of the blocks that made them.
+template <int ES>
+__global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a) {
+    pdl_wait();
+    const long long w = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (w >= (long long)a.bt.rows * a.q_heads) return;
+    const int row = (int)(w / a.q_heads), qh = (int)(w - (long long)row * a.q_heads);
+    const int h = qh / a.G;
+    const int NS = a.n_groups + a.bt.B;
+    const long long total = a.seg_off[NS];
+    const int b = row_sequence(a.bt, row);
+    const int D = a.c.head_dim, D4 = D / 4;
+    float m = -INFINITY, l = 0.0f;
+    float4 o[2] = {};
+    for (int which = a.n_groups ? 0 : 1; which < 2; ++which) {
+        const int s = which == 0 ? group_of(a, b) : a.n_groups + b;
+        const Seg g = seg_of(a, s, false);
+        if (row < g.r0 || row >= g.r0 + g.n || total == 0) continue;
+        const int mm = (row - g.r0) * a.G + (qh - h * a.G), t = mm / a.TM;
+        const int kt = seg_tiles(a, g, t);
+        if (kt <= 0) continue;
+        const long long per = seg_head_tiles(a, g);
+        long long first = a.seg_off[s] + per * h;
+        if (!g.chain) first += (long long)t * kt;
+        else
+            for (int u = 0; u < t; ++u) first += seg_tiles(a, g, u);
+        const int parts = range_blocks(total, a.blocks);
+        const int c0 = block_of_tile(first, total, parts), c1 = block_of_tile(first + kt - 1, total, parts);
+        if (which == 1 && c0 == c1 && seg_alone(g)) return;   // written by its piece
+        const size_t base = unit_slot(a, g, which == 0, h, t) + (mm - t * a.TM);
+        for (int c = c0; c <= c1; ++c) {
+            const size_t slot = base + (size_t)c * a.TM;
+            const float2 ml = a.part_ml[slot];
+            if (ml.y == 0.0f) continue;   // the row saw none of the piece's tokens
+            const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.0f : top;
+            const float f0 = exp2f(m - ref), f1 = exp2f(ml.x - ref);
+            m = top;
+            l = l * f0 + ml.y * f1;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int col = lane + 32 * j;
+                if (col < D4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(a.part + slot * D + col * 4);
+                    o[j].x = o[j].x * f0 + x.x * f1;
+                    o[j].y = o[j].y * f0 + x.y * f1;
+                    o[j].z = o[j].z * f0 + x.z * f1;
+                    o[j].w = o[j].w * f0 + x.w * f1;
+                }
+            }
+        }
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    char *dst = a.out + (int64_t)row * a.o_row + (int64_t)qh * a.o_head;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int col = lane + 32 * j;
+        if (col >= D4) continue;
+        const float4 x = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
+        if constexpr (ES == 4) {
+            *reinterpret_cast<float4 *>(dst + col * 16) = x;
+        } else {
+            const float f[8] = {x.x, x.y, x.z, x.w, 0.f, 0.f, 0.f, 0.f};
+            const uint4 wv = pack16<2>(f);
+            *reinterpret_cast<uint2 *>(dst + col * 8) = make_uint2(wv.x, wv.y);
+        }
+    }
+    if (a.lse && lane == 0) a.lse[(size_t)row * a.q_heads + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) / kLog2e;
+}
+
+cudaError_t launch_attend_join(const AttendArgs &a, int es, cudaStream_t stream) {
+    const long long warps = (long long)a.bt.rows * a.q_heads;
+    const dim3 grid((unsigned)((warps + 7) / 8));
+    return es == 4 ? launch_pdl(k_attend_join<4>, grid, dim3(256), 0, stream, a)
+                   : launch_pdl(k_attend_join<2>, grid, dim3(256), 0, stream, a);
+}
+
+template <int ES, int DP, int TM>
+static sv_status run_f32(AttendArgs &a, const DeviceInfo &di, cudaStream_t stream) {
+    using S = F32Shape<ES, DP, TM>;
+    const int res = prepare_kernel((const void *)k_attend_f32<ES, DP, TM>, kAttThreads, S::BYTES);
+    if (res < 1) return SV_ERR_CUDA;
+    a.TM = TM;
+    a.TK = S::TK;
+    a.blocks = di.sms;
+    k_attend_f32<ES, DP, TM><<<a.blocks, kAttThreads, S::BYTES, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+    return cuda_status(launch_attend_join(a, ES, stream));
+}
+
+sv_status launch_attend_f32(AttendArgs a, int es, const DeviceInfo &di, cudaStream_t stream) {
+    const int D = a.c.head_dim;
+    const bool small = a.bt.n * a.G <= 16 && a.n_groups == 0;
+#define SV_ATT(ES, DP) (small ? run_f32<ES, DP, 16>(a, di, stream) : run_f32<ES, DP, 64>(a, di, stream))
+    if (es == 4) return D <= 64 ? SV_ATT(4, 64) : D <= 128 ? SV_ATT(4, 128) : SV_ATT(4, 256);
+    return D <= 64 ? SV_ATT(2, 64) : D <= 128 ? SV_ATT(2, 128) : SV_ATT(2, 256);
+#undef SV_ATT
+}
+
+// Tiles hold up to 256 rows.
+constexpr int kAttMaxTile = 256;
+
+AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, int n_groups, int blocks) {
+    AttendPlan p;
+    Carver cv;
+    const size_t slots = attend_slots(rows, q_heads, n_groups, kAttMaxTile, blocks);
+    p.off_seg = cv.take<long long>((size_t)n_groups + B + 1);
+    p.off_ml = cv.take<float2>(slots);
+    p.off_part = cv.take<float>(slots * head_dim);
+    p.bytes = cv.off + 256;
+    return p;
+}
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t sv_kv_attend_workspace_size(int64_t rows, int q_heads, int head_dim, int B, int n_groups) {
+    if (rows < 0 || q_heads < 1 || head_dim < 1 || head_dim > SV_KV_MAX_HEAD_DIM || B < 1 || n_groups < 0) return 0;
+    return plan_attend(rows, q_heads, head_dim, B, n_groups, kAttBlocks).bytes;
+}
+
+extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *batch, const void *q,
+                                  int64_t q_row_stride, int64_t q_head_stride, int q_heads, float scale,
+                                  const int32_t *group_start, const int32_t *prefix_len, int n_groups, void *out,
+                                  int64_t out_row_stride, int64_t out_head_stride, float *lse, sv_stats *stats,
+                                  void *workspace, size_t workspace_bytes, sv_stream_t stream) {
+    if (!kv_args_ok(cache, batch, true) || q_heads < 1 || q_heads % cache->kv_heads != 0 || !isfinite(scale))
+        return SV_ERR_INVALID_ARG;
+    if (n_groups < 0 || n_groups > batch->B || (n_groups > 0 && (group_start == nullptr || prefix_len == nullptr)))
+        return SV_ERR_INVALID_ARG;
+    const int es = elem_size((sv_dtype)cache->dtype);
+    if (batch->rows > 0 && (q == nullptr || out == nullptr)) return SV_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !strides16(es, q_row_stride, q_head_stride) ||
+        !strides16(es, out_row_stride, out_head_stride) || (int64_t)batch->rows * q_heads > INT32_MAX)
+        return SV_ERR_INVALID_ARG;
+    const AttendPlan pl = plan_attend(batch->rows, q_heads, cache->head_dim, batch->B, n_groups, kAttBlocks);
+    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.bytes) return SV_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!on_current_device(s, cache->k, q)) return SV_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (!device_info(di)) return SV_ERR_CUDA;
+    if (di.sms > kAttBlocks) di.sms = kAttBlocks;
+    if (stats && cudaMemsetAsync(stats, 0, sizeof(sv_stats), s) != cudaSuccess) return SV_ERR_CUDA;
+    if (batch->rows == 0) return SV_OK;
+    char *w = static_cast<char *>(workspace);
+    AttendArgs a{};
+    a.c = kv_cache_of(*cache);
+    a.bt = kv_batch_of(*batch);
+    a.q = static_cast<const char *>(q);
+    a.out = static_cast<char *>(out);
+    a.q_row = q_row_stride * es;
+    a.q_head = q_head_stride * es;
+    a.o_row = out_row_stride * es;
+    a.o_head = out_head_stride * es;
+    a.q_heads = q_heads;
+    a.G = q_heads / cache->kv_heads;
+    a.scale_log2 = (float)((double)scale * 1.44269504088896340736);
+    a.group_start = group_start;
+    a.prefix_len = prefix_len;
+    a.n_groups = n_groups;
+    a.lse = lse;
+    a.stats = stats;
+    a.seg_off = reinterpret_cast<long long *>(w + pl.off_seg);
+    a.part_ml = reinterpret_cast<float2 *>(w + pl.off_ml);
+    a.part = reinterpret_cast<float *>(w + pl.off_part);
+    return launch_attend_f32(a, es, di, s);
+}

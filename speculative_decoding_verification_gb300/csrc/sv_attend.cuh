@@ -1,0 +1,284 @@
+// sv_attend.cuh — how sv_kv_attend's work is cut up, shared by its kernels.
+//
+// Segments.  Each group's shared prefix is one segment, read with the rows of all its sequences; each
+// sequence's own tokens (from its prefix's end to its block's end) are another.  Inside a segment, rows and
+// the query heads of one key/value head are packed: packed row m is row m / G, head m % G of the G =
+// q_heads / kv_heads that share it, so that keys are read once for all of them.
+//
+// Units and tiles.  A unit is (segment, key/value head, tile of TM packed rows); it walks its keys in tiles of TK.
+// All tiles of all units, in order, are cut into one equal range a block, whatever the lengths are: a block's
+// range starts and ends inside units.  The part of a unit in one block is a piece; it leaves its running
+// maximum, sum and weighted values in the workspace, and k_attend_join adds a row's pieces in order.  A unit
+// that is one piece and the only one of its rows writes its output itself.
+//
+// Everything is derived from device arrays inside the call; the host knows bounds only.
+#pragma once
+
+#include "sv_kv.cuh"
+
+namespace sv {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct AttendArgs {
+    KvCache c;
+    KvBatch bt;
+    const char *q;
+    char *out;
+    int64_t q_row, q_head, o_row, o_head;   // bytes
+    int q_heads, G;
+    float scale_log2;                       // scale * log2(e)
+    const int32_t *group_start, *prefix_len;
+    int n_groups;
+    float *lse;
+    sv_stats *stats;
+    // geometry of the launch
+    int TM, TK, blocks;
+    // workspace
+    long long *seg_off;   // [n_groups + B + 1] first tile of each segment, in the unit order
+    float *part;          // [slots][head_dim] weighted values of a packed row of a piece
+    float2 *part_ml;      // [slots] its maximum (of scale * log2(e) * q.k) and sum
+};
+
+// Slots: a piece of unit u in block c starts at unit_slot(u) + c * TM.  Units' slots rise by their rows and
+// blocks' by TM, and along the walk either the unit or the block moves on, so pieces never share a slot.
+inline size_t attend_slots(int64_t rows, int q_heads, int n_groups, int TM, int blocks) {
+    return (size_t)rows * q_heads * (n_groups > 0 ? 2 : 1) + (size_t)TM * blocks;
+}
+
+struct Seg {
+    int r0, n;            // its rows
+    int table;            // sequence whose page table it reads
+    int key0, end;        // its tokens: [key0, end)
+    int ctx;              // own segments: cached tokens before the block; prefixes: end
+    int packed, tiles_m;  // packed rows; tiles of TM of them
+    bool chain;           // row i sees tokens up to ctx + i only
+};
+
+// The group of sequence b: the last g with group_start[g] <= b.
+__device__ __forceinline__ int group_of(const AttendArgs &a, int b) {
+    int lo = 0, hi = a.n_groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.group_start[mid] <= b) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int clamp_int(long long x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : (int)x; }
+
+// Segment s, with every device value clamped to what the arrays hold.  `check` reports what had to be.
+__device__ __forceinline__ Seg seg_of(const AttendArgs &a, int s, bool check) {
+    Seg g;
+    const int cap = a.bt.max_pages * a.c.page_size;
+    if (s < a.n_groups) {
+        const int b0 = clamp_int(a.group_start[s], 0, a.bt.B - 1), b1 = clamp_int(a.group_start[s + 1], b0, a.bt.B);
+        const int len = a.prefix_len[s];
+        g.r0 = b1 > b0 ? seq_rows(a.bt, b0).r0 : 0;
+        int r1 = g.r0;
+        if (b1 > b0) {
+            const SeqRows last = seq_rows(a.bt, b1 - 1);
+            r1 = clamp_int((long long)last.r0 + last.n, g.r0, a.bt.rows);
+        }
+        g.n = r1 - g.r0;
+        g.table = b0;
+        g.key0 = 0;
+        g.end = clamp_int(len, 0, cap);
+        g.ctx = g.end;
+        g.chain = false;
+        if (check && (g.end != len || a.group_start[s] != b0 || a.group_start[s + 1] != b1 || (s == 0 && b0 != 0) ||
+                      (s == a.n_groups - 1 && b1 != a.bt.B)))
+            report_error(a.stats, SV_ERR_INVALID_ARG, b0);
+    } else {
+        const int b = s - a.n_groups;
+        const SeqRows sr = seq_rows(a.bt, b);
+        const int ctx = a.bt.context_len[b];
+        const int start = a.n_groups ? a.prefix_len[group_of(a, b)] : 0;
+        g.r0 = sr.r0;
+        g.n = sr.n;
+        g.table = b;
+        g.ctx = clamp_int(ctx, 0, cap);
+        g.key0 = clamp_int(start, 0, g.ctx);
+        g.end = clamp_int((long long)g.ctx + sr.n, 0, cap);
+        g.chain = a.bt.parents == nullptr;
+        if (check && (!sr.ok || g.ctx != ctx || g.key0 != start || (long long)g.ctx + sr.n > cap))
+            report_error(a.stats, SV_ERR_INVALID_ARG, b);
+    }
+    g.packed = g.n * a.G;
+    g.tiles_m = (g.packed + a.TM - 1) / a.TM;
+    return g;
+}
+
+// One past the last token that row tile t of the segment sees, and its tiles of keys.
+__device__ __forceinline__ int seg_end(const AttendArgs &a, const Seg &g, int t) {
+    if (!g.chain) return g.end;
+    const int last = min((t + 1) * a.TM, g.packed) - 1;
+    return min(g.ctx + last / a.G + 1, g.end);
+}
+
+__device__ __forceinline__ int seg_tiles(const AttendArgs &a, const Seg &g, int t) {
+    return (seg_end(a, g, t) - g.key0 + a.TK - 1) / a.TK;
+}
+
+__device__ __forceinline__ long long seg_head_tiles(const AttendArgs &a, const Seg &g) {
+    if (!g.chain) return (long long)g.tiles_m * seg_tiles(a, g, 0);
+    long long n = 0;
+    for (int t = 0; t < g.tiles_m; ++t) n += seg_tiles(a, g, t);
+    return n;
+}
+
+// First workspace slot of unit (h, t) of a segment.
+__device__ __forceinline__ size_t unit_slot(const AttendArgs &a, const Seg &g, bool prefix, int h, int t) {
+    const size_t own = a.n_groups > 0 && !prefix ? (size_t)a.bt.rows * a.q_heads : 0;
+    return own + (size_t)g.r0 * a.q_heads + (size_t)h * g.packed + (size_t)t * a.TM;
+}
+
+// Ranges are those of the first range_blocks blocks, so that none is empty: range c is
+// [total c / parts, total (c + 1) / parts).
+__device__ __forceinline__ int range_blocks(long long total, int blocks) { return (int)min(total, (long long)blocks); }
+
+// The block whose range holds tile x.
+__device__ __forceinline__ int block_of_tile(long long x, long long total, int parts) {
+    return (int)(((x + 1) * parts - 1) / total);
+}
+
+// A row's output is complete in its own piece when no prefix adds to it.
+__device__ __forceinline__ bool seg_alone(const Seg &g) { return g.key0 == 0; }
+
+struct Piece {
+    Seg g;
+    int seg, h, t;      // unit
+    int vr;             // packed rows of the unit, the first at t * TM
+    int k0, k1, kt;     // tiles of keys [k0, k1) of kt
+    int end;            // one past the last token the unit sees
+};
+
+// Walks the pieces of one block's range [pos, stop) of tiles.
+struct Walk {
+    long long pos, stop, seg_start, per_head;
+    int s;
+    Seg g;
+
+    __device__ __forceinline__ void open(const AttendArgs &a) {
+        g = seg_of(a, s, false);
+        per_head = seg_head_tiles(a, g);
+    }
+
+    __device__ __forceinline__ bool next(const AttendArgs &a, Piece &p) {
+        if (pos >= stop) return false;
+        while (pos >= seg_start + per_head * a.c.kv_heads) {
+            seg_start += per_head * a.c.kv_heads;
+            ++s;
+            open(a);
+        }
+        const long long at = pos - seg_start;
+        int rem;
+        p.h = (int)(at / per_head);
+        rem = (int)(at - p.h * per_head);
+        p.t = 0;
+        p.kt = seg_tiles(a, g, 0);
+        if (!g.chain) {
+            p.t = rem / p.kt;
+            rem -= p.t * p.kt;
+        } else {
+            while (rem >= p.kt) {
+                rem -= p.kt;
+                p.kt = seg_tiles(a, g, ++p.t);
+            }
+        }
+        p.g = g;
+        p.seg = s;
+        p.vr = min(a.TM, g.packed - p.t * a.TM);
+        p.k0 = rem;
+        p.k1 = (int)min((long long)p.kt, rem + (stop - pos));
+        p.end = seg_end(a, g, p.t);
+        pos += p.k1 - p.k0;
+        return true;
+    }
+};
+
+// Block-wide: the total of tiles and, for this block's range, where its walk starts.  Each thread takes a
+// run of consecutive segments.  Block 0 leaves the segments' offsets for the join and reports bad input.
+template <int THREADS>
+__device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w) {
+    __shared__ long long warp_sum[THREADS / 32];
+    const int NS = a.n_groups + a.bt.B;
+    const int each = (NS + THREADS - 1) / THREADS;
+    const int s0 = min((int)threadIdx.x * each, NS), s1 = min(s0 + each, NS);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += seg_head_tiles(a, seg_of(a, s, blockIdx.x == 0)) * a.c.kv_heads;
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    long long inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+        if (lane >= d) inc += v;
+    }
+    if (lane == 31) warp_sum[wp] = inc;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < wp) before += warp_sum[i];
+        total += warp_sum[i];
+    }
+    const int parts = range_blocks(total, a.blocks), c = min((int)blockIdx.x, parts);
+    const long long pos = total * c / max(parts, 1), stop = total * min(c + 1, parts) / max(parts, 1);
+    if (threadIdx.x == 0 && pos >= stop) w->pos = w->stop = 0;
+    long long at = before;
+    for (int s = s0; s < s1; ++s) {
+        const Seg g = seg_of(a, s, false);
+        const long long per = seg_head_tiles(a, g), n = per * a.c.kv_heads;
+        if (pos < stop && pos >= at && pos < at + n) {
+            w->pos = pos;
+            w->stop = stop;
+            w->s = s;
+            w->seg_start = at;
+            w->g = g;
+            w->per_head = per;
+        }
+        if (blockIdx.x == 0) {
+            a.seg_off[s] = at;
+            if (s == NS - 1) a.seg_off[NS] = at + n;
+        }
+        at += n;
+    }
+    __syncthreads();
+}
+
+// Whether a row sees block token j (both as rows of the block), for a tree: j is the row or an ancestor of it.
+// parents[i - 1] < i is checked by the caller that fills the words.
+__device__ __forceinline__ void ancestor_words(const int32_t *parents, int i, int n, uint32_t (&w)[(SV_MAX_TREE + 32) / 32],
+                                               sv_stats *stats, int b) {
+#pragma unroll
+    for (int k = 0; k < (SV_MAX_TREE + 32) / 32; ++k) w[k] = 0;
+    for (int steps = 0; i >= 0 && steps < n; ++steps) {
+#pragma unroll
+        for (int k = 0; k < (SV_MAX_TREE + 32) / 32; ++k)
+            if ((i >> 5) == k) w[k] |= 1u << (i & 31);
+        if (i == 0) break;
+        const int p = parents[i - 1];
+        if (p < 0 || p >= i) {
+            report_error(stats, SV_ERR_INVALID_ARG, b);
+            break;
+        }
+        i = p;
+    }
+}
+
+// k_attend_join: adds the pieces of each row, one warp a (row, query head).
+cudaError_t launch_attend_join(const AttendArgs &a, int es, cudaStream_t stream);
+
+// The kernels, each followed by the join.  attend_f32 (any head_dim, float32 arithmetic) and attend_tc (bf16,
+// head_dim <= 128, tensor cores).
+sv_status launch_attend_f32(AttendArgs a, int es, const DeviceInfo &di, cudaStream_t stream);
+
+// Workspace of a call: segment offsets, then the slots of the widest tiles on the most blocks.
+constexpr int kAttBlocks = 160;   // most persistent blocks (a GB300 has 152 SMs)
+struct AttendPlan {
+    size_t off_seg = 0, off_ml = 0, off_part = 0, bytes = 0;
+};
+AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, int n_groups, int blocks);
+
+}  // namespace sv
