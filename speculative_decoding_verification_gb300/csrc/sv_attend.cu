@@ -8,16 +8,6 @@ namespace sv {
 
 constexpr int kAttThreads = 256;
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(valid ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Four consecutive elements in shared memory, as float32.
 template <int ES>
 __device__ __forceinline__ float4 lds4(const char *p) {
@@ -57,6 +47,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     constexpr int TK = S::TK;
     extern __shared__ __align__(128) char smem[];
     __shared__ Walk s_walk;
+    __shared__ long long warp_sum[kAttThreads / 32];
     float *sq = reinterpret_cast<float *>(smem);
     char *sk = smem + S::OFF_K, *sv_ = smem + S::OFF_V;
     float *ss = reinterpret_cast<float *>(smem + S::OFF_S);
@@ -64,7 +55,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     int *row_lim = reinterpret_cast<int *>(row_a + TM);
     uint32_t *row_anc = reinterpret_cast<uint32_t *>(row_lim + TM);
 
-    walk_start<kAttThreads>(a, &s_walk);
+    walk_start<kAttThreads>(a, &s_walk, warp_sum);
     Walk w = s_walk;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
     const int D = a.c.head_dim, D4 = D / 4, chunks = D * ES / 16;
@@ -87,8 +78,8 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
                 const size_t dst = (size_t)(buf * TK + wp * (TK / 8) + r) * S::ROW;
                 for (int c = lane; c < chunks; c += 32) {
                     const int64_t src = o < 0 ? 0 : o + h * a.c.head_b + c * 16;
-                    cp_async16(sk + dst + c * 16, a.c.k + src, o >= 0);
-                    cp_async16(sv_ + dst + c * 16, a.c.v + src, o >= 0);
+                    cp_async16(smem_addr(sk + dst + c * 16), a.c.k + src, o >= 0);
+                    cp_async16(smem_addr(sv_ + dst + c * 16), a.c.v + src, o >= 0);
                 }
             }
             cp_async_commit();
@@ -463,5 +454,7 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     a.seg_off = reinterpret_cast<long long *>(w + pl.off_seg);
     a.part_ml = reinterpret_cast<float2 *>(w + pl.off_ml);
     a.part = reinterpret_cast<float *>(w + pl.off_part);
+    // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.
+    if (es == 2 && cache->head_dim <= 128) return launch_attend_tc(a, di, s);
     return launch_attend_f32(a, es, di, s);
 }

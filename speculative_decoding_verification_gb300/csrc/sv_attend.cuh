@@ -199,10 +199,9 @@ struct Walk {
 };
 
 // Block-wide: the total of tiles and, for this block's range, where its walk starts.  Each thread takes a
-// run of consecutive segments.  Block 0 leaves the segments' offsets for the join and reports bad input.
+// run of consecutive segments; warp_sum has THREADS / 32 places.  Block 0 leaves the segments' offsets for the join and reports bad input.
 template <int THREADS>
-__device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w) {
-    __shared__ long long warp_sum[THREADS / 32];
+__device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long long *warp_sum) {
     const int NS = a.n_groups + a.bt.B;
     const int each = (NS + THREADS - 1) / THREADS;
     const int s0 = min((int)threadIdx.x * each, NS), s1 = min(s0 + each, NS);
@@ -273,6 +272,16 @@ cudaError_t launch_attend_join(const AttendArgs &a, int es, cudaStream_t stream)
 // The kernels, each followed by the join.  attend_f32 (any head_dim, float32 arithmetic) and attend_tc (bf16,
 // head_dim <= 128, tensor cores).
 sv_status launch_attend_f32(AttendArgs a, int es, const DeviceInfo &di, cudaStream_t stream);
+sv_status launch_attend_tc(AttendArgs a, const DeviceInfo &di, cudaStream_t stream);
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Workspace of a call: segment offsets, then the slots of the widest tiles on the most blocks.
 constexpr int kAttBlocks = 160;   // most persistent blocks (a GB300 has 152 SMs)
