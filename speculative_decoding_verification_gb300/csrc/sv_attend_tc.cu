@@ -30,7 +30,7 @@ struct PieceInfo {
     int r0, m0, vr, h;                // segment's first row, first packed row, rows, key head
     int table, key0, ctx, end;        // page table's sequence, tokens
     int k0, k1;                       // key tiles; k0 == k1: no more pieces
-    int own, tree, whole, seg_end;    // own segment, tree mask, output complete here, the segment's last token + 1
+    int own, tree, whole, boxes;      // own segment, tree mask, output complete here, full tiles load as boxes
     uint8_t par[SV_MAX_TREE];         // a tree's parents (255: invalid)
 };
 
@@ -134,12 +134,20 @@ __device__ __forceinline__ uint32_t anc_at(const uint32_t (&anc)[5], int k) {
     return w;
 }
 
+// Keys and values as 4-D tensors (element, head, slot, page) with boxes of 64 elements by box_rows slots, loaded with the
+// 128-byte swizzle; box_rows is 0 where a box could not stay inside a page.
+struct TcArgs {
+    CUtensorMap k, v;
+    int box_rows;
+    uint32_t shape_s;     // of the score product
+};
+
 template <int DP>
-__global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_constant__ AttendArgs a, const uint32_t shape_s) {
+__global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ TcArgs a2) {
     using S = TcShape<DP>;
     extern __shared__ __align__(1024) char smem[];
     Misc *ms = reinterpret_cast<Misc *>(smem + S::OFF_MISC);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
 
     if (smem_addr(smem) & 1023) {   // the swizzle goes by address bits
         if (tid == 0) report_error(a.stats, SV_ERR_CUDA, -1);
@@ -432,8 +440,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
         CopyQueue cq;
         uint32_t seq = 0, q_use[2] = {0, 0};
         int qnext = 0;
+        // Waits for a barrier and passes on the copies that land meanwhile: whoever completes the barrier may be waiting for them.
         auto acquire = [&](uint64_t *bar, uint32_t parity) {
-            while (!mbar_try_wait(bar, parity)) {
+            // A test, not a try: a try may suspend the warp for microseconds, and copies that land meanwhile have to be
+            // passed on.  The whole warp takes one way: lanes may see the phase end at different tests.
+            while (!__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) {
                 if (cq.n == 0) {
                     wait_phase(ms, bar, parity, a.stats);
                     return;
@@ -445,18 +456,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
         auto place = [&](uint32_t tile, int r) { return tile + (ch >> 3) * S::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
         for (int it = 0;; ++it) {
             const PieceInfo *pi = &ms->pd[it % kRing];
-            wait_phase(ms, &ms->pd_full[it % kRing], (it / kRing) & 1, a.stats);
+            acquire(&ms->pd_full[it % kRing], (it / kRing) & 1);
             const int k0 = pi->k0, k1 = pi->k1;
             if (k0 >= k1) break;
-            const int vr = pi->vr, key0 = pi->key0, end = pi->seg_end, ctx = pi->ctx, own = pi->own, h = pi->h, m0 = pi->m0, r0 = pi->r0;
+            const int vr = pi->vr, key0 = pi->key0, end = pi->end, ctx = pi->ctx, own = pi->own, h = pi->h, m0 = pi->m0, r0 = pi->r0, pi_boxes = pi->boxes;
             const int32_t *table = a.bt.page_table + pi->table * a.bt.table_pitch;
             const int tab = pi->table;
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms->pd_empty[it % kRing]);
             const bool two = vr > 128;
-            // this lane's token of a tile, and its page
+            // A tile that every row sees whole goes as boxes where it can, the others by rows: a lane's token of a tile, and its
+            // page, are those of the lane's box or row.
+            const int boxes = pi_boxes ? 32 / a2.box_rows : 0;
+            auto by_box = [&](int k) { return boxes > 0 && key0 + (k + 1) * kTcKeys <= (own ? ctx : end); };
+            auto key_of = [&](int k) { return key0 + k * kTcKeys + wl * 32 + (by_box(k) ? lane * a2.box_rows : lane); };
             auto page_of = [&](int k) {
-                const int key = key0 + k * kTcKeys + wl * 32 + lane;
+                if (by_box(k) && lane >= boxes) return kNoPage;
+                const int key = key_of(k);
                 return key < end ? table[key / a.c.page_size] : kNoPage;
             };
             int page = page_of(k0);
@@ -482,13 +498,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
             }
             if (!two) qnext ^= 1;
             for (int k = k0; k < k1; ++k) {
-                const int key = key0 + k * kTcKeys + wl * 32 + lane;
+                const int key = key_of(k), pg = page, slot = key - key / a.c.page_size * a.c.page_size;
+                const bool box = by_box(k);
                 int64_t off = -1;
-                if (page >= 0 && page < a.c.n_pages) {
-                    off = page * a.c.page_b + (int64_t)(key - key / a.c.page_size * a.c.page_size) * a.c.slot_b + h * a.c.head_b;
-                } else if (page != kNoPage) {
-                    report_error(a.stats, SV_ERR_INVALID_ARG, tab);
-                }
+                if (pg >= 0 && pg < a.c.n_pages) off = pg * a.c.page_b + slot * a.c.slot_b + h * a.c.head_b;
+                else if (pg != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
                 if (k + 1 < k1) page = page_of(k + 1);
                 const bool masked = own && key0 + (k + 1) * kTcKeys > ctx;
 #pragma unroll
@@ -498,6 +512,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
                     ++seq;
                     const uint32_t tile = sbase + S::OFF_KV + stage * S::TILE;
                     const char *src = kv ? a.c.v : a.c.k;
+                    if (box) {   // a bad page id lies outside the tensor and reads zeros
+                        if (elect_one()) mbar_arrive_expect_tx(&ms->kv_full[stage], 32 * DP * 2);
+                        __syncwarp();
+                        for (int b = 0; b < boxes; ++b) {
+                            const int bp = __shfl_sync(0xFFFFFFFFu, pg, b), bs = __shfl_sync(0xFFFFFFFFu, slot, b);
+                            const uint32_t dst = tile + (wl * 32 + b * a2.box_rows) * 128;
+                            if (elect_one()) {
+                                const CUtensorMap *map = kv ? &a2.v : &a2.k;
+                                box_load(dst, map, &ms->kv_full[stage], 0, h, bs, bp);
+                                if (DP == 128) box_load(dst + S::HALF, map, &ms->kv_full[stage], 64, h, bs, bp);
+                            }
+                            __syncwarp();
+                        }
+                        continue;
+                    }
                     if (kv == 1 && masked) {
                         // values through registers: a token whose values are not all finite goes in as zeros and is flagged
                         uint32_t flags = 0;
@@ -541,19 +570,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
         while (cq.n) cq.retire(bars, lane);
     } else {
         regs_dec<80>();
-        if (warp == 12 && lane == 0) {
+        if (warp == 12) {   // the whole warp runs this, with uniform values
             // ------------------------------------------------------------ matrix products
-            const uint32_t sbase = smem_addr(smem);
+            const uint32_t sbase = smem_addr(smem), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             constexpr uint32_t shape_o = mma_shape(DP, true, false);
             uint32_t p_phase[2] = {0, 0}, seq = 0, q_use[2] = {0, 0};
             int qnext = 0;
             for (int it = 0;; ++it) {
                 const PieceInfo *pi = &ms->pd[it % kRing];
                 wait_phase(ms, &ms->pd_full[it % kRing], (it / kRing) & 1, a.stats);
-                const int nk = pi->k1 - pi->k0;
-                const bool two = pi->vr > 128;
+                __syncwarp();
+                const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
+                const bool two = __shfl_sync(0xFFFFFFFFu, pi->vr, 0) > 128;
                 if (nk <= 0) break;
-                mbar_arrive(&ms->pd_empty[it % kRing]);
+                if (lane == 0) mbar_arrive(&ms->pd_empty[it % kRing]);
                 const int jobs = two ? 2 * nk : nk;
                 auto weigh = [&](int n) {   // O += P V of job n
                     const int s = n & 1, tile = two ? n >> 1 : n;
@@ -561,14 +591,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
                     wait_phase(ms, &ms->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
                     wait_phase(ms, &ms->p_full[s], p_phase[s], a.stats);
                     p_phase[s] ^= 1;
+                    __syncwarp();
                     tc_fence_after();
-                    const uint32_t v = sbase + S::OFF_KV + stage * S::TILE;
+                    const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, S::HALF, 1024);
+                    const uint32_t o = tm + kColO + s * 128, w = tm + kColS + s * 128;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 16; ++kk)   // the weights' upper parts, then the lower ones
-                        mma_ts(tmem + kColO + s * 128, tmem + kColS + s * 128 + kk * 8, smem_operand(v + (kk & 7) * 2048, S::HALF, 1024),
-                               shape_o, 1u);
-                    if (!two || s == 1) mma_commit(&ms->kv_empty[stage]);
-                    if (n + 2 >= jobs) mma_commit(&ms->o_full[s]);
+                        for (int kk = 0; kk < 16; ++kk)   // the weights' upper parts, then the lower ones
+                            mma_ts(o, w + kk * 8, v + (kk & 7) * (2048 >> 4), shape_o, 1u);
+                        if (!two || s == 1) mma_commit(&ms->kv_empty[stage]);
+                        if (n + 2 >= jobs) mma_commit(&ms->o_full[s]);
+                    }
+                    __syncwarp();
                 };
                 for (int n = 0; n < jobs; ++n) {
                     const int s = n & 1, tile = two ? n >> 1 : n;
@@ -579,24 +613,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
                         ++q_use[qs];
                     }
                     wait_phase(ms, &ms->kv_full[stage], (ks / S::STAGES) & 1, a.stats);
+                    __syncwarp();
                     tc_fence_after();
-                    const uint32_t q = sbase + qs * S::TILE, kt = sbase + S::OFF_KV + stage * S::TILE;
+                    const uint64_t q = smem_operand(sbase + qs * S::TILE, 16, 1024);
+                    const uint64_t kt = smem_operand(sbase + S::OFF_KV + stage * S::TILE, 16, 1024);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < DP / 16; ++kk) {
-                        const uint32_t at = (kk >> 2) * S::HALF + (kk & 3) * 32;
-                        mma_ss(tmem + kColS + s * 128, smem_operand(q + at, 16, 1024), smem_operand(kt + at, 16, 1024), shape_s, kk > 0);
+                        for (int kk = 0; kk < DP / 16; ++kk) {
+                            const uint32_t at = ((kk >> 2) * S::HALF + (kk & 3) * 32) >> 4;
+                            mma_ss(tm + kColS + s * 128, q + at, kt + at, a2.shape_s, kk > 0);
+                        }
+                        mma_commit(&ms->s_full[s]);
+                        if (!two || s == 1) mma_commit(&ms->kv_empty[stage]);
+                        if (two ? n >= jobs - 2 : n == jobs - 1) mma_commit(&ms->q_empty[qs]);
                     }
-                    mma_commit(&ms->s_full[s]);
-                    if (!two || s == 1) mma_commit(&ms->kv_empty[stage]);
-                    if (two ? n >= jobs - 2 : n == jobs - 1) mma_commit(&ms->q_empty[qs]);
+                    __syncwarp();
                     if (n > 0) weigh(n - 1);
                 }
                 weigh(jobs - 1);
                 if (!two) qnext ^= 1;
                 seq += 2 * nk;
             }
-            mma_commit(&ms->done);
+            if (elect_one()) mma_commit(&ms->done);
             wait_phase(ms, &ms->done, 0, a.stats);
+            __syncwarp();
         } else if (warp == 13) {
             // ------------------------------------------------------------ the walk
             Walk w = ms->walk;
@@ -626,7 +666,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
                         pi->key0 = p.g.key0;
                         pi->ctx = p.g.ctx;
                         pi->end = p.end;
-                        pi->seg_end = p.end;
+                        pi->boxes = a2.box_rows > 0 && p.g.key0 % a2.box_rows == 0;
                         pi->k0 = p.k0;
                         pi->k1 = p.k1;
                         pi->own = own;
@@ -648,6 +688,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tc(const __grid_consta
     if (warp == 12) tmem_free(tmem, 512);
 }
 
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult res;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &res) != cudaSuccess ||
+            res != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+bool cache_map(CUtensorMap *map, char *base, const KvCache &c, int box_rows) {
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.kv_heads, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.head_b, (cuuint64_t)c.slot_b, (cuuint64_t)c.page_b};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1}, one[4] = {1, 1, 1, 1};
+    return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DP>
 sv_status run_tc(AttendArgs &a, const DeviceInfo &di, bool negate, cudaStream_t stream) {
     constexpr size_t bytes = TcShape<DP>::OFF_MISC + sizeof(Misc);
@@ -656,7 +720,16 @@ sv_status run_tc(AttendArgs &a, const DeviceInfo &di, bool negate, cudaStream_t 
     a.TM = kTcRows;
     a.TK = kTcKeys;
     a.blocks = di.sms;
-    k_attend_tc<DP><<<a.blocks, kTcThreads, bytes, stream>>>(a, mma_shape(128, false, negate));
+    TcArgs a2{};
+    a2.shape_s = mma_shape(128, false, negate);
+    // Boxes of up to 32 slots (a producer warp's share of a tile), whole swizzle groups of 8 rows, that never cross a page.
+    const int ps = a.c.page_size;
+    if (ps >= 32 ? ps % 32 == 0 : ps == 8 || ps == 16) {
+        a2.box_rows = ps < 32 ? ps : 32;
+        if (encode_tiled() == nullptr || !cache_map(&a2.k, a.c.k, a.c, a2.box_rows) || !cache_map(&a2.v, a.c.v, a.c, a2.box_rows))
+            a2.box_rows = 0;
+    }
+    k_attend_tc<DP><<<a.blocks, kTcThreads, bytes, stream>>>(a, a2);
     if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
     return cuda_status(launch_attend_join(a, 2, stream));
 }

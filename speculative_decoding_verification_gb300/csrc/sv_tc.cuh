@@ -2,9 +2,19 @@
 // tensor memory, its completion barriers, and the moves between registers and tensor memory.
 #pragma once
 
+#include <cuda.h>
+
 #include "sv_device.cuh"
 
 namespace sv {
+
+// A box of the tensor that `map` describes, to shared memory; completes its bytes on `bar`.
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
 
 // Shared-memory operand of tcgen05.mma in the 128-byte swizzle: rows of 128 bytes, 16-byte chunk c of row r at
 // chunk c ^ (r & 7), groups of 8 rows `stride` bytes apart.  `lead` is the distance of the next 64 elements of an operand
@@ -18,6 +28,15 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, u
 __host__ __device__ constexpr uint32_t mma_shape(int N, bool b_rows_summed, bool negate_a) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (negate_a ? 1u << 13 : 0u) | (b_rows_summed ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
            (128u >> 4) << 24;
+}
+
+// One thread of the warp, the same one every time.  Products are issued inside `if (elect_one())` in code that the whole
+// warp runs with uniform operands: they then cost 13 (A in tensor memory) to 33 cycles each to issue, against 75 to 100 when
+// the thread is picked by its number, and the tensor cores take 64 for 128 x 128 x 16.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // D (tensor memory) = or += A B, both from shared memory.

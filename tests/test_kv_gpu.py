@@ -384,3 +384,34 @@ def test_commit_reports_bad_paths(sv):
         assert sv.read_stats(st)["status"] == 1 and sv.read_stats(st)["error_index"] == 0
         assert out.tolist() == [5, 7, 8, 9]
         assert torch.equal(k, k0) and torch.equal(v, v0)
+
+
+# ---- many pieces a block --------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,n,heads,kv,dim,page,tree,pre,longest", [
+    (40, 3, 16, 8, 128, 16, False, 0, 700),     # more tiles than blocks: ranges that start and end inside units
+    (24, 20, 16, 4, 128, 32, True, 0, 900),     # short tiles of rows
+    (12, 40, 16, 4, 64, 64, True, 0, 1500),     # two row tiles that share keys
+    (30, 6, 8, 8, 128, 8, False, 0, 40),        # units of one key tile
+    (48, 6, 16, 4, 128, 16, False, 1280, 300),  # prefixes of three groups, tall tiles, then own tokens
+    (36, 9, 16, 8, 64, 96, True, 2016, 130),    # a prefix that is no whole number of tiles
+    (20, 5, 8, 4, 96, 24, False, 1200, 260),    # pages that no box fits
+])
+def test_attend_many_pieces(sv, dtype, B, n, heads, kv, dim, page, tree, pre, longest):
+    """Thousands of key tiles, so that every block walks several pieces of several units; a sample of the sequences is checked."""
+    rng = np.random.default_rng(B)
+    ctx = [pre + int(x) for x in rng.integers(0, longest + 1, B)]
+    groups = [(0, pre), (B // 3, pre), (2 * B // 3 + 1, pre)] if pre else None
+    c = Cache(B + dim, dtype, ctx, n, kv, dim, page, groups=groups)
+    q = blocks(c, 46, B, n, heads, kv, dim, dtype)
+    par = random_tree(c.rng, B, n) if tree else None
+    st = sv.new_stats("cuda")
+    out, lse = sv.sv_kv_attend(q, c.k, c.v, parents=par.cuda() if tree else None, lse=True, stats=st, **c.args, **c.group_args)
+    assert sv.read_stats(st)["status"] == 0
+    rows = [slice(b * n, b * n + n) for b in range(B)]
+    seqs = sorted({0, 1, B // 3, B // 2, 2 * B // 3, B - 2, B - 1})
+    check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), dim ** -0.5, rows, par, seqs)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    again, _ = sv.sv_kv_attend(q, c.k, c.v, parents=par.cuda() if tree else None, **c.args, **c.group_args)
+    assert torch.equal(out, again)
