@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
             }
         }
         const bool whole = p.k0 == 0 && p.k1 == p.kt && p.seg >= a.n_groups && seg_alone(p.g);
-        const size_t slot = unit_slot(a, p.g, p.seg < a.n_groups, h, p.t) + (size_t)blockIdx.x * TM;
+        const size_t slot = unit_slot(a, a.geo, p.g, p.seg < a.n_groups, h, p.t) + (size_t)blockIdx.x * TM;
         if (ks == 0) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -290,37 +290,37 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
 // Adds the pieces of a row's units: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  One warp a (row, query
 // head), prefix pieces first, then own ones, each in the order of the blocks that made them.
 template <int ES>
-__global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a) {
+__global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a, const AttendGeo prefix, const AttendGeo own) {
     pdl_wait();
     const long long w = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (w >= (long long)a.bt.rows * a.q_heads) return;
     const int row = (int)(w / a.q_heads), qh = (int)(w - (long long)row * a.q_heads);
     const int h = qh / a.G;
-    const int NS = a.n_groups + a.bt.B;
-    const long long total = a.seg_off[NS];
     const int b = row_sequence(a.bt, row);
     const int D = a.c.head_dim, D4 = D / 4;
     float m = -INFINITY, l = 0.0f;
     float4 o[2] = {};
     for (int which = a.n_groups ? 0 : 1; which < 2; ++which) {
         const int s = which == 0 ? group_of(a, b) : a.n_groups + b;
-        const Seg g = seg_of(a, s, false);
+        const AttendGeo &geo = which == 0 ? prefix : own;
+        const Seg g = seg_of(a, geo, s, false);
+        const long long total = geo.seg_off[geo.s1 - geo.s0];
         if (row < g.r0 || row >= g.r0 + g.n || total == 0) continue;
-        const int mm = (row - g.r0) * a.G + (qh - h * a.G), t = mm / a.TM;
-        const int kt = seg_tiles(a, g, t);
+        const int mm = (row - g.r0) * a.G + (qh - h * a.G), t = mm / geo.TM;
+        const int kt = seg_tiles(a, geo, g, t);
         if (kt <= 0) continue;
-        const long long per = seg_head_tiles(a, g);
-        long long first = a.seg_off[s] + per * h;
+        const long long per = seg_head_tiles(a, geo, g);
+        long long first = geo.seg_off[s - geo.s0] + per * h;
         if (!g.chain) first += (long long)t * kt;
         else
-            for (int u = 0; u < t; ++u) first += seg_tiles(a, g, u);
-        const int parts = range_blocks(total, a.blocks);
+            for (int u = 0; u < t; ++u) first += seg_tiles(a, geo, g, u);
+        const int parts = range_blocks(total, geo.blocks);
         const int c0 = block_of_tile(first, total, parts), c1 = block_of_tile(first + kt - 1, total, parts);
         if (which == 1 && c0 == c1 && seg_alone(g)) return;   // written by its piece
-        const size_t base = unit_slot(a, g, which == 0, h, t) + (mm - t * a.TM);
+        const size_t base = unit_slot(a, geo, g, which == 0, h, t) + (mm - t * geo.TM);
         for (int c = c0; c <= c1; ++c) {
-            const size_t slot = base + (size_t)c * a.TM;
+            const size_t slot = base + (size_t)c * geo.TM;
             const float2 ml = a.part_ml[slot];
             if (ml.y == 0.0f) continue;   // the row saw none of the piece's tokens
             const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.0f : top;
@@ -358,43 +358,47 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a) {
     if (a.lse && lane == 0) a.lse[(size_t)row * a.q_heads + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) / kLog2e;
 }
 
-cudaError_t launch_attend_join(const AttendArgs &a, int es, cudaStream_t stream) {
+cudaError_t launch_attend_join(const AttendArgs &a, const AttendGeo &prefix, const AttendGeo &own, int es, cudaStream_t stream) {
     const long long warps = (long long)a.bt.rows * a.q_heads;
     const dim3 grid((unsigned)((warps + 7) / 8));
-    return es == 4 ? launch_pdl(k_attend_join<4>, grid, dim3(256), 0, stream, a)
-                   : launch_pdl(k_attend_join<2>, grid, dim3(256), 0, stream, a);
+    return es == 4 ? launch_pdl(k_attend_join<4>, grid, dim3(256), 0, stream, a, prefix, own)
+                   : launch_pdl(k_attend_join<2>, grid, dim3(256), 0, stream, a, prefix, own);
 }
 
 template <int ES, int DP, int TM>
-static sv_status run_f32(AttendArgs &a, const DeviceInfo &di, cudaStream_t stream) {
+static cudaError_t run_f32(AttendArgs &a, cudaStream_t stream) {
     using S = F32Shape<ES, DP, TM>;
-    const int res = prepare_kernel((const void *)k_attend_f32<ES, DP, TM>, kAttThreads, S::BYTES);
-    if (res < 1) return SV_ERR_CUDA;
-    a.TM = TM;
-    a.TK = S::TK;
-    a.blocks = di.sms;
-    k_attend_f32<ES, DP, TM><<<a.blocks, kAttThreads, S::BYTES, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-    return cuda_status(launch_attend_join(a, ES, stream));
+    if (prepare_kernel((const void *)k_attend_f32<ES, DP, TM>, kAttThreads, S::BYTES) < 1) return cudaErrorInvalidConfiguration;
+    a.geo.TM = TM;
+    a.geo.TK = S::TK;
+    k_attend_f32<ES, DP, TM><<<a.geo.blocks, kAttThreads, S::BYTES, stream>>>(a);
+    return cudaGetLastError();
 }
 
-sv_status launch_attend_f32(AttendArgs a, int es, const DeviceInfo &di, cudaStream_t stream) {
+cudaError_t launch_attend_f32(AttendArgs &a, int es, cudaStream_t stream) {
     const int D = a.c.head_dim;
     const bool small = a.bt.n * a.G <= 16 && a.n_groups == 0;
-#define SV_ATT(ES, DP) (small ? run_f32<ES, DP, 16>(a, di, stream) : run_f32<ES, DP, 64>(a, di, stream))
+#define SV_ATT(ES, DP) (small ? run_f32<ES, DP, 16>(a, stream) : run_f32<ES, DP, 64>(a, stream))
     if (es == 4) return D <= 64 ? SV_ATT(4, 64) : D <= 128 ? SV_ATT(4, 128) : SV_ATT(4, 256);
-    return D <= 64 ? SV_ATT(2, 64) : D <= 128 ? SV_ATT(2, 128) : SV_ATT(2, 256);
+    return SV_ATT(2, 256);   // narrower bf16 heads go to the tensor cores
 #undef SV_ATT
 }
 
-// Tiles hold up to 256 rows.
+// Workspace of a call: segment offsets, then the slots of the widest tiles (256 rows) on the most blocks, once for the prefixes and
+// once for the own tokens.
+constexpr int kAttBlocks = 160;   // most persistent blocks (a GB300 has 152 SMs)
 constexpr int kAttMaxTile = 256;
 
-AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, int n_groups, int blocks) {
+struct AttendPlan {
+    size_t off_seg = 0, off_ml = 0, off_part = 0, bytes = 0;
+};
+
+static AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, int n_groups) {
     AttendPlan p;
     Carver cv;
-    const size_t slots = attend_slots(rows, q_heads, n_groups, kAttMaxTile, blocks);
-    p.off_seg = cv.take<long long>((size_t)n_groups + B + 1);
+    const size_t slots = attend_slots(rows, q_heads, n_groups > 0, true, kAttMaxTile, kAttBlocks) +
+                         (n_groups > 0 ? (size_t)kFewRows * kAttBlocks : 0);
+    p.off_seg = cv.take<long long>((size_t)n_groups + B + 2);
     p.off_ml = cv.take<float2>(slots);
     p.off_part = cv.take<float>(slots * head_dim);
     p.bytes = cv.off + 256;
@@ -407,7 +411,7 @@ using namespace sv;
 
 extern "C" size_t sv_kv_attend_workspace_size(int64_t rows, int q_heads, int head_dim, int B, int n_groups) {
     if (rows < 0 || q_heads < 1 || head_dim < 1 || head_dim > SV_KV_MAX_HEAD_DIM || B < 1 || n_groups < 0) return 0;
-    return plan_attend(rows, q_heads, head_dim, B, n_groups, kAttBlocks).bytes;
+    return plan_attend(rows, q_heads, head_dim, B, n_groups).bytes;
 }
 
 extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *batch, const void *q,
@@ -424,13 +428,12 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     if (!aligned(q, 16) || !aligned(out, 16) || !strides16(es, q_row_stride, q_head_stride) ||
         !strides16(es, out_row_stride, out_head_stride) || (int64_t)batch->rows * q_heads > INT32_MAX)
         return SV_ERR_INVALID_ARG;
-    const AttendPlan pl = plan_attend(batch->rows, q_heads, cache->head_dim, batch->B, n_groups, kAttBlocks);
+    const AttendPlan pl = plan_attend(batch->rows, q_heads, cache->head_dim, batch->B, n_groups);
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.bytes) return SV_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (!on_current_device(s, cache->k, q)) return SV_ERR_INVALID_ARG;
     DeviceInfo di;
     if (!device_info(di)) return SV_ERR_CUDA;
-    if (di.sms > kAttBlocks) di.sms = kAttBlocks;
     if (stats && cudaMemsetAsync(stats, 0, sizeof(sv_stats), s) != cudaSuccess) return SV_ERR_CUDA;
     if (batch->rows == 0) return SV_OK;
     char *w = static_cast<char *>(workspace);
@@ -451,10 +454,38 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     a.n_groups = n_groups;
     a.lse = lse;
     a.stats = stats;
-    a.seg_off = reinterpret_cast<long long *>(w + pl.off_seg);
     a.part_ml = reinterpret_cast<float2 *>(w + pl.off_ml);
     a.part = reinterpret_cast<float *>(w + pl.off_part);
+    long long *seg = reinterpret_cast<long long *>(w + pl.off_seg);
+    const int blocks = di.sms < kAttBlocks ? di.sms : kAttBlocks;
+    const AttendGeo all{0, n_groups + batch->B, 0, 0, blocks, seg, 0};
+    AttendGeo prefix = all, own = all;
+    cudaError_t e = cudaSuccess;
     // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.
-    if (es == 2 && cache->head_dim <= 128) return launch_attend_tc(a, di, s);
-    return launch_attend_f32(a, es, di, s);
+    if (es == 4 || cache->head_dim > 128) {
+        a.geo = all;
+        e = launch_attend_f32(a, es, s);
+        prefix = own = a.geo;
+    } else if ((int64_t)batch->n * a.G > kFewRows) {
+        a.geo = all;
+        e = launch_attend_tall(a, s);
+        prefix = own = a.geo;
+    } else {
+        if (n_groups > 0) {
+            a.geo = all;
+            a.geo.s1 = n_groups;
+            e = launch_attend_tall(a, s);
+            prefix = a.geo;
+            own.s0 = n_groups;
+            own.seg_off = seg + n_groups + 1;
+            own.slot0 = attend_slots(batch->rows, q_heads, true, false, a.geo.TM, blocks);
+        }
+        if (e == cudaSuccess) {
+            a.geo = own;
+            e = launch_attend_few(a, s);
+            own = a.geo;
+        }
+    }
+    if (e == cudaSuccess) e = launch_attend_join(a, prefix, own, es, s);
+    return cuda_status(e);
 }

@@ -20,6 +20,13 @@ namespace sv {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// What one launch covers and how it cuts it: segments [s0, s1), row and key tiles, blocks.
+struct AttendGeo {
+    int s0, s1, TM, TK, blocks;
+    long long *seg_off;   // [s1 - s0 + 1] first tile of each segment, in the unit order
+    size_t slot0;         // its first workspace slot
+};
+
 struct AttendArgs {
     KvCache c;
     KvBatch bt;
@@ -32,18 +39,16 @@ struct AttendArgs {
     int n_groups;
     float *lse;
     sv_stats *stats;
-    // geometry of the launch
-    int TM, TK, blocks;
+    AttendGeo geo;        // of this launch
     // workspace
-    long long *seg_off;   // [n_groups + B + 1] first tile of each segment, in the unit order
     float *part;          // [slots][head_dim] weighted values of a packed row of a piece
     float2 *part_ml;      // [slots] its maximum (of scale * log2(e) * q.k) and sum
 };
 
 // Slots: a piece of unit u in block c starts at unit_slot(u) + c * TM.  Units' slots rise by their rows and
 // blocks' by TM, and along the walk either the unit or the block moves on, so pieces never share a slot.
-inline size_t attend_slots(int64_t rows, int q_heads, int n_groups, int TM, int blocks) {
-    return (size_t)rows * q_heads * (n_groups > 0 ? 2 : 1) + (size_t)TM * blocks;
+inline size_t attend_slots(int64_t rows, int q_heads, bool prefix, bool own, int TM, int blocks) {
+    return (size_t)rows * q_heads * ((prefix ? 1 : 0) + (own ? 1 : 0)) + (size_t)TM * blocks;
 }
 
 struct Seg {
@@ -69,7 +74,7 @@ __device__ __forceinline__ int group_of(const AttendArgs &a, int b) {
 __device__ __forceinline__ int clamp_int(long long x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : (int)x; }
 
 // Segment s, with every device value clamped to what the arrays hold.  `check` reports what had to be.
-__device__ __forceinline__ Seg seg_of(const AttendArgs &a, int s, bool check) {
+__device__ __forceinline__ Seg seg_of(const AttendArgs &a, const AttendGeo &geo, int s, bool check) {
     Seg g;
     const int cap = a.bt.max_pages * a.c.page_size;
     if (s < a.n_groups) {
@@ -106,32 +111,32 @@ __device__ __forceinline__ Seg seg_of(const AttendArgs &a, int s, bool check) {
             report_error(a.stats, SV_ERR_INVALID_ARG, b);
     }
     g.packed = g.n * a.G;
-    g.tiles_m = (g.packed + a.TM - 1) / a.TM;
+    g.tiles_m = (g.packed + geo.TM - 1) / geo.TM;
     return g;
 }
 
 // One past the last token that row tile t of the segment sees, and its tiles of keys.
-__device__ __forceinline__ int seg_end(const AttendArgs &a, const Seg &g, int t) {
+__device__ __forceinline__ int seg_end(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
     if (!g.chain) return g.end;
-    const int last = min((t + 1) * a.TM, g.packed) - 1;
+    const int last = min((t + 1) * geo.TM, g.packed) - 1;
     return min(g.ctx + last / a.G + 1, g.end);
 }
 
-__device__ __forceinline__ int seg_tiles(const AttendArgs &a, const Seg &g, int t) {
-    return (seg_end(a, g, t) - g.key0 + a.TK - 1) / a.TK;
+__device__ __forceinline__ int seg_tiles(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+    return (seg_end(a, geo, g, t) - g.key0 + geo.TK - 1) / geo.TK;
 }
 
-__device__ __forceinline__ long long seg_head_tiles(const AttendArgs &a, const Seg &g) {
-    if (!g.chain) return (long long)g.tiles_m * seg_tiles(a, g, 0);
+__device__ __forceinline__ long long seg_head_tiles(const AttendArgs &a, const AttendGeo &geo, const Seg &g) {
+    if (!g.chain) return (long long)g.tiles_m * seg_tiles(a, geo, g, 0);
     long long n = 0;
-    for (int t = 0; t < g.tiles_m; ++t) n += seg_tiles(a, g, t);
+    for (int t = 0; t < g.tiles_m; ++t) n += seg_tiles(a, geo, g, t);
     return n;
 }
 
 // First workspace slot of unit (h, t) of a segment.
-__device__ __forceinline__ size_t unit_slot(const AttendArgs &a, const Seg &g, bool prefix, int h, int t) {
-    const size_t own = a.n_groups > 0 && !prefix ? (size_t)a.bt.rows * a.q_heads : 0;
-    return own + (size_t)g.r0 * a.q_heads + (size_t)h * g.packed + (size_t)t * a.TM;
+__device__ __forceinline__ size_t unit_slot(const AttendArgs &a, const AttendGeo &geo, const Seg &g, bool prefix, int h, int t) {
+    const size_t own = geo.s0 < a.n_groups && !prefix ? (size_t)a.bt.rows * a.q_heads : 0;
+    return geo.slot0 + own + (size_t)g.r0 * a.q_heads + (size_t)h * g.packed + (size_t)t * geo.TM;
 }
 
 // Ranges are those of the first range_blocks blocks, so that none is empty: range c is
@@ -161,8 +166,8 @@ struct Walk {
     Seg g;
 
     __device__ __forceinline__ void open(const AttendArgs &a) {
-        g = seg_of(a, s, false);
-        per_head = seg_head_tiles(a, g);
+        g = seg_of(a, a.geo, s, false);
+        per_head = seg_head_tiles(a, a.geo, g);
     }
 
     __device__ __forceinline__ bool next(const AttendArgs &a, Piece &p) {
@@ -177,22 +182,22 @@ struct Walk {
         p.h = (int)(at / per_head);
         rem = (int)(at - p.h * per_head);
         p.t = 0;
-        p.kt = seg_tiles(a, g, 0);
+        p.kt = seg_tiles(a, a.geo, g, 0);
         if (!g.chain) {
             p.t = rem / p.kt;
             rem -= p.t * p.kt;
         } else {
             while (rem >= p.kt) {
                 rem -= p.kt;
-                p.kt = seg_tiles(a, g, ++p.t);
+                p.kt = seg_tiles(a, a.geo, g, ++p.t);
             }
         }
         p.g = g;
         p.seg = s;
-        p.vr = min(a.TM, g.packed - p.t * a.TM);
+        p.vr = min(a.geo.TM, g.packed - p.t * a.geo.TM);
         p.k0 = rem;
         p.k1 = (int)min((long long)p.kt, rem + (stop - pos));
-        p.end = seg_end(a, g, p.t);
+        p.end = seg_end(a, a.geo, g, p.t);
         pos += p.k1 - p.k0;
         return true;
     }
@@ -202,11 +207,12 @@ struct Walk {
 // run of consecutive segments; warp_sum has THREADS / 32 places.  Block 0 leaves the segments' offsets for the join and reports bad input.
 template <int THREADS>
 __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long long *warp_sum) {
-    const int NS = a.n_groups + a.bt.B;
+    const AttendGeo &geo = a.geo;
+    const int NS = geo.s1 - geo.s0;
     const int each = (NS + THREADS - 1) / THREADS;
     const int s0 = min((int)threadIdx.x * each, NS), s1 = min(s0 + each, NS);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += seg_head_tiles(a, seg_of(a, s, blockIdx.x == 0)) * a.c.kv_heads;
+    for (int s = s0; s < s1; ++s) mine += seg_head_tiles(a, geo, seg_of(a, geo, geo.s0 + s, blockIdx.x == 0)) * a.c.kv_heads;
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     long long inc = mine;
 #pragma unroll
@@ -222,24 +228,24 @@ __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long lo
         if (i < wp) before += warp_sum[i];
         total += warp_sum[i];
     }
-    const int parts = range_blocks(total, a.blocks), c = min((int)blockIdx.x, parts);
+    const int parts = range_blocks(total, geo.blocks), c = min((int)blockIdx.x, parts);
     const long long pos = total * c / max(parts, 1), stop = total * min(c + 1, parts) / max(parts, 1);
     if (threadIdx.x == 0 && pos >= stop) w->pos = w->stop = 0;
     long long at = before;
     for (int s = s0; s < s1; ++s) {
-        const Seg g = seg_of(a, s, false);
-        const long long per = seg_head_tiles(a, g), n = per * a.c.kv_heads;
+        const Seg g = seg_of(a, geo, geo.s0 + s, false);
+        const long long per = seg_head_tiles(a, geo, g), n = per * a.c.kv_heads;
         if (pos < stop && pos >= at && pos < at + n) {
             w->pos = pos;
             w->stop = stop;
-            w->s = s;
+            w->s = geo.s0 + s;
             w->seg_start = at;
             w->g = g;
             w->per_head = per;
         }
         if (blockIdx.x == 0) {
-            a.seg_off[s] = at;
-            if (s == NS - 1) a.seg_off[NS] = at + n;
+            geo.seg_off[s] = at;
+            if (s == NS - 1) geo.seg_off[NS] = at + n;
         }
         at += n;
     }
@@ -266,13 +272,16 @@ __device__ __forceinline__ void ancestor_words(const int32_t *parents, int i, in
     }
 }
 
-// k_attend_join: adds the pieces of each row, one warp a (row, query head).
-cudaError_t launch_attend_join(const AttendArgs &a, int es, cudaStream_t stream);
+// k_attend_join: adds the pieces of each row, one warp a (row, query head).  The launches that made them: of the prefixes'
+// segments (not read without groups) and of the own ones; the same where one launch covered both.
+cudaError_t launch_attend_join(const AttendArgs &a, const AttendGeo &prefix, const AttendGeo &own, int es, cudaStream_t stream);
 
-// The kernels, each followed by the join.  attend_f32 (any head_dim, float32 arithmetic) and attend_tc (bf16,
-// head_dim <= 128, tensor cores).
-sv_status launch_attend_f32(AttendArgs a, int es, const DeviceInfo &di, cudaStream_t stream);
-sv_status launch_attend_tc(AttendArgs a, const DeviceInfo &di, cudaStream_t stream);
+// The kernels: any head_dim in float32 arithmetic; bf16 with head_dim <= 128 on the tensor cores, a tall form for any number
+// of rows and one for up to kFewRows packed rows a sequence.  Each fills in a.geo's tiles.
+constexpr int kFewRows = 32;
+cudaError_t launch_attend_f32(AttendArgs &a, int es, cudaStream_t stream);
+cudaError_t launch_attend_tall(AttendArgs &a, cudaStream_t stream);
+cudaError_t launch_attend_few(AttendArgs &a, cudaStream_t stream);
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -282,12 +291,5 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// Workspace of a call: segment offsets, then the slots of the widest tiles on the most blocks.
-constexpr int kAttBlocks = 160;   // most persistent blocks (a GB300 has 152 SMs)
-struct AttendPlan {
-    size_t off_seg = 0, off_ml = 0, off_part = 0, bytes = 0;
-};
-AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, int n_groups, int blocks);
 
 }  // namespace sv

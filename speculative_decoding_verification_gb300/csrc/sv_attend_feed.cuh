@@ -1,0 +1,349 @@
+// sv_attend_feed.cuh — what the tensor-core kernels of sv_kv_attend share: the walk that describes a block's pieces, the
+// producer warps that gather keys, values and queries from their pages into swizzled shared memory, bounded waits.
+//
+// Ring.  Stages of 128 tokens (keys, then values of a tile, in turn) are filled by four producer warps, 32 tokens each, and
+// freed by the commit of the product that read them.
+#pragma once
+
+#include "sv_attend.cuh"
+#include "sv_tc.cuh"
+
+namespace sv {
+
+constexpr int kTcThreads = 512;       // four warpgroups: two of softmax, producers, products and the walk
+constexpr int kTcKeys = 128;          // tokens of a tile
+constexpr int kRing = 3;              // piece descriptions in flight
+constexpr int kNoPage = INT32_MIN;    // a token past the unit's last
+// Registers: 256 softmax threads take 176, the other 256 give down to 80; 512 x 128 at launch.
+constexpr int kRegsSoftmax = 176, kRegsOther = 80;
+
+struct PieceInfo {
+    long long slot;                   // first workspace slot
+    int r0, m0, vr, h;                // segment's first row, first packed row, rows, key head
+    int table, key0, ctx, end;        // page table's sequence, tokens
+    int k0, k1;                       // key tiles; k0 == k1: no more pieces
+    uint32_t seq;                     // ring number of the first tile's keys
+    int own, tree, whole, boxes;      // own segment, tree mask, output complete here, full tiles load as boxes
+    uint8_t par[SV_MAX_TREE];         // a tree's parents (255: invalid)
+};
+
+struct Feed {
+    uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], pd_full[kRing], pd_empty[kRing];
+    PieceInfo pd[kRing];
+    uint32_t vflag[8][4];             // per stage: tokens whose values are not finite (tiles with hidden tokens only)
+    uint32_t tmem;
+    int dead;                         // a wait gave up: nobody waits any more
+};
+
+// Waits for a phase.  Gives up for everybody after the library's limit: waits return at once from then on, the block
+// runs to its end with meaningless results and the error is reported.
+__device__ __forceinline__ void wait_phase(Feed *fd, uint64_t *bar, uint32_t parity, sv_stats *stats) {
+    if (mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!mbar_try_wait_sleep(bar, parity, kSuspendHintNs)) {
+        if (*reinterpret_cast<volatile int *>(&fd->dead)) return;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *reinterpret_cast<volatile int *>(&fd->dead) = 1;
+            report_error(stats, SV_ERR_TIMEOUT, -1);
+            return;
+        }
+    }
+}
+
+// `readers`: warps that read a piece description.
+__device__ __forceinline__ void feed_init(Feed *fd, int readers) {
+    for (int i = 0; i < 8; ++i) {
+        mbar_init(&fd->kv_full[i], 4);
+        mbar_init(&fd->kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&fd->q_full[i], 4);
+        mbar_init(&fd->q_empty[i], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+        mbar_init(&fd->pd_full[i], 1);
+        mbar_init(&fd->pd_empty[i], readers);
+    }
+    fd->dead = 0;
+}
+
+__device__ __forceinline__ bool not_finite16(uint4 w) {
+    auto bad = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
+    return bad(w.x) || bad(w.y) || bad(w.z) || bad(w.w);
+}
+
+// Waits until at most `left` of the thread's copy groups are in flight.
+__device__ __forceinline__ void copies_wait(int left) {
+    switch (left) {
+        case 0: cp_async_wait<0>(); break;
+        case 1: cp_async_wait<1>(); break;
+        case 2: cp_async_wait<2>(); break;
+        case 3: cp_async_wait<3>(); break;
+        case 4: cp_async_wait<4>(); break;
+        case 5: cp_async_wait<5>(); break;
+        case 6: cp_async_wait<6>(); break;
+        default: cp_async_wait<7>(); break;
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(f32x2 x) {
+    float lo, hi;
+    uint32_t w;
+    f2_unpack(x, lo, hi);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+// Keys and values as 4-D tensors (element, head, slot, page) with boxes of 64 elements by box_rows slots, loaded with the
+// 128-byte swizzle; box_rows is 0 where a box could not stay inside a page.
+struct TcArgs {
+    CUtensorMap k, v;
+    int box_rows;
+    uint32_t shape_s;     // of the score product
+};
+
+// The producers' part, a warp of four.  QROWS rows a query tile; query tiles at q_base, stages at kv_base.
+template <int DP, int STAGES, int QROWS>
+__device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &a2, Feed *fd, uint32_t q_base, uint32_t kv_base, int wl,
+                                             int lane) {
+    constexpr int TILE = 128 * DP * 2, HALF = 128 * 128;
+    uint64_t *bars = fd->kv_full;
+    const int bar_q = (int)(fd->q_full - fd->kv_full);
+    const int D = a.c.head_dim;
+    constexpr int CH = DP / 8;            // 16-byte chunks of a row
+    constexpr int RP = 32 / CH;           // rows of a warp's pass
+    const int ch = lane % CH, rsub = lane / CH;
+    const bool real = ch * 8 < D;         // chunks past the head are zero
+    uint32_t seq = 0, q_use[2] = {0, 0};
+    int qnext = 0;
+    // destination of this lane's chunk of row r (r & 7 is the swizzle)
+    auto place = [&](uint32_t tile, int r, int half) { return tile + (ch >> 3) * half + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+    // Copy groups in flight, oldest first, 8 bits each: the barrier a group completes (one arrival a warp), and kScan for
+    // values of a tile with hidden tokens.
+    constexpr uint64_t kScan = 0x80;
+    uint64_t queue = 0;
+    int queued = 0;
+    auto retire = [&]() {
+        copies_wait(queued - 1);
+        const int bar = (int)(queue & 0x7F);
+        if (queue & kScan) {
+            // A token whose values are not all finite becomes zeros and is flagged; each lane looks at what it copied.
+            uint32_t flags = 0;
+            const uint32_t tile = kv_base + bar * TILE;
+#pragma unroll 4
+            for (int p = 0; p < 32 / RP; ++p) {
+                const uint32_t at = place(tile, wl * 32 + p * RP + rsub, HALF);
+                uint4 w;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
+                const uint32_t bad = __ballot_sync(0xFFFFFFFFu, not_finite16(w));
+                if (bad) {
+#pragma unroll
+                    for (int g = 0; g < RP; ++g)
+                        if ((bad >> (g * CH)) & ((1u << CH) - 1u)) {
+                            flags |= 1u << (p * RP + g);
+                            if (rsub == g) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                        }
+                }
+            }
+            if (lane == 0) fd->vflag[bar][wl] = flags;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + bar);
+        queue >>= 8;
+        --queued;
+    };
+    auto enqueue = [&](uint64_t what) {
+        if (queued == 8) retire();
+        cp_async_commit();
+        queue |= what << (8 * queued);
+        ++queued;
+    };
+    // Waits for a barrier and passes on the copies that land meanwhile: whoever completes the barrier may be waiting for them.
+    auto acquire = [&](uint64_t *bar, uint32_t parity) {
+        // A test, not a try: a try may suspend the warp for microseconds, and copies that land meanwhile have to be
+        // passed on.  The whole warp takes one way: lanes may see the phase end at different tests.
+        while (!__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) {
+            if (queued == 0) {
+                wait_phase(fd, bar, parity, a.stats);
+                return;
+            }
+            retire();
+        }
+    };
+    for (int it = 0;; ++it) {
+        const PieceInfo *pi = &fd->pd[it % kRing];
+        acquire(&fd->pd_full[it % kRing], (it / kRing) & 1);
+        const int k0 = pi->k0, k1 = pi->k1;
+        if (k0 >= k1) break;
+        const int vr = pi->vr, key0 = pi->key0, end = pi->end, ctx = pi->ctx, own = pi->own, h = pi->h, m0 = pi->m0, r0 = pi->r0, pi_boxes = pi->boxes;
+        const int32_t *table = a.bt.page_table + pi->table * a.bt.table_pitch;
+        const int tab = pi->table;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
+        const bool two = vr > QROWS;   // two row tiles share the keys
+        // A tile that every row sees whole goes as boxes where it can, the others by rows: a lane's token of a tile, and its
+        // page, are those of the lane's box or row.
+        const int boxes = pi_boxes ? 32 / a2.box_rows : 0;
+        auto by_box = [&](int k) { return boxes > 0 && key0 + (k + 1) * kTcKeys <= (own ? ctx : end); };
+        auto key_of = [&](int k) { return key0 + k * kTcKeys + wl * 32 + (by_box(k) ? lane * a2.box_rows : lane); };
+        auto page_of = [&](int k) {
+            if (by_box(k) && lane >= boxes) return kNoPage;
+            const int key = key_of(k);
+            return key < end ? table[key / a.c.page_size] : kNoPage;
+        };
+        int page = page_of(k0);
+        // queries: a quarter of the tile a warp
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+            const int qs = two ? t : qnext;
+            acquire(&fd->q_empty[qs], (q_use[qs] & 1) ^ 1);
+            ++q_use[qs];
+            const int m = t * QROWS + wl * (QROWS / 4) + lane;
+            int64_t off = -1;
+            if (lane < QROWS / 4 && m < vr) {
+                const int r = (m0 + m) / a.G;
+                off = (int64_t)(r0 + r) * a.q_row + (int64_t)(h * a.G + (m0 + m - r * a.G)) * a.q_head;
+            }
+            const uint32_t tile = q_base + qs * (QROWS * DP * 2);
+#pragma unroll
+            for (int p = 0; p < QROWS / 4 / RP; ++p) {
+                const int64_t o = __shfl_sync(0xFFFFFFFFu, off, p * RP + rsub);
+                const bool ok = o >= 0 && real;
+                cp_async16(place(tile, wl * (QROWS / 4) + p * RP + rsub, QROWS * 128), a.q + (ok ? o + ch * 16 : 0), ok);
+            }
+            enqueue(bar_q + qs);
+        }
+        if (!two) qnext ^= 1;
+        for (int k = k0; k < k1; ++k) {
+            const int key = key_of(k), pg = page, slot = key - key / a.c.page_size * a.c.page_size;
+            const bool box = by_box(k);
+            int64_t off = -1;
+            if (pg >= 0 && pg < a.c.n_pages) off = pg * a.c.page_b + slot * a.c.slot_b + h * a.c.head_b;
+            else if (pg != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+            if (k + 1 < k1) page = page_of(k + 1);
+            const bool masked = own && key0 + (k + 1) * kTcKeys > ctx;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t stage = seq % STAGES;
+                acquire(&fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1);
+                ++seq;
+                const uint32_t tile = kv_base + stage * TILE;
+                const char *src = kv ? a.c.v : a.c.k;
+                if (box) {   // a bad page id lies outside the tensor and reads zeros
+                    if (elect_one()) mbar_arrive_expect_tx(&fd->kv_full[stage], 32 * DP * 2);
+                    __syncwarp();
+                    for (int b = 0; b < boxes; ++b) {
+                        const int bp = __shfl_sync(0xFFFFFFFFu, pg, b), bs = __shfl_sync(0xFFFFFFFFu, slot, b);
+                        const uint32_t dst = tile + (wl * 32 + b * a2.box_rows) * 128;
+                        if (elect_one()) {
+                            const CUtensorMap *map = kv ? &a2.v : &a2.k;
+                            box_load(dst, map, &fd->kv_full[stage], 0, h, bs, bp);
+                            if (DP == 128) box_load(dst + HALF, map, &fd->kv_full[stage], 64, h, bs, bp);
+                        }
+                        __syncwarp();
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int p = 0; p < 32 / RP; ++p) {
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, p * RP + rsub);
+                    const bool ok = o >= 0 && real;
+                    cp_async16(place(tile, wl * 32 + p * RP + rsub, HALF), src + (ok ? o + ch * 16 : 0), ok);
+                }
+                enqueue(kv == 1 && masked ? kScan | stage : stage);
+            }
+            // A long piece's last copies are passed on before the next piece is set up, which takes as long as they do; after short
+            // pieces the next loads matter more.
+            if (k + 1 == k1 && k1 - k0 >= 4)
+                while (queued) retire();
+        }
+    }
+    while (queued) retire();
+}
+
+// The walk's part, one warp: describes the pieces, then `ends` times that there are no more.
+__device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2, Feed *fd, Walk w, int ends, int lane) {
+    uint32_t seq = 0;
+    int ended = 0;
+    for (int it = 0;; ++it) {
+        Piece p;
+        const bool more = w.next(a, p);
+        wait_phase(fd, &fd->pd_empty[it % kRing], ((it / kRing) & 1) ^ 1, a.stats);
+        PieceInfo *pi = &fd->pd[it % kRing];
+        const bool own = more && p.seg >= a.n_groups, tree = own && a.bt.parents != nullptr;
+        if (more && tree) {
+            const int32_t *par = a.bt.parents + (int64_t)p.g.table * (a.bt.n - 1);
+            for (int j = lane; j < a.bt.n - 1; j += 32) {
+                const int v = par[j];
+                const bool ok = v >= 0 && v <= j;
+                if (!ok) report_error(a.stats, SV_ERR_INVALID_ARG, p.g.table);
+                pi->par[j] = ok ? (uint8_t)v : (uint8_t)255;
+            }
+        }
+        if (lane == 0) {
+            if (more) {
+                pi->slot = (long long)(unit_slot(a, a.geo, p.g, !own, p.h, p.t) + (size_t)blockIdx.x * a.geo.TM);
+                pi->r0 = p.g.r0;
+                pi->m0 = p.t * a.geo.TM;
+                pi->vr = p.vr;
+                pi->h = p.h;
+                pi->table = p.g.table;
+                pi->key0 = p.g.key0;
+                pi->ctx = p.g.ctx;
+                pi->end = p.end;
+                pi->boxes = a2.box_rows > 0 && p.g.key0 % a2.box_rows == 0;
+                pi->k0 = p.k0;
+                pi->k1 = p.k1;
+                pi->seq = seq;
+                pi->own = own;
+                pi->tree = tree;
+                pi->whole = p.k0 == 0 && p.k1 == p.kt && own && seg_alone(p.g);
+            } else {
+                pi->k0 = pi->k1 = 0;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&fd->pd_full[it % kRing]);
+        if (more) seq += 2 * (p.k1 - p.k0);
+        else if (++ended == ends) break;
+    }
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult res;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &res) != cudaSuccess ||
+            res != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+inline bool cache_map(CUtensorMap *map, char *base, const KvCache &c, int box_rows) {
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.kv_heads, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.head_b, (cuuint64_t)c.slot_b, (cuuint64_t)c.page_b};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1}, one[4] = {1, 1, 1, 1};
+    return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The tensors of a call.  Boxes of up to 32 slots (a producer warp's share of a tile), whole swizzle groups of 8 rows, that never
+// cross a page; other page sizes load by rows.
+inline TcArgs tc_args(const KvCache &c, uint32_t shape_s) {
+    TcArgs t{};
+    t.shape_s = shape_s;
+    const int ps = c.page_size;
+    if (ps >= 32 ? ps % 32 == 0 : ps == 8 || ps == 16) {
+        t.box_rows = ps < 32 ? ps : 32;
+        if (encode_tiled() == nullptr || !cache_map(&t.k, c.k, c, t.box_rows) || !cache_map(&t.v, c.v, c, t.box_rows)) t.box_rows = 0;
+    }
+    return t;
+}
+
+}  // namespace sv

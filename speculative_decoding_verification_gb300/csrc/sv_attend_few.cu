@@ -1,0 +1,434 @@
+// sv_attend_few.cu — sv_kv_attend on the tensor cores for up to 32 packed rows a sequence and key head (a single token or a drafted
+// block times the query heads that share a key head): bf16, heads up to 128 wide.
+//
+// Few rows leave a tile of 128 rows mostly empty, so the products are turned round: tokens lie along the 128 rows of tensor
+// memory and the packed rows along its columns,
+//   S^T [128 tokens][32] = K Q^T          O^T [head element][32 + 32] += V^T [P high | P low]
+// with V as stored (its contiguous axis is not the one summed over) and P^T written by the softmax to shared memory, one token's
+// 32 weights a row.  A thread owns a token and its 32 scores: 32 exponentials a tile instead of 128, none of them for empty
+// rows.  A weight enters as two bf16 parts (16 bits in all; one part alone is off by 2^-8, as much as the rounding of the output):
+// they are two halves of the product's columns and cost no further read of V, which bounds it.
+//
+// The maximum of a row is kept until a score passes it by 2^8: then, and on a piece's first tile, the four warps exchange theirs and
+// the output is rescaled.  Other tiles need one vote.
+//
+// A persistent block of 16 warps.  Warps 0-3 take even pieces and warps 4-7 odd ones, so that one piece's end runs beside the
+// next one's start; 8-11 produce, 12 issues the products, 13 walks the range.
+// Tensor memory (256 columns): scores 2 groups x 2 tiles x 32, outputs 2 groups x 64.
+//
+// What bounds it: memory.  A tile is 64 KB (heads of 128), 2800 cycles of an SM's share of the measured copy bandwidth; its
+// products take about 700 and its softmax about 600.
+#include "sv_attend_feed.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int NR = kFewRows;
+constexpr int kFewReaders = 9;        // warps that read a piece description: four producers, the products', one softmax group
+constexpr float kNoMax = -1e30f;      // maximum of a row that has seen no token yet
+
+template <int DP>
+struct FewShape {
+    static constexpr int TILE = 128 * DP * 2;
+    static constexpr int STAGES = DP == 128 ? 5 : 8;
+    static constexpr int HALF = 128 * 128;
+    static constexpr int OFF_P = 2 * NR * DP * 2;                 // after two query tiles
+    static constexpr int PBUF = 128 * 4 * NR;                     // a group's weights: 128 tokens x (32 high + 32 low)
+    static constexpr int OFF_KV = OFF_P + 2 * PBUF;
+    static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
+};
+
+struct FewShared {
+    Feed fd;
+    uint64_t s_full[2][2], p_full[2], p_done[2], done;
+    Walk walk;
+    long long warp_sum[kTcThreads / 32];
+    float top[2][4][NR];              // per group: the warps' maxima of a row, later their sums
+    float inv[2][NR];
+};
+
+// Element-wise reduction of x[0..31] over the warp's lanes: lane r gets that of x[r].
+template <class F>
+__device__ __forceinline__ float reduce_rows(float (&x)[NR], int lane, F f) {
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i < w) {
+                const float mine = up ? x[i + w] : x[i], other = up ? x[i] : x[i + w];
+                x[i] = f(mine, __shfl_xor_sync(0xFFFFFFFFu, other, w));
+            }
+        }
+    }
+    return x[0];
+}
+
+// The packed rows of a unit that see token `key`, as bits.
+__device__ __forceinline__ uint32_t rows_that_see(const PieceInfo *pi, int key, int G, int n) {
+    if (key >= pi->end) return 0;
+    const int rel = key - pi->ctx;
+    if (rel <= 0) return 0xFFFFFFFFu;
+    if (!pi->tree) return rel * G >= 32 ? 0u : 0xFFFFFFFFu << (rel * G);
+    uint32_t below = 1u << rel, rows = 0;   // the node and what descends from it: parents come before their children
+    for (int i = rel + 1; i < n; ++i) {
+        const int p = pi->par[i - 1];
+        if (p != 255 && ((below >> p) & 1u)) below |= 1u << i;
+    }
+    const uint32_t heads = G >= 32 ? 0xFFFFFFFFu : (1u << G) - 1u;
+    for (int i = rel; i < n; ++i)
+        if ((below >> i) & 1u) rows |= heads << (i * G);
+    return rows;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_constant__ AttendArgs a, const __grid_constant__ TcArgs a2) {
+    using S = FewShape<DP>;
+    extern __shared__ __align__(1024) char smem[];
+    FewShared *ms = reinterpret_cast<FewShared *>(smem + S::OFF_MISC);
+    Feed *fd = &ms->fd;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+
+    if (smem_addr(smem) & 1023) {   // the swizzle goes by address bits
+        if (tid == 0) report_error(a.stats, SV_ERR_CUDA, -1);
+        return;
+    }
+    if (tid == 0) {
+        feed_init(fd, kFewReaders);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ms->s_full[i][0], 1);
+            mbar_init(&ms->s_full[i][1], 1);
+            mbar_init(&ms->p_full[i], 4);
+            mbar_init(&ms->p_done[i], 1);
+        }
+        mbar_init(&ms->done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 12) tmem_alloc(&fd->tmem, 256);
+    tc_fence_before();
+    walk_start<kTcThreads>(a, &ms->walk, ms->warp_sum);   // has block-wide barriers
+    tc_fence_after();
+    const uint32_t tmem = fd->tmem;
+    const uint32_t sbase = smem_addr(smem);
+
+    if (warp < 8) {
+        regs_inc<kRegsSoftmax>();
+        // ---------------------------------------------------------------- softmax
+        const int gr = warp >> 2, wl = warp & 3, t = wl * 32 + lane;   // group, warp of it, token of the tile (head element at the end)
+        const uint32_t base = tmem + ((uint32_t)(wl * 32) << 16);
+        const uint32_t colO = base + 128 + gr * 64;
+        char *prow = smem + S::OFF_P + gr * S::PBUF + t * (4 * NR);     // this token's weights
+        const float c = a.scale_log2;
+        uint32_t u = 0;   // tiles this group has worked on
+        auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + gr) : "memory"); };
+        for (int it = gr;; it += 2) {
+            const PieceInfo *pi = &fd->pd[it % kRing];
+            wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
+            __syncwarp();
+            const int k0 = pi->k0, k1 = pi->k1;
+            if (k0 >= k1) break;
+            const int key0 = pi->key0, ctx = pi->ctx;
+            {
+                uint32_t zero[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) zero[j] = 0;
+                tmem_st32(colO, zero);
+                tmem_st32(colO + 32, zero);
+                tc_wait_st();
+            }
+            float mc[NR], l[NR];   // maxima (of scale * log2(e) * q.k), this token column's sums
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                mc[r] = kNoMax;
+                l[r] = 0.0f;
+            }
+            for (int k = k0; k < k1; ++k, ++u) {
+                const int buf = u & 1;
+                wait_phase(fd, &ms->s_full[gr][buf], (u >> 1) & 1, a.stats);
+                __syncwarp();
+                tc_fence_after();
+                float x[NR];
+                {
+                    uint32_t raw[32];
+                    tmem_ld32(base + (gr * 2 + buf) * 32, raw);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(raw[r]) * c;
+                }
+                const int key = key0 + k * kTcKeys + t;
+                const bool masked = key0 + (k + 1) * kTcKeys > ctx;
+                if (masked) {
+                    const uint32_t sees = rows_that_see(pi, key, a.G, a.bt.n);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (!((sees >> r) & 1u)) x[r] = -INFINITY;
+                }
+                float over = x[0] - mc[0];
+#pragma unroll
+                for (int r = 1; r < NR; ++r) over = fmaxf(over, x[r] - mc[r]);
+                uint32_t grow;
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\tsetp.gt.f32 p, %1, 0f41000000;\n\t"
+                    "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                    : "=r"(grow)
+                    : "f"(over), "r"(1 + gr)
+                    : "memory");
+                // the group's previous product has read the weights and written the output
+                if (u > 0) wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
+                __syncwarp();
+                tc_fence_after();
+                if (grow) {
+                    float y[NR];
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) y[r] = x[r];
+                    ms->top[gr][wl][lane] = reduce_rows(y, lane, [](float p, float q) { return fmaxf(p, q); });
+                    group_sync();
+                    uint32_t o[32], o2[32];
+                    if (k > k0) {
+                        tmem_ld32(colO, o);
+                        tmem_ld32(colO + 32, o2);
+                        tc_wait_ld();
+                    }
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        const float top = fmaxf(fmaxf(ms->top[gr][0][r], ms->top[gr][1][r]), fmaxf(ms->top[gr][2][r], ms->top[gr][3][r]));
+                        const float now = fmaxf(mc[r], top);
+                        const float alpha = ex2_fast(mc[r] - now);
+                        mc[r] = now;
+                        l[r] *= alpha;
+                        o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha);
+                        o2[r] = __float_as_uint(__uint_as_float(o2[r]) * alpha);
+                    }
+                    if (k > k0) {
+                        tmem_st32(colO, o);
+                        tmem_st32(colO + 32, o2);
+                        tc_wait_st();
+                    }
+                    group_sync();   // the maxima have been read
+                }
+#pragma unroll
+                for (int q = 0; q < NR / 8; ++q) {   // eight rows: one 16-byte chunk of high parts and one of low parts
+                    uint4 hi, lo;
+                    uint32_t *hp = &hi.x, *lp = &lo.x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = q * 8 + j * 2;
+                        const f32x2 e = f2_ex2(f2_pack(x[r] - mc[r], x[r + 1] - mc[r + 1]));
+                        float e0, e1;
+                        f2_unpack(e, e0, e1);
+                        l[r] += e0;
+                        l[r + 1] += e1;
+                        hp[j] = bf16_pair(e);
+                        lp[j] = bf16_pair(f2_fma(f2_from_bf16x2(hp[j]), f2_pack(-1.0f, -1.0f), e));
+                    }
+                    *reinterpret_cast<uint4 *>(prow + ((q ^ (t & 7)) << 4)) = hi;
+                    *reinterpret_cast<uint4 *>(prow + (((q + 4) ^ (t & 7)) << 4)) = lo;
+                }
+                if (masked) {
+                    // Values that are not finite were replaced by zeros on the way in; they are added here for the rows that see them,
+                    // with the weights that the product would have used.
+                    const uint32_t vs = pi->seq + 2 * (k - k0) + 1, stage = vs % S::STAGES;
+                    wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
+                    __syncwarp();
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) any |= *reinterpret_cast<volatile uint32_t *>(&fd->vflag[stage][q]);
+                    if (any) {
+                        group_sync();   // every token's weights are written
+#pragma unroll 1
+                        for (int j = 0; j < 128; ++j) {
+                            if (!((*reinterpret_cast<volatile uint32_t *>(&fd->vflag[stage][j >> 5]) >> (j & 31)) & 1u)) continue;
+                            const int kk = key0 + k * kTcKeys + j;
+                            const uint32_t sees = rows_that_see(pi, kk, a.G, a.bt.n);
+                            const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, kk);
+                            const float v = t < a.c.head_dim
+                                                ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a.c.v + off + pi->h * a.c.head_b)[t] << 16)
+                                                : 0.0f;
+                            const char *pj = smem + S::OFF_P + gr * S::PBUF + j * (4 * NR);
+                            uint32_t o[32];
+                            tmem_ld32(colO, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) {
+                                const int at = (r & 7) * 2;
+                                const uint16_t ph = *reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ (j & 7)) << 4) + at);
+                                const uint16_t pl = *reinterpret_cast<const uint16_t *>(pj + ((((r >> 3) + 4) ^ (j & 7)) << 4) + at);
+                                const float w = __uint_as_float((uint32_t)ph << 16) + __uint_as_float((uint32_t)pl << 16);
+                                if ((sees >> r) & 1u) o[r] = __float_as_uint(__uint_as_float(o[r]) + w * v);
+                            }
+                            tmem_st32(colO, o);
+                            tc_wait_st();
+                        }
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms->p_full[gr]);
+            }
+            // ---- the piece's end: thread t has head element t of every row
+            const int vr = pi->vr, D = a.c.head_dim, qh0 = pi->h * a.G, r0 = pi->r0;
+            const bool whole = pi->whole;
+            const size_t slot = (size_t)pi->slot;
+            ms->top[gr][wl][lane] = reduce_rows(l, lane, [](float p, float q) { return p + q; });
+            float mine = 0.0f;   // maximum of row `lane`
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                if (r == lane) mine = mc[r];
+            group_sync();
+            if (wl == 0) {
+                const float sum = (ms->top[gr][0][lane] + ms->top[gr][1][lane]) + (ms->top[gr][2][lane] + ms->top[gr][3][lane]);
+                ms->inv[gr][lane] = whole ? (sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f) : 1.0f;
+                if (lane < vr) {
+                    const int i = lane / a.G, g = lane - i * a.G;
+                    if (!whole) a.part_ml[slot + lane] = make_float2(mine, sum);
+                    else if (a.lse) a.lse[(size_t)(r0 + i) * a.q_heads + qh0 + g] = sum == 0.0f ? -INFINITY : (mine + log2f(sum)) / kLog2e;
+                }
+            }
+            if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
+            wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
+            __syncwarp();
+            tc_fence_after();
+            uint32_t o[32], o2[32];
+            tmem_ld32(colO, o);
+            tmem_ld32(colO + 32, o2);
+            group_sync();
+            tc_wait_ld();
+            if (t < D) {
+                if (whole) {
+                    int i = 0, g = 0;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        if (r < vr) {
+                            const float y = (__uint_as_float(o[r]) + __uint_as_float(o2[r])) * ms->inv[gr][r];
+                            store_elem<2>(a.out + (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head + t * 2, y);
+                            if (++g == a.G) {
+                                g = 0;
+                                ++i;
+                            }
+                        }
+                    }
+                } else {
+                    float *dst = a.part + slot * D + t;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (r < vr) dst[(size_t)r * D] = __uint_as_float(o[r]) + __uint_as_float(o2[r]);
+                }
+            }
+            tc_fence_before();
+            group_sync();   // the sums and maxima may be written again
+        }
+    } else if (warp < 12) {
+        regs_dec<kRegsOther>();
+        feed_produce<DP, S::STAGES, NR>(a, a2, fd, sbase, sbase + S::OFF_KV, warp - 8, lane);
+    } else {
+        regs_dec<kRegsOther>();
+        if (warp == 12) {   // the whole warp runs this, with uniform values
+            // ------------------------------------------------------------ matrix products
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            constexpr uint32_t shape_o = mma_shape(2 * NR, true, true, false, false);
+            uint32_t seq = 0, tiles0 = 0, tiles1 = 0, q_use0 = 0, q_use1 = 0;
+            // O^T += V^T P^T of the tile whose scores were issued before the last
+            int late = 0, late_gr = 0;
+            uint32_t late_seq = 0, late_u = 0;
+            auto weigh = [&]() {
+                const uint32_t stage = late_seq % S::STAGES;
+                wait_phase(fd, &fd->kv_full[stage], (late_seq / S::STAGES) & 1, a.stats);
+                wait_phase(fd, &ms->p_full[late_gr], late_u & 1, a.stats);
+                __syncwarp();
+                tc_fence_after();
+                const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, DP == 128 ? S::HALF : 0, 1024);
+                const uint64_t p = smem_operand(sbase + S::OFF_P + late_gr * S::PBUF, 0, 1024);
+                const uint32_t o = tm + 128 + late_gr * 64;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) mma_ss(o, v + kk * (2048 >> 4), p + kk * (2048 >> 4), shape_o, 1u);
+                    mma_commit(&fd->kv_empty[stage]);
+                    mma_commit(&ms->p_done[late_gr]);
+                }
+                __syncwarp();
+            };
+            // Waits for what the next scores need; the weighted sum does not wait for it too.
+            auto ready = [&](uint64_t *bar, uint32_t parity) {
+                if (late && !__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) {
+                    weigh();
+                    late = 0;
+                }
+                wait_phase(fd, bar, parity, a.stats);
+                __syncwarp();
+            };
+            for (int it = 0;; ++it) {
+                const PieceInfo *pi = &fd->pd[it % kRing];
+                ready(&fd->pd_full[it % kRing], (it / kRing) & 1);
+                const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
+                if (nk <= 0) break;
+                if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
+                const int gr = it & 1;
+                ready(&fd->q_full[gr], (gr ? q_use1 : q_use0) & 1);
+                if (gr) ++q_use1;
+                else ++q_use0;
+                const uint64_t q = smem_operand(sbase + gr * (NR * DP * 2), 16, 1024);
+                for (int n = 0; n < nk; ++n) {
+                    const uint32_t stage = seq % S::STAGES, u = gr ? tiles1 : tiles0;
+                    ready(&fd->kv_full[stage], (seq / S::STAGES) & 1);
+                    tc_fence_after();
+                    const uint64_t kt = smem_operand(sbase + S::OFF_KV + stage * S::TILE, 16, 1024);
+                    const uint32_t s = tm + (gr * 2 + (u & 1)) * 32;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < DP / 16; ++kk) {
+                            const uint32_t ka = ((kk >> 2) * S::HALF + (kk & 3) * 32) >> 4, qa = ((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4;
+                            mma_ss(s, kt + ka, q + qa, a2.shape_s, kk > 0);
+                        }
+                        mma_commit(&ms->s_full[gr][u & 1]);
+                        mma_commit(&fd->kv_empty[stage]);
+                        if (n == nk - 1) mma_commit(&fd->q_empty[gr]);
+                    }
+                    __syncwarp();
+                    if (late) weigh();
+                    late = 1;
+                    late_gr = gr;
+                    late_seq = seq + 1;
+                    late_u = u;
+                    seq += 2;
+                    if (gr) ++tiles1;
+                    else ++tiles0;
+                }
+            }
+            if (late) weigh();
+            if (elect_one()) mma_commit(&ms->done);
+            wait_phase(fd, &ms->done, 0, a.stats);
+            __syncwarp();
+        } else if (warp == 13) {
+            feed_walk(a, a2, fd, ms->walk, 2, lane);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_free(tmem, 256);
+}
+
+template <int DP>
+cudaError_t run_few(AttendArgs &a, bool negate, cudaStream_t stream) {
+    constexpr size_t bytes = FewShape<DP>::OFF_MISC + sizeof(FewShared);
+    static_assert(bytes <= 232448, "shared memory of a block");
+    if (prepare_kernel((const void *)k_attend_few<DP>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
+    k_attend_few<DP><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, tc_args(a.c, mma_shape(NR, false, false, false, negate)));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_few(AttendArgs &a, cudaStream_t stream) {
+    a.geo.TM = NR;
+    a.geo.TK = kTcKeys;
+    AttendArgs t = a;
+    // The maximum is taken after the scale; a negative scale negates the queries in the product, and zero stays zero.
+    const bool negate = a.scale_log2 < 0.0f;
+    t.scale_log2 = fabsf(a.scale_log2);
+    return a.c.head_dim <= 64 ? run_few<64>(t, negate, stream) : run_few<128>(t, negate, stream);
+}
+
+}  // namespace sv

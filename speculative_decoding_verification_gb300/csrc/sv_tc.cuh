@@ -24,10 +24,11 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, u
            1ull << 46 | 2ull << 61;
 }
 
-// bf16 operands, float32 accumulation, M = 128 rows by N columns.
-__host__ __device__ constexpr uint32_t mma_shape(int N, bool b_rows_summed, bool negate_a) {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (negate_a ? 1u << 13 : 0u) | (b_rows_summed ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
-           (128u >> 4) << 24;
+// bf16 operands, float32 accumulation, M = 128 rows by N columns.  a_t, b_t: the operand's contiguous axis in shared memory is not
+// the one summed over; a_neg, b_neg: the operand enters negated.
+__host__ __device__ constexpr uint32_t mma_shape(int N, bool a_t, bool b_t, bool a_neg, bool b_neg) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (a_neg ? 1u << 13 : 0u) | (b_neg ? 1u << 14 : 0u) | (a_t ? 1u << 15 : 0u) |
+           (b_t ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
 }
 
 // One thread of the warp, the same one every time.  Products are issued inside `if (elect_one())` in code that the whole
