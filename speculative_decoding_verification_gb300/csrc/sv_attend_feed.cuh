@@ -86,6 +86,16 @@ __device__ __forceinline__ void copies_wait(int left) {
     }
 }
 
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&x)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+}
+
+__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t bf16_pair(f32x2 x) {
     float lo, hi;
     uint32_t w;

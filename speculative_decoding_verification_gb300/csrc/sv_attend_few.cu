@@ -44,8 +44,10 @@ struct FewShared {
     uint64_t s_full[2][2], p_full[2], p_done[2], done;
     Walk walk;
     long long warp_sum[kTcThreads / 32];
-    float top[2][4][NR];              // per group: the warps' maxima of a row, later their sums
-    float inv[2][NR];
+    // per group
+    float top[2][4][NR];              // the warps' maxima of a row, later their sums
+    alignas(16) float shift[2][NR];   // minus a row's maximum (of scale * log2(e) * q.k)
+    alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end 1 / sum
 };
 
 // Element-wise reduction of x[0..31] over the warp's lanes: lane r gets that of x[r].
@@ -118,8 +120,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         const int gr = warp >> 2, wl = warp & 3, t = wl * 32 + lane;   // group, warp of it, token of the tile (head element at the end)
         const uint32_t base = tmem + ((uint32_t)(wl * 32) << 16);
         const uint32_t colO = base + 128 + gr * 64;
-        char *prow = smem + S::OFF_P + gr * S::PBUF + t * (4 * NR);     // this token's weights
-        const float c = a.scale_log2;
+        const uint32_t prow = sbase + S::OFF_P + gr * S::PBUF + t * (4 * NR);     // this token's weights
+        const f32x2 c2 = f2_pack(a.scale_log2, a.scale_log2);
         uint32_t u = 0;   // tiles this group has worked on
         auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + gr) : "memory"); };
         for (int it = gr;; it += 2) {
@@ -137,93 +139,94 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 tmem_st32(colO + 32, zero);
                 tc_wait_st();
             }
-            float mc[NR], l[NR];   // maxima (of scale * log2(e) * q.k), this token column's sums
+            f32x2 l[NR / 2];   // this token column's sums
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                mc[r] = kNoMax;
-                l[r] = 0.0f;
-            }
+            for (int r = 0; r < NR / 2; ++r) l[r] = 0;
+            float *shift = ms->shift[gr], *alpha = ms->alpha[gr];
             for (int k = k0; k < k1; ++k, ++u) {
                 const int buf = u & 1;
+                const uint32_t colS = base + (gr * 2 + buf) * 32;
                 wait_phase(fd, &ms->s_full[gr][buf], (u >> 1) & 1, a.stats);
                 __syncwarp();
                 tc_fence_after();
-                float x[NR];
-                {
+                const bool masked = key0 + (k + 1) * kTcKeys > ctx;
+                const uint32_t sees = masked ? rows_that_see(pi, key0 + k * kTcKeys + t, a.G, a.bt.n) : 0xFFFFFFFFu;
+                float x[NR];   // score - maximum
+                auto scores = [&](bool shifted) {
                     uint32_t raw[32];
-                    tmem_ld32(base + (gr * 2 + buf) * 32, raw);
+                    tmem_ld32(colS, raw);
                     tc_wait_ld();
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(raw[r]) * c;
-                }
-                const int key = key0 + k * kTcKeys + t;
-                const bool masked = key0 + (k + 1) * kTcKeys > ctx;
-                if (masked) {
-                    const uint32_t sees = rows_that_see(pi, key, a.G, a.bt.n);
+                    for (int r = 0; r < NR; r += 4) {
+                        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (shifted) m = *reinterpret_cast<const float4 *>(shift + r);
+                        f2_unpack(f2_fma(f2_from_u32x2(raw[r], raw[r + 1]), c2, f2_pack(m.x, m.y)), x[r], x[r + 1]);
+                        f2_unpack(f2_fma(f2_from_u32x2(raw[r + 2], raw[r + 3]), c2, f2_pack(m.z, m.w)), x[r + 2], x[r + 3]);
+                    }
+                    if (masked) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        if (!((sees >> r) & 1u)) x[r] = -INFINITY;
-                }
-                float over = x[0] - mc[0];
+                        for (int r = 0; r < NR; ++r)
+                            if (!((sees >> r) & 1u)) x[r] = -INFINITY;
+                    }
+                };
+                uint32_t grow = 1;   // a piece's first tile sets the maxima
+                if (k > k0) {
+                    scores(true);
+                    float over = x[0];
 #pragma unroll
-                for (int r = 1; r < NR; ++r) over = fmaxf(over, x[r] - mc[r]);
-                uint32_t grow;
-                asm volatile(
-                    "{\n\t.reg .pred p, q;\n\tsetp.gt.f32 p, %1, 0f41000000;\n\t"
-                    "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                    : "=r"(grow)
-                    : "f"(over), "r"(1 + gr)
-                    : "memory");
+                    for (int r = 1; r < NR; ++r) over = fmaxf(over, x[r]);
+                    asm volatile(
+                        "{\n\t.reg .pred p, q;\n\tsetp.gt.f32 p, %1, 0f41000000;\n\t"
+                        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                        : "=r"(grow)
+                        : "f"(over), "r"(1 + gr)
+                        : "memory");
+                }
                 // the group's previous product has read the weights and written the output
                 if (u > 0) wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
                 __syncwarp();
                 tc_fence_after();
                 if (grow) {
-                    float y[NR];
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) y[r] = x[r];
-                    ms->top[gr][wl][lane] = reduce_rows(y, lane, [](float p, float q) { return fmaxf(p, q); });
+                    scores(false);
+                    ms->top[gr][wl][lane] = reduce_rows(x, lane, [](float p, float q) { return fmaxf(p, q); });
                     group_sync();
-                    uint32_t o[32], o2[32];
-                    if (k > k0) {
-                        tmem_ld32(colO, o);
-                        tmem_ld32(colO + 32, o2);
-                        tc_wait_ld();
+                    if (wl == 0) {
+                        const float old = k > k0 ? -shift[lane] : kNoMax;
+                        const float now = fmaxf(fmaxf(fmaxf(ms->top[gr][0][lane], ms->top[gr][1][lane]), old),
+                                                fmaxf(ms->top[gr][2][lane], ms->top[gr][3][lane]));
+                        alpha[lane] = ex2_fast(old - now);
+                        shift[lane] = -now;
                     }
+                    group_sync();
+                    if (k > k0) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        const float top = fmaxf(fmaxf(ms->top[gr][0][r], ms->top[gr][1][r]), fmaxf(ms->top[gr][2][r], ms->top[gr][3][r]));
-                        const float now = fmaxf(mc[r], top);
-                        const float alpha = ex2_fast(mc[r] - now);
-                        mc[r] = now;
-                        l[r] *= alpha;
-                        o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha);
-                        o2[r] = __float_as_uint(__uint_as_float(o2[r]) * alpha);
-                    }
-                    if (k > k0) {
-                        tmem_st32(colO, o);
-                        tmem_st32(colO + 32, o2);
+                        for (int r = 0; r < NR / 2; ++r) l[r] = f2_mul(l[r], *reinterpret_cast<const f32x2 *>(alpha + 2 * r));
+#pragma unroll 1
+                        for (int j = 0; j < 64; j += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(colO + j, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
+                            tmem_st32(colO + j, o);
+                        }
                         tc_wait_st();
                     }
-                    group_sync();   // the maxima have been read
+                    scores(true);
                 }
 #pragma unroll
                 for (int q = 0; q < NR / 8; ++q) {   // eight rows: one 16-byte chunk of high parts and one of low parts
-                    uint4 hi, lo;
-                    uint32_t *hp = &hi.x, *lp = &lo.x;
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = q * 8 + j * 2;
-                        const f32x2 e = f2_ex2(f2_pack(x[r] - mc[r], x[r + 1] - mc[r + 1]));
-                        float e0, e1;
-                        f2_unpack(e, e0, e1);
-                        l[r] += e0;
-                        l[r + 1] += e1;
-                        hp[j] = bf16_pair(e);
-                        lp[j] = bf16_pair(f2_fma(f2_from_bf16x2(hp[j]), f2_pack(-1.0f, -1.0f), e));
+                        const f32x2 e = f2_ex2(f2_pack(x[r], x[r + 1]));
+                        l[r / 2] = f2_add(l[r / 2], e);
+                        hi[j] = bf16_pair(e);
+                        lo[j] = bf16_pair(f2_fma(f2_from_bf16x2(hi[j]), f2_pack(-1.0f, -1.0f), e));
                     }
-                    *reinterpret_cast<uint4 *>(prow + ((q ^ (t & 7)) << 4)) = hi;
-                    *reinterpret_cast<uint4 *>(prow + (((q + 4) ^ (t & 7)) << 4)) = lo;
+                    sts128(prow + ((q ^ (t & 7)) << 4), hi);
+                    sts128(prow + (((q + 4) ^ (t & 7)) << 4), lo);
                 }
                 if (masked) {
                     // Values that are not finite were replaced by zeros on the way in; they are added here for the rows that see them,
@@ -271,15 +274,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             const int vr = pi->vr, D = a.c.head_dim, qh0 = pi->h * a.G, r0 = pi->r0;
             const bool whole = pi->whole;
             const size_t slot = (size_t)pi->slot;
-            ms->top[gr][wl][lane] = reduce_rows(l, lane, [](float p, float q) { return p + q; });
-            float mine = 0.0f;   // maximum of row `lane`
+            {
+                float x[NR];
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-                if (r == lane) mine = mc[r];
+                for (int r = 0; r < NR; r += 2) f2_unpack(l[r / 2], x[r], x[r + 1]);
+                ms->top[gr][wl][lane] = reduce_rows(x, lane, [](float p, float q) { return p + q; });
+            }
             group_sync();
             if (wl == 0) {
                 const float sum = (ms->top[gr][0][lane] + ms->top[gr][1][lane]) + (ms->top[gr][2][lane] + ms->top[gr][3][lane]);
-                ms->inv[gr][lane] = whole ? (sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f) : 1.0f;
+                const float mine = -shift[lane];
+                alpha[lane] = whole ? (sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f) : 1.0f;
                 if (lane < vr) {
                     const int i = lane / a.G, g = lane - i * a.G;
                     if (!whole) a.part_ml[slot + lane] = make_float2(mine, sum);
@@ -290,19 +295,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
             __syncwarp();
             tc_fence_after();
-            uint32_t o[32], o2[32];
-            tmem_ld32(colO, o);
-            tmem_ld32(colO + 32, o2);
+            float y[NR];   // the row's weighted values: the products with high and low parts
+            {
+                uint32_t o[32], o2[32];
+                tmem_ld32(colO, o);
+                tmem_ld32(colO + 32, o2);
+                tc_wait_ld();
+#pragma unroll
+                for (int r = 0; r < NR; ++r) y[r] = __uint_as_float(o[r]) + __uint_as_float(o2[r]);
+            }
             group_sync();
-            tc_wait_ld();
             if (t < D) {
                 if (whole) {
                     int i = 0, g = 0;
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
                         if (r < vr) {
-                            const float y = (__uint_as_float(o[r]) + __uint_as_float(o2[r])) * ms->inv[gr][r];
-                            store_elem<2>(a.out + (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head + t * 2, y);
+                            store_elem<2>(a.out + (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head + t * 2, y[r] * alpha[r]);
                             if (++g == a.G) {
                                 g = 0;
                                 ++i;
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                     float *dst = a.part + slot * D + t;
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
-                        if (r < vr) dst[(size_t)r * D] = __uint_as_float(o[r]) + __uint_as_float(o2[r]);
+                        if (r < vr) dst[(size_t)r * D] = y[r];
                 }
             }
             tc_fence_before();

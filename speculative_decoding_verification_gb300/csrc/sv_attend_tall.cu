@@ -128,12 +128,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 __syncwarp();
                 if (active) {
                     tc_fence_after();
-                    uint32_t x[128];
-#pragma unroll
-                    for (int j = 0; j < 128; j += 32) tmem_ld32(colS + j, x + j);
                     const int first = key0 + k * kTcKeys;
                     const bool masked = own ? first + kTcKeys > ctx : first + kTcKeys > end;
-                    tc_wait_ld();
                     uint32_t vis[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
                     if (masked) {
 #pragma unroll
@@ -146,17 +142,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                                 vis[q] = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
                             }
                         }
-#pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if (!((vis[j >> 5] >> (j & 31)) & 1u)) x[j] = 0xFF800000u;   // -inf
                     }
+                    // The scores' second half stays in registers, the first is read twice: the weights go where the scores were, in
+                    // the order 0 (columns 0-15 and 64-79), 1, 2, 3 of 32 scores each.
+                    uint32_t x[32], hold[64];
                     float top[4] = {m_used, -INFINITY, -INFINITY, -INFINITY};
+                    auto mask32 = [&](uint32_t *y, uint32_t v) {
+                        if (masked) {
 #pragma unroll
-                    for (int j = 0; j < 128; j += 8) {
+                            for (int j = 0; j < 32; ++j)
+                                if (!((v >> j) & 1u)) y[j] = 0xFF800000u;   // -inf
+                        }
+                    };
+                    auto max32 = [&](const uint32_t *y) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            top[u] = fmaxf(top[u], fmaxf(__uint_as_float(x[j + 2 * u]), __uint_as_float(x[j + 2 * u + 1])));
-                    }
+                        for (int j = 0; j < 32; j += 8) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                top[u] = fmaxf(top[u], fmaxf(__uint_as_float(y[j + 2 * u]), __uint_as_float(y[j + 2 * u + 1])));
+                        }
+                    };
+                    tmem_ld32(colS + 64, hold);
+                    tmem_ld32(colS + 96, hold + 32);
+                    tmem_ld32(colS + 32, x);
+                    tc_wait_ld();
+                    mask32(hold, vis[2]);
+                    mask32(hold + 32, vis[3]);
+                    mask32(x, vis[1]);
+                    max32(x);
+                    tmem_ld32(colS, x);
+                    max32(hold);
+                    max32(hold + 32);
+                    tc_wait_ld();
+                    mask32(x, vis[0]);
+                    max32(x);
                     const float m_new = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     // The output is rescaled only when the maximum has grown by more than 2^8: weights up to 2^8 are as
                     // exact as those up to 1, and most tiles then leave the output alone.
@@ -181,19 +200,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     const f32x2 c2 = f2_pack(c, c), s2 = f2_pack(-shift, -shift);
                     const f32x2 minus1 = f2_pack(-1.0f, -1.0f);
                     f32x2 sum[2] = {f2_pack(l, 0.0f), f2_pack(0.0f, 0.0f)};
+                    auto weights = [&](const uint32_t *y, int q) {
+                        uint32_t p[16], r[16];
 #pragma unroll
-                    for (int j = 0; j < 128; j += 64) {
-                        uint32_t p[32], r[32];
-#pragma unroll
-                        for (int u = 0; u < 32; ++u) {
-                            const f32x2 e = f2_ex2(f2_fma(f2_from_u32x2(x[j + 2 * u], x[j + 2 * u + 1]), c2, s2));
+                        for (int u = 0; u < 16; ++u) {
+                            const f32x2 e = f2_ex2(f2_fma(f2_from_u32x2(y[2 * u], y[2 * u + 1]), c2, s2));
                             sum[u & 1] = f2_add(sum[u & 1], e);
                             p[u] = bf16_pair(e);
                             r[u] = bf16_pair(f2_fma(f2_from_bf16x2(p[u]), minus1, e));
                         }
-                        tmem_st32(colS + j / 2, p);
-                        tmem_st32(colS + 64 + j / 2, r);
-                    }
+                        tmem_st16(colS + q * 16, p);
+                        tmem_st16(colS + 64 + q * 16, r);
+                    };
+                    weights(x, 0);
+                    tmem_ld32(colS + 32, x);
+                    tc_wait_ld();
+                    mask32(x, vis[1]);
+                    weights(x, 1);
+                    weights(hold, 2);
+                    weights(hold + 32, 3);
                     l = f2_sum(f2_add(sum[0], sum[1]));
                     tc_wait_st();
                     if (own && masked) {
