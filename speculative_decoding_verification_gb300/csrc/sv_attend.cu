@@ -56,13 +56,17 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     uint32_t *row_anc = reinterpret_cast<uint32_t *>(row_lim + TM);
 
     walk_start<kAttThreads>(a, &s_walk, warp_sum);
+    pdl_trigger();
     Walk w = s_walk;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
     const int D = a.c.head_dim, D4 = D / 4, chunks = D * ES / 16;
     const int rg = tid / S::TPR, tx = tid % S::TPR;
     const int cx = tx % S::CG, ks = S::KS > 1 ? tx / S::CG : 0;
     Piece p;
-    while (w.next(a, p)) {
+    for (long long pos = w.pos, first = 1;; first = 0) {
+        const bool more = w.next(a, p);
+        if (first && tid == 0) leave_tail(a, p, more, pos, w.total);
+        if (!more) break;
         const int m0 = p.t * TM, h = p.h;
         const int32_t *table = a.bt.page_table + p.g.table * a.bt.table_pitch;
         auto load_tile = [&](int k, int buf) {
@@ -287,55 +291,46 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     }
 }
 
-// Adds the pieces of a row's units: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  One warp a (row, query
-// head), prefix pieces first, then own ones, each in the order of the blocks that made them.
-template <int ES>
-__global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a, const AttendGeo prefix, const AttendGeo own) {
-    pdl_wait();
-    const long long w = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    if (w >= (long long)a.bt.rows * a.q_heads) return;
-    const int row = (int)(w / a.q_heads), qh = (int)(w - (long long)row * a.q_heads);
-    const int h = qh / a.G;
-    const int b = row_sequence(a.bt, row);
+// Adds the pieces of one row, a warp: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over n pieces, in order; slot_of(p) is
+// piece p's slot.  Lanes take the pieces' maxima and sums, then the row's elements.
+template <int ES, class F>
+__device__ __forceinline__ void join_row(const AttendArgs &a, int row, int qh, int n, int lane, F slot_of) {
     const int D = a.c.head_dim, D4 = D / 4;
     float m = -INFINITY, l = 0.0f;
     float4 o[2] = {};
-    for (int which = a.n_groups ? 0 : 1; which < 2; ++which) {
-        const int s = which == 0 ? group_of(a, b) : a.n_groups + b;
-        const AttendGeo &geo = which == 0 ? prefix : own;
-        const Seg g = seg_of(a, geo, s, false);
-        const long long total = geo.seg_off[geo.s1 - geo.s0];
-        if (row < g.r0 || row >= g.r0 + g.n || total == 0) continue;
-        const int mm = (row - g.r0) * a.G + (qh - h * a.G), t = mm / geo.TM;
-        const int kt = seg_tiles(a, geo, g, t);
-        if (kt <= 0) continue;
-        const long long per = seg_head_tiles(a, geo, g);
-        long long first = geo.seg_off[s - geo.s0] + per * h;
-        if (!g.chain) first += (long long)t * kt;
-        else
-            for (int u = 0; u < t; ++u) first += seg_tiles(a, geo, g, u);
-        const int parts = range_blocks(total, geo.blocks);
-        const int c0 = block_of_tile(first, total, parts), c1 = block_of_tile(first + kt - 1, total, parts);
-        if (which == 1 && c0 == c1 && seg_alone(g)) return;   // written by its piece
-        const size_t base = unit_slot(a, geo, g, which == 0, h, t) + (mm - t * geo.TM);
-        for (int c = c0; c <= c1; ++c) {
-            const size_t slot = base + (size_t)c * geo.TM;
-            const float2 ml = a.part_ml[slot];
-            if (ml.y == 0.0f) continue;   // the row saw none of the piece's tokens
-            const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.0f : top;
-            const float f0 = exp2f(m - ref), f1 = exp2f(ml.x - ref);
-            m = top;
-            l = l * f0 + ml.y * f1;
+    for (int base = 0; base < n; base += 32) {
+        const int p = base + lane;
+        const size_t slot = slot_of(p < n ? p : n - 1);
+        const float2 ml = p < n ? a.part_ml[slot] : make_float2(-INFINITY, 0.0f);
+        float top = ml.y == 0.0f ? -INFINITY : ml.x;   // a piece whose tokens the row did not see adds nothing
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int col = lane + 32 * j;
-                if (col < D4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(a.part + slot * D + col * 4);
-                    o[j].x = o[j].x * f0 + x.x * f1;
-                    o[j].y = o[j].y * f0 + x.y * f1;
-                    o[j].z = o[j].z * f0 + x.z * f1;
-                    o[j].w = o[j].w * f0 + x.w * f1;
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        top = fmaxf(top, m);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        const float w = ml.y == 0.0f ? 0.0f : exp2f(ml.x - ref), before = exp2f(m - ref);
+        float sum = w * ml.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        l = l * before + sum;
+        m = top;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) o[j] = make_float4(o[j].x * before, o[j].y * before, o[j].z * before, o[j].w * before);
+        const int many = min(32, n - base);
+#pragma unroll 4
+        for (int q = 0; q < many; ++q) {
+            const float f = __shfl_sync(0xFFFFFFFFu, w, q);
+            const size_t at = __shfl_sync(0xFFFFFFFFu, slot, q) * D;
+            if (f != 0.0f) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int col = lane + 32 * j;
+                    if (col < D4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(a.part + at + col * 4);
+                        o[j].x = fmaf(x.x, f, o[j].x);
+                        o[j].y = fmaf(x.y, f, o[j].y);
+                        o[j].z = fmaf(x.z, f, o[j].z);
+                        o[j].w = fmaf(x.w, f, o[j].w);
+                    }
                 }
             }
         }
@@ -358,9 +353,94 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a, const A
     if (a.lse && lane == 0) a.lse[(size_t)row * a.q_heads + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) / kLog2e;
 }
 
+// Without prefixes: the units that several blocks share, one block of the grid eight rows of a tail.
+template <int ES>
+__global__ void __launch_bounds__(256) k_attend_join_tails(const AttendArgs a) {
+    pdl_wait();
+    const AttendTail t = a.tails[blockIdx.x];
+    const int lane = threadIdx.x & 31, m = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (m >= t.vr || t.pieces == 0) return;
+    const int i = (t.m0 + m) / a.G, g = t.m0 + m - i * a.G;
+    join_row<ES>(a, t.r0 + i, t.h * a.G + g, t.pieces, lane, [&](int p) { return (size_t)t.slot + m + (size_t)p * a.geo.TM; });
+}
+
+// With prefixes: every row adds those of its group's prefix, then its own.  A block takes kJoinRows packed rows of one
+// (sequence, key head); its segments are looked up once, its rows' pieces by a lane each.
+constexpr int kJoinRows = 8;
+
+struct JoinSeg {
+    Seg g;
+    long long first, total;   // the key head's first tile; all tiles
+    int parts, kt;            // blocks; tiles of a unit (not chain)
+};
+
+__device__ __forceinline__ void join_seg(const AttendArgs &a, const AttendGeo &geo, int s, int h, JoinSeg *j) {
+    j->total = geo.seg_off[geo.s1 - geo.s0];
+    j->g = seg_of(a, geo, s, false);
+    j->first = geo.seg_off[s - geo.s0] + seg_head_tiles(a, geo, j->g) * h;
+    j->parts = range_blocks(j->total, geo.blocks);
+    j->kt = j->g.tiles_m > 0 ? seg_tiles(a, geo, j->g, 0) : 0;
+}
+
+// Blocks [c0, c1] that hold pieces of the unit with row tile t; c1 < c0: none.
+__device__ __forceinline__ void join_blocks(const AttendArgs &a, const AttendGeo &geo, const JoinSeg &j, int t, int &c0, int &c1) {
+    c0 = 0;
+    c1 = -1;
+    int kt = j.kt;
+    long long first = j.first;
+    if (!j.g.chain) {
+        first += (long long)t * kt;
+    } else if (t > 0) {
+        for (int u = 0; u < t; ++u) first += seg_tiles(a, geo, j.g, u);
+        kt = seg_tiles(a, geo, j.g, t);
+    }
+    if (kt <= 0 || j.total == 0) return;
+    c0 = block_of_tile(first, j.total, j.parts);
+    c1 = block_of_tile(first + kt - 1, j.total, j.parts);
+}
+
+template <int ES>
+__global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a, const AttendGeo prefix, const AttendGeo own) {
+    __shared__ JoinSeg sj[2];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int h = blockIdx.x % a.c.kv_heads, unit = blockIdx.x / a.c.kv_heads;
+    const bool ragged = a.bt.row_start != nullptr;   // then a block takes the heads of one row
+    const int b = ragged ? row_sequence(a.bt, unit) : unit;
+    if (threadIdx.x == 0) join_seg(a, own, a.n_groups + b, h, &sj[1]);
+    if (threadIdx.x == 32) join_seg(a, prefix, group_of(a, b), h, &sj[0]);
+    __syncthreads();
+    const JoinSeg &jo = sj[1], &jp = sj[0];
+    const int start = ragged ? (unit - jo.g.r0) * a.G : blockIdx.y * kJoinRows;
+    const int stop = start < 0 ? start : min(jo.g.packed, start + (ragged ? a.G : kJoinRows));
+    for (int mm = start + wp; mm < stop; mm += 8) {
+        const int i = mm / a.G, row = jo.g.r0 + i, qh = h * a.G + mm - i * a.G;
+        const int to = mm / own.TM;
+        int o0, o1, p0 = 0, p1 = -1;
+        join_blocks(a, own, jo, to, o0, o1);
+        if (o0 == o1 && seg_alone(jo.g)) continue;   // written by its piece
+        size_t sp = 0;
+        if (row >= jp.g.r0 && row < jp.g.r0 + jp.g.n) {
+            const int mp = (row - jp.g.r0) * a.G + mm - i * a.G, t = mp / prefix.TM;
+            join_blocks(a, prefix, jp, t, p0, p1);
+            sp = unit_slot(a, prefix, jp.g, true, h, t) + (mp - t * prefix.TM);
+        }
+        const size_t so = unit_slot(a, own, jo.g, false, h, to) + (mm - to * own.TM);
+        const int np = p1 - p0 + 1;
+        join_row<ES>(a, row, qh, np + (o1 - o0 + 1), lane, [&](int p) {
+            return p < np ? sp + (size_t)(p0 + p) * prefix.TM : so + (size_t)(o0 + p - np) * own.TM;
+        });
+    }
+}
+
 cudaError_t launch_attend_join(const AttendArgs &a, const AttendGeo &prefix, const AttendGeo &own, int es, cudaStream_t stream) {
-    const long long warps = (long long)a.bt.rows * a.q_heads;
-    const dim3 grid((unsigned)((warps + 7) / 8));
+    if (a.n_groups == 0) {
+        const dim3 grid((unsigned)own.blocks, (unsigned)((own.TM + 7) / 8));
+        return es == 4 ? launch_pdl(k_attend_join_tails<4>, grid, dim3(256), 0, stream, a)
+                       : launch_pdl(k_attend_join_tails<2>, grid, dim3(256), 0, stream, a);
+    }
+    const dim3 grid = a.bt.row_start ? dim3((unsigned)(a.bt.rows * a.c.kv_heads))
+                                     : dim3((unsigned)(a.bt.B * a.c.kv_heads), (unsigned)div_up((long long)a.bt.n * a.G, kJoinRows));
     return es == 4 ? launch_pdl(k_attend_join<4>, grid, dim3(256), 0, stream, a, prefix, own)
                    : launch_pdl(k_attend_join<2>, grid, dim3(256), 0, stream, a, prefix, own);
 }
@@ -390,7 +470,7 @@ constexpr int kAttBlocks = 160;   // most persistent blocks (a GB300 has 152 SMs
 constexpr int kAttMaxTile = 256;
 
 struct AttendPlan {
-    size_t off_seg = 0, off_ml = 0, off_part = 0, bytes = 0;
+    size_t off_seg = 0, off_tails = 0, off_ml = 0, off_part = 0, bytes = 0;
 };
 
 static AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, int n_groups) {
@@ -399,6 +479,7 @@ static AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, in
     const size_t slots = attend_slots(rows, q_heads, n_groups > 0, true, kAttMaxTile, kAttBlocks) +
                          (n_groups > 0 ? (size_t)kFewRows * kAttBlocks : 0);
     p.off_seg = cv.take<long long>((size_t)n_groups + B + 2);
+    p.off_tails = cv.take<AttendTail>(kAttBlocks);
     p.off_ml = cv.take<float2>(slots);
     p.off_part = cv.take<float>(slots * head_dim);
     p.bytes = cv.off + 256;
@@ -426,7 +507,8 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     const int es = elem_size((sv_dtype)cache->dtype);
     if (batch->rows > 0 && (q == nullptr || out == nullptr)) return SV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !strides16(es, q_row_stride, q_head_stride) ||
-        !strides16(es, out_row_stride, out_head_stride) || (int64_t)batch->rows * q_heads > INT32_MAX)
+        !strides16(es, out_row_stride, out_head_stride) || (int64_t)batch->rows * q_heads > INT32_MAX ||
+        (int64_t)batch->B * cache->kv_heads > INT32_MAX || (n_groups > 0 && batch->row_start == nullptr && (int64_t)batch->n * q_heads > 65535LL * kJoinRows))
         return SV_ERR_INVALID_ARG;
     const AttendPlan pl = plan_attend(batch->rows, q_heads, cache->head_dim, batch->B, n_groups);
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.bytes) return SV_ERR_WORKSPACE;
@@ -454,6 +536,7 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     a.n_groups = n_groups;
     a.lse = lse;
     a.stats = stats;
+    a.tails = reinterpret_cast<AttendTail *>(w + pl.off_tails);
     a.part_ml = reinterpret_cast<float2 *>(w + pl.off_ml);
     a.part = reinterpret_cast<float *>(w + pl.off_part);
     long long *seg = reinterpret_cast<long long *>(w + pl.off_seg);

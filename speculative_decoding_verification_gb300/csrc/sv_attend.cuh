@@ -20,6 +20,14 @@ namespace sv {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// A unit cut by the ranges of several blocks, left by the block that ends it (only its first piece can): without prefixes
+// these are all that has to be joined.
+struct AttendTail {
+    long long slot;   // of the first piece; the next ones follow TM slots apart
+    int pieces;       // 0: none
+    int r0, m0, vr, h;
+};
+
 // What one launch covers and how it cuts it: segments [s0, s1), row and key tiles, blocks.
 struct AttendGeo {
     int s0, s1, TM, TK, blocks;
@@ -41,6 +49,7 @@ struct AttendArgs {
     sv_stats *stats;
     AttendGeo geo;        // of this launch
     // workspace
+    struct AttendTail *tails;   // [blocks] the unit that a block ends and an earlier one began
     float *part;          // [slots][head_dim] weighted values of a packed row of a piece
     float2 *part_ml;      // [slots] its maximum (of scale * log2(e) * q.k) and sum
 };
@@ -161,7 +170,7 @@ struct Piece {
 
 // Walks the pieces of one block's range [pos, stop) of tiles.
 struct Walk {
-    long long pos, stop, seg_start, per_head;
+    long long pos, stop, seg_start, per_head, total;
     int s;
     Seg g;
 
@@ -203,6 +212,21 @@ struct Walk {
     }
 };
 
+// Block c's tail, from its first piece p (`more` false: the range is empty), whose first tile was at `pos` of `total`.
+__device__ __forceinline__ void leave_tail(const AttendArgs &a, const Piece &p, bool more, long long pos, long long total) {
+    AttendTail t{};
+    if (more && p.k0 > 0 && p.k1 == p.kt) {
+        const int c0 = block_of_tile(pos - p.k0, total, range_blocks(total, a.geo.blocks));
+        t.pieces = (int)blockIdx.x - c0 + 1;
+        t.slot = (long long)(unit_slot(a, a.geo, p.g, p.seg < a.n_groups, p.h, p.t) + (size_t)c0 * a.geo.TM);
+        t.r0 = p.g.r0;
+        t.m0 = p.t * a.geo.TM;
+        t.vr = p.vr;
+        t.h = p.h;
+    }
+    a.tails[blockIdx.x] = t;
+}
+
 // Block-wide: the total of tiles and, for this block's range, where its walk starts.  Each thread takes a
 // run of consecutive segments; warp_sum has THREADS / 32 places.  Block 0 leaves the segments' offsets for the join and reports bad input.
 template <int THREADS>
@@ -230,6 +254,7 @@ __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long lo
     }
     const int parts = range_blocks(total, geo.blocks), c = min((int)blockIdx.x, parts);
     const long long pos = total * c / max(parts, 1), stop = total * min(c + 1, parts) / max(parts, 1);
+    if (threadIdx.x == 0) w->total = total;
     if (threadIdx.x == 0 && pos >= stop) w->pos = w->stop = 0;
     long long at = before;
     for (int s = s0; s < s1; ++s) {
@@ -272,8 +297,8 @@ __device__ __forceinline__ void ancestor_words(const int32_t *parents, int i, in
     }
 }
 
-// k_attend_join: adds the pieces of each row, one warp a (row, query head).  The launches that made them: of the prefixes'
-// segments (not read without groups) and of the own ones; the same where one launch covered both.
+// Adds the pieces of the rows that have several.  The launches that made them: of the prefixes' segments (not read without
+// groups) and of the own ones; the same where one launch covered both.
 cudaError_t launch_attend_join(const AttendArgs &a, const AttendGeo &prefix, const AttendGeo &own, int es, cudaStream_t stream);
 
 // The kernels: any head_dim in float32 arithmetic; bf16 with head_dim <= 128 on the tensor cores, a tall form for any number

@@ -124,7 +124,7 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
     constexpr int RP = 32 / CH;           // rows of a warp's pass
     const int ch = lane % CH, rsub = lane / CH;
     const bool real = ch * 8 < D;         // chunks past the head are zero
-    uint32_t seq = 0, q_use[2] = {0, 0};
+    uint32_t seq = 0, q_phases = 0;   // q_phases: a bit a query tile
     int qnext = 0;
     // destination of this lane's chunk of row r (r & 7 is the swizzle)
     auto place = [&](uint32_t tile, int r, int half) { return tile + (ch >> 3) * half + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
@@ -206,8 +206,8 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
         // queries: a quarter of the tile a warp
         for (int t = 0; t < (two ? 2 : 1); ++t) {
             const int qs = two ? t : qnext;
-            acquire(&fd->q_empty[qs], (q_use[qs] & 1) ^ 1);
-            ++q_use[qs];
+            acquire(&fd->q_empty[qs], ((q_phases >> qs) & 1) ^ 1);
+            q_phases ^= 1u << qs;
             const int m = t * QROWS + wl * (QROWS / 4) + lane;
             int64_t off = -1;
             if (lane < QROWS / 4 && m < vr) {
@@ -277,7 +277,9 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
     int ended = 0;
     for (int it = 0;; ++it) {
         Piece p;
+        const long long pos = w.pos;
         const bool more = w.next(a, p);
+        if (it == 0 && lane == 0) leave_tail(a, p, more, pos, w.total);
         wait_phase(fd, &fd->pd_empty[it % kRing], ((it / kRing) & 1) ^ 1, a.stats);
         PieceInfo *pi = &fd->pd[it % kRing];
         const bool own = more && p.seg >= a.n_groups, tree = own && a.bt.parents != nullptr;

@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
     if (warp == 12) tmem_alloc(&fd->tmem, 256);
     tc_fence_before();
     walk_start<kTcThreads>(a, &ms->walk, ms->warp_sum);   // has block-wide barriers
+    pdl_trigger();
     tc_fence_after();
     const uint32_t tmem = fd->tmem;
     const uint32_t sbase = smem_addr(smem);
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
     __syncthreads();
     tc_fence_after();
     if (warp == 12) tmem_free(tmem, 256);
+    pdl_wait();   // launched beside the prefixes' kernel: done only when that is, for the join waits for this one
 }
 
 template <int DP>
@@ -424,7 +426,10 @@ cudaError_t run_few(AttendArgs &a, bool negate, cudaStream_t stream) {
     constexpr size_t bytes = FewShape<DP>::OFF_MISC + sizeof(FewShared);
     static_assert(bytes <= 232448, "shared memory of a block");
     if (prepare_kernel((const void *)k_attend_few<DP>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
-    k_attend_few<DP><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, tc_args(a.c, mma_shape(NR, false, false, false, negate)));
+    const TcArgs t = tc_args(a.c, mma_shape(NR, false, false, false, negate));
+    // After the prefixes' kernel of the same call, blocks start as that one's end: they need nothing of it.
+    if (a.geo.s0 > 0) return launch_pdl(k_attend_few<DP>, dim3(a.geo.blocks), dim3(kTcThreads), bytes, stream, a, t);
+    k_attend_few<DP><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, t);
     return cudaGetLastError();
 }
 

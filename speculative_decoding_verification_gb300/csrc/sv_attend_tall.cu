@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
     if (warp == 12) tmem_alloc(&fd->tmem, 512);
     tc_fence_before();
     walk_start<kTcThreads>(a, &ms->walk, ms->warp_sum);   // has block-wide barriers
+    pdl_trigger();
     tc_fence_after();
     const uint32_t tmem = fd->tmem;
 
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
         const int wl = warp & 3, row = wl * 32 + lane;          // tensor-memory lane
         const uint32_t base = tmem + ((uint32_t)(wl * 32) << 16);
         const uint32_t colS = base + kColS + st * 128, colO = base + kColO + st * 128;
-        uint32_t s_phase = 0, o_phase[2] = {0, 0}, seq = 0;
+        uint32_t s_phase = 0, o_phases = 0, seq = 0;   // o_phases: a bit a stream
         const float c = a.scale_log2;
         for (int it = 0;; ++it) {
             PieceInfo *pi = &fd->pd[it % kRing];
@@ -280,16 +281,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 l_all = st == 0 ? l * mine + o.y * other : o.y * other + l * mine;
                 f0 = st == 0 ? mine : other;
                 f1 = st == 0 ? other : mine;
-                wait_phase(fd, &ms->o_full[0], o_phase[0], a.stats);
-                o_phase[0] ^= 1;
+                wait_phase(fd, &ms->o_full[0], o_phases & 1, a.stats);
+                o_phases ^= 1;
                 if (has1) {
-                    wait_phase(fd, &ms->o_full[1], o_phase[1], a.stats);
-                    o_phase[1] ^= 1;
+                    wait_phase(fd, &ms->o_full[1], (o_phases >> 1) & 1, a.stats);
+                    o_phases ^= 2;
                 }
             } else {
-                wait_phase(fd, &ms->o_full[st], o_phase[st], a.stats);
-                o_phase[st] ^= 1;
-                o_phase[st ^ 1] ^= 1;   // the other stream's warps see that one
+                wait_phase(fd, &ms->o_full[st], (o_phases >> st) & 1, a.stats);
+                o_phases ^= 3;   // the other stream's warps see that one
             }
             __syncwarp();
             tc_fence_after();
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
             // ------------------------------------------------------------ matrix products
             const uint32_t sbase = smem_addr(smem), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             constexpr uint32_t shape_o = mma_shape(DP, false, true, false, false);
-            uint32_t p_phase[2] = {0, 0}, seq = 0, q_use[2] = {0, 0};
+            uint32_t p_phases = 0, q_phases = 0, seq = 0;   // a bit a stream, a query tile
             int qnext = 0;
             for (int it = 0;; ++it) {
                 const PieceInfo *pi = &fd->pd[it % kRing];
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     const int s = n & 1, tile = two ? n >> 1 : n;
                     const uint32_t vs = seq + 2 * tile + 1, stage = vs % S::STAGES;
                     wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
-                    wait_phase(fd, &ms->p_full[s], p_phase[s], a.stats);
-                    p_phase[s] ^= 1;
+                    wait_phase(fd, &ms->p_full[s], (p_phases >> s) & 1, a.stats);
+                    p_phases ^= 1u << s;
                     __syncwarp();
                     tc_fence_after();
                     const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, S::HALF, 1024);
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     const int qs = two ? s : qnext;
                     const uint32_t ks = seq + 2 * tile, stage = ks % S::STAGES;
                     if (n == 0 || (two && n == 1)) {
-                        wait_phase(fd, &fd->q_full[qs], q_use[qs] & 1, a.stats);
-                        ++q_use[qs];
+                        wait_phase(fd, &fd->q_full[qs], (q_phases >> qs) & 1, a.stats);
+                        q_phases ^= 1u << qs;
                     }
                     wait_phase(fd, &fd->kv_full[stage], (ks / S::STAGES) & 1, a.stats);
                     __syncwarp();
