@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     const int rg = tid / S::TPR, tx = tid % S::TPR;
     const int cx = tx % S::CG, ks = S::KS > 1 ? tx / S::CG : 0;
     Piece p;
-    for (long long pos = w.pos, first = 1;; first = 0) {
+    for (int pos = w.pos, first = 1;; first = 0) {
         const bool more = w.next(a, p);
         if (first && tid == 0) leave_tail(a, p, more, pos, w.total);
         if (!more) break;
@@ -370,15 +370,14 @@ constexpr int kJoinRows = 8;
 
 struct JoinSeg {
     Seg g;
-    long long first, total;   // the key head's first tile; all tiles
-    int parts, kt;            // blocks; tiles of a unit (not chain)
+    Ranges r;
+    int first, kt;   // the key head's first tile; tiles of a unit (not chain)
 };
 
 __device__ __forceinline__ void join_seg(const AttendArgs &a, const AttendGeo &geo, int s, int h, JoinSeg *j) {
-    j->total = geo.seg_off[geo.s1 - geo.s0];
+    j->r = ranges_of(geo.seg_off[geo.s1 - geo.s0], geo.blocks);
     j->g = seg_of(a, geo, s, false);
     j->first = geo.seg_off[s - geo.s0] + seg_head_tiles(a, geo, j->g) * h;
-    j->parts = range_blocks(j->total, geo.blocks);
     j->kt = j->g.tiles_m > 0 ? seg_tiles(a, geo, j->g, 0) : 0;
 }
 
@@ -387,16 +386,16 @@ __device__ __forceinline__ void join_blocks(const AttendArgs &a, const AttendGeo
     c0 = 0;
     c1 = -1;
     int kt = j.kt;
-    long long first = j.first;
+    int first = j.first;
     if (!j.g.chain) {
-        first += (long long)t * kt;
+        first += t * kt;
     } else if (t > 0) {
         for (int u = 0; u < t; ++u) first += seg_tiles(a, geo, j.g, u);
         kt = seg_tiles(a, geo, j.g, t);
     }
-    if (kt <= 0 || j.total == 0) return;
-    c0 = block_of_tile(first, j.total, j.parts);
-    c1 = block_of_tile(first + kt - 1, j.total, j.parts);
+    if (kt <= 0 || j.r.parts == 0) return;
+    c0 = block_of_tile(j.r, first);
+    c1 = block_of_tile(j.r, first + kt - 1);
 }
 
 template <int ES>
@@ -478,7 +477,7 @@ static AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, in
     Carver cv;
     const size_t slots = attend_slots(rows, q_heads, n_groups > 0, true, kAttMaxTile, kAttBlocks) +
                          (n_groups > 0 ? (size_t)kFewRows * kAttBlocks : 0);
-    p.off_seg = cv.take<long long>((size_t)n_groups + B + 2);
+    p.off_seg = cv.take<int>((size_t)n_groups + B + 2);
     p.off_tails = cv.take<AttendTail>(kAttBlocks);
     p.off_ml = cv.take<float2>(slots);
     p.off_part = cv.take<float>(slots * head_dim);
@@ -539,7 +538,7 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     a.tails = reinterpret_cast<AttendTail *>(w + pl.off_tails);
     a.part_ml = reinterpret_cast<float2 *>(w + pl.off_ml);
     a.part = reinterpret_cast<float *>(w + pl.off_part);
-    long long *seg = reinterpret_cast<long long *>(w + pl.off_seg);
+    int *seg = reinterpret_cast<int *>(w + pl.off_seg);
     const int blocks = di.sms < kAttBlocks ? di.sms : kAttBlocks;
     const AttendGeo all{0, n_groups + batch->B, 0, 0, blocks, seg, 0};
     AttendGeo prefix = all, own = all;

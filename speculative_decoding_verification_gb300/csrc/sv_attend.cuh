@@ -31,7 +31,7 @@ struct AttendTail {
 // What one launch covers and how it cuts it: segments [s0, s1), row and key tiles, blocks.
 struct AttendGeo {
     int s0, s1, TM, TK, blocks;
-    long long *seg_off;   // [s1 - s0 + 1] first tile of each segment, in the unit order
+    int *seg_off;         // [s1 - s0 + 1] first tile of each segment, in the unit order
     size_t slot0;         // its first workspace slot
 };
 
@@ -135,9 +135,9 @@ __device__ __forceinline__ int seg_tiles(const AttendArgs &a, const AttendGeo &g
     return (seg_end(a, geo, g, t) - g.key0 + geo.TK - 1) / geo.TK;
 }
 
-__device__ __forceinline__ long long seg_head_tiles(const AttendArgs &a, const AttendGeo &geo, const Seg &g) {
-    if (!g.chain) return (long long)g.tiles_m * seg_tiles(a, geo, g, 0);
-    long long n = 0;
+__device__ __forceinline__ int seg_head_tiles(const AttendArgs &a, const AttendGeo &geo, const Seg &g) {
+    if (!g.chain) return g.tiles_m * seg_tiles(a, geo, g, 0);
+    int n = 0;
     for (int t = 0; t < g.tiles_m; ++t) n += seg_tiles(a, geo, g, t);
     return n;
 }
@@ -148,13 +148,25 @@ __device__ __forceinline__ size_t unit_slot(const AttendArgs &a, const AttendGeo
     return geo.slot0 + own + (size_t)g.r0 * a.q_heads + (size_t)h * g.packed + (size_t)t * geo.TM;
 }
 
-// Ranges are those of the first range_blocks blocks, so that none is empty: range c is
-// [total c / parts, total (c + 1) / parts).
-__device__ __forceinline__ int range_blocks(long long total, int blocks) { return (int)min(total, (long long)blocks); }
+// Ranges are those of the first range_blocks blocks, so that none is empty; the first total % parts of them have one tile more.
+struct Ranges {
+    int parts, each, more;
+};
+
+__device__ __forceinline__ Ranges ranges_of(int total, int blocks) {
+    Ranges r;
+    r.parts = min(total, blocks);
+    r.each = r.parts > 0 ? total / r.parts : 0;
+    r.more = total - r.each * r.parts;
+    return r;
+}
+
+__device__ __forceinline__ int range_start(const Ranges &r, int c) { return c * r.each + min(c, r.more); }
 
 // The block whose range holds tile x.
-__device__ __forceinline__ int block_of_tile(long long x, long long total, int parts) {
-    return (int)(((x + 1) * parts - 1) / total);
+__device__ __forceinline__ int block_of_tile(const Ranges &r, int x) {
+    const int split = r.more * (r.each + 1);
+    return x < split ? x / (r.each + 1) : r.more + (x - split) / r.each;
 }
 
 // A row's output is complete in its own piece when no prefix adds to it.
@@ -170,8 +182,7 @@ struct Piece {
 
 // Walks the pieces of one block's range [pos, stop) of tiles.
 struct Walk {
-    long long pos, stop, seg_start, per_head, total;
-    int s;
+    int pos, stop, seg_start, per_head, total, s;
     Seg g;
 
     __device__ __forceinline__ void open(const AttendArgs &a) {
@@ -186,10 +197,9 @@ struct Walk {
             ++s;
             open(a);
         }
-        const long long at = pos - seg_start;
-        int rem;
-        p.h = (int)(at / per_head);
-        rem = (int)(at - p.h * per_head);
+        const int at = pos - seg_start;
+        p.h = at / per_head;
+        int rem = at - p.h * per_head;
         p.t = 0;
         p.kt = seg_tiles(a, a.geo, g, 0);
         if (!g.chain) {
@@ -205,7 +215,7 @@ struct Walk {
         p.seg = s;
         p.vr = min(a.geo.TM, g.packed - p.t * a.geo.TM);
         p.k0 = rem;
-        p.k1 = (int)min((long long)p.kt, rem + (stop - pos));
+        p.k1 = min(p.kt, rem + (stop - pos));
         p.end = seg_end(a, a.geo, g, p.t);
         pos += p.k1 - p.k0;
         return true;
@@ -213,10 +223,10 @@ struct Walk {
 };
 
 // Block c's tail, from its first piece p (`more` false: the range is empty), whose first tile was at `pos` of `total`.
-__device__ __forceinline__ void leave_tail(const AttendArgs &a, const Piece &p, bool more, long long pos, long long total) {
+__device__ __forceinline__ void leave_tail(const AttendArgs &a, const Piece &p, bool more, int pos, int total) {
     AttendTail t{};
     if (more && p.k0 > 0 && p.k1 == p.kt) {
-        const int c0 = block_of_tile(pos - p.k0, total, range_blocks(total, a.geo.blocks));
+        const int c0 = block_of_tile(ranges_of(total, a.geo.blocks), pos - p.k0);
         t.pieces = (int)blockIdx.x - c0 + 1;
         t.slot = (long long)(unit_slot(a, a.geo, p.g, p.seg < a.n_groups, p.h, p.t) + (size_t)c0 * a.geo.TM);
         t.r0 = p.g.r0;
@@ -228,7 +238,8 @@ __device__ __forceinline__ void leave_tail(const AttendArgs &a, const Piece &p, 
 }
 
 // Block-wide: the total of tiles and, for this block's range, where its walk starts.  Each thread takes a
-// run of consecutive segments; warp_sum has THREADS / 32 places.  Block 0 leaves the segments' offsets for the join and reports bad input.
+// run of consecutive segments; warp_sum has THREADS / 32 places.  Block 0 leaves the segments' offsets for the join and reports bad
+// input, a total past 2^30 tiles among it (nothing is computed then).
 template <int THREADS>
 __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long long *warp_sum) {
     const AttendGeo &geo = a.geo;
@@ -236,7 +247,13 @@ __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long lo
     const int each = (NS + THREADS - 1) / THREADS;
     const int s0 = min((int)threadIdx.x * each, NS), s1 = min(s0 + each, NS);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += seg_head_tiles(a, geo, seg_of(a, geo, geo.s0 + s, blockIdx.x == 0)) * a.c.kv_heads;
+    Seg g{};
+    int per = 0;
+    for (int s = s0; s < s1; ++s) {
+        g = seg_of(a, geo, geo.s0 + s, blockIdx.x == 0);
+        per = seg_head_tiles(a, geo, g);
+        mine += (long long)per * a.c.kv_heads;
+    }
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     long long inc = mine;
 #pragma unroll
@@ -246,33 +263,45 @@ __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long lo
     }
     if (lane == 31) warp_sum[wp] = inc;
     __syncthreads();
-    long long before = inc - mine, total = 0;
+    long long before = inc - mine, sum = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
         if (i < wp) before += warp_sum[i];
-        total += warp_sum[i];
+        sum += warp_sum[i];
     }
-    const int parts = range_blocks(total, geo.blocks), c = min((int)blockIdx.x, parts);
-    const long long pos = total * c / max(parts, 1), stop = total * min(c + 1, parts) / max(parts, 1);
-    if (threadIdx.x == 0) w->total = total;
-    if (threadIdx.x == 0 && pos >= stop) w->pos = w->stop = 0;
-    long long at = before;
-    for (int s = s0; s < s1; ++s) {
-        const Seg g = seg_of(a, geo, geo.s0 + s, false);
-        const long long per = seg_head_tiles(a, geo, g), n = per * a.c.kv_heads;
-        if (pos < stop && pos >= at && pos < at + n) {
-            w->pos = pos;
-            w->stop = stop;
-            w->s = geo.s0 + s;
-            w->seg_start = at;
-            w->g = g;
-            w->per_head = per;
+    if (sum > 1 << 30) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.stats, SV_ERR_INVALID_ARG, -1);
+        sum = 0;
+    }
+    const int total = (int)sum;
+    const Ranges r = ranges_of(total, geo.blocks);
+    const int c = blockIdx.x, pos = c < r.parts ? range_start(r, c) : total, stop = c < r.parts ? range_start(r, c + 1) : total;
+    if (threadIdx.x == 0) {
+        w->total = total;
+        if (pos >= stop) w->pos = w->stop = 0;
+    }
+    if (blockIdx.x == 0 || (pos < stop && pos >= before && pos < before + mine)) {
+        int at = total > 0 ? (int)before : 0;
+        for (int s = s0; s < s1; ++s) {
+            if (each > 1) {   // with one segment a thread, g and per are still those
+                g = seg_of(a, geo, geo.s0 + s, false);
+                per = seg_head_tiles(a, geo, g);
+            }
+            const int n = total > 0 ? per * a.c.kv_heads : 0;
+            if (pos < stop && pos >= at && pos < at + n) {
+                w->pos = pos;
+                w->stop = stop;
+                w->s = geo.s0 + s;
+                w->seg_start = at;
+                w->g = g;
+                w->per_head = per;
+            }
+            if (blockIdx.x == 0) {
+                geo.seg_off[s] = at;
+                if (s == NS - 1) geo.seg_off[NS] = at + n;
+            }
+            at += n;
         }
-        if (blockIdx.x == 0) {
-            geo.seg_off[s] = at;
-            if (s == NS - 1) geo.seg_off[NS] = at + n;
-        }
-        at += n;
     }
     __syncthreads();
 }

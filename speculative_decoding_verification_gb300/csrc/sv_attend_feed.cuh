@@ -53,11 +53,11 @@ __device__ __forceinline__ void wait_phase(Feed *fd, uint64_t *bar, uint32_t par
 // `readers`: warps that read a piece description.
 __device__ __forceinline__ void feed_init(Feed *fd, int readers) {
     for (int i = 0; i < 8; ++i) {
-        mbar_init(&fd->kv_full[i], 4);
+        mbar_init(&fd->kv_full[i], 128);
         mbar_init(&fd->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-        mbar_init(&fd->q_full[i], 4);
+        mbar_init(&fd->q_full[i], 128);
         mbar_init(&fd->q_empty[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -72,18 +72,16 @@ __device__ __forceinline__ bool not_finite16(uint4 w) {
     return bad(w.x) || bad(w.y) || bad(w.z) || bad(w.w);
 }
 
-// Waits until at most `left` of the thread's copy groups are in flight.
-__device__ __forceinline__ void copies_wait(int left) {
-    switch (left) {
-        case 0: cp_async_wait<0>(); break;
-        case 1: cp_async_wait<1>(); break;
-        case 2: cp_async_wait<2>(); break;
-        case 3: cp_async_wait<3>(); break;
-        case 4: cp_async_wait<4>(); break;
-        case 5: cp_async_wait<5>(); break;
-        case 6: cp_async_wait<6>(); break;
-        default: cp_async_wait<7>(); break;
-    }
+// The barrier gets this thread's arrival once its copies so far have landed.  The copies are ordinary writes to shared memory: who
+// waits for the barrier fences them (fence_async_smem) before the tensor cores read them.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// `bytes` more to come and n arrivals.
+__device__ __forceinline__ void mbar_arrive_expect_tx_n(uint64_t *bar, uint32_t bytes, uint32_t n) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&x)[4]) {
@@ -104,6 +102,28 @@ __device__ __forceinline__ uint32_t bf16_pair(f32x2 x) {
     return w;
 }
 
+// Values of a tile with hidden tokens, by 128 threads: thread t looks at token t.  A token whose values are not all finite becomes
+// zeros, so that 0 * inf of a row that does not see it cannot reach the output, and its bit is set in flags[t / 32].
+template <int DP>
+__device__ __forceinline__ void scan_values(uint32_t tile, int t, uint32_t *flags) {
+    uint4 w[DP / 8];
+    bool bad = false;
+#pragma unroll
+    for (int ch = 0; ch < DP / 8; ++ch) {
+        const uint32_t at = tile + (ch >> 3) * (128 * 128) + t * 128 + (((ch & 7) ^ (t & 7)) << 4);
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[ch].x), "=r"(w[ch].y), "=r"(w[ch].z), "=r"(w[ch].w) : "r"(at));
+    }
+#pragma unroll
+    for (int ch = 0; ch < DP / 8; ++ch) bad |= not_finite16(w[ch]);
+    if (bad) {
+        const uint32_t zero[4] = {0, 0, 0, 0};
+        for (int ch = 0; ch < DP / 8; ++ch) sts128(tile + (ch >> 3) * (128 * 128) + t * 128 + (((ch & 7) ^ (t & 7)) << 4), zero);
+    }
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, bad);
+    if ((t & 31) == 0) flags[t >> 5] = all;
+    fence_async_smem();
+}
+
 // Keys and values as 4-D tensors (element, head, slot, page) with boxes of 64 elements by box_rows slots, loaded with the
 // 128-byte swizzle; box_rows is 0 where a box could not stay inside a page.
 struct TcArgs {
@@ -117,8 +137,6 @@ template <int DP, int STAGES, int QROWS>
 __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &a2, Feed *fd, uint32_t q_base, uint32_t kv_base, int wl,
                                              int lane) {
     constexpr int TILE = 128 * DP * 2, HALF = 128 * 128;
-    uint64_t *bars = fd->kv_full;
-    const int bar_q = (int)(fd->q_full - fd->kv_full);
     const int D = a.c.head_dim;
     constexpr int CH = DP / 8;            // 16-byte chunks of a row
     constexpr int RP = 32 / CH;           // rows of a warp's pass
@@ -128,62 +146,10 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
     int qnext = 0;
     // destination of this lane's chunk of row r (r & 7 is the swizzle)
     auto place = [&](uint32_t tile, int r, int half) { return tile + (ch >> 3) * half + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
-    // Copy groups in flight, oldest first, 8 bits each: the barrier a group completes (one arrival a warp), and kScan for
-    // values of a tile with hidden tokens.
-    constexpr uint64_t kScan = 0x80;
-    uint64_t queue = 0;
-    int queued = 0;
-    auto retire = [&]() {
-        copies_wait(queued - 1);
-        const int bar = (int)(queue & 0x7F);
-        if (queue & kScan) {
-            // A token whose values are not all finite becomes zeros and is flagged; each lane looks at what it copied.
-            uint32_t flags = 0;
-            const uint32_t tile = kv_base + bar * TILE;
-#pragma unroll 4
-            for (int p = 0; p < 32 / RP; ++p) {
-                const uint32_t at = place(tile, wl * 32 + p * RP + rsub, HALF);
-                uint4 w;
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
-                const uint32_t bad = __ballot_sync(0xFFFFFFFFu, not_finite16(w));
-                if (bad) {
-#pragma unroll
-                    for (int g = 0; g < RP; ++g)
-                        if ((bad >> (g * CH)) & ((1u << CH) - 1u)) {
-                            flags |= 1u << (p * RP + g);
-                            if (rsub == g) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                        }
-                }
-            }
-            if (lane == 0) fd->vflag[bar][wl] = flags;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + bar);
-        queue >>= 8;
-        --queued;
-    };
-    auto enqueue = [&](uint64_t what) {
-        if (queued == 8) retire();
-        cp_async_commit();
-        queue |= what << (8 * queued);
-        ++queued;
-    };
-    // Waits for a barrier and passes on the copies that land meanwhile: whoever completes the barrier may be waiting for them.
-    auto acquire = [&](uint64_t *bar, uint32_t parity) {
-        // A test, not a try: a try may suspend the warp for microseconds, and copies that land meanwhile have to be
-        // passed on.  The whole warp takes one way: lanes may see the phase end at different tests.
-        while (!__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) {
-            if (queued == 0) {
-                wait_phase(fd, bar, parity, a.stats);
-                return;
-            }
-            retire();
-        }
-    };
     for (int it = 0;; ++it) {
         const PieceInfo *pi = &fd->pd[it % kRing];
-        acquire(&fd->pd_full[it % kRing], (it / kRing) & 1);
+        wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
+        __syncwarp();
         const int k0 = pi->k0, k1 = pi->k1;
         if (k0 >= k1) break;
         const int vr = pi->vr, key0 = pi->key0, end = pi->end, ctx = pi->ctx, own = pi->own, h = pi->h, m0 = pi->m0, r0 = pi->r0, pi_boxes = pi->boxes;
@@ -204,26 +170,28 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
         };
         int page = page_of(k0);
         // queries: a quarter of the tile a warp
-        for (int t = 0; t < (two ? 2 : 1); ++t) {
-            const int qs = two ? t : qnext;
-            acquire(&fd->q_empty[qs], ((q_phases >> qs) & 1) ^ 1);
-            q_phases ^= 1u << qs;
-            const int m = t * QROWS + wl * (QROWS / 4) + lane;
-            int64_t off = -1;
-            if (lane < QROWS / 4 && m < vr) {
-                const int r = (m0 + m) / a.G;
-                off = (int64_t)(r0 + r) * a.q_row + (int64_t)(h * a.G + (m0 + m - r * a.G)) * a.q_head;
-            }
-            const uint32_t tile = q_base + qs * (QROWS * DP * 2);
+        auto queries = [&]() {
+            for (int t = 0; t < (two ? 2 : 1); ++t) {
+                const int qs = two ? t : qnext;
+                wait_phase(fd, &fd->q_empty[qs], ((q_phases >> qs) & 1) ^ 1, a.stats);
+                q_phases ^= 1u << qs;
+                const int m = t * QROWS + wl * (QROWS / 4) + lane;
+                int64_t off = -1;
+                if (lane < QROWS / 4 && m < vr) {
+                    const int r = (m0 + m) / a.G;
+                    off = (int64_t)(r0 + r) * a.q_row + (int64_t)(h * a.G + (m0 + m - r * a.G)) * a.q_head;
+                }
+                const uint32_t tile = q_base + qs * (QROWS * DP * 2);
 #pragma unroll
-            for (int p = 0; p < QROWS / 4 / RP; ++p) {
-                const int64_t o = __shfl_sync(0xFFFFFFFFu, off, p * RP + rsub);
-                const bool ok = o >= 0 && real;
-                cp_async16(place(tile, wl * (QROWS / 4) + p * RP + rsub, QROWS * 128), a.q + (ok ? o + ch * 16 : 0), ok);
+                for (int p = 0; p < QROWS / 4 / RP; ++p) {
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, p * RP + rsub);
+                    const bool ok = o >= 0 && real;
+                    cp_async16(place(tile, wl * (QROWS / 4) + p * RP + rsub, QROWS * 128), a.q + (ok ? o + ch * 16 : 0), ok);
+                }
+                cp_async_arrive(&fd->q_full[qs]);
             }
-            enqueue(bar_q + qs);
-        }
-        if (!two) qnext ^= 1;
+            if (!two) qnext ^= 1;
+        };
         for (int k = k0; k < k1; ++k) {
             const int key = key_of(k), pg = page, slot = key - key / a.c.page_size * a.c.page_size;
             const bool box = by_box(k);
@@ -231,16 +199,17 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
             if (pg >= 0 && pg < a.c.n_pages) off = pg * a.c.page_b + slot * a.c.slot_b + h * a.c.head_b;
             else if (pg != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
             if (k + 1 < k1) page = page_of(k + 1);
-            const bool masked = own && key0 + (k + 1) * kTcKeys > ctx;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
+                if (kv == 1 && k == k0) queries();   // keys first: they are what memory has to bring
                 const uint32_t stage = seq % STAGES;
-                acquire(&fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1);
+                wait_phase(fd, &fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1, a.stats);
+                __syncwarp();
                 ++seq;
                 const uint32_t tile = kv_base + stage * TILE;
                 const char *src = kv ? a.c.v : a.c.k;
                 if (box) {   // a bad page id lies outside the tensor and reads zeros
-                    if (elect_one()) mbar_arrive_expect_tx(&fd->kv_full[stage], 32 * DP * 2);
+                    if (elect_one()) mbar_arrive_expect_tx_n(&fd->kv_full[stage], 32 * DP * 2, 32);
                     __syncwarp();
                     for (int b = 0; b < boxes; ++b) {
                         const int bp = __shfl_sync(0xFFFFFFFFu, pg, b), bs = __shfl_sync(0xFFFFFFFFu, slot, b);
@@ -260,15 +229,12 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
                     const bool ok = o >= 0 && real;
                     cp_async16(place(tile, wl * 32 + p * RP + rsub, HALF), src + (ok ? o + ch * 16 : 0), ok);
                 }
-                enqueue(kv == 1 && masked ? kScan | stage : stage);
+                cp_async_arrive(&fd->kv_full[stage]);
             }
-            // A long piece's last copies are passed on before the next piece is set up, which takes as long as they do; after short
-            // pieces the next loads matter more.
-            if (k + 1 == k1 && k1 - k0 >= 4)
-                while (queued) retire();
         }
     }
-    while (queued) retire();
+    cp_async_commit();
+    cp_async_wait<0>();   // nothing is in flight when the block ends
 }
 
 // The walk's part, one warp: describes the pieces, then `ends` times that there are no more.
@@ -277,7 +243,7 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
     int ended = 0;
     for (int it = 0;; ++it) {
         Piece p;
-        const long long pos = w.pos;
+        const int pos = w.pos;
         const bool more = w.next(a, p);
         if (it == 0 && lane == 0) leave_tail(a, p, more, pos, w.total);
         wait_phase(fd, &fd->pd_empty[it % kRing], ((it / kRing) & 1) ^ 1, a.stats);

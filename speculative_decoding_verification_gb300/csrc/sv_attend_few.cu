@@ -230,16 +230,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                     sts128(prow + (((q + 4) ^ (t & 7)) << 4), lo);
                 }
                 if (masked) {
-                    // Values that are not finite were replaced by zeros on the way in; they are added here for the rows that see them,
-                    // with the weights that the product would have used.
+                    // Values that are not finite are replaced by zeros; they are added here for the rows that see them, with the
+                    // weights that the product would have used.
                     const uint32_t vs = pi->seq + 2 * (k - k0) + 1, stage = vs % S::STAGES;
                     wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
                     __syncwarp();
+                    scan_values<DP>(sbase + S::OFF_KV + stage * S::TILE, t, fd->vflag[stage]);
+                    group_sync();   // the flags and every token's weights are written
                     uint32_t any = 0;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) any |= *reinterpret_cast<volatile uint32_t *>(&fd->vflag[stage][q]);
                     if (any) {
-                        group_sync();   // every token's weights are written
 #pragma unroll 1
                         for (int j = 0; j < 128; ++j) {
                             if (!((*reinterpret_cast<volatile uint32_t *>(&fd->vflag[stage][j >> 5]) >> (j & 31)) & 1u)) continue;
@@ -347,6 +348,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 wait_phase(fd, &fd->kv_full[stage], (late_seq / S::STAGES) & 1, a.stats);
                 wait_phase(fd, &ms->p_full[late_gr], late_u & 1, a.stats);
                 __syncwarp();
+                fence_async_smem();
                 tc_fence_after();
                 const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, DP == 128 ? S::HALF : 0, 1024);
                 const uint64_t p = smem_operand(sbase + S::OFF_P + late_gr * S::PBUF, 0, 1024);
@@ -375,13 +377,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 if (nk <= 0) break;
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
                 const int gr = it & 1;
-                ready(&fd->q_full[gr], (gr ? q_use1 : q_use0) & 1);
-                if (gr) ++q_use1;
-                else ++q_use0;
                 const uint64_t q = smem_operand(sbase + gr * (NR * DP * 2), 16, 1024);
                 for (int n = 0; n < nk; ++n) {
                     const uint32_t stage = seq % S::STAGES, u = gr ? tiles1 : tiles0;
                     ready(&fd->kv_full[stage], (seq / S::STAGES) & 1);
+                    if (n == 0) {
+                        ready(&fd->q_full[gr], (gr ? q_use1 : q_use0) & 1);
+                        if (gr) ++q_use1;
+                        else ++q_use0;
+                    }
+                    fence_async_smem();
                     tc_fence_after();
                     const uint64_t kt = smem_operand(sbase + S::OFF_KV + stage * S::TILE, 16, 1024);
                     const uint32_t s = tm + (gr * 2 + (u & 1)) * 32;

@@ -127,10 +127,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 wait_phase(fd, &ms->s_full[st], s_phase, a.stats);
                 s_phase ^= 1;
                 __syncwarp();
+                const int first = key0 + k * kTcKeys;
+                const bool masked = own ? first + kTcKeys > ctx : first + kTcKeys > end;
+                // Tokens that some row does not see: the stream's threads (the first stream's, where both share the tile, whose
+                // products come first) clear values that are not finite.
+                const uint32_t vs = seq + 2 * (k - k0) + 1, vstage = vs % S::STAGES;
+                if (own && masked) {
+                    if (!two || st == 0) {
+                        wait_phase(fd, &fd->kv_full[vstage], (vs / S::STAGES) & 1, a.stats);
+                        __syncwarp();
+                        scan_values<DP>(smem_addr(smem) + S::OFF_KV + vstage * S::TILE, row, fd->vflag[vstage]);
+                    }
+                    if (two) asm volatile("bar.sync 1, 256;" ::: "memory");
+                    else asm volatile("bar.sync %0, 128;" ::"r"(2 + st) : "memory");
+                }
                 if (active) {
                     tc_fence_after();
-                    const int first = key0 + k * kTcKeys;
-                    const bool masked = own ? first + kTcKeys > ctx : first + kTcKeys > end;
                     uint32_t vis[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
                     if (masked) {
 #pragma unroll
@@ -223,14 +235,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     l = f2_sum(f2_add(sum[0], sum[1]));
                     tc_wait_st();
                     if (own && masked) {
-                        // Values that are not finite were replaced by zeros on the way in; they are added here for the rows
-                        // that see them, with the weight that the product would have used.
-                        const uint32_t vs = seq + 2 * (k - k0) + 1, stage = vs % S::STAGES;
-                        wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
-                        __syncwarp();
+                        // The cleared values are added here for the rows that see them, with the weight that the product would
+                        // have used.
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q) {
-                            uint32_t f = *reinterpret_cast<volatile uint32_t *>(&fd->vflag[stage][q]);
+                            uint32_t f = *reinterpret_cast<volatile uint32_t *>(&fd->vflag[vstage][q]);
                             uint32_t mine = vis[0];
                             if (q == 1) mine = vis[1];
                             if (q == 2) mine = vis[2];
@@ -379,6 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     wait_phase(fd, &ms->p_full[s], (p_phases >> s) & 1, a.stats);
                     p_phases ^= 1u << s;
                     __syncwarp();
+                    fence_async_smem();
                     tc_fence_after();
                     const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, S::HALF, 1024);
                     const uint32_t o = tm + kColO + s * 128, w = tm + kColS + s * 128;
@@ -401,6 +411,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     }
                     wait_phase(fd, &fd->kv_full[stage], (ks / S::STAGES) & 1, a.stats);
                     __syncwarp();
+                    fence_async_smem();
                     tc_fence_after();
                     const uint64_t q = smem_operand(sbase + qs * S::TILE, 16, 1024);
                     const uint64_t kt = smem_operand(sbase + S::OFF_KV + stage * S::TILE, 16, 1024);
