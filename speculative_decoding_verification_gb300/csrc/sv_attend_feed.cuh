@@ -1,8 +1,8 @@
 // sv_attend_feed.cuh — what the tensor-core kernels of sv_kv_attend share: the walk that describes a block's pieces, the
 // producer warps that gather keys, values and queries from their pages into swizzled shared memory, bounded waits.
 //
-// Ring.  Stages of 128 tokens (keys, then values of a tile, in turn) are filled by four producer warps, 32 tokens each, and
-// freed by the commit of the product that read them.
+// Ring.  Stages of 128 tokens (keys, then values of a tile, in turn) are filled by two producer warps each and freed by the commit of
+// the product that read them.
 #pragma once
 
 #include "sv_attend.cuh"
@@ -53,7 +53,7 @@ __device__ __forceinline__ void wait_phase(Feed *fd, uint64_t *bar, uint32_t par
 // `readers`: warps that read a piece description.
 __device__ __forceinline__ void feed_init(Feed *fd, int readers) {
     for (int i = 0; i < 8; ++i) {
-        mbar_init(&fd->kv_full[i], 128);
+        mbar_init(&fd->kv_full[i], 64);
         mbar_init(&fd->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -129,107 +129,115 @@ __device__ __forceinline__ void scan_values(uint32_t tile, int t, uint32_t *flag
 struct TcArgs {
     CUtensorMap k, v;
     int box_rows;
+    int page_shift;       // log2(page_size), or -1
     uint32_t shape_s;     // of the score product
 };
 
-// The producers' part, a warp of four.  QROWS rows a query tile; query tiles at q_base, stages at kv_base.
+// The producers' part, a warp of four.  QROWS rows a query tile; query tiles at q_base, stages at kv_base.  Two warps load the keys and
+// two the values; of a pair, each takes 64 elements of all 128 tokens (heads of 128), or 64 tokens.  A warp so waits for one
+// stage a tile and issues its boxes in one go: with the four sharing every stage, 32 tokens each, the producers set the pace.
 template <int DP, int STAGES, int QROWS>
 __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &a2, Feed *fd, uint32_t q_base, uint32_t kv_base, int wl,
                                              int lane) {
     constexpr int TILE = 128 * DP * 2, HALF = 128 * 128;
-    const int D = a.c.head_dim;
-    constexpr int CH = DP / 8;            // 16-byte chunks of a row
-    constexpr int RP = 32 / CH;           // rows of a warp's pass
-    const int ch = lane % CH, rsub = lane / CH;
-    const bool real = ch * 8 < D;         // chunks past the head are zero
-    uint32_t seq = 0, q_phases = 0;   // q_phases: a bit a query tile
+    constexpr int ROWS = DP == 128 ? 128 : 64;   // tokens of a warp
+    const int D = a.c.head_dim, kv = wl >> 1, sub = wl & 1;
+    const int row0 = DP == 128 ? 0 : sub * 64, col0 = DP == 128 ? sub * 64 : 0;   // its tokens and elements of a tile
+    const uint32_t part = DP == 128 ? sub * HALF : sub * 64 * 128;               // where they are
+    const CUtensorMap *map = kv ? &a2.v : &a2.k;
+    const char *src = kv ? a.c.v : a.c.k;
+    const int ch = lane & 7, rsub = lane >> 3;   // rows go four at a time, 8 chunks of 16 bytes each
+    const bool real = col0 + ch * 8 < D;         // chunks past the head are zero
+    const int psize = a.c.page_size, pshift = a2.page_shift;
+    auto page_index = [&](int key) { return pshift >= 0 ? key >> pshift : key / psize; };
+    uint32_t seq = kv, q_phases = 0;   // q_phases: a bit a query tile
     int qnext = 0;
-    // destination of this lane's chunk of row r (r & 7 is the swizzle)
-    auto place = [&](uint32_t tile, int r, int half) { return tile + (ch >> 3) * half + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
     for (int it = 0;; ++it) {
         const PieceInfo *pi = &fd->pd[it % kRing];
         wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
         __syncwarp();
         const int k0 = pi->k0, k1 = pi->k1;
         if (k0 >= k1) break;
-        const int vr = pi->vr, key0 = pi->key0, end = pi->end, ctx = pi->ctx, own = pi->own, h = pi->h, m0 = pi->m0, r0 = pi->r0, pi_boxes = pi->boxes;
-        const int32_t *table = a.bt.page_table + pi->table * a.bt.table_pitch;
-        const int tab = pi->table;
+        const int vr = pi->vr, key0 = pi->key0, end = pi->end, h = pi->h, m0 = pi->m0, r0 = pi->r0, tab = pi->table;
+        // A tile that every row sees whole goes as boxes where it can, the others by rows.
+        const int whole_end = pi->own ? pi->ctx : end;
+        const int boxes = pi->boxes ? ROWS / a2.box_rows : 0;
+        const int32_t *table = a.bt.page_table + tab * a.bt.table_pitch;
         __syncwarp();
         if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
         const bool two = vr > QROWS;   // two row tiles share the keys
-        // A tile that every row sees whole goes as boxes where it can, the others by rows: a lane's token of a tile, and its
-        // page, are those of the lane's box or row.
-        const int boxes = pi_boxes ? 32 / a2.box_rows : 0;
-        auto by_box = [&](int k) { return boxes > 0 && key0 + (k + 1) * kTcKeys <= (own ? ctx : end); };
-        auto key_of = [&](int k) { return key0 + k * kTcKeys + wl * 32 + (by_box(k) ? lane * a2.box_rows : lane); };
-        auto page_of = [&](int k) {
-            if (by_box(k) && lane >= boxes) return kNoPage;
-            const int key = key_of(k);
-            return key < end ? table[key / a.c.page_size] : kNoPage;
-        };
-        int page = page_of(k0);
-        // queries: a quarter of the tile a warp
-        auto queries = [&]() {
-            for (int t = 0; t < (two ? 2 : 1); ++t) {
-                const int qs = two ? t : qnext;
-                wait_phase(fd, &fd->q_empty[qs], ((q_phases >> qs) & 1) ^ 1, a.stats);
-                q_phases ^= 1u << qs;
-                const int m = t * QROWS + wl * (QROWS / 4) + lane;
-                int64_t off = -1;
-                if (lane < QROWS / 4 && m < vr) {
-                    const int r = (m0 + m) / a.G;
-                    off = (int64_t)(r0 + r) * a.q_row + (int64_t)(h * a.G + (m0 + m - r * a.G)) * a.q_head;
-                }
-                const uint32_t tile = q_base + qs * (QROWS * DP * 2);
-#pragma unroll
-                for (int p = 0; p < QROWS / 4 / RP; ++p) {
-                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, p * RP + rsub);
-                    const bool ok = o >= 0 && real;
-                    cp_async16(place(tile, wl * (QROWS / 4) + p * RP + rsub, QROWS * 128), a.q + (ok ? o + ch * 16 : 0), ok);
-                }
-                cp_async_arrive(&fd->q_full[qs]);
-            }
-            if (!two) qnext ^= 1;
-        };
+        auto by_box = [&](int k) { return boxes > 0 && key0 + (k + 1) * kTcKeys <= whole_end; };
+        // this lane's box of a tile, as (page, slot); fetched a tile ahead
+        auto box_key = [&](int k) { return key0 + k * kTcKeys + row0 + lane * a2.box_rows; };
+        auto box_page = [&](int k) { return k < k1 && by_box(k) && lane < boxes ? table[page_index(box_key(k))] : kNoPage; };
+        int page = box_page(k0);
         for (int k = k0; k < k1; ++k) {
-            const int key = key_of(k), pg = page, slot = key - key / a.c.page_size * a.c.page_size;
-            const bool box = by_box(k);
-            int64_t off = -1;
-            if (pg >= 0 && pg < a.c.n_pages) off = pg * a.c.page_b + slot * a.c.slot_b + h * a.c.head_b;
-            else if (pg != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
-            if (k + 1 < k1) page = page_of(k + 1);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                if (kv == 1 && k == k0) queries();   // keys first: they are what memory has to bring
-                const uint32_t stage = seq % STAGES;
-                wait_phase(fd, &fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1, a.stats);
+            const int pg = page;
+            page = box_page(k + 1);
+            const uint32_t stage = seq % STAGES;
+            const uint32_t tile = kv_base + stage * TILE + part;
+            wait_phase(fd, &fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1, a.stats);
+            __syncwarp();
+            seq += 2;
+            if (by_box(k)) {
+                const int key = box_key(k), slot = key - page_index(key) * psize;
+                if ((unsigned)pg >= (unsigned)a.c.n_pages && pg != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                if (elect_one()) mbar_arrive_expect_tx_n(&fd->kv_full[stage], ROWS * 128, 32);
                 __syncwarp();
-                ++seq;
-                const uint32_t tile = kv_base + stage * TILE;
-                const char *src = kv ? a.c.v : a.c.k;
-                if (box) {   // a bad page id lies outside the tensor and reads zeros
-                    if (elect_one()) mbar_arrive_expect_tx_n(&fd->kv_full[stage], 32 * DP * 2, 32);
-                    __syncwarp();
-                    for (int b = 0; b < boxes; ++b) {
-                        const int bp = __shfl_sync(0xFFFFFFFFu, pg, b), bs = __shfl_sync(0xFFFFFFFFu, slot, b);
-                        const uint32_t dst = tile + (wl * 32 + b * a2.box_rows) * 128;
-                        if (elect_one()) {
-                            const CUtensorMap *map = kv ? &a2.v : &a2.k;
-                            box_load(dst, map, &fd->kv_full[stage], 0, h, bs, bp);
-                            if (DP == 128) box_load(dst + HALF, map, &fd->kv_full[stage], 64, h, bs, bp);
-                        }
-                        __syncwarp();
+                // a bad page id lies outside the tensor and reads zeros
+                if (lane < boxes) box_load(tile + lane * a2.box_rows * 128, map, &fd->kv_full[stage], col0, h, slot, pg);
+                __syncwarp();
+            } else {
+                int64_t off[ROWS / 32];
+#pragma unroll
+                for (int i = 0; i < ROWS / 32; ++i) {
+                    const int key = key0 + k * kTcKeys + row0 + i * 32 + lane;
+                    off[i] = -1;
+                    if (key < end) {
+                        const int pn = page_index(key), id = table[pn];
+                        if (id >= 0 && id < a.c.n_pages) off[i] = id * a.c.page_b + (key - pn * psize) * a.c.slot_b + h * a.c.head_b;
+                        else report_error(a.stats, SV_ERR_INVALID_ARG, tab);
                     }
-                    continue;
                 }
 #pragma unroll
-                for (int p = 0; p < 32 / RP; ++p) {
-                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, p * RP + rsub);
-                    const bool ok = o >= 0 && real;
-                    cp_async16(place(tile, wl * 32 + p * RP + rsub, HALF), src + (ok ? o + ch * 16 : 0), ok);
+                for (int i = 0; i < ROWS / 32; ++i) {
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off[i], p * 4 + rsub);
+                        const bool ok = o >= 0 && real;
+                        const int r = row0 + i * 32 + p * 4 + rsub;   // r & 7 is the swizzle
+                        cp_async16(tile + (i * 32 + p * 4 + rsub) * 128 + ((ch ^ (r & 7)) << 4), src + (ok ? o + (col0 + ch * 8) * 2 : 0), ok);
+                    }
                 }
                 cp_async_arrive(&fd->kv_full[stage]);
+            }
+            if (k == k0) {   // queries, a quarter of the tile a warp; after the first keys, which memory has to bring
+                for (int t = 0; t < (two ? 2 : 1); ++t) {
+                    const int qs = two ? t : qnext;
+                    wait_phase(fd, &fd->q_empty[qs], ((q_phases >> qs) & 1) ^ 1, a.stats);
+                    __syncwarp();
+                    q_phases ^= 1u << qs;
+                    const int m = t * QROWS + wl * (QROWS / 4) + lane;
+                    int64_t off = -1;
+                    if (lane < QROWS / 4 && m < vr) {
+                        const int r = (m0 + m) / a.G;
+                        off = (int64_t)(r0 + r) * a.q_row + (int64_t)(h * a.G + (m0 + m - r * a.G)) * a.q_head;
+                    }
+                    const uint32_t qtile = q_base + qs * (QROWS * DP * 2);
+#pragma unroll
+                    for (int p = 0; p < QROWS / 16; ++p) {
+                        const int r = p * 4 + rsub;
+                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+#pragma unroll
+                        for (int half = 0; half < DP / 64; ++half) {
+                            const bool ok = o >= 0 && half * 64 + ch * 8 < D;
+                            cp_async16(qtile + half * (QROWS * 128) + (wl * (QROWS / 4) + r) * 128 + ((ch ^ (r & 7)) << 4),
+                                       a.q + (ok ? o + (half * 64 + ch * 8) * 2 : 0), ok);
+                        }
+                    }
+                    cp_async_arrive(&fd->q_full[qs]);
+                }
+                if (!two) qnext ^= 1;
             }
         }
     }
@@ -237,10 +245,9 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
     cp_async_wait<0>();   // nothing is in flight when the block ends
 }
 
-// The walk's part, one warp: describes the pieces, then `ends` times that there are no more.
-__device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2, Feed *fd, Walk w, int ends, int lane) {
+// The walk's part, one warp: describes the pieces, then that there are no more.
+__device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2, Feed *fd, Walk w, int lane) {
     uint32_t seq = 0;
-    int ended = 0;
     for (int it = 0;; ++it) {
         Piece p;
         const int pos = w.pos;
@@ -283,7 +290,7 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
         __syncwarp();
         if (lane == 0) mbar_arrive(&fd->pd_full[it % kRing]);
         if (more) seq += 2 * (p.k1 - p.k0);
-        else if (++ended == ends) break;
+        else break;
     }
 }
 
@@ -311,14 +318,16 @@ inline bool cache_map(CUtensorMap *map, char *base, const KvCache &c, int box_ro
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The tensors of a call.  Boxes of up to 32 slots (a producer warp's share of a tile), whole swizzle groups of 8 rows, that never
+// The tensors of a call.  Boxes of up to 64 slots, whole swizzle groups of 8 rows, that never
 // cross a page; other page sizes load by rows.
 inline TcArgs tc_args(const KvCache &c, uint32_t shape_s) {
     TcArgs t{};
     t.shape_s = shape_s;
     const int ps = c.page_size;
-    if (ps >= 32 ? ps % 32 == 0 : ps == 8 || ps == 16) {
-        t.box_rows = ps < 32 ? ps : 32;
+    t.page_shift = (ps & (ps - 1)) == 0 ? __builtin_ctz(ps) : -1;
+    const int rows = ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : ps == 16 || ps == 8 ? ps : 0;
+    if (rows > 0) {
+        t.box_rows = rows;
         if (encode_tiled() == nullptr || !cache_map(&t.k, c.k, c, t.box_rows) || !cache_map(&t.v, c.v, c, t.box_rows)) t.box_rows = 0;
     }
     return t;

@@ -12,8 +12,8 @@
 // The maximum of a row is kept until a score passes it by 2^8: then, and on a piece's first tile, the four warps exchange theirs and
 // the output is rescaled.  Other tiles need one vote.
 //
-// A persistent block of 16 warps.  Warps 0-3 take even pieces and warps 4-7 odd ones, so that one piece's end runs beside the
-// next one's start; 8-11 produce, 12 issues the products, 13 walks the range.
+// A persistent block of 16 warps.  Warps 0-3 take a piece's even tiles and warps 4-7 its odd ones, each group with its own maxima,
+// sums and output, which are added at the piece's end; 8-11 produce, 12 issues the products, 13 walks the range.
 // Tensor memory (256 columns): scores 2 groups x 2 tiles x 32, outputs 2 groups x 64.
 //
 // What bounds it: memory.  A tile is 64 KB (heads of 128), 2800 cycles of an SM's share of the measured copy bandwidth; its
@@ -25,7 +25,7 @@ namespace sv {
 namespace {
 
 constexpr int NR = kFewRows;
-constexpr int kFewReaders = 9;        // warps that read a piece description: four producers, the products', one softmax group
+constexpr int kFewReaders = 13;       // warps that read a piece description
 constexpr float kNoMax = -1e30f;      // maximum of a row that has seen no token yet
 
 template <int DP>
@@ -47,7 +47,7 @@ struct FewShared {
     // per group
     float top[2][4][NR];              // the warps' maxima of a row, later their sums
     alignas(16) float shift[2][NR];   // minus a row's maximum (of scale * log2(e) * q.k)
-    alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end 1 / sum
+    alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end what the group's output is scaled by
 };
 
 // Element-wise reduction of x[0..31] over the warp's lanes: lane r gets that of x[r].
@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         const f32x2 c2 = f2_pack(a.scale_log2, a.scale_log2);
         uint32_t u = 0;   // tiles this group has worked on
         auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + gr) : "memory"); };
-        for (int it = gr;; it += 2) {
+        auto both_sync = [&]() { asm volatile("bar.sync 3, 256;" ::: "memory"); };
+        for (int it = 0;; ++it) {
             const PieceInfo *pi = &fd->pd[it % kRing];
             wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
             __syncwarp();
@@ -144,7 +145,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
 #pragma unroll
             for (int r = 0; r < NR / 2; ++r) l[r] = 0;
             float *shift = ms->shift[gr], *alpha = ms->alpha[gr];
-            for (int k = k0; k < k1; ++k, ++u) {
+            const int begin = k0 + gr;
+            for (int k = begin; k < k1; k += 2, ++u) {
                 const int buf = u & 1;
                 const uint32_t colS = base + (gr * 2 + buf) * 32;
                 wait_phase(fd, &ms->s_full[gr][buf], (u >> 1) & 1, a.stats);
@@ -170,8 +172,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                             if (!((sees >> r) & 1u)) x[r] = -INFINITY;
                     }
                 };
-                uint32_t grow = 1;   // a piece's first tile sets the maxima
-                if (k > k0) {
+                uint32_t grow = 1;   // the first tile sets the maxima
+                if (k > begin) {
                     scores(true);
                     float over = x[0];
 #pragma unroll
@@ -192,14 +194,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                     ms->top[gr][wl][lane] = reduce_rows(x, lane, [](float p, float q) { return fmaxf(p, q); });
                     group_sync();
                     if (wl == 0) {
-                        const float old = k > k0 ? -shift[lane] : kNoMax;
+                        const float old = k > begin ? -shift[lane] : kNoMax;
                         const float now = fmaxf(fmaxf(fmaxf(ms->top[gr][0][lane], ms->top[gr][1][lane]), old),
                                                 fmaxf(ms->top[gr][2][lane], ms->top[gr][3][lane]));
                         alpha[lane] = ex2_fast(old - now);
                         shift[lane] = -now;
                     }
                     group_sync();
-                    if (k > k0) {
+                    if (k > begin) {
 #pragma unroll
                         for (int r = 0; r < NR / 2; ++r) l[r] = f2_mul(l[r], *reinterpret_cast<const f32x2 *>(alpha + 2 * r));
 #pragma unroll 1
@@ -272,9 +274,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms->p_full[gr]);
             }
-            // ---- the piece's end: thread t has head element t of every row
+            // ---- the piece's end: thread t has head element t of half of the rows
             const int vr = pi->vr, D = a.c.head_dim, qh0 = pi->h * a.G, r0 = pi->r0;
-            const bool whole = pi->whole;
+            const bool whole = pi->whole, has1 = k1 - k0 > 1;   // the second group has scored something
             const size_t slot = (size_t)pi->slot;
             {
                 float x[NR];
@@ -282,38 +284,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 for (int r = 0; r < NR; r += 2) f2_unpack(l[r / 2], x[r], x[r + 1]);
                 ms->top[gr][wl][lane] = reduce_rows(x, lane, [](float p, float q) { return p + q; });
             }
-            group_sync();
-            if (wl == 0) {
-                const float sum = (ms->top[gr][0][lane] + ms->top[gr][1][lane]) + (ms->top[gr][2][lane] + ms->top[gr][3][lane]);
-                const float mine = -shift[lane];
-                alpha[lane] = whole ? (sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f) : 1.0f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
+            both_sync();
+            if (warp == 0) {
+                float sum[2], top[2];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    sum[g] = (ms->top[g][0][lane] + ms->top[g][1][lane]) + (ms->top[g][2][lane] + ms->top[g][3][lane]);
+                    top[g] = g == 0 || has1 ? -ms->shift[g][lane] : kNoMax;
+                }
+                const float m = fmaxf(top[0], top[1]), f0 = ex2_fast(top[0] - m), f1 = ex2_fast(top[1] - m);
+                const float all = sum[0] * f0 + sum[1] * f1;
+                const float inv = whole ? (all > 0.0f || all != all ? 1.0f / all : 0.0f) : 1.0f;
+                ms->alpha[0][lane] = f0 * inv;
+                ms->alpha[1][lane] = f1 * inv;
                 if (lane < vr) {
                     const int i = lane / a.G, g = lane - i * a.G;
-                    if (!whole) a.part_ml[slot + lane] = make_float2(mine, sum);
-                    else if (a.lse) a.lse[(size_t)(r0 + i) * a.q_heads + qh0 + g] = sum == 0.0f ? -INFINITY : (mine + log2f(sum)) / kLog2e;
+                    if (!whole) a.part_ml[slot + lane] = make_float2(m, all);
+                    else if (a.lse) a.lse[(size_t)(r0 + i) * a.q_heads + qh0 + g] = all == 0.0f ? -INFINITY : (m + log2f(all)) / kLog2e;
                 }
             }
-            if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
-            wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
-            __syncwarp();
+            if (begin < k1) wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
+            both_sync();
             tc_fence_after();
-            float y[NR];   // the row's weighted values: the products with high and low parts
-            {
-                uint32_t o[32], o2[32];
-                tmem_ld32(colO, o);
-                tmem_ld32(colO + 32, o2);
+            const int rb = gr * (NR / 2);   // this group's rows
+            float y[NR / 2];
+#pragma unroll
+            for (int r = 0; r < NR / 2; ++r) y[r] = 0.0f;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (g == 1 && !has1) continue;
+                uint32_t o[16], o2[16];   // the products with the weights' high and low parts
+                tmem_ld16(base + 128 + g * 64 + rb, o);
+                tmem_ld16(base + 128 + g * 64 + 32 + rb, o2);
                 tc_wait_ld();
 #pragma unroll
-                for (int r = 0; r < NR; ++r) y[r] = __uint_as_float(o[r]) + __uint_as_float(o2[r]);
+                for (int r = 0; r < NR / 2; ++r)
+                    y[r] = fmaf(__uint_as_float(o[r]) + __uint_as_float(o2[r]), ms->alpha[g][rb + r], y[r]);
             }
-            group_sync();
             if (t < D) {
                 if (whole) {
-                    int i = 0, g = 0;
+                    int i = rb / a.G, g = rb - i * a.G;
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        if (r < vr) {
-                            store_elem<2>(a.out + (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head + t * 2, y[r] * alpha[r]);
+                    for (int r = 0; r < NR / 2; ++r) {
+                        if (rb + r < vr) {
+                            store_elem<2>(a.out + (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head + t * 2, y[r]);
                             if (++g == a.G) {
                                 g = 0;
                                 ++i;
@@ -321,14 +337,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                         }
                     }
                 } else {
-                    float *dst = a.part + slot * D + t;
+                    float *dst = a.part + (slot + rb) * D + t;
 #pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        if (r < vr) dst[(size_t)r * D] = y[r];
+                    for (int r = 0; r < NR / 2; ++r)
+                        if (rb + r < vr) dst[(size_t)r * D] = y[r];
                 }
             }
             tc_fence_before();
-            group_sync();   // the sums and maxima may be written again
+            both_sync();   // outputs, sums and maxima may be written again
         }
     } else if (warp < 12) {
         regs_dec<kRegsOther>();
@@ -339,7 +355,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             // ------------------------------------------------------------ matrix products
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             constexpr uint32_t shape_o = mma_shape(2 * NR, true, true, false, false);
-            uint32_t seq = 0, tiles0 = 0, tiles1 = 0, q_use0 = 0, q_use1 = 0;
+            uint32_t seq = 0, tiles0 = 0, tiles1 = 0;
             // O^T += V^T P^T of the tile whose scores were issued before the last
             int late = 0, late_gr = 0;
             uint32_t late_seq = 0, late_u = 0;
@@ -376,15 +392,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 if (nk <= 0) break;
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
-                const int gr = it & 1;
-                const uint64_t q = smem_operand(sbase + gr * (NR * DP * 2), 16, 1024);
+                const int qs = it & 1;
+                const uint64_t q = smem_operand(sbase + qs * (NR * DP * 2), 16, 1024);
                 for (int n = 0; n < nk; ++n) {
+                    const int gr = n & 1;
                     const uint32_t stage = seq % S::STAGES, u = gr ? tiles1 : tiles0;
                     ready(&fd->kv_full[stage], (seq / S::STAGES) & 1);
                     if (n == 0) {
-                        ready(&fd->q_full[gr], (gr ? q_use1 : q_use0) & 1);
-                        if (gr) ++q_use1;
-                        else ++q_use0;
+                        ready(&fd->q_full[qs], (it >> 1) & 1);
                     }
                     fence_async_smem();
                     tc_fence_after();
@@ -398,7 +413,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                         }
                         mma_commit(&ms->s_full[gr][u & 1]);
                         mma_commit(&fd->kv_empty[stage]);
-                        if (n == nk - 1) mma_commit(&fd->q_empty[gr]);
+                        if (n == nk - 1) mma_commit(&fd->q_empty[qs]);
                     }
                     __syncwarp();
                     if (late) weigh();
@@ -416,7 +431,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             wait_phase(fd, &ms->done, 0, a.stats);
             __syncwarp();
         } else if (warp == 13) {
-            feed_walk(a, a2, fd, ms->walk, 2, lane);
+            feed_walk(a, a2, fd, ms->walk, lane);
         }
     }
     tc_fence_before();

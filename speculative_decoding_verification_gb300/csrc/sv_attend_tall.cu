@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
             __syncwarp();
         } else if (warp == 13) {
             // ------------------------------------------------------------ the walk
-            feed_walk(a, a2, fd, ms->walk, 1, lane);
+            feed_walk(a, a2, fd, ms->walk, lane);
         }
     }
     tc_fence_before();
