@@ -45,6 +45,19 @@ def _on(dev, fn, *args):
         return fn(*args)
 
 
+def _call(dev, stream, fn, *args):
+    """_on with the stream (_stream's rule) as the last argument, without the context manager where `dev` is current
+    already: the short calls of a decoding step are bound by what the host does for them."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        raw = _stream(stream, dev)
+    if torch._C._cuda_getDevice() == dev.index:
+        return fn(*args, raw)
+    with torch.cuda.device(dev):
+        return fn(*args, raw)
+
+
 def _dtype_code(t):
     if t.dtype == torch.float32:
         return SV_F32
@@ -499,19 +512,30 @@ def _style(style):
 def _heads(t, name, like=None):
     """(row stride, head stride) in elements of a [rows, heads, dim] or [B, n, heads, dim] tensor whose
     rows lie one stride apart."""
-    if t.dim() not in (3, 4):
+    shape, st = t.shape, t.stride()
+    if len(shape) == 4:
+        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+            raise ValueError(f"{name}: rows of a sequence must be consecutive rows of one stride")
+        row = st[1] if shape[1] > 1 else st[0]
+    elif len(shape) == 3:
+        row = st[0]
+    else:
         raise ValueError(f"{name}: expected [rows, heads, dim] or [B, n, heads, dim]")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
-        raise ValueError(f"{name}: rows of a sequence must be consecutive rows of one stride")
-    row = t.stride(1) if t.dim() == 4 and t.shape[1] > 1 else t.stride(0)
     if like is not None:
-        if t.device != like.device:
+        if t.get_device() != like.get_device():
             raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-        if t.dtype != like.dtype:
+        if t.dtype is not like.dtype:
             raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    return row, t.stride(-2)
+    return row, st[-2]
+
+
+def _ints(t, name, dtype, n, dev):
+    """_arr's checks for the small arrays of a block, cheapest first; its address."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev.index and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    return _arr(t, name, dtype, n, dev).data_ptr()
 
 
 def sv_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -536,66 +560,71 @@ def sv_rope(x, positions, inv_freq, style="half", magnitude=1.0, backward=False,
     backward=True takes the gradient of the output to the input's.  out may be x.  Returns out."""
     lib = load()
     dev = _cuda(x, "x")
-    row, head = _heads(x, "x")
-    rows, heads, dim = x.shape[:-2].numel(), x.shape[-2], x.shape[-1]
-    _arr(positions, "positions", torch.int32, rows, dev)
-    _arr(inv_freq, "inv_freq", torch.float32, 1, dev)
+    shape, (row, head) = x.shape, _heads(x, "x")
+    rows = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+    pos = _ints(positions, "positions", torch.int32, rows, dev)
+    freq = _ints(inv_freq, "inv_freq", torch.float32, 1, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    elif out.shape != x.shape:
-        raise ValueError(f"out must have shape {tuple(x.shape)}")
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
     o_row, o_head = _heads(out, "out", x)
-    code = _on(dev, lib.sv_rope, x.data_ptr(), row, head, out.data_ptr(), o_row, o_head, _dtype_code(x), rows, heads, dim,
-               positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), _style(style), float(magnitude),
-               int(bool(backward)), _stream(stream, dev))
-    _abi.check("sv_rope", code)
+    if out.shape != shape:
+        raise ValueError(f"out must have shape {tuple(shape)}")
+    code = _call(dev, stream, lib.sv_rope, x.data_ptr(), row, head, out.data_ptr(), o_row, o_head, _dtype_code(x), rows, shape[-2],
+                 shape[-1], pos, freq, 2 * inv_freq.numel(), _style(style), magnitude, bool(backward))
+    if code:
+        _abi.check("sv_rope", code)
     return out
 
 
 def _kv_cache(k_cache, v_cache, dims):
-    """The sv_kv_cache of paged tensors [pages, page_size, kv_heads, dim] (with a leading layer axis where
-    dims is 5): one shape, dtype, device and set of strides for keys and values."""
+    """(device, shape, strides, packed sv_kv_cache) of paged tensors [pages, page_size, kv_heads, dim] (with a leading layer axis
+    where dims is 5): one shape, dtype, device and set of strides for keys and values."""
     dev = _cuda(k_cache, "k_cache")
-    if k_cache.dim() != dims:
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != dims:
         raise ValueError(f"k_cache: expected {dims} axes, [{'layers, ' if dims == 5 else ''}pages, page_size, kv_heads, dim]")
-    strides = k_cache.stride()
-    if v_cache.shape != k_cache.shape or v_cache.stride() != strides:
+    if v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("k_cache and v_cache must share their shape and strides")
-    if v_cache.dtype != k_cache.dtype:
+    if v_cache.dtype is not k_cache.dtype:
         raise TypeError("k_cache and v_cache must share a dtype")
-    if v_cache.device != dev:
+    if v_cache.get_device() != dev.index:
         raise ValueError("k_cache and v_cache must be on one device")
-    shape = k_cache.shape
-    if shape[-1] > 1 and strides[-1] != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError("k_cache: the last axis must be contiguous")
-    return dev, _abi.SvKvCache(k_cache.data_ptr(), v_cache.data_ptr(), strides[-4], strides[-3], strides[-2], shape[-4],
-                               shape[-3], shape[-2], shape[-1], _dtype_code(k_cache))
+    return dev, shape, st, _abi.KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), st[-4], st[-3], st[-2], shape[-4], shape[-3],
+                                              shape[-2], shape[-1], _dtype_code(k_cache))
 
 
-def _kv_batch(dev, context_len, page_table, rows_of, row_start, parents, max_rows):
-    """The sv_kv_batch of a call whose rows are those of the tensor `rows_of`."""
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != dev or page_table.stride(1) != 1:
-        raise ValueError(f"page_table must be an int32 [B, pages] tensor on {dev} with contiguous rows")
-    B = page_table.shape[0]
-    _arr(context_len, "context_len", torch.int32, B, dev)
+def _page_table(page_table, B, dev):
+    """(address, pitch, pages, B) of a page table, checked."""
+    shape, st = page_table.shape, page_table.stride()
+    if len(shape) != 2 or (B is not None and shape[0] != B) or page_table.dtype is not torch.int32 or \
+            page_table.get_device() != dev.index or (st[1] != 1 and shape[1] > 1):
+        raise ValueError(f"page_table must be an int32 [{'B' if B is None else B}, pages] tensor on {dev} with contiguous rows")
+    return page_table.data_ptr(), st[0], shape[1], shape[0]
+
+
+def _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows):
+    """(B, rows, packed sv_kv_batch) of a call whose row tensors have `shape`."""
+    table, pitch, pages, B = _page_table(page_table, None, dev)
+    ctx = _ints(context_len, "context_len", torch.int32, B, dev)
+    starts = par = 0
     if row_start is None:
-        if rows_of.dim() != 4 or rows_of.shape[0] != B:
+        if len(shape) != 4 or shape[0] != B:
             raise ValueError(f"without row_start the block's tensors are [B, n, heads, dim] with B = {B}")
-        n = rows_of.shape[1]
+        n = shape[1]
         rows = B * n
         if parents is not None:
-            _arr(parents, "parents", torch.int32, B * (n - 1), dev)
+            par = _ints(parents, "parents", torch.int32, B * (n - 1), dev)
     else:
-        if rows_of.dim() != 3:
+        if len(shape) != 3:
             raise ValueError("with row_start the block's tensors are [rows, heads, dim]")
         if parents is not None:
             raise ValueError("parents needs blocks of one size (no row_start)")
-        _arr(row_start, "row_start", torch.int32, B + 1, dev)
-        rows = rows_of.shape[0]
+        starts = _ints(row_start, "row_start", torch.int32, B + 1, dev)
+        rows = shape[0]
         n = rows if max_rows is None else int(max_rows)
-    return _abi.SvKvBatch(context_len.data_ptr(), page_table.data_ptr(), row_start.data_ptr() if row_start is not None else 0,
-                          parents.data_ptr() if parents is not None else 0, page_table.stride(0), page_table.shape[1], B,
-                          max(n, 1), rows)
+    return B, rows, _abi.KV_BATCH.pack(ctx, table, starts, par, pitch, pages, B, max(n, 1), rows)
 
 
 def sv_kv_append(k, v, k_cache, v_cache, context_len, page_table, q=None, q_out=None, inv_freq=None, style="half",
@@ -608,38 +637,35 @@ def sv_kv_append(k, v, k_cache, v_cache, context_len, page_table, q=None, q_out=
     row_start int32 [B+1]: ragged blocks, with k, v, q [rows, heads, dim] and at most max_rows rows a sequence.
     Returns the rotated queries (q_out, which may be q), or None without q.  Device-side errors are written to
     stats where one is passed (new_stats)."""
-    lib = load()
-    dev, cache = _kv_cache(k_cache, v_cache, 4)
-    k_row, k_head = _heads(k, "k", k_cache)
-    v_row, v_head = _heads(v, "v", k_cache)
-    if k.shape != v.shape or tuple(k.shape[-2:]) != tuple(k_cache.shape[-2:]):
+    lib = _abi.load_packed()
+    dev, c_shape, _, cache = _kv_cache(k_cache, v_cache, 4)
+    shape, (k_row, k_head), (v_row, v_head) = k.shape, _heads(k, "k", k_cache), _heads(v, "v", k_cache)
+    if v.shape != shape or shape[-2:] != c_shape[-2:]:
         raise ValueError("k and v must share a shape that ends in the cache's [kv_heads, dim]")
-    batch = _kv_batch(dev, context_len, page_table, k, row_start, parents, max_rows)
+    _, rows, batch = _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
+    freq = rotary = 0
     if inv_freq is not None:
-        _arr(inv_freq, "inv_freq", torch.float32, 1, dev)
-    q_row = q_head = o_row = o_head = heads = 0
+        freq, rotary = _ints(inv_freq, "inv_freq", torch.float32, 1, dev), 2 * inv_freq.numel()
+    q_row = q_head = o_row = o_head = heads = q_ptr = o_ptr = 0
     if q is not None:
-        q_row, q_head = _heads(q, "q", k_cache)
-        heads = q.shape[-2]
-        if q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+        q_shape, (q_row, q_head) = q.shape, _heads(q, "q", k_cache)
+        if q_shape[:-2] != shape[:-2] or q_shape[-1] != shape[-1]:
             raise ValueError("q must have the rows and head width of k")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        elif q_out.shape != q.shape:
-            raise ValueError(f"q_out must have shape {tuple(q.shape)}")
+            q_out = torch.empty(q_shape, dtype=q.dtype, device=dev)
         o_row, o_head = _heads(q_out, "q_out", k_cache)
+        if q_out.shape != q_shape:
+            raise ValueError(f"q_out must have shape {tuple(q_shape)}")
+        heads, q_ptr, o_ptr = q_shape[-2], q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if stats is not None:
-        _stats(stats, dev)
-    if batch.rows == 0:
+    st = _stats(stats, dev).data_ptr() if stats is not None else 0
+    if rows == 0:
         return q_out
-    code = _on(dev, lib.sv_kv_append, cache, batch, q.data_ptr() if q is not None else 0, q_row, q_head,
-               q_out.data_ptr() if q is not None else 0, o_row, o_head, heads, k.data_ptr(), k_row, k_head, v.data_ptr(),
-               v_row, v_head, inv_freq.data_ptr() if inv_freq is not None else 0,
-               2 * inv_freq.numel() if inv_freq is not None else 0, _style(style), float(magnitude),
-               stats.data_ptr() if stats is not None else 0, _stream(stream, dev))
-    _abi.check("sv_kv_append", code)
+    code = _call(dev, stream, lib.sv_kv_append, cache, batch, q_ptr, q_row, q_head, o_ptr, o_row, o_head, heads, k.data_ptr(), k_row,
+                 k_head, v.data_ptr(), v_row, v_head, freq, rotary, _style(style), magnitude, st)
+    if code:
+        _abi.check("sv_kv_append", code)
     return q_out
 
 
@@ -651,41 +677,40 @@ def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, paren
     dim ** -0.5.  group_start int32 [G+1] and prefix_len int32 [G]: the sequences of a group share their first
     prefix_len tokens, which are read once for all of them.  lse: True, or a float32 tensor of q's shape without
     the last axis.  Returns (out, lse or None)."""
-    lib = load()
-    dev, cache = _kv_cache(k_cache, v_cache, 4)
-    q_row, q_head = _heads(q, "q", k_cache)
-    heads, dim = q.shape[-2], q.shape[-1]
-    if dim != k_cache.shape[-1]:
+    lib = _abi.load_packed()
+    dev, c_shape, _, cache = _kv_cache(k_cache, v_cache, 4)
+    shape, (q_row, q_head) = q.shape, _heads(q, "q", k_cache)
+    heads, dim = shape[-2], shape[-1]
+    if dim != c_shape[-1]:
         raise ValueError("q must have the cache's head width")
-    batch = _kv_batch(dev, context_len, page_table, q, row_start, parents, max_rows)
-    groups = 0
+    B, rows, batch = _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
+    groups = starts = lens = 0
     if (group_start is None) != (prefix_len is None):
         raise ValueError("group_start and prefix_len come together")
     if prefix_len is not None:
         groups = prefix_len.numel()
-        _arr(prefix_len, "prefix_len", torch.int32, 1, dev)
-        _arr(group_start, "group_start", torch.int32, groups + 1, dev)
+        lens = _ints(prefix_len, "prefix_len", torch.int32, 1, dev)
+        starts = _ints(group_start, "group_start", torch.int32, groups + 1, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif out.shape != q.shape:
-        raise ValueError(f"out must have shape {tuple(q.shape)}")
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
     o_row, o_head = _heads(out, "out", k_cache)
+    if out.shape != shape:
+        raise ValueError(f"out must have shape {tuple(shape)}")
     if lse is True:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     elif lse is False:
         lse = None
-    _opt(lse, "lse", torch.float32, batch.rows * heads, dev)
-    if stats is not None:
-        _stats(stats, dev)
-    if batch.rows == 0:
+    else:
+        _opt(lse, "lse", torch.float32, rows * heads, dev)
+    st = _stats(stats, dev).data_ptr() if stats is not None else 0
+    if rows == 0:
         return out, lse
-    ws = (workspace or _default_ws).get(lib.sv_kv_attend_workspace_size(batch.rows, heads, dim, batch.B, groups), dev)
-    code = _on(dev, lib.sv_kv_attend, cache, batch, q.data_ptr(), q_row, q_head, heads,
-               float(dim ** -0.5 if scale is None else scale), group_start.data_ptr() if groups else 0,
-               prefix_len.data_ptr() if groups else 0, groups, out.data_ptr(), o_row, o_head,
-               lse.data_ptr() if lse is not None else 0, stats.data_ptr() if stats is not None else 0, ws.data_ptr(),
-               ws.numel(), _stream(stream, dev))
-    _abi.check("sv_kv_attend", code)
+    ws = (workspace or _default_ws).get(load().sv_kv_attend_workspace_size(rows, heads, dim, B, groups), dev)
+    code = _call(dev, stream, lib.sv_kv_attend, cache, batch, q.data_ptr(), q_row, q_head, heads,
+                 dim ** -0.5 if scale is None else scale, starts, lens, groups, out.data_ptr(), o_row, o_head,
+                 lse.data_ptr() if lse is not None else 0, st, ws.data_ptr(), ws.numel())
+    if code:
+        _abi.check("sv_kv_attend", code)
     return out, lse
 
 
@@ -693,26 +718,21 @@ def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, co
     """sv_kv_commit: after sv_tree_verify, move the accepted path's keys and values to consecutive slots in every
     layer.  k_cache, v_cache [layers, pages, page_size, kv_heads, dim]; accept_len int32 [B] and path int32 [B, N]
     as sv_tree_verify gives them.  Returns context_out int32 [B]: context_len + 1 + accept_len."""
-    lib = load()
-    dev, cache = _kv_cache(k_cache, v_cache, 5)
+    lib = _abi.load_packed()
+    dev, c_shape, strides, cache = _kv_cache(k_cache, v_cache, 5)
     B, N = path.shape
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32 or page_table.device != dev or \
-            page_table.stride(1) != 1:
-        raise ValueError(f"page_table must be an int32 [{B}, pages] tensor on {dev} with contiguous rows")
-    _arr(context_len, "context_len", torch.int32, B, dev)
-    _arr(accept_len, "accept_len", torch.int32, B, dev)
-    _arr(path, "path", torch.int32, B * N, dev)
-    if context_out is not None and context_out.data_ptr() == context_len.data_ptr():
+    table, pitch, pages, _ = _page_table(page_table, B, dev)
+    ctx = _ints(context_len, "context_len", torch.int32, B, dev)
+    acc = _ints(accept_len, "accept_len", torch.int32, B, dev)
+    nodes = _ints(path, "path", torch.int32, B * N, dev)
+    if context_out is not None and context_out.data_ptr() == ctx:
         raise ValueError("context_out must not be context_len")
     context_out = _out(context_out, "context_out", torch.int32, (B,), dev)
-    if stats is not None:
-        _stats(stats, dev)
-    batch = _abi.SvKvBatch(context_len.data_ptr(), page_table.data_ptr(), 0, 0, page_table.stride(0), page_table.shape[1], B,
-                           N + 1, B * (N + 1))
-    code = _on(dev, lib.sv_kv_commit, cache, batch, k_cache.shape[0], k_cache.stride(0), accept_len.data_ptr(),
-               path.data_ptr() if N else 0, context_out.data_ptr(), stats.data_ptr() if stats is not None else 0,
-               _stream(stream, dev))
-    _abi.check("sv_kv_commit", code)
+    st = _stats(stats, dev).data_ptr() if stats is not None else 0
+    batch = _abi.KV_BATCH.pack(ctx, table, 0, 0, pitch, pages, B, N + 1, B * (N + 1))
+    code = _call(dev, stream, lib.sv_kv_commit, cache, batch, c_shape[0], strides[0], acc, nodes if N else 0, context_out.data_ptr(), st)
+    if code:
+        _abi.check("sv_kv_commit", code)
     return context_out
 
 
