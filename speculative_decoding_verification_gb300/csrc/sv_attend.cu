@@ -465,7 +465,7 @@ cudaError_t launch_attend_f32(AttendArgs &a, int es, cudaStream_t stream) {
 
 // Workspace of a call: segment offsets, then the slots of the widest tiles (256 rows) on the most blocks, once for the prefixes and
 // once for the own tokens.
-constexpr int kAttBlocks = 160;   // most persistent blocks (a GB300 has 152 SMs)
+constexpr int kAttBlocks = 160;   // most persistent blocks, one an SM (a GB300 has 152); few32 has two
 constexpr int kAttMaxTile = 256;
 
 struct AttendPlan {
@@ -478,7 +478,7 @@ static AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, in
     const size_t slots = attend_slots(rows, q_heads, n_groups > 0, true, kAttMaxTile, kAttBlocks) +
                          (n_groups > 0 ? (size_t)kFewRows * kAttBlocks : 0);
     p.off_seg = cv.take<int>((size_t)n_groups + B + 2);
-    p.off_tails = cv.take<AttendTail>(kAttBlocks);
+    p.off_tails = cv.take<AttendTail>(2 * kAttBlocks);
     p.off_ml = cv.take<float2>(slots);
     p.off_part = cv.take<float>(slots * head_dim);
     p.bytes = cv.off + 256;
@@ -544,7 +544,12 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     AttendGeo prefix = all, own = all;
     cudaError_t e = cudaSuccess;
     // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.
-    if (es == 4 || cache->head_dim > 128) {
+    // Float32 with up to 8 rows and no prefix to share goes through registers: a tile of 16 rows or more would be mostly empty.
+    if (es == 4 && cache->head_dim <= 128 && n_groups == 0 && (int64_t)batch->n * a.G <= kFewRows32) {
+        a.geo = all;
+        e = launch_attend_few32(a, s);
+        own = a.geo;
+    } else if (es == 4 || cache->head_dim > 128) {
         a.geo = all;
         e = launch_attend_f32(a, es, s);
         prefix = own = a.geo;
