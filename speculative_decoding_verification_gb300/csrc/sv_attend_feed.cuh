@@ -23,7 +23,8 @@ struct PieceInfo {
     int table, key0, ctx, end;        // page table's sequence, tokens
     int k0, k1;                       // key tiles; k0 == k1: no more pieces
     uint32_t seq;                     // ring number of the first tile's keys
-    int own, tree, whole, boxes;      // own segment, tree mask, output complete here, full tiles load as boxes
+    int own, tree, whole;             // own segment, tree mask, output complete here
+    int box_tiles;                    // tiles before this one load as boxes, the others by rows
     uint8_t par[SV_MAX_TREE];         // a tree's parents (255: invalid)
 };
 
@@ -159,14 +160,12 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
         const int k0 = pi->k0, k1 = pi->k1;
         if (k0 >= k1) break;
         const int vr = pi->vr, key0 = pi->key0, end = pi->end, h = pi->h, m0 = pi->m0, r0 = pi->r0, tab = pi->table;
-        // A tile that every row sees whole goes as boxes where it can, the others by rows.
-        const int whole_end = pi->own ? pi->ctx : end;
-        const int boxes = pi->boxes ? ROWS / a2.box_rows : 0;
+        const int box_tiles = pi->box_tiles, boxes = box_tiles > 0 ? ROWS / a2.box_rows : 0;
         const int32_t *table = a.bt.page_table + tab * a.bt.table_pitch;
         __syncwarp();
         if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
         const bool two = vr > QROWS;   // two row tiles share the keys
-        auto by_box = [&](int k) { return boxes > 0 && key0 + (k + 1) * kTcKeys <= whole_end; };
+        auto by_box = [&](int k) { return k < box_tiles; };
         // this lane's box of a tile, as (page, slot); fetched a tile ahead
         auto box_key = [&](int k) { return key0 + k * kTcKeys + row0 + lane * a2.box_rows; };
         auto box_page = [&](int k) { return k < k1 && by_box(k) && lane < boxes ? table[page_index(box_key(k))] : kNoPage; };
@@ -276,7 +275,8 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
                 pi->key0 = p.g.key0;
                 pi->ctx = p.g.ctx;
                 pi->end = p.end;
-                pi->boxes = a2.box_rows > 0 && p.g.key0 % a2.box_rows == 0;
+                // a tile that every row sees whole goes as boxes where no box would cross a page
+                pi->box_tiles = a2.box_rows > 0 && p.g.key0 % a2.box_rows == 0 ? ((own ? p.g.ctx : p.end) - p.g.key0) / kTcKeys : 0;
                 pi->k0 = p.k0;
                 pi->k1 = p.k1;
                 pi->seq = seq;

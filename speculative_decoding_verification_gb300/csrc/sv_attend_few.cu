@@ -357,14 +357,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             constexpr uint32_t shape_o = mma_shape(2 * NR, true, true, false, false);
             uint32_t seq = 0, tiles0 = 0, tiles1 = 0;
             // O^T += V^T P^T of the tile whose scores were issued before the last
-            int late = 0, late_gr = 0;
+            int late = 0, late_gr = 0, late_rows = 0;
             uint32_t late_seq = 0, late_u = 0;
             auto weigh = [&]() {
                 const uint32_t stage = late_seq % S::STAGES;
                 wait_phase(fd, &fd->kv_full[stage], (late_seq / S::STAGES) & 1, a.stats);
                 wait_phase(fd, &ms->p_full[late_gr], late_u & 1, a.stats);
                 __syncwarp();
-                fence_async_smem();
+                if (late_rows) fence_async_smem();
                 tc_fence_after();
                 const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, DP == 128 ? S::HALF : 0, 1024);
                 const uint64_t p = smem_operand(sbase + S::OFF_P + late_gr * S::PBUF, 0, 1024);
@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 ready(&fd->pd_full[it % kRing], (it / kRing) & 1);
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 if (nk <= 0) break;
+                const int rows_from = __shfl_sync(0xFFFFFFFFu, pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
                 const int qs = it & 1;
                 const uint64_t q = smem_operand(sbase + qs * (NR * DP * 2), 16, 1024);
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                     if (n == 0) {
                         ready(&fd->q_full[qs], (it >> 1) & 1);
                     }
-                    fence_async_smem();
+                    if (n == 0 || n >= rows_from) fence_async_smem();
                     tc_fence_after();
                     const uint64_t kt = smem_operand(sbase + S::OFF_KV + stage * S::TILE, 16, 1024);
                     const uint32_t s = tm + (gr * 2 + (u & 1)) * 32;
@@ -419,6 +420,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                     if (late) weigh();
                     late = 1;
                     late_gr = gr;
+                    late_rows = n >= rows_from;
                     late_seq = seq + 1;
                     late_u = u;
                     seq += 2;

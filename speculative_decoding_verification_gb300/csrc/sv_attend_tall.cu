@@ -32,7 +32,7 @@ struct TallShape {
 
 struct TallShared {
     Feed fd;
-    uint64_t s_full[2], p_full[2], o_full[2], done;
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], done;   // p_half: the first 64 tokens' weights
     union {
         struct {
             Walk walk;                // read before the first piece is described
@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
         feed_init(fd, kTallReaders);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i], 1);
+            mbar_init(&ms->p_half[i], 4);
             mbar_init(&ms->p_full[i], 4);
             mbar_init(&ms->o_full[i], 1);
         }
@@ -230,6 +231,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     tc_wait_ld();
                     mask32(x, vis[1]);
                     weights(x, 1);
+                    if (!(own && masked)) {   // there the output may have to be touched before any product
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ms->p_half[st]);
+                    }
                     weights(hold, 2);
                     weights(hold + 32, 3);
                     l = f2_sum(f2_add(sum[0], sum[1]));
@@ -274,7 +281,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms->p_full[st]);
+                if (lane == 0) {
+                    if (!active || (own && masked)) mbar_arrive(&ms->p_half[st]);
+                    mbar_arrive(&ms->p_full[st]);
+                }
             }
             // ---- the piece's end
             const int nk = k1 - k0;
@@ -379,56 +389,85 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 const bool two = __shfl_sync(0xFFFFFFFFu, pi->vr, 0) > 128;
                 if (nk <= 0) break;
+                const int rows_from = __shfl_sync(0xFFFFFFFFu, pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
-                const int jobs = two ? 2 * nk : nk;
-                auto weigh = [&](int n) {   // O += P V of job n
-                    const int s = n & 1, tile = two ? n >> 1 : n;
-                    const uint32_t vs = seq + 2 * tile + 1, stage = vs % S::STAGES;
-                    wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
-                    wait_phase(fd, &ms->p_full[s], (p_phases >> s) & 1, a.stats);
-                    p_phases ^= 1u << s;
-                    __syncwarp();
-                    fence_async_smem();
-                    tc_fence_after();
-                    const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, S::HALF, 1024);
-                    const uint32_t o = tm + kColO + s * 128, w = tm + kColS + s * 128;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 16; ++kk)   // the weights' upper parts, then the lower ones
-                            mma_ts(o, w + kk * 8, v + (kk & 7) * (2048 >> 4), shape_o, 1u);
-                        if (!two || s == 1) mma_commit(&fd->kv_empty[stage]);
-                        if (n + 2 >= jobs) mma_commit(&ms->o_full[s]);
-                    }
-                    __syncwarp();
-                };
-                for (int n = 0; n < jobs; ++n) {
-                    const int s = n & 1, tile = two ? n >> 1 : n;
-                    const int qs = two ? s : qnext;
-                    const uint32_t ks = seq + 2 * tile, stage = ks % S::STAGES;
-                    if (n == 0 || (two && n == 1)) {
-                        wait_phase(fd, &fd->q_full[qs], (q_phases >> qs) & 1, a.stats);
-                        q_phases ^= 1u << qs;
-                    }
-                    wait_phase(fd, &fd->kv_full[stage], (ks / S::STAGES) & 1, a.stats);
-                    __syncwarp();
-                    fence_async_smem();
-                    tc_fence_after();
+                // Job n: stream n & 1, key tile n / 2 (two row tiles) or n.
+                const int jobs = two ? 2 * nk : nk, shift = two ? 1 : 0;
+                for (int t = 0; t < (two ? 2 : 1); ++t) {
+                    const int qs = two ? t : qnext;
+                    wait_phase(fd, &fd->q_full[qs], (q_phases >> qs) & 1, a.stats);
+                    q_phases ^= 1u << qs;
+                }
+                __syncwarp();
+                fence_async_smem();
+                // S = Q K^T of job n, inside elect_one; its keys have been waited for
+                auto scores = [&](int n) {
+                    const int s = n & 1, qs = two ? s : qnext;
+                    const uint32_t stage = (seq + 2 * (n >> shift)) % S::STAGES;
                     const uint64_t q = smem_operand(sbase + qs * S::TILE, 16, 1024);
                     const uint64_t kt = smem_operand(sbase + S::OFF_KV + stage * S::TILE, 16, 1024);
-                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < DP / 16; ++kk) {
-                            const uint32_t at = ((kk >> 2) * S::HALF + (kk & 3) * 32) >> 4;
-                            mma_ss(tm + kColS + s * 128, q + at, kt + at, a2.shape_s, kk > 0);
-                        }
-                        mma_commit(&ms->s_full[s]);
-                        if (!two || s == 1) mma_commit(&fd->kv_empty[stage]);
-                        if (two ? n >= jobs - 2 : n == jobs - 1) mma_commit(&fd->q_empty[qs]);
+                    for (int kk = 0; kk < DP / 16; ++kk) {
+                        const uint32_t at = ((kk >> 2) * S::HALF + (kk & 3) * 32) >> 4;
+                        mma_ss(tm + kColS + s * 128, q + at, kt + at, a2.shape_s, kk > 0);
                     }
+                    mma_commit(&ms->s_full[s]);
+                    if (!two || s == 1) mma_commit(&fd->kv_empty[stage]);
+                    if (two ? n >= jobs - 2 : n == jobs - 1) mma_commit(&fd->q_empty[qs]);
+                };
+                auto keys_bar = [&](int n) { return &fd->kv_full[(seq + 2 * (n >> shift)) % S::STAGES]; };
+                auto keys_phase = [&](int n) { return ((seq + 2 * (n >> shift)) / S::STAGES) & 1; };
+                auto keys_wait = [&](int n) {
+                    wait_phase(fd, keys_bar(n), keys_phase(n), a.stats);
                     __syncwarp();
-                    if (n > 0) weigh(n - 1);
+                    if ((n >> shift) >= rows_from) fence_async_smem();
+                    tc_fence_after();
+                };
+                for (int n = 0; n < min(jobs, 2); ++n) {
+                    keys_wait(n);
+                    if (elect_one()) scores(n);
+                    __syncwarp();
                 }
-                weigh(jobs - 1);
+                for (int n = 0; n < jobs; ++n) {   // O += P V of job n, and S of the stream's next job right behind it
+                    const int s = n & 1, tile = n >> shift;
+                    const uint32_t vs = seq + 2 * tile + 1, stage = vs % S::STAGES;
+                    const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, S::HALF, 1024);
+                    const uint32_t o = tm + kColO + s * 128, w = tm + kColS + s * 128, phase = (p_phases >> s) & 1;
+                    p_phases ^= 1u << s;
+                    // The next keys are looked at before the weights are waited for: where they are there, nothing stands between
+                    // the two groups of products.
+                    const bool next = n + 2 < jobs;
+                    bool ready = next && __all_sync(0xFFFFFFFFu, mbar_test_wait(keys_bar(n + 2), keys_phase(n + 2)));
+                    if (ready && ((n + 2) >> shift) >= rows_from) fence_async_smem();
+                    wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
+                    // Half of the tokens at a time, so that one half's products run while the other's weights are made; of each
+                    // the weights' upper parts, then the lower ones.
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        wait_phase(fd, half ? &ms->p_full[s] : &ms->p_half[s], phase, a.stats);
+                        __syncwarp();
+                        if (half == 0 && tile >= rows_from) fence_async_smem();
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                                for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                                    mma_ts(o, w + part * 64 + kk * 8, v + kk * (2048 >> 4), shape_o, 1u);
+                            if (half) {
+                                if (!two || s == 1) mma_commit(&fd->kv_empty[stage]);
+                                if (n + 2 >= jobs) mma_commit(&ms->o_full[s]);
+                                if (ready) scores(n + 2);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (next && !ready) {
+                        keys_wait(n + 2);
+                        if (elect_one()) scores(n + 2);
+                        __syncwarp();
+                    }
+                }
                 if (!two) qnext ^= 1;
                 seq += 2 * nk;
             }
