@@ -187,22 +187,27 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
                 if (lane < boxes) box_load(tile + lane * a2.box_rows * 128, map, &fd->kv_full[stage], col0, h, slot, pg);
                 __syncwarp();
             } else {
-                int64_t off[ROWS / 32];
+                // Not unrolled: the block's five kinds of warps share the instruction cache, and these loops laid out in full
+                // cost the whole kernel a seventh of its speed.
+                int id[ROWS / 32];   // all pages are asked for before the first is needed
 #pragma unroll
                 for (int i = 0; i < ROWS / 32; ++i) {
                     const int key = key0 + k * kTcKeys + row0 + i * 32 + lane;
-                    off[i] = -1;
-                    if (key < end) {
-                        const int pn = page_index(key), id = table[pn];
-                        if (id >= 0 && id < a.c.n_pages) off[i] = id * a.c.page_b + (key - pn * psize) * a.c.slot_b + h * a.c.head_b;
-                        else report_error(a.stats, SV_ERR_INVALID_ARG, tab);
-                    }
+                    id[i] = key < end ? table[page_index(key)] : kNoPage;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < ROWS / 32; ++i) {
+                    const int key = key0 + k * kTcKeys + row0 + i * 32 + lane;
+                    int64_t off = -1;
+                    if ((unsigned)id[0] < (unsigned)a.c.n_pages)
+                        off = id[0] * a.c.page_b + (key - page_index(key) * psize) * a.c.slot_b + h * a.c.head_b;
+                    else if (id[0] != kNoPage)
+                        report_error(a.stats, SV_ERR_INVALID_ARG, tab);
 #pragma unroll
+                    for (int j = 0; j + 1 < ROWS / 32; ++j) id[j] = id[j + 1];
+#pragma unroll 2
                     for (int p = 0; p < 8; ++p) {
-                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off[i], p * 4 + rsub);
+                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, p * 4 + rsub);
                         const bool ok = o >= 0 && real;
                         const int r = row0 + i * 32 + p * 4 + rsub;   // r & 7 is the swizzle
                         cp_async16(tile + (i * 32 + p * 4 + rsub) * 128 + ((ch ^ (r & 7)) << 4), src + (ok ? o + (col0 + ch * 8) * 2 : 0), ok);
@@ -223,7 +228,7 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
                         off = (int64_t)(r0 + r) * a.q_row + (int64_t)(h * a.G + (m0 + m - r * a.G)) * a.q_head;
                     }
                     const uint32_t qtile = q_base + qs * (QROWS * DP * 2);
-#pragma unroll
+#pragma unroll 2
                     for (int p = 0; p < QROWS / 16; ++p) {
                         const int r = p * 4 + rsub;
                         const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);

@@ -47,6 +47,7 @@ struct FewShared {
     // per group
     float top[2][4][NR];              // the warps' maxima of a row, later their sums
     alignas(16) float shift[2][NR];   // minus a row's maximum (of scale * log2(e) * q.k)
+    alignas(16) float zero[NR];
     alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end what the group's output is scaled by
 };
 
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             mbar_init(&ms->p_done[i], 1);
         }
         mbar_init(&ms->done, 1);
+        for (int i = 0; i < NR; ++i) ms->zero[i] = 0.0f;
         fence_barrier_init();
     }
     if (warp == 12) tmem_alloc(&fd->tmem, 256);
@@ -154,43 +156,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 tc_fence_after();
                 const bool masked = key0 + (k + 1) * kTcKeys > ctx;
                 const uint32_t sees = masked ? rows_that_see(pi, key0 + k * kTcKeys + t, a.G, a.bt.n) : 0xFFFFFFFFu;
-                float x[NR];   // score - maximum
-                auto scores = [&](bool shifted) {
-                    uint32_t raw[32];
-                    tmem_ld32(colS, raw);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int r = 0; r < NR; r += 4) {
-                        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (shifted) m = *reinterpret_cast<const float4 *>(shift + r);
-                        f2_unpack(f2_fma(f2_from_u32x2(raw[r], raw[r + 1]), c2, f2_pack(m.x, m.y)), x[r], x[r + 1]);
-                        f2_unpack(f2_fma(f2_from_u32x2(raw[r + 2], raw[r + 3]), c2, f2_pack(m.z, m.w)), x[r + 2], x[r + 3]);
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int r = 0; r < NR; ++r)
-                            if (!((sees >> r) & 1u)) x[r] = -INFINITY;
-                    }
-                };
-                uint32_t grow = 1;   // the first tile sets the maxima
-                if (k > begin) {
-                    scores(true);
-                    float over = x[0];
-#pragma unroll
-                    for (int r = 1; r < NR; ++r) over = fmaxf(over, x[r]);
-                    asm volatile(
-                        "{\n\t.reg .pred p, q;\n\tsetp.gt.f32 p, %1, 0f41000000;\n\t"
-                        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                        : "=r"(grow)
-                        : "f"(over), "r"(1 + gr)
-                        : "memory");
-                }
                 // the group's previous product has read the weights and written the output
                 if (u > 0) wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
                 __syncwarp();
                 tc_fence_after();
-                if (grow) {
-                    scores(false);
+                // The scores less their maxima (step 0); where one passes 2^8, and on the group's first tile, the scores as they are
+                // for new maxima (1), then less those (2).  One copy of the code serves all three.
+                float x[NR];
+#pragma unroll 1
+                for (int step = k > begin ? 0 : 1; step < 3; ++step) {
+                    {
+                        const float *less = step == 1 ? ms->zero : shift;
+                        uint32_t raw[32];
+                        tmem_ld32(colS, raw);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int r = 0; r < NR; r += 4) {
+                            const float4 m = *reinterpret_cast<const float4 *>(less + r);
+                            f2_unpack(f2_fma(f2_from_u32x2(raw[r], raw[r + 1]), c2, f2_pack(m.x, m.y)), x[r], x[r + 1]);
+                            f2_unpack(f2_fma(f2_from_u32x2(raw[r + 2], raw[r + 3]), c2, f2_pack(m.z, m.w)), x[r + 2], x[r + 3]);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int r = 0; r < NR; ++r)
+                                if (!((sees >> r) & 1u)) x[r] = -INFINITY;
+                        }
+                    }
+                    if (step == 2) break;
+                    if (step == 0) {
+                        float over = x[0];
+#pragma unroll
+                        for (int r = 1; r < NR; ++r) over = fmaxf(over, x[r]);
+                        uint32_t grow;
+                        asm volatile(
+                            "{\n\t.reg .pred p, q;\n\tsetp.gt.f32 p, %1, 0f41000000;\n\t"
+                            "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                            : "=r"(grow)
+                            : "f"(over), "r"(1 + gr)
+                            : "memory");
+                        if (!grow) break;
+                        continue;
+                    }
                     ms->top[gr][wl][lane] = reduce_rows(x, lane, [](float p, float q) { return fmaxf(p, q); });
                     group_sync();
                     if (wl == 0) {
@@ -205,17 +211,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
 #pragma unroll
                         for (int r = 0; r < NR / 2; ++r) l[r] = f2_mul(l[r], *reinterpret_cast<const f32x2 *>(alpha + 2 * r));
 #pragma unroll 1
-                        for (int j = 0; j < 64; j += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(colO + j, o);
+                        for (int j = 0; j < 64; j += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(colO + j, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
-                            tmem_st32(colO + j, o);
+                            for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[(j & 16) + r]);
+                            tmem_st16(colO + j, o);
                         }
                         tc_wait_st();
                     }
-                    scores(true);
                 }
 #pragma unroll
                 for (int q = 0; q < NR / 8; ++q) {   // eight rows: one 16-byte chunk of high parts and one of low parts

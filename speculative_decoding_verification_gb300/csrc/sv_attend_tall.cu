@@ -157,39 +157,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                             }
                         }
                     }
-                    // The scores' second half stays in registers, the first is read twice: the weights go where the scores were, in
-                    // the order 0 (columns 0-15 and 64-79), 1, 2, 3 of 32 scores each.
-                    uint32_t x[32], hold[64];
                     float top[4] = {m_used, -INFINITY, -INFINITY, -INFINITY};
-                    auto mask32 = [&](uint32_t *y, uint32_t v) {
+                    auto mask32 = [&](uint32_t *y, int q) {
                         if (masked) {
+                            uint32_t v = vis[0];
+                            if (q == 1) v = vis[1];
+                            if (q == 2) v = vis[2];
+                            if (q == 3) v = vis[3];
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 if (!((v >> j) & 1u)) y[j] = 0xFF800000u;   // -inf
                         }
                     };
-                    auto max32 = [&](const uint32_t *y) {
+                    // Scores are read twice, 32 at a time, for the maximum and for the weights; the loops stay rolled for the sake
+                    // of the instruction cache, which the block's kinds of warps share.
+#pragma unroll 1
+                    for (int q = 0; q < 4; q += 2) {
+                        uint32_t x[32], y[32];
+                        tmem_ld32(colS + q * 32, x);
+                        tmem_ld32(colS + q * 32 + 32, y);
+                        tc_wait_ld();
+                        mask32(x, q);
+                        mask32(y, q + 1);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
+                        for (int j = 0; j < 32; j += 4) {
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                top[u] = fmaxf(top[u], fmaxf(__uint_as_float(y[j + 2 * u]), __uint_as_float(y[j + 2 * u + 1])));
+                            for (int u = 0; u < 4; ++u) top[u] = fmaxf(top[u], fmaxf(__uint_as_float(x[j + u]), __uint_as_float(y[j + u])));
                         }
-                    };
-                    tmem_ld32(colS + 64, hold);
-                    tmem_ld32(colS + 96, hold + 32);
-                    tmem_ld32(colS + 32, x);
-                    tc_wait_ld();
-                    mask32(hold, vis[2]);
-                    mask32(hold + 32, vis[3]);
-                    mask32(x, vis[1]);
-                    max32(x);
-                    tmem_ld32(colS, x);
-                    max32(hold);
-                    max32(hold + 32);
-                    tc_wait_ld();
-                    mask32(x, vis[0]);
-                    max32(x);
+                    }
                     const float m_new = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     // The output is rescaled only when the maximum has grown by more than 2^8: weights up to 2^8 are as
                     // exact as those up to 1, and most tiles then leave the output alone.
@@ -214,31 +209,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     const f32x2 c2 = f2_pack(c, c), s2 = f2_pack(-shift, -shift);
                     const f32x2 minus1 = f2_pack(-1.0f, -1.0f);
                     f32x2 sum[2] = {f2_pack(l, 0.0f), f2_pack(0.0f, 0.0f)};
-                    auto weights = [&](const uint32_t *y, int q) {
-                        uint32_t p[16], r[16];
+                    // A chunk's weights go where its scores were: upper parts, then lower ones.
+                    uint32_t x[32];
+                    tmem_ld32(colS, x);
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t p[32];
+                        tc_wait_ld();
+                        mask32(x, q);
 #pragma unroll
                         for (int u = 0; u < 16; ++u) {
-                            const f32x2 e = f2_ex2(f2_fma(f2_from_u32x2(y[2 * u], y[2 * u + 1]), c2, s2));
+                            const f32x2 e = f2_ex2(f2_fma(f2_from_u32x2(x[2 * u], x[2 * u + 1]), c2, s2));
                             sum[u & 1] = f2_add(sum[u & 1], e);
                             p[u] = bf16_pair(e);
-                            r[u] = bf16_pair(f2_fma(f2_from_bf16x2(p[u]), minus1, e));
+                            p[16 + u] = bf16_pair(f2_fma(f2_from_bf16x2(p[u]), minus1, e));
                         }
-                        tmem_st16(colS + q * 16, p);
-                        tmem_st16(colS + 64 + q * 16, r);
-                    };
-                    weights(x, 0);
-                    tmem_ld32(colS + 32, x);
-                    tc_wait_ld();
-                    mask32(x, vis[1]);
-                    weights(x, 1);
-                    if (!(own && masked)) {   // there the output may have to be touched before any product
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ms->p_half[st]);
+                        if (q < 3) tmem_ld32(colS + q * 32 + 32, x);
+                        tmem_st32(colS + q * 32, p);
+                        if (q == 1 && !(own && masked)) {   // there the output may have to be touched before any product
+                            tc_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&ms->p_half[st]);
+                        }
                     }
-                    weights(hold, 2);
-                    weights(hold + 32, 3);
                     l = f2_sum(f2_add(sum[0], sum[1]));
                     tc_wait_st();
                     if (own && masked) {
@@ -254,7 +248,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                             while (f) {
                                 const int b = __ffs(f) - 1, j = q * 32 + b;
                                 f &= f - 1;
-                                const uint32_t pw = tmem_ld1(colS + j / 2), rw = tmem_ld1(colS + 64 + j / 2);
+                                const uint32_t at = colS + (j & ~31) + (j & 31) / 2, pw = tmem_ld1(at), rw = tmem_ld1(at + 16);
                                 tc_wait_ld();
                                 const float w = j & 1 ? bf16_hi(pw) + bf16_hi(rw) : bf16_lo(pw) + bf16_lo(rw);
                                 const bool sees = (mine >> b) & 1u;
@@ -453,7 +447,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                             for (int part = 0; part < 2; ++part)
 #pragma unroll
                                 for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                                    mma_ts(o, w + part * 64 + kk * 8, v + kk * (2048 >> 4), shape_o, 1u);
+                                    mma_ts(o, w + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, v + kk * (2048 >> 4), shape_o, 1u);
                             if (half) {
                                 if (!two || s == 1) mma_commit(&fd->kv_empty[stage]);
                                 if (n + 2 >= jobs) mma_commit(&ms->o_full[s]);
