@@ -63,9 +63,9 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     const int rg = tid / S::TPR, tx = tid % S::TPR;
     const int cx = tx % S::CG, ks = S::KS > 1 ? tx / S::CG : 0;
     Piece p;
-    for (int pos = w.pos, first = 1;; first = 0) {
+    for (int first = 1;; first = 0) {
         const bool more = w.next(a, p);
-        if (first && tid == 0) leave_tail(a, p, more, pos, w.total);
+        if (first && tid == 0) leave_tail(a, p, more, w.total);
         if (!more) break;
         const int m0 = p.t * TM, h = p.h;
         const int32_t *table = a.bt.page_table + p.g.table * a.bt.table_pitch;
@@ -291,8 +291,10 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     }
 }
 
-// Adds the pieces of one row, a warp: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over n pieces, in order; slot_of(p) is
-// piece p's slot.  Lanes take the pieces' maxima and sums, then the row's elements.
+constexpr size_t kNoSlot = ~(size_t)0;   // a block whose range holds no tile of the unit
+
+// Adds the pieces of one row, a warp: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over n blocks, in order; slot_of(p) is
+// the p-th one's slot.  Lanes take the pieces' maxima and sums, then the row's elements.
 template <int ES, class F>
 __device__ __forceinline__ void join_row(const AttendArgs &a, int row, int qh, int n, int lane, F slot_of) {
     const int D = a.c.head_dim, D4 = D / 4;
@@ -300,8 +302,8 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, int row, int qh, i
     float4 o[2] = {};
     for (int base = 0; base < n; base += 32) {
         const int p = base + lane;
-        const size_t slot = slot_of(p < n ? p : n - 1);
-        const float2 ml = p < n ? a.part_ml[slot] : make_float2(-INFINITY, 0.0f);
+        const size_t slot = p < n ? slot_of(p) : kNoSlot;
+        const float2 ml = slot != kNoSlot ? a.part_ml[slot] : make_float2(-INFINITY, 0.0f);
         float top = ml.y == 0.0f ? -INFINITY : ml.x;   // a piece whose tokens the row did not see adds nothing
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
@@ -361,7 +363,10 @@ __global__ void __launch_bounds__(256) k_attend_join_tails(const AttendArgs a) {
     const int lane = threadIdx.x & 31, m = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (m >= t.vr || t.pieces == 0) return;
     const int i = (t.m0 + m) / a.G, g = t.m0 + m - i * a.G;
-    join_row<ES>(a, t.r0 + i, t.h * a.G + g, t.pieces, lane, [&](int p) { return (size_t)t.slot + m + (size_t)p * a.geo.TM; });
+    const Ranges r = ranges_of(t.total, a.geo);
+    join_row<ES>(a, t.r0 + i, t.h * a.G + g, t.pieces, lane, [&](int p) {
+        return block_has(r, t.c0 + p, t.at, t.cost, t.tiles) ? (size_t)t.slot + m + (size_t)p * a.geo.TM : kNoSlot;
+    });
 }
 
 // With prefixes: every row adds those of its group's prefix, then its own.  A block takes kJoinRows packed rows of one
@@ -371,31 +376,28 @@ constexpr int kJoinRows = 8;
 struct JoinSeg {
     Seg g;
     Ranges r;
-    int first, kt;   // the key head's first tile; tiles of a unit (not chain)
+    int first;   // the key head's place
 };
 
 __device__ __forceinline__ void join_seg(const AttendArgs &a, const AttendGeo &geo, int s, int h, JoinSeg *j) {
-    j->r = ranges_of(geo.seg_off[geo.s1 - geo.s0], geo.blocks);
+    j->r = ranges_of(geo.seg_off[geo.s1 - geo.s0], geo);
     j->g = seg_of(a, geo, s, false);
-    j->first = geo.seg_off[s - geo.s0] + seg_head_tiles(a, geo, j->g) * h;
-    j->kt = j->g.tiles_m > 0 ? seg_tiles(a, geo, j->g, 0) : 0;
+    j->first = geo.seg_off[s - geo.s0] + units_before(a, geo, j->g, j->g.tiles_m) * h;
 }
 
-// Blocks [c0, c1] that hold pieces of the unit with row tile t; c1 < c0: none.
-__device__ __forceinline__ void join_blocks(const AttendArgs &a, const AttendGeo &geo, const JoinSeg &j, int t, int &c0, int &c1) {
-    c0 = 0;
-    c1 = -1;
-    int kt = j.kt;
-    int first = j.first;
-    if (!j.g.chain) {
-        first += t * kt;
-    } else if (t > 0) {
-        for (int u = 0; u < t; ++u) first += seg_tiles(a, geo, j.g, u);
-        kt = seg_tiles(a, geo, j.g, t);
-    }
-    if (kt <= 0 || j.r.parts == 0) return;
-    c0 = block_of_tile(j.r, first);
-    c1 = block_of_tile(j.r, first + kt - 1);
+// The unit with row tile t: its tiles and the blocks [c0, c1] that may hold pieces of it; c1 < c0: none.
+struct JoinUnit {
+    int at, cost, tiles, c0, c1;
+};
+
+__device__ __forceinline__ JoinUnit join_unit(const AttendArgs &a, const AttendGeo &geo, const JoinSeg &j, int t) {
+    JoinUnit u{0, 1, seg_tiles(a, geo, j.g, t), 0, -1};
+    if (u.tiles <= 0 || j.r.parts == 0) return u;
+    u.at = j.first + units_before(a, geo, j.g, t) + geo.unit_cost;
+    u.cost = tile_cost(geo, j.g, t);
+    u.c0 = block_of_place(j.r, u.at);
+    u.c1 = block_of_place(j.r, u.at + (u.tiles - 1) * u.cost);
+    return u;
 }
 
 template <int ES>
@@ -415,19 +417,22 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a, const A
     for (int mm = start + wp; mm < stop; mm += 8) {
         const int i = mm / a.G, row = jo.g.r0 + i, qh = h * a.G + mm - i * a.G;
         const int to = mm / own.TM;
-        int o0, o1, p0 = 0, p1 = -1;
-        join_blocks(a, own, jo, to, o0, o1);
-        if (o0 == o1 && seg_alone(jo.g)) continue;   // written by its piece
+        const JoinUnit uo = join_unit(a, own, jo, to);
+        if (uo.c0 == uo.c1 && seg_alone(jo.g)) continue;   // written by its piece
+        JoinUnit up{0, 1, 0, 0, -1};
         size_t sp = 0;
         if (row >= jp.g.r0 && row < jp.g.r0 + jp.g.n) {
             const int mp = (row - jp.g.r0) * a.G + mm - i * a.G, t = mp / prefix.TM;
-            join_blocks(a, prefix, jp, t, p0, p1);
+            up = join_unit(a, prefix, jp, t);
             sp = unit_slot(a, prefix, jp.g, true, h, t) + (mp - t * prefix.TM);
         }
         const size_t so = unit_slot(a, own, jo.g, false, h, to) + (mm - to * own.TM);
-        const int np = p1 - p0 + 1;
-        join_row<ES>(a, row, qh, np + (o1 - o0 + 1), lane, [&](int p) {
-            return p < np ? sp + (size_t)(p0 + p) * prefix.TM : so + (size_t)(o0 + p - np) * own.TM;
+        const int np = up.c1 - up.c0 + 1;
+        join_row<ES>(a, row, qh, np + (uo.c1 - uo.c0 + 1), lane, [&](int p) {
+            const bool pre = p < np;
+            const int c = pre ? up.c0 + p : uo.c0 + p - np;
+            if (!(pre ? block_has(jp.r, c, up.at, up.cost, up.tiles) : block_has(jo.r, c, uo.at, uo.cost, uo.tiles))) return kNoSlot;
+            return pre ? sp + (size_t)c * prefix.TM : so + (size_t)c * own.TM;
         });
     }
 }
@@ -450,6 +455,8 @@ static cudaError_t run_f32(AttendArgs &a, cudaStream_t stream) {
     if (prepare_kernel((const void *)k_attend_f32<ES, DP, TM>, kAttThreads, S::BYTES) < 1) return cudaErrorInvalidConfiguration;
     a.geo.TM = TM;
     a.geo.TK = S::TK;
+    a.geo.tile_cost = a.geo.tall_cost = 1;
+    a.geo.unit_cost = 0;
     k_attend_f32<ES, DP, TM><<<a.geo.blocks, kAttThreads, S::BYTES, stream>>>(a);
     return cudaGetLastError();
 }
@@ -540,7 +547,7 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     a.part = reinterpret_cast<float *>(w + pl.off_part);
     int *seg = reinterpret_cast<int *>(w + pl.off_seg);
     const int blocks = di.sms < kAttBlocks ? di.sms : kAttBlocks;
-    const AttendGeo all{0, n_groups + batch->B, 0, 0, blocks, seg, 0};
+    const AttendGeo all{0, n_groups + batch->B, 0, 0, blocks, 1, 1, 0, seg, 0};
     AttendGeo prefix = all, own = all;
     cudaError_t e = cudaSuccess;
     // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.

@@ -6,8 +6,10 @@
 // q_heads / kv_heads that share it, so that keys are read once for all of them.
 //
 // Units and tiles.  A unit is (segment, key/value head, tile of TM packed rows); it walks its keys in tiles of TK.
-// All tiles of all units, in order, are cut into one equal range a block, whatever the lengths are: a block's
-// range starts and ends inside units.  The part of a unit in one block is a piece; it leaves its running
+// All tiles of all units, in order, are cut into one range of equal cost a block, whatever the lengths are: a block's
+// range starts and ends inside units.  Costs are small whole numbers: a tile's (more where a row tile is more than half full
+// and the kernel works on its halves in turn) and a unit's own, for setting it up and writing it out.  The part of a
+// unit in one block is a piece; it leaves its running
 // maximum, sum and weighted values in the workspace, and k_attend_join adds a row's pieces in order.  A unit
 // that is one piece and the only one of its rows writes its output itself.
 //
@@ -23,15 +25,18 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // A unit cut by the ranges of several blocks, left by the block that ends it (only its first piece can): without prefixes
 // these are all that has to be joined.
 struct AttendTail {
-    long long slot;   // of the first piece; the next ones follow TM slots apart
-    int pieces;       // 0: none
+    long long slot;         // of the first piece; the next ones follow TM slots apart
+    int c0, pieces;         // the first piece's block; blocks up to the last's (0: none)
+    int at, cost, tiles;    // place of the unit's first tile, cost of a tile, tiles
+    int total;              // cost of the launch
     int r0, m0, vr, h;
 };
 
-// What one launch covers and how it cuts it: segments [s0, s1), row and key tiles, blocks.
+// What one launch covers and how it cuts it: segments [s0, s1), row and key tiles, blocks, costs.
 struct AttendGeo {
     int s0, s1, TM, TK, blocks;
-    int *seg_off;         // [s1 - s0 + 1] first tile of each segment, in the unit order
+    int tile_cost, tall_cost, unit_cost;   // of a key tile, of one for more than TM / 2 rows, of a unit
+    int *seg_off;         // [s1 - s0 + 1] place of each segment, in the unit order
     size_t slot0;         // its first workspace slot
 };
 
@@ -135,10 +140,21 @@ __device__ __forceinline__ int seg_tiles(const AttendArgs &a, const AttendGeo &g
     return (seg_end(a, geo, g, t) - g.key0 + geo.TK - 1) / geo.TK;
 }
 
-__device__ __forceinline__ int seg_head_tiles(const AttendArgs &a, const AttendGeo &geo, const Seg &g) {
-    if (!g.chain) return g.tiles_m * seg_tiles(a, geo, g, 0);
+// Cost of a key tile of row tile t, and of the unit.
+__device__ __forceinline__ int tile_cost(const AttendGeo &geo, const Seg &g, int t) {
+    return 2 * min(geo.TM, g.packed - t * geo.TM) > geo.TM ? geo.tall_cost : geo.tile_cost;
+}
+__device__ __forceinline__ int unit_span(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+    const int kt = seg_tiles(a, geo, g, t);
+    return kt > 0 ? geo.unit_cost + kt * tile_cost(geo, g, t) : 0;
+}
+
+// Place of row tile t among a key head's units (t = tiles_m: the cost of all).
+__device__ __forceinline__ int units_before(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+    if (t <= 0) return 0;
+    if (!g.chain) return (t - 1) * unit_span(a, geo, g, 0) + unit_span(a, geo, g, t - 1);   // all but the last are full
     int n = 0;
-    for (int t = 0; t < g.tiles_m; ++t) n += seg_tiles(a, geo, g, t);
+    for (int u = 0; u < t; ++u) n += unit_span(a, geo, g, u);
     return n;
 }
 
@@ -148,14 +164,14 @@ __device__ __forceinline__ size_t unit_slot(const AttendArgs &a, const AttendGeo
     return geo.slot0 + own + (size_t)g.r0 * a.q_heads + (size_t)h * g.packed + (size_t)t * geo.TM;
 }
 
-// Ranges are those of the first range_blocks blocks, so that none is empty; the first total % parts of them have one tile more.
+// Ranges of equal cost, the first `more` one longer, of as many blocks as there is a tile's cost for each.
 struct Ranges {
     int parts, each, more;
 };
 
-__device__ __forceinline__ Ranges ranges_of(int total, int blocks) {
+__device__ __forceinline__ Ranges ranges_of(int total, const AttendGeo &geo) {
     Ranges r;
-    r.parts = min(total, blocks);
+    r.parts = total > 0 ? max(1, min(total / geo.tile_cost, geo.blocks)) : 0;
     r.each = r.parts > 0 ? total / r.parts : 0;
     r.more = total - r.each * r.parts;
     return r;
@@ -163,10 +179,19 @@ __device__ __forceinline__ Ranges ranges_of(int total, int blocks) {
 
 __device__ __forceinline__ int range_start(const Ranges &r, int c) { return c * r.each + min(c, r.more); }
 
-// The block whose range holds tile x.
-__device__ __forceinline__ int block_of_tile(const Ranges &r, int x) {
+// The block whose range holds place x.
+__device__ __forceinline__ int block_of_place(const Ranges &r, int x) {
     const int split = r.more * (r.each + 1);
     return x < split ? x / (r.each + 1) : r.more + (x - split) / r.each;
+}
+
+// First of a unit's tiles (the first at place `at`, `cost` each) at or after place x.
+__device__ __forceinline__ int tile_from(int at, int cost, int tiles, int x) {
+    return x <= at ? 0 : min(tiles, (x - at + cost - 1) / cost);
+}
+// Whether block c holds any.
+__device__ __forceinline__ bool block_has(const Ranges &r, int c, int at, int cost, int tiles) {
+    return tile_from(at, cost, tiles, range_start(r, c)) < tile_from(at, cost, tiles, range_start(r, c + 1));
 }
 
 // A row's output is complete in its own piece when no prefix adds to it.
@@ -177,58 +202,65 @@ struct Piece {
     int seg, h, t;      // unit
     int vr;             // packed rows of the unit, the first at t * TM
     int k0, k1, kt;     // tiles of keys [k0, k1) of kt
+    int at, cost;       // place of the unit's first tile, cost of a tile
     int end;            // one past the last token the unit sees
 };
 
-// Walks the pieces of one block's range [pos, stop) of tiles.
+// Walks the pieces of one block's range [pos, stop) of places.
 struct Walk {
     int pos, stop, seg_start, per_head, total, s;
     Seg g;
 
-    __device__ __forceinline__ void open(const AttendArgs &a) {
-        g = seg_of(a, a.geo, s, false);
-        per_head = seg_head_tiles(a, a.geo, g);
-    }
-
     __device__ __forceinline__ bool next(const AttendArgs &a, Piece &p) {
-        if (pos >= stop) return false;
-        while (pos >= seg_start + per_head * a.c.kv_heads) {
-            seg_start += per_head * a.c.kv_heads;
-            ++s;
-            open(a);
-        }
-        const int at = pos - seg_start;
-        p.h = at / per_head;
-        int rem = at - p.h * per_head;
-        p.t = 0;
-        p.kt = seg_tiles(a, a.geo, g, 0);
-        if (!g.chain) {
-            p.t = rem / p.kt;
-            rem -= p.t * p.kt;
-        } else {
-            while (rem >= p.kt) {
-                rem -= p.kt;
-                p.kt = seg_tiles(a, a.geo, g, ++p.t);
+        while (pos < stop) {
+            while (pos >= seg_start + per_head * a.c.kv_heads) {
+                seg_start += per_head * a.c.kv_heads;
+                ++s;
+                g = seg_of(a, a.geo, s, false);
+                per_head = units_before(a, a.geo, g, g.tiles_m);
             }
+            p.h = (pos - seg_start) / per_head;
+            const int head = seg_start + p.h * per_head;   // the key head's place
+            p.t = 0;
+            int unit = head, span = unit_span(a, a.geo, g, 0);
+            if (!g.chain) {
+                p.t = min((pos - head) / span, g.tiles_m - 1);
+                unit += p.t * span;
+                span = unit_span(a, a.geo, g, p.t);
+            } else {
+                while (pos >= unit + span) {
+                    unit += span;
+                    span = unit_span(a, a.geo, g, ++p.t);
+                }
+            }
+            p.kt = seg_tiles(a, a.geo, g, p.t);
+            p.cost = tile_cost(a.geo, g, p.t);
+            p.at = unit + a.geo.unit_cost;
+            p.k0 = tile_from(p.at, p.cost, p.kt, pos);
+            p.k1 = tile_from(p.at, p.cost, p.kt, stop);
+            pos = min(stop, unit + span);
+            if (p.k0 >= p.k1) continue;   // the range holds none of the unit's tiles
+            p.g = g;
+            p.seg = s;
+            p.vr = min(a.geo.TM, g.packed - p.t * a.geo.TM);
+            p.end = seg_end(a, a.geo, g, p.t);
+            return true;
         }
-        p.g = g;
-        p.seg = s;
-        p.vr = min(a.geo.TM, g.packed - p.t * a.geo.TM);
-        p.k0 = rem;
-        p.k1 = min(p.kt, rem + (stop - pos));
-        p.end = seg_end(a, a.geo, g, p.t);
-        pos += p.k1 - p.k0;
-        return true;
+        return false;
     }
 };
 
-// Block c's tail, from its first piece p (`more` false: the range is empty), whose first tile was at `pos` of `total`.
-__device__ __forceinline__ void leave_tail(const AttendArgs &a, const Piece &p, bool more, int pos, int total) {
+// Block c's tail, from its first piece p (`more` false: it has none).
+__device__ __forceinline__ void leave_tail(const AttendArgs &a, const Piece &p, bool more, int total) {
     AttendTail t{};
     if (more && p.k0 > 0 && p.k1 == p.kt) {
-        const int c0 = block_of_tile(ranges_of(total, a.geo.blocks), pos - p.k0);
-        t.pieces = (int)blockIdx.x - c0 + 1;
-        t.slot = (long long)(unit_slot(a, a.geo, p.g, p.seg < a.n_groups, p.h, p.t) + (size_t)c0 * a.geo.TM);
+        t.c0 = block_of_place(ranges_of(total, a.geo), p.at);
+        t.pieces = (int)blockIdx.x - t.c0 + 1;
+        t.slot = (long long)(unit_slot(a, a.geo, p.g, p.seg < a.n_groups, p.h, p.t) + (size_t)t.c0 * a.geo.TM);
+        t.at = p.at;
+        t.cost = p.cost;
+        t.tiles = p.kt;
+        t.total = total;
         t.r0 = p.g.r0;
         t.m0 = p.t * a.geo.TM;
         t.vr = p.vr;
@@ -237,9 +269,9 @@ __device__ __forceinline__ void leave_tail(const AttendArgs &a, const Piece &p, 
     a.tails[blockIdx.x] = t;
 }
 
-// Block-wide: the total of tiles and, for this block's range, where its walk starts.  Each thread takes a
-// run of consecutive segments; warp_sum has THREADS / 32 places.  Block 0 leaves the segments' offsets for the join and reports bad
-// input, a total past 2^30 tiles among it (nothing is computed then).
+// Block-wide: the total cost and, for this block's range, where its walk starts.  Each thread takes a
+// run of consecutive segments; warp_sum has THREADS / 32 places.  Block 0 leaves the segments' places for the join and reports bad
+// input, a total past 2^30 among it (nothing is computed then).
 template <int THREADS>
 __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long long *warp_sum) {
     const AttendGeo &geo = a.geo;
@@ -251,7 +283,7 @@ __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long lo
     int per = 0;
     for (int s = s0; s < s1; ++s) {
         g = seg_of(a, geo, geo.s0 + s, blockIdx.x == 0);
-        per = seg_head_tiles(a, geo, g);
+        per = units_before(a, geo, g, g.tiles_m);
         mine += (long long)per * a.c.kv_heads;
     }
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -274,7 +306,7 @@ __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long lo
         sum = 0;
     }
     const int total = (int)sum;
-    const Ranges r = ranges_of(total, geo.blocks);
+    const Ranges r = ranges_of(total, geo);
     const int c = blockIdx.x, pos = c < r.parts ? range_start(r, c) : total, stop = c < r.parts ? range_start(r, c + 1) : total;
     if (threadIdx.x == 0) {
         w->total = total;
@@ -285,7 +317,7 @@ __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long lo
         for (int s = s0; s < s1; ++s) {
             if (each > 1) {   // with one segment a thread, g and per are still those
                 g = seg_of(a, geo, geo.s0 + s, false);
-                per = seg_head_tiles(a, geo, g);
+                per = units_before(a, geo, g, g.tiles_m);
             }
             const int n = total > 0 ? per * a.c.kv_heads : 0;
             if (pos < stop && pos >= at && pos < at + n) {

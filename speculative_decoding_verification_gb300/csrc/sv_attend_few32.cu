@@ -71,9 +71,9 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
     }
     const int step_pages = 64 / psize, step_slots = 64 - step_pages * psize;   // a tile further in the page table
     Piece p;
-    for (int pos = w.pos, first = 1;; first = 0) {
+    for (int first = 1;; first = 0) {
         const bool more = w.next(a, p);
-        if (first && tid == 0) leave_tail(a, p, more, pos, w.total);
+        if (first && tid == 0) leave_tail(a, p, more, w.total);
         if (!more) break;
         const int h = p.h;
         const int32_t *table = a.bt.page_table + p.g.table * a.bt.table_pitch;
@@ -249,6 +249,8 @@ template <int R>
 cudaError_t run_few32(AttendArgs &a, cudaStream_t stream) {
     a.geo.TM = R;
     a.geo.TK = 64;
+    a.geo.tile_cost = a.geo.tall_cost = 1;
+    a.geo.unit_cost = 1;
     const size_t bytes = (size_t)kWarps32 * 32 * a.c.head_dim * 4;
     const int resident = prepare_kernel((const void *)k_attend_few32<R>, kThreads32, bytes);
     if (resident < 1) return cudaErrorInvalidConfiguration;

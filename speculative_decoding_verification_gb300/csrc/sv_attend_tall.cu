@@ -486,6 +486,9 @@ cudaError_t run_tall(AttendArgs &a, bool negate, cudaStream_t stream) {
     if (prepare_kernel((const void *)k_attend_tall<DP>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
     a.geo.TM = kTallRows;
     a.geo.TK = kTcKeys;
+    a.geo.tile_cost = 2;   // one row tile, the streams taking its key tiles in turn
+    a.geo.tall_cost = 3;
+    a.geo.unit_cost = 8;   // setting a piece up and writing it out
     k_attend_tall<DP><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, tc_args(a.c, mma_shape(128, false, false, negate, false)));
     return cudaGetLastError();
 }
