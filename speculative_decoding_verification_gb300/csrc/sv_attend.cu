@@ -40,7 +40,8 @@ struct F32Shape {
 
 // Scores, softmax and weighted sum in float32 FMA, a tile of TM packed rows by TK keys at a time.  Threads hold
 // 4 rows by NK keys of the scores and 4 rows by 4 NC columns of the output; keys and values are
-// double buffered with asynchronous copies.
+// double buffered with asynchronous copies.  For float32 with more rows than few32 takes and for bf16 heads wider than 128: the
+// FMA rate and, with few rows, the four block barriers a tile bound it.
 template <int ES, int DP, int TM>
 __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) {
     using S = F32Shape<ES, DP, TM>;
@@ -413,8 +414,9 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a, const A
     __syncthreads();
     const JoinSeg &jo = sj[1], &jp = sj[0];
     const int start = ragged ? (unit - jo.g.r0) * a.G : blockIdx.y * kJoinRows;
-    const int stop = start < 0 ? start : min(jo.g.packed, start + (ragged ? a.G : kJoinRows));
-    for (int mm = start + wp; mm < stop; mm += 8) {
+    const int stop = start < 0 ? start : ragged ? min(jo.g.packed, start + a.G) : jo.g.packed;
+    const int stride = ragged ? 8 : (int)gridDim.y * kJoinRows;   // rows go kJoinRows (ragged: a.G) at a time, a warp each
+    for (int mm = start + wp; mm < stop; mm += stride) {
         const int i = mm / a.G, row = jo.g.r0 + i, qh = h * a.G + mm - i * a.G;
         const int to = mm / own.TM;
         const JoinUnit uo = join_unit(a, own, jo, to);
@@ -444,7 +446,7 @@ cudaError_t launch_attend_join(const AttendArgs &a, const AttendGeo &prefix, con
                        : launch_pdl(k_attend_join_tails<2>, grid, dim3(256), 0, stream, a);
     }
     const dim3 grid = a.bt.row_start ? dim3((unsigned)(a.bt.rows * a.c.kv_heads))
-                                     : dim3((unsigned)(a.bt.B * a.c.kv_heads), (unsigned)div_up((long long)a.bt.n * a.G, kJoinRows));
+                                     : dim3((unsigned)(a.bt.B * a.c.kv_heads), (unsigned)min(65535LL, ((long long)a.bt.n * a.G + kJoinRows - 1) / kJoinRows));
     return es == 4 ? launch_pdl(k_attend_join<4>, grid, dim3(256), 0, stream, a, prefix, own)
                    : launch_pdl(k_attend_join<2>, grid, dim3(256), 0, stream, a, prefix, own);
 }
@@ -513,8 +515,8 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     const int es = elem_size((sv_dtype)cache->dtype);
     if (batch->rows > 0 && (q == nullptr || out == nullptr)) return SV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !strides16(es, q_row_stride, q_head_stride) ||
-        !strides16(es, out_row_stride, out_head_stride) || (int64_t)batch->rows * q_heads > INT32_MAX ||
-        (int64_t)batch->B * cache->kv_heads > INT32_MAX || (n_groups > 0 && batch->row_start == nullptr && (int64_t)batch->n * q_heads > 65535LL * kJoinRows))
+        !strides16(es, out_row_stride, out_head_stride) || (int64_t)batch->rows * q_heads > (1 << 30) ||
+        (int64_t)batch->B * cache->kv_heads > INT32_MAX)
         return SV_ERR_INVALID_ARG;
     const AttendPlan pl = plan_attend(batch->rows, q_heads, cache->head_dim, batch->B, n_groups);
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.bytes) return SV_ERR_WORKSPACE;
@@ -550,8 +552,12 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     const AttendGeo all{0, n_groups + batch->B, 0, 0, blocks, 1, 1, 0, seg, 0};
     AttendGeo prefix = all, own = all;
     cudaError_t e = cudaSuccess;
-    // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.
-    // Float32 with up to 8 rows and no prefix to share goes through registers: a tile of 16 rows or more would be mostly empty.
+    // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.  Up to 32 packed rows of a
+    // sequence's own tokens go with the tokens along the tile's rows (512 x 6 rows over 1-2k tokens: 545 us, against 1,040 in the tall
+    // kernel).  Beside prefixes too, in a launch of their own: in the prefixes' launch 64 x 6 rows behind 32k tokens would take 266 us
+    // instead of 293, but twice as long where own tokens outweigh the prefix, and the lengths are on the device.
+    // Float32 with up to 8 rows and no prefix to share: a tile of 16 rows or more would be mostly empty (64 single tokens of 4 rows
+    // 111 us, against 360).
     if (es == 4 && cache->head_dim <= 128 && n_groups == 0 && (int64_t)batch->n * a.G <= kFewRows32) {
         a.geo = all;
         e = launch_attend_few32(a, s);

@@ -7,7 +7,9 @@
 // (31 shuffles, after which lane j R + r has that of token j and row r), each lane does one exponential, and the weights are handed
 // round for the weighted sum.  Warps keep maxima, sums and outputs of their own and are added at the piece's end.
 //
-// What bounds it: issue slots as much as memory.
+// What bounds it: issue slots as much as memory (725 instructions a warp and 8 tokens of 4 rows, 62% of slots used).  64 sequences of
+// up to 8,192 tokens, 3 key heads of 80, 4 rows: 111 us, 4.6 TB/s or 0.68 of the measured copy bandwidth.  With the tiles held in
+// registers instead of copied ahead 176 us, in the kernel for any number of rows 360 us.
 #include <type_traits>
 
 #include "sv_attend.cuh"

@@ -11,6 +11,11 @@
 // Tensor memory (512 columns): scores 2 x 128, the weights over the scores they came from, outputs 2 x 128.
 // Weights.  A weight enters the product with V as two bf16 parts, its rounding and what that left (16 bits in all): one
 // part alone is off by 2^-8, as much as the rounding of the output.
+//
+// What bounds it: a stream's softmax (1,600 cycles a tile of 128 x 128) and its products (1,536: 8 for the scores, 16 for the weighted
+// sum, 64 cycles each) follow one another; the two streams together take 4,060 cycles for a pair of tiles, against 3,077 for the
+// products alone.  64 x 6 rows of 32 heads over a prefix of 32,768 tokens: 213 us, 62% of tensor cycles.  One warp issues for both
+// streams: with a warp a stream their products interleave and each ends later (355 us for the call against 300).
 #include "sv_attend_feed.cuh"
 
 namespace sv {

@@ -17,7 +17,8 @@ struct RopeArgs {
     float magnitude, sign;
 };
 
-// One block a row: its angles once, for all heads.
+// One block a row: its angles once, for all heads.  Memory bounds it: 8,192 rows of 32 heads of 128, bf16, take 24.9 us, 5.4 TB/s or
+// 0.79 of the measured copy bandwidth.  (Loading a thread's first item before the angles cost registers and took 27.2 us.)
 template <int ES, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a) {
     __shared__ float2 cs[SV_KV_MAX_HEAD_DIM / 2];
@@ -46,7 +47,8 @@ struct AppendArgs {
     sv_stats *stats;
 };
 
-// One block a row: the row's depth, its angles, then queries, keys and values as one list of items.
+// One block a row: the row's depth, its angles, then queries, keys and values as one list of items.  512 x 6 rows of 32 + 2 x 8 heads of
+// 128, bf16: 16.3 us, 4.6 TB/s or 0.68 of the measured copy bandwidth; one block of 5 rows 3.1 us.
 template <int ES, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) k_kv_append(const AppendArgs a) {
     __shared__ float2 cs[SV_KV_MAX_HEAD_DIM / 2];
@@ -116,7 +118,7 @@ struct CommitArgs {
     sv_stats *stats;
 };
 
-// One block a (layer, sequence).  Thread t holds one 16-byte column of a slot.  Slot path[j] moves to
+// One block a (layer, sequence): 32 layers x 64 sequences of 8 heads of 128 take 9.1 us, 0.94 of the measured copy bandwidth.  Thread t holds one 16-byte column of a slot.  Slot path[j] moves to
 // slot 1 + j; the path rises, so path[j'] > 1 + j for j' > j and moves in order of j never overwrite
 // a slot that a later move reads.
 __global__ void __launch_bounds__(256) k_kv_commit(const CommitArgs a, int es) {
