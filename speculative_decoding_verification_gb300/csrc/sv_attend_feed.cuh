@@ -79,10 +79,10 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// `bytes` more to come and n arrivals.
-__device__ __forceinline__ void mbar_arrive_expect_tx_n(uint64_t *bar, uint32_t bytes, uint32_t n) {
+// `bytes` more to come, and n arrivals.
+__device__ __forceinline__ void mbar_expect_arrive_n(uint64_t *bar, uint32_t bytes, uint32_t n) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+    if (n) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&x)[4]) {
@@ -126,10 +126,11 @@ __device__ __forceinline__ void scan_values(uint32_t tile, int t, uint32_t *flag
 }
 
 // Keys and values as 4-D tensors (element, head, slot, page) with boxes of 64 elements by box_rows slots, loaded with the
-// 128-byte swizzle; box_rows is 0 where a box could not stay inside a page.
+// 128-byte swizzle.  Where the page size is no multiple of 8 (split), boxes of 8 whose slots lie in two pages are copied by rows;
+// box_rows is 0, and everything goes by rows, where a page has fewer than 8 slots.
 struct TcArgs {
     CUtensorMap k, v;
-    int box_rows;
+    int box_rows, split;
     int page_shift;       // log2(page_size), or -1
     uint32_t shape_s;     // of the score product
 };
@@ -137,9 +138,9 @@ struct TcArgs {
 // The producers' part, a warp of four.  QROWS rows a query tile; query tiles at q_base, stages at kv_base.  Two warps load the keys and
 // two the values; of a pair, each takes 64 elements of all 128 tokens (heads of 128), or 64 tokens.  A warp so waits for one
 // stage a tile and issues its boxes in one go: with the four sharing every stage, 32 tokens each, the producers set the pace.
-template <int DP, int STAGES, int QROWS>
-__device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &a2, Feed *fd, uint32_t q_base, uint32_t kv_base, int wl,
-                                             int lane) {
+template <int DP, int STAGES, int QROWS, bool SPLIT>
+__device__ __forceinline__ void feed_produce_as(const AttendArgs &a, const TcArgs &a2, Feed *fd, uint32_t q_base, uint32_t kv_base, int wl,
+                                                int lane) {
     constexpr int TILE = 128 * DP * 2, HALF = 128 * 128;
     constexpr int ROWS = DP == 128 ? 128 : 64;   // tokens of a warp
     const int D = a.c.head_dim, kv = wl >> 1, sub = wl & 1;
@@ -181,11 +182,34 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
             if (by_box(k)) {
                 const int key = box_key(k), slot = key - page_index(key) * psize;
                 if ((unsigned)pg >= (unsigned)a.c.n_pages && pg != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
-                if (elect_one()) mbar_arrive_expect_tx_n(&fd->kv_full[stage], ROWS * 128, 32);
+                // split: a box that reaches into the next page goes by rows
+                const uint32_t split = SPLIT ? __ballot_sync(0xFFFFFFFFu, lane < boxes && slot + 8 > psize) : 0;
+                if (elect_one()) mbar_expect_arrive_n(&fd->kv_full[stage], (ROWS - 8 * __popc(split)) * 128, split ? 0 : 32);
                 __syncwarp();
                 // a bad page id lies outside the tensor and reads zeros
-                if (lane < boxes) box_load(tile + lane * a2.box_rows * 128, map, &fd->kv_full[stage], col0, h, slot, pg);
+                if (lane < boxes && !((split >> lane) & 1u)) box_load(tile + lane * a2.box_rows * 128, map, &fd->kv_full[stage], col0, h, slot, pg);
                 __syncwarp();
+                if (split) {
+                    int pg2 = 0;
+                    if ((split >> lane) & 1u) {
+                        pg2 = table[page_index(key) + 1];
+                        if ((unsigned)pg2 >= (unsigned)a.c.n_pages) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                    }
+#pragma unroll 1
+                    for (uint32_t left = split; left; left &= left - 1) {
+                        const int b = __ffs(left) - 1, s0 = __shfl_sync(0xFFFFFFFFu, slot, b);
+                        const int p0 = __shfl_sync(0xFFFFFFFFu, pg, b), p1 = __shfl_sync(0xFFFFFFFFu, pg2, b);
+#pragma unroll 1
+                        for (int r = rsub; r < 8; r += 4) {
+                            const bool over = s0 + r >= psize;
+                            const int id = over ? p1 : p0, sl = over ? s0 + r - psize : s0 + r;
+                            const bool ok = (unsigned)id < (unsigned)a.c.n_pages && real;
+                            const int64_t o = id * a.c.page_b + sl * a.c.slot_b + h * a.c.head_b + (col0 + ch * 8) * 2;
+                            cp_async16(tile + (b * 8 + r) * 128 + ((ch ^ r) << 4), src + (ok ? o : 0), ok);
+                        }
+                    }
+                    cp_async_arrive(&fd->kv_full[stage]);
+                }
             } else {
                 // Not unrolled: the block's five kinds of warps share the instruction cache, and these loops laid out in full
                 // cost the whole kernel a seventh of its speed.
@@ -249,6 +273,15 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
     cp_async_wait<0>();   // nothing is in flight when the block ends
 }
 
+// Two copies of the loop: with the code for split boxes in it, pages without them took 595 us instead of 545 (512 x 6 rows over 1-2k
+// tokens; the instruction cache again).
+template <int DP, int STAGES, int QROWS>
+__device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &a2, Feed *fd, uint32_t q_base, uint32_t kv_base, int wl,
+                                             int lane) {
+    if (a2.split) feed_produce_as<DP, STAGES, QROWS, true>(a, a2, fd, q_base, kv_base, wl, lane);
+    else feed_produce_as<DP, STAGES, QROWS, false>(a, a2, fd, q_base, kv_base, wl, lane);
+}
+
 // The walk's part, one warp: describes the pieces, then that there are no more.
 __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2, Feed *fd, Walk w, int lane) {
     uint32_t seq = 0;
@@ -280,7 +313,7 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
                 pi->ctx = p.g.ctx;
                 pi->end = p.end;
                 // a tile that every row sees whole goes as boxes where no box would cross a page
-                pi->box_tiles = a2.box_rows > 0 && p.g.key0 % a2.box_rows == 0 ? ((own ? p.g.ctx : p.end) - p.g.key0) / kTcKeys : 0;
+                pi->box_tiles = a2.box_rows > 0 && (a2.split || p.g.key0 % a2.box_rows == 0) ? ((own ? p.g.ctx : p.end) - p.g.key0) / kTcKeys : 0;
                 pi->k0 = p.k0;
                 pi->k1 = p.k1;
                 pi->seq = seq;
@@ -322,14 +355,15 @@ inline bool cache_map(CUtensorMap *map, char *base, const KvCache &c, int box_ro
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The tensors of a call.  Boxes of up to 64 slots, whole swizzle groups of 8 rows, that never
-// cross a page; other page sizes load by rows.
+// The tensors of a call.  Boxes of up to 64 slots, whole swizzle groups of 8 rows, that never cross a page.  512 x 6 rows over 1-2k
+// tokens: in pages of 8 to 64 slots 541-552 us, of 24 561, of 100 609; copied by rows 816, as pages of fewer than 8 slots are.
 inline TcArgs tc_args(const KvCache &c, uint32_t shape_s) {
     TcArgs t{};
     t.shape_s = shape_s;
     const int ps = c.page_size;
     t.page_shift = (ps & (ps - 1)) == 0 ? __builtin_ctz(ps) : -1;
-    const int rows = ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : ps == 16 || ps == 8 ? ps : 0;
+    const int rows = ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : ps % 16 == 0 ? 16 : ps >= 8 ? 8 : 0;
+    t.split = rows == 8 && ps % 8 != 0;
     if (rows > 0) {
         t.box_rows = rows;
         if (encode_tiled() == nullptr || !cache_map(&t.k, c.k, c, t.box_rows) || !cache_map(&t.v, c.v, c, t.box_rows)) t.box_rows = 0;

@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 ready(&fd->pd_full[it % kRing], (it / kRing) & 1);
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 if (nk <= 0) break;
-                const int rows_from = __shfl_sync(0xFFFFFFFFu, pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
+                const int rows_from = __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
                 const int qs = it & 1;
                 const uint64_t q = smem_operand(sbase + qs * (NR * DP * 2), 16, 1024);

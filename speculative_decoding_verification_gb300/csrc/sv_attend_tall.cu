@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 const bool two = __shfl_sync(0xFFFFFFFFu, pi->vr, 0) > 128;
                 if (nk <= 0) break;
-                const int rows_from = __shfl_sync(0xFFFFFFFFu, pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
+                const int rows_from = __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
                 // Job n: stream n & 1, key tile n / 2 (two row tiles) or n.
                 const int jobs = two ? 2 * nk : nk, shift = two ? 1 : 0;

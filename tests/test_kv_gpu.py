@@ -415,3 +415,35 @@ def test_attend_many_pieces(sv, dtype, B, n, heads, kv, dim, page, tree, pre, lo
     assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
     again, _ = sv.sv_kv_attend(q, c.k, c.v, parents=par.cuda() if tree else None, **c.args, **c.group_args)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("B,n,heads,kv,dim,page,tree,pre,longest", [
+    (24, 6, 16, 4, 128, 100, False, 0, 900),    # groups of 8 tokens, one in 25 of them over two pages
+    (16, 4, 8, 4, 64, 9, False, 0, 700),        # nearly all of them
+    (12, 30, 8, 2, 96, 20, True, 0, 800),       # tall tiles
+    (20, 5, 8, 4, 80, 12, False, 1100, 260),    # prefixes that end inside a page and a group
+    (16, 3, 8, 4, 128, 40, False, 0, 600),      # whole groups, no power of two
+    (16, 3, 8, 4, 128, 7, False, 0, 600),       # pages smaller than a group
+])
+def test_attend_odd_pages(sv, B, n, heads, kv, dim, page, tree, pre, longest):
+    """Page sizes that groups of 8 tokens do not divide into, over whole tiles; a bad page behind a good one is reported and the other
+    sequences stay."""
+    rng = np.random.default_rng(page)
+    ctx = [pre + int(x) for x in rng.integers(longest // 2, longest + 1, B)]
+    groups = [(0, pre), (B // 2, pre)] if pre else None
+    c = Cache(B + page, BF, ctx, n, kv, dim, page, groups=groups)
+    q = blocks(c, 47, B, n, heads, kv, dim, BF)
+    par = random_tree(c.rng, B, n) if tree else None
+    kw = dict(parents=par.cuda() if tree else None, **c.group_args)
+    st = sv.new_stats("cuda")
+    out, lse = sv.sv_kv_attend(q, c.k, c.v, lse=True, stats=st, **kw, **c.args)
+    assert sv.read_stats(st)["status"] == 0
+    rows = [slice(b * n, b * n + n) for b in range(B)]
+    check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), dim ** -0.5, rows, par, [0, 1, B // 2, B - 1])
+    table = c.table.clone()
+    last = B - 1
+    table[last, (ctx[last] - 1) // page] = c.k.shape[0]
+    st = sv.new_stats("cuda")
+    bad, _ = sv.sv_kv_attend(q, c.k, c.v, stats=st, **kw, **dict(c.args, page_table=table.cuda()))
+    assert sv.read_stats(st)["status"] == 1
+    assert torch.equal(bad[:last], out[:last])
