@@ -49,6 +49,7 @@ struct FewShared {
     float top[2][4][NR];              // the warps' maxima of a row, later their sums
     alignas(16) float shift[2][NR];   // minus a row's maximum (of scale * log2(e) * q.k)
     alignas(16) float zero[NR];
+    int64_t to[NR];                   // where a row's output goes
     alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end what the group's output is scaled by
 };
 
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms->p_full[gr]);
             }
-            // ---- the piece's end: thread t has head element t of half of the rows
+            // ---- the piece's end: thread t has head element t
             const int vr = pi->vr, D = a.c.head_dim, qh0 = pi->h * a.G, r0 = pi->r0;
             const bool whole = pi->whole, has1 = k1 - k0 > 1;   // the second group has scored something
             const size_t slot = (size_t)pi->slot;
@@ -306,47 +307,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 ms->alpha[0][lane] = f0 * inv;
                 ms->alpha[1][lane] = f1 * inv;
                 if (lane < vr) {
-                    const int i = lane / a.G, g = lane - i * a.G;
-                    if (!whole) a.part_ml[slot + lane] = make_float2(m, all);
-                    else if (a.lse) a.lse[(size_t)(r0 + i) * a.q_heads + qh0 + g] = all == 0.0f ? -INFINITY : (m + log2f(all)) / kLog2e;
+                    if (!whole) {
+                        a.part_ml[slot + lane] = make_float2(m, all);
+                    } else if (a.lse) {
+                        const int i = lane / a.G, g = lane - i * a.G;
+                        a.lse[(size_t)(r0 + i) * a.q_heads + qh0 + g] = all == 0.0f ? -INFINITY : (m + log2f(all)) / kLog2e;
+                    }
                 }
+            } else if (warp == 4) {   // meanwhile
+                const int i = lane / a.G, g = lane - i * a.G;
+                ms->to[lane] = (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head;
             }
             if (begin < k1) wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
             both_sync();
             tc_fence_after();
-            const int rb = gr * (NR / 2);   // this group's rows
-            float y[NR / 2];
+            // Four rows at a time, the groups taking turns.  Rolled: a piece of one tile goes through all of this once, and the
+            // instructions come from far.
+#pragma unroll 1
+            for (int rb = gr * 4; rb < vr; rb += 8) {
+                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+                for (int g = 0; g < (has1 ? 2 : 1); ++g) {
+                    uint32_t o[4], o2[4];   // the products with the weights' high and low parts
+                    tmem_ld4(base + 128 + g * 64 + rb, o);
+                    tmem_ld4(base + 128 + g * 64 + 32 + rb, o2);
+                    tc_wait_ld();
+                    const float4 f = *reinterpret_cast<const float4 *>(ms->alpha[g] + rb);
+                    y[0] = fmaf(__uint_as_float(o[0]) + __uint_as_float(o2[0]), f.x, y[0]);
+                    y[1] = fmaf(__uint_as_float(o[1]) + __uint_as_float(o2[1]), f.y, y[1]);
+                    y[2] = fmaf(__uint_as_float(o[2]) + __uint_as_float(o2[2]), f.z, y[2]);
+                    y[3] = fmaf(__uint_as_float(o[3]) + __uint_as_float(o2[3]), f.w, y[3]);
+                }
+                if (t < D) {
 #pragma unroll
-            for (int r = 0; r < NR / 2; ++r) y[r] = 0.0f;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (g == 1 && !has1) continue;
-                uint32_t o[16], o2[16];   // the products with the weights' high and low parts
-                tmem_ld16(base + 128 + g * 64 + rb, o);
-                tmem_ld16(base + 128 + g * 64 + 32 + rb, o2);
-                tc_wait_ld();
-#pragma unroll
-                for (int r = 0; r < NR / 2; ++r)
-                    y[r] = fmaf(__uint_as_float(o[r]) + __uint_as_float(o2[r]), ms->alpha[g][rb + r], y[r]);
-            }
-            if (t < D) {
-                if (whole) {
-                    int i = rb / a.G, g = rb - i * a.G;
-#pragma unroll
-                    for (int r = 0; r < NR / 2; ++r) {
-                        if (rb + r < vr) {
-                            store_elem<2>(a.out + (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head + t * 2, y[r]);
-                            if (++g == a.G) {
-                                g = 0;
-                                ++i;
-                            }
-                        }
+                    for (int r = 0; r < 4; ++r) {
+                        if (rb + r >= vr) continue;
+                        if (whole) store_elem<2>(a.out + ms->to[rb + r] + t * 2, y[r]);
+                        else a.part[(slot + rb + r) * D + t] = y[r];
                     }
-                } else {
-                    float *dst = a.part + (slot + rb) * D + t;
-#pragma unroll
-                    for (int r = 0; r < NR / 2; ++r)
-                        if (rb + r < vr) dst[(size_t)r * D] = y[r];
                 }
             }
             tc_fence_before();

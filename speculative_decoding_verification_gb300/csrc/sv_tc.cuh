@@ -107,6 +107,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *x) {
                  "r"(addr)
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld4(uint32_t at, uint32_t (&x)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+}
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
     uint32_t x;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(addr));
