@@ -18,7 +18,7 @@
 //
 // What bounds it: memory.  A tile is 64 KB (heads of 128), 2800 cycles of an SM's share of the measured copy bandwidth; its
 // products take about 700 and its softmax about 1300, which the two groups share.  512 sequences x 6 rows, 8 key heads, 1,024 to
-// 2,048 tokens: 545 us, 6.0 TB/s or 0.89 of the measured copy bandwidth (the tall kernel: 1,040 us).
+// 2,048 tokens: 523 us, 6.3 TB/s or 0.93 of the measured copy bandwidth (the tall kernel: 1,040 us).
 #include "sv_attend_feed.cuh"
 
 namespace sv {
@@ -49,7 +49,7 @@ struct FewShared {
     float top[2][4][NR];              // the warps' maxima of a row, later their sums
     alignas(16) float shift[2][NR];   // minus a row's maximum (of scale * log2(e) * q.k)
     alignas(16) float zero[NR];
-    int64_t to[NR];                   // where a row's output goes
+    int64_t to[2][NR];                // where a row's output goes (the first's, where both groups work on the piece)
     alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end what the group's output is scaled by
 };
 
@@ -128,14 +128,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         const uint32_t prow = sbase + S::OFF_P + gr * S::PBUF + t * (4 * NR);     // this token's weights
         const f32x2 c2 = f2_pack(a.scale_log2, a.scale_log2);
         uint32_t u = 0;   // tiles this group has worked on
+        int rests = 0;    // the group that left the last piece of one tile to the other
         auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + gr) : "memory"); };
-        auto both_sync = [&]() { asm volatile("bar.sync 3, 256;" ::: "memory"); };
         for (int it = 0;; ++it) {
             const PieceInfo *pi = &fd->pd[it % kRing];
             wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
             __syncwarp();
             const int k0 = pi->k0, k1 = pi->k1;
             if (k0 >= k1) break;
+            const bool solo = k1 - k0 == 1;   // one group works on it, the other goes on to the next piece
+            if (solo) {
+                rests ^= 1;
+                if (rests == gr) {
+                    if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
+                    continue;
+                }
+            }
             const int key0 = pi->key0, ctx = pi->ctx;
             {
                 uint32_t zero[32];
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
 #pragma unroll
             for (int r = 0; r < NR / 2; ++r) l[r] = 0;
             float *shift = ms->shift[gr], *alpha = ms->alpha[gr];
-            const int begin = k0 + gr;
+            const int begin = solo ? k0 : k0 + gr;
             for (int k = begin; k < k1; k += 2, ++u) {
                 const int buf = u & 1;
                 const uint32_t colS = base + (gr * 2 + buf) * 32;
@@ -283,7 +291,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             }
             // ---- the piece's end: thread t has head element t
             const int vr = pi->vr, D = a.c.head_dim, qh0 = pi->h * a.G, r0 = pi->r0;
-            const bool whole = pi->whole, has1 = k1 - k0 > 1;   // the second group has scored something
+            const bool whole = pi->whole;
+            const int ga = solo ? gr : 0;                      // the group that works on it, or the first of the two
+            const int bar = solo ? 1 + gr : 3, threads = solo ? 128 : 256;
+            auto end_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory"); };
             const size_t slot = (size_t)pi->slot;
             {
                 float x[NR];
@@ -293,19 +304,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
-            both_sync();
-            if (warp == 0) {
-                float sum[2], top[2];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    sum[g] = (ms->top[g][0][lane] + ms->top[g][1][lane]) + (ms->top[g][2][lane] + ms->top[g][3][lane]);
-                    top[g] = g == 0 || has1 ? -ms->shift[g][lane] : kNoMax;
+            end_sync();
+            if (warp == ga * 4) {
+                auto sum_of = [&](int g) { return (ms->top[g][0][lane] + ms->top[g][1][lane]) + (ms->top[g][2][lane] + ms->top[g][3][lane]); };
+                float m = -ms->shift[ga][lane], f0 = 1.0f, f1 = 0.0f, all = sum_of(ga);
+                if (!solo) {
+                    const float top0 = m, top1 = -ms->shift[1][lane];
+                    m = fmaxf(top0, top1);
+                    f0 = ex2_fast(top0 - m);
+                    f1 = ex2_fast(top1 - m);
+                    all = all * f0 + sum_of(1) * f1;
                 }
-                const float m = fmaxf(top[0], top[1]), f0 = ex2_fast(top[0] - m), f1 = ex2_fast(top[1] - m);
-                const float all = sum[0] * f0 + sum[1] * f1;
                 const float inv = whole ? (all > 0.0f || all != all ? 1.0f / all : 0.0f) : 1.0f;
-                ms->alpha[0][lane] = f0 * inv;
-                ms->alpha[1][lane] = f1 * inv;
+                ms->alpha[ga][lane] = f0 * inv;
+                if (!solo) ms->alpha[1][lane] = f1 * inv;
                 if (lane < vr) {
                     if (!whole) {
                         a.part_ml[slot + lane] = make_float2(m, all);
@@ -314,20 +326,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                         a.lse[(size_t)(r0 + i) * a.q_heads + qh0 + g] = all == 0.0f ? -INFINITY : (m + log2f(all)) / kLog2e;
                     }
                 }
-            } else if (warp == 4) {   // meanwhile
+            } else if (warp == (solo ? ga * 4 + 1 : 4)) {   // meanwhile
                 const int i = lane / a.G, g = lane - i * a.G;
-                ms->to[lane] = (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head;
+                ms->to[ga][lane] = (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head;
             }
-            if (begin < k1) wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
-            both_sync();
+            wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
+            end_sync();
             tc_fence_after();
             // Four rows at a time, the groups taking turns.  Rolled: a piece of one tile goes through all of this once, and the
             // instructions come from far.
 #pragma unroll 1
-            for (int rb = gr * 4; rb < vr; rb += 8) {
+            for (int rb = solo ? 0 : gr * 4; rb < vr; rb += solo ? 4 : 8) {
                 float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-                for (int g = 0; g < (has1 ? 2 : 1); ++g) {
+                for (int g = ga; g < (solo ? ga + 1 : 2); ++g) {
                     uint32_t o[4], o2[4];   // the products with the weights' high and low parts
                     tmem_ld4(base + 128 + g * 64 + rb, o);
                     tmem_ld4(base + 128 + g * 64 + 32 + rb, o2);
@@ -342,13 +354,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         if (rb + r >= vr) continue;
-                        if (whole) store_elem<2>(a.out + ms->to[rb + r] + t * 2, y[r]);
+                        if (whole) store_elem<2>(a.out + ms->to[ga][rb + r] + t * 2, y[r]);
                         else a.part[(slot + rb + r) * D + t] = y[r];
                     }
                 }
             }
             tc_fence_before();
-            both_sync();   // outputs, sums and maxima may be written again
+            end_sync();   // outputs, sums and maxima may be written again
         }
     } else if (warp < 12) {
         regs_dec<kRegsOther>();
@@ -360,6 +372,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             constexpr uint32_t shape_o = mma_shape(2 * NR, true, true, false, false);
             uint32_t seq = 0, tiles0 = 0, tiles1 = 0;
+            int rests = 0;   // as in the softmax
             // O^T += V^T P^T of the tile whose scores were issued before the last
             int late = 0, late_gr = 0, late_rows = 0;
             uint32_t late_seq = 0, late_u = 0;
@@ -397,10 +410,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 if (nk <= 0) break;
                 const int rows_from = __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
+                if (nk == 1) rests ^= 1;
+                const int first = __shfl_sync(0xFFFFFFFFu, nk == 1 ? rests ^ 1 : 0, 0);   // uniform for the compiler too
                 const int qs = it & 1;
                 const uint64_t q = smem_operand(sbase + qs * (NR * DP * 2), 16, 1024);
                 for (int n = 0; n < nk; ++n) {
-                    const int gr = n & 1;
+                    const int gr = first ^ (n & 1);
                     const uint32_t stage = seq % S::STAGES, u = gr ? tiles1 : tiles0;
                     ready(&fd->kv_full[stage], (seq / S::STAGES) & 1);
                     if (n == 0) {
