@@ -463,10 +463,10 @@ static cudaError_t run_f32(AttendArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_attend_f32(AttendArgs &a, int es, cudaStream_t stream) {
+// `small`: tiles of kSmallRows rows.
+cudaError_t launch_attend_f32(AttendArgs &a, int es, bool small, cudaStream_t stream) {
     const int D = a.c.head_dim;
-    const bool small = a.bt.n * a.G <= 16 && a.n_groups == 0;
-#define SV_ATT(ES, DP) (small ? run_f32<ES, DP, 16>(a, stream) : run_f32<ES, DP, 64>(a, stream))
+#define SV_ATT(ES, DP) (small ? run_f32<ES, DP, kSmallRows>(a, stream) : run_f32<ES, DP, 64>(a, stream))
     if (es == 4) return D <= 64 ? SV_ATT(4, 64) : D <= 128 ? SV_ATT(4, 128) : SV_ATT(4, 256);
     return SV_ATT(2, 256);   // narrower bf16 heads go to the tensor cores
 #undef SV_ATT
@@ -552,39 +552,33 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     const AttendGeo all{0, n_groups + batch->B, 0, 0, blocks, 1, 1, 0, seg, 0};
     AttendGeo prefix = all, own = all;
     cudaError_t e = cudaSuccess;
-    // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.  Up to 32 packed rows of a
-    // sequence's own tokens go with the tokens along the tile's rows (512 x 6 rows over 1-2k tokens: 545 us, against 1,040 in the tall
-    // kernel).  Beside prefixes too, in a launch of their own: in the prefixes' launch 64 x 6 rows behind 32k tokens would take 266 us
-    // instead of 293, but twice as long where own tokens outweigh the prefix, and the lengths are on the device.
-    // Float32 with up to 8 rows and no prefix to share: a tile of 16 rows or more would be mostly empty (64 single tokens of 4 rows
-    // 111 us, against 360).
-    if (es == 4 && cache->head_dim <= 128 && n_groups == 0 && (int64_t)batch->n * a.G <= kFewRows32) {
-        a.geo = all;
-        e = launch_attend_few32(a, s);
-        own = a.geo;
-    } else if (es == 4 || cache->head_dim > 128) {
-        a.geo = all;
-        e = launch_attend_f32(a, es, s);
+    // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.  Where a sequence's own
+    // tokens meet few packed rows they have a kernel of their own: up to 32 rows on the tensor cores, with the tokens along the
+    // tile's rows (512 x 6 rows over 1-2k tokens: 523 us, against 1,040 in the tall kernel); up to 8 in float32 by warps (64 single
+    // tokens of 4 rows: 111 us, against 360 in tiles); up to 16 otherwise in tiles of 16 rows.  Beside prefixes too, in a second
+    // launch: 64 x 16 float32 rows over 1.9-3.5k own tokens take 676 us, in the prefixes' tiles of 64 rows 2,230.  On the tensor cores
+    // 64 x 6 rows behind 32k tokens would take 266 us in one launch instead of 293, but twice as long where own tokens outweigh the
+    // prefix, and the lengths are on the device.
+    const bool fma = es == 4 || cache->head_dim > 128;
+    const int64_t packed = (int64_t)batch->n * a.G;
+    const bool few = packed <= (fma ? kSmallRows : kFewRows);
+    a.geo = all;
+    if (!few || n_groups > 0) {
+        if (few) a.geo.s1 = n_groups;
+        e = fma ? launch_attend_f32(a, es, false, s) : launch_attend_tall(a, s);
         prefix = own = a.geo;
-    } else if ((int64_t)batch->n * a.G > kFewRows) {
+    }
+    if (few && e == cudaSuccess) {
         a.geo = all;
-        e = launch_attend_tall(a, s);
-        prefix = own = a.geo;
-    } else {
         if (n_groups > 0) {
-            a.geo = all;
-            a.geo.s1 = n_groups;
-            e = launch_attend_tall(a, s);
-            prefix = a.geo;
-            own.s0 = n_groups;
-            own.seg_off = seg + n_groups + 1;
-            own.slot0 = attend_slots(batch->rows, q_heads, true, false, a.geo.TM, blocks);
+            a.geo.s0 = n_groups;
+            a.geo.seg_off = seg + n_groups + 1;
+            a.geo.slot0 = attend_slots(batch->rows, q_heads, true, false, prefix.TM, blocks);
         }
-        if (e == cudaSuccess) {
-            a.geo = own;
-            e = launch_attend_few(a, s);
-            own = a.geo;
-        }
+        e = !fma ? launch_attend_few(a, s)
+            : es == 4 && cache->head_dim <= 128 && packed <= kFewRows32 ? launch_attend_few32(a, s)
+                                                                         : launch_attend_f32(a, es, true, s);
+        own = a.geo;
     }
     if (e == cudaSuccess) e = launch_attend_join(a, prefix, own, es, s);
     return cuda_status(e);

@@ -362,11 +362,13 @@ __device__ __forceinline__ void ancestor_words(const int32_t *parents, int i, in
 // groups) and of the own ones; the same where one launch covered both.
 cudaError_t launch_attend_join(const AttendArgs &a, const AttendGeo &prefix, const AttendGeo &own, int es, cudaStream_t stream);
 
-// The kernels: any head_dim in float32 arithmetic, any number of rows or up to 8 packed rows a sequence (float32, head_dim <= 128); bf16 with head_dim <= 128 on the tensor cores, a tall form for any number
-// of rows and one for up to kFewRows packed rows a sequence.  Each fills in a.geo's tiles.
+// The kernels: float32 arithmetic for any head_dim, in tiles of 64 rows or of kSmallRows, or by warps for up to kFewRows32 packed rows a
+// sequence (float32, head_dim <= 128); bf16 with head_dim <= 128 on the tensor cores, a tall form for any number of rows and one for up
+// to kFewRows packed rows.  Each fills in a.geo's tiles.
 constexpr int kFewRows = 32;
-cudaError_t launch_attend_f32(AttendArgs &a, int es, cudaStream_t stream);
+constexpr int kSmallRows = 16;
 constexpr int kFewRows32 = 8;
+cudaError_t launch_attend_f32(AttendArgs &a, int es, bool small, cudaStream_t stream);
 cudaError_t launch_attend_few32(AttendArgs &a, cudaStream_t stream);
 cudaError_t launch_attend_tall(AttendArgs &a, cudaStream_t stream);
 cudaError_t launch_attend_few(AttendArgs &a, cudaStream_t stream);

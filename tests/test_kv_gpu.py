@@ -447,3 +447,26 @@ def test_attend_odd_pages(sv, B, n, heads, kv, dim, page, tree, pre, longest):
     bad, _ = sv.sv_kv_attend(q, c.k, c.v, stats=st, **kw, **dict(c.args, page_table=table.cuda()))
     assert sv.read_stats(st)["status"] == 1
     assert torch.equal(bad[:last], out[:last])
+
+
+@pytest.mark.parametrize("dtype,B,n,heads,kv,dim,page,tree,pre,longest", [
+    (F32, 40, 2, 8, 4, 80, 16, False, 700, 500),     # 4 packed rows
+    (F32, 30, 4, 6, 2, 128, 24, True, 333, 300),     # 12, a prefix that ends inside a page
+    (F32, 24, 1, 8, 1, 64, 8, False, 1000, 20),      # 8 of one token
+    (F32, 12, 3, 8, 2, 200, 16, False, 150, 400),    # wide heads
+    (BF, 16, 4, 8, 2, 192, 32, False, 500, 300),
+])
+def test_attend_few_rows_beside_prefixes(sv, dtype, B, n, heads, kv, dim, page, tree, pre, longest):
+    """Own tokens of few packed rows in a launch behind the prefixes', in every arithmetic."""
+    rng = np.random.default_rng(dim)
+    ctx = [pre + int(x) for x in rng.integers(0, longest + 1, B)]
+    c = Cache(B + n, dtype, ctx, n, kv, dim, page, groups=[(0, pre), (B // 3, pre), (B // 2, pre)])
+    q = blocks(c, 48, B, n, heads, kv, dim, dtype)
+    par = random_tree(c.rng, B, n) if tree else None
+    kw = dict(parents=par.cuda() if tree else None, **c.args, **c.group_args)
+    st = sv.new_stats("cuda")
+    out, lse = sv.sv_kv_attend(q, c.k, c.v, lse=True, stats=st, **kw)
+    assert sv.read_stats(st)["status"] == 0
+    rows = [slice(b * n, b * n + n) for b in range(B)]
+    check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), dim ** -0.5, rows, par, [0, 1, B // 3, B // 2, B - 1])
+    assert torch.equal(out, sv.sv_kv_attend(q, c.k, c.v, **kw)[0])
