@@ -614,6 +614,14 @@ sv_status sv_kv_commit(const sv_kv_cache *cache, const sv_kv_batch *batch, int n
                        sv_stream_t stream);
 
 /* ----------------------------------------------------------------------------------------
+ * sv_stream_capture_id — the id of the CUDA graph capture that a stream takes part in, 0 for none
+ * (no counterpart on the pages).  A captured call's workspace belongs to the graph from then on: it must live as long as the
+ * graph, and no call that may run beside a replay may use it.  Callers that keep workspaces can tell by the id
+ * which ones these are.
+ * -------------------------------------------------------------------------------------- */
+uint64_t sv_stream_capture_id(sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
  * sv_set_profile_events — measurement hook (no counterpart on the pages).  begin and end are
  * cudaEvent_t handles (or NULL to disable).  While set, every call made from this host thread
  * records `begin` on its stream just before its statistics pass (the one streaming read of the

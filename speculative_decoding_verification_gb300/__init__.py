@@ -9,6 +9,9 @@ other implementation stands in.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
+import threading
 
 import torch
 
@@ -58,6 +61,32 @@ def _call(dev, stream, fn, *args):
         return fn(*args, raw)
 
 
+def _on_stream(fn):
+    """Runs a call with its `stream` argument as the current stream: what the call allocates is that stream's memory, and the
+    caller's tensors are marked as used there (and its results on the caller's stream), so that none of them is given out
+    again while one of the two streams still works on it."""
+    place = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        s = kw.get("stream") if len(args) <= place else args[place]
+        if s is None:
+            return fn(*args, **kw)
+        outer = torch.cuda.current_stream(s.device)
+        if s == outer:
+            return fn(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(s)
+        with torch.cuda.stream(s):
+            out = fn(*args, **kw)
+        for t in out if isinstance(out, tuple) else (out,):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(outer)
+        return out
+    return call
+
+
 def _dtype_code(t):
     if t.dtype == torch.float32:
         return SV_F32
@@ -80,18 +109,48 @@ def _rows(t, name):
     raise ValueError(f"{name}: expected [B, R, V] or [N, V]")
 
 
+def _current_raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _capture_id(index, raw):
+    """The capture that `raw`, the current stream of device `index`, belongs to; 0 for none."""
+    if torch._C._cuda_getDevice() == index and not torch.cuda.is_current_stream_capturing():
+        return 0
+    return load().sv_stream_capture_id(raw)
+
+
 class Workspace:
-    """A caller-owned device workspace (torch memory) reused across calls on one stream."""
+    """Device workspaces (torch memory) reused from call to call: one for each host thread, device and current stream, so
+    that calls which may run at the same time never share one.
+
+    A call that is captured into a CUDA graph gets a buffer of that capture alone, which is kept as long as the
+    Workspace: the graph holds its address.  Capture with a Workspace of your own (workspace=), dropped with the graph,
+    to have that memory back."""
 
     def __init__(self):
-        self._buf = {}
+        self._local = threading.local()   # .bufs: (device, stream) -> buffer of that stream's memory
+        self._captured = {}               # (device, stream, capture) -> buffers, the largest last
 
     def get(self, nbytes: int, device) -> torch.Tensor:
-        key = torch.device(device)
-        buf = self._buf.get(key)
+        index = torch.device(device).index
+        if index is None:
+            index = torch.cuda.current_device()
+        raw = _current_raw_stream(index)
+        capture = _capture_id(index, raw)
+        if capture:
+            bufs = self._captured.setdefault((index, raw, capture), [])
+            if not bufs or bufs[-1].numel() < nbytes:
+                bufs.append(torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device))
+            return bufs[-1]
+        try:
+            bufs = self._local.bufs
+        except AttributeError:
+            bufs = self._local.bufs = {}
+        buf = bufs.get((index, raw))
         if buf is None or buf.numel() < nbytes:
-            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-            self._buf[key] = buf
+            # The old one goes back to the memory of its own stream, which runs what still uses it first.
+            buf = bufs[index, raw] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         return buf
 
 
@@ -179,6 +238,7 @@ def _stats(stats, dev):
     return new_stats(dev) if stats is None else _arr(stats, "stats", torch.uint8, STATS_BYTES, dev)
 
 
+@_on_stream
 def sv_verify(target, draft, draft_tokens, uniforms, temperature, top_p=None, saguaro_F=0, saguaro_C=1.0,
               accept_len=None, out_tokens=None, debug=False, stats=None, workspace=None, stream=None, lazy=False,
               top_k=None):
@@ -212,6 +272,7 @@ def sv_verify(target, draft, draft_tokens, uniforms, temperature, top_p=None, sa
     return accept_len, out_tokens, dbg, stats
 
 
+@_on_stream
 def sv_verify_host(target, draft, draft_tokens, uniforms, temperature, top_p=None, saguaro_F=0, saguaro_C=1.0,
                    accept_len=None, out_tokens=None, stats=None, workspace=None, stream=None, top_k=None,
                    device=None):
@@ -267,6 +328,7 @@ def sv_verify_host(target, draft, draft_tokens, uniforms, temperature, top_p=Non
     return accept_len, out_tokens, stats, moved.value
 
 
+@_on_stream
 def sv_verify_static(target, draft, draft_tokens, uniforms, temperature, top_p=None, saguaro_F=0, saguaro_C=1.0,
                      accept_len=None, out_tokens=None, debug=None, stats=None, stream=None, top_k=None):
     """sv_verify without a workspace, for callers that cannot allocate device memory (a server
@@ -304,6 +366,7 @@ def sv_verify_static(target, draft, draft_tokens, uniforms, temperature, top_p=N
     return accept_len, out_tokens, debug, stats
 
 
+@_on_stream
 def sv_fuzzy_verify(verifier, drafter, draft_tokens, uniforms, temperature, tau=0.5, mode="divergence",
                     divergence=False, accept_len=None, out_tokens=None, stats=None, workspace=None, stream=None):
     """sv_fuzzy_verify: one stage of three-model speculative decoding on torch CUDA tensors.
@@ -334,6 +397,7 @@ def sv_fuzzy_verify(verifier, drafter, draft_tokens, uniforms, temperature, tau=
     return accept_len, out_tokens, (div[:, :K] if div is not None else None), stats
 
 
+@_on_stream
 def sv_tree_verify(target, draft, parents, tokens, uniforms, temperature, accept_len=None, out_tokens=None, path=True,
                    stats=None, workspace=None, stream=None):
     """sv_tree_verify on torch CUDA tensors: target and draft [B, N+1, V] (same dtype; row i follows
@@ -371,6 +435,7 @@ def sv_tree_verify(target, draft, parents, tokens, uniforms, temperature, accept
     return accept_len, out_tokens, (path[:, :N] if path is not None else None), stats
 
 
+@_on_stream
 def sv_tree_reuse(parents, tokens, accept_len, out_tokens, reuse_node=None, stream=None):
     """sv_tree_reuse: per sequence the node where the committed prefix ends as a path of the
     drafted tree (parents / tokens int32 [B, N]), or -1."""
@@ -389,6 +454,7 @@ def sv_tree_reuse(parents, tokens, accept_len, out_tokens, reuse_node=None, stre
     return reuse_node
 
 
+@_on_stream
 def sv_saguaro_sample(draft, uniforms, temperature, top_p=None, F=0, C=1.0, n_rows=None, tokens=None, debug=False,
                       stats=None, workspace=None, stream=None, top_k=None):
     """sv_saguaro_sample: one token per row j < n_rows of each sequence of draft [B, R, V].
@@ -433,6 +499,7 @@ def _host_i32(values):
     return arr, ctypes.cast(arr, ctypes.c_void_p)
 
 
+@_on_stream
 def sv_cache_keys(draft, draft_tokens, F_int, keys=None, stats=None, workspace=None, stream=None):
     """sv_cache_keys: draft [B, R>=K+1, V]; draft_tokens int32 [B, K]; F_int host list of K+1 ints.
     Returns keys int32 [B, sum F_int]."""
@@ -454,6 +521,7 @@ def sv_cache_keys(draft, draft_tokens, F_int, keys=None, stats=None, workspace=N
     return keys, stats
 
 
+@_on_stream
 def sv_cache_lookup(accept_len, out_tokens, keys, F_int, hit=None, stream=None):
     lib = load()
     B = accept_len.shape[0]
@@ -470,6 +538,7 @@ def sv_cache_lookup(accept_len, out_tokens, keys, F_int, hit=None, stream=None):
     return hit
 
 
+@_on_stream
 def sv_topk_rows(logits, kappa, temperature=None, ids=None, logprobs=None, stats=None, workspace=None, stream=None):
     """sv_topk_rows: logits [N, V]; returns (ids int32 [N, kappa], logprobs float64 [N, kappa], stats)."""
     lib = load()
@@ -488,6 +557,7 @@ def sv_topk_rows(logits, kappa, temperature=None, ids=None, logprobs=None, stats
     return ids, logprobs, stats
 
 
+@_on_stream
 def sv_mirror_reuse(branches, accept_len, out_tokens, reuse=None, stream=None):
     lib = load()
     B, kappa, gamma = branches.shape
@@ -553,6 +623,7 @@ def sv_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "
     return list(f), mag.value
 
 
+@_on_stream
 def sv_rope(x, positions, inv_freq, style="half", magnitude=1.0, backward=False, out=None, stream=None):
     """sv_rope: rotary positions of x [rows, heads, dim] or [B, n, heads, dim] (float32 or bfloat16).
 
@@ -627,6 +698,7 @@ def _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
     return B, rows, _abi.KV_BATCH.pack(ctx, table, starts, par, pitch, pages, B, max(n, 1), rows)
 
 
+@_on_stream
 def sv_kv_append(k, v, k_cache, v_cache, context_len, page_table, q=None, q_out=None, inv_freq=None, style="half",
                  magnitude=1.0, parents=None, row_start=None, max_rows=None, stats=None, stream=None):
     """sv_kv_append: write the block's keys and values to the paged cache, rotating keys and queries.
@@ -669,6 +741,7 @@ def sv_kv_append(k, v, k_cache, v_cache, context_len, page_table, q=None, q_out=
     return q_out
 
 
+@_on_stream
 def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, parents=None, row_start=None, max_rows=None,
                  group_start=None, prefix_len=None, out=None, lse=False, stats=None, workspace=None, stream=None):
     """sv_kv_attend: attention of the block's rows over the paged cache, their own tokens included.
@@ -714,6 +787,7 @@ def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, paren
     return out, lse
 
 
+@_on_stream
 def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, context_out=None, stats=None, stream=None):
     """sv_kv_commit: after sv_tree_verify, move the accepted path's keys and values to consecutive slots in every
     layer.  k_cache, v_cache [layers, pages, page_size, kv_heads, dim]; accept_len int32 [B] and path int32 [B, N]
@@ -736,6 +810,7 @@ def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, co
     return context_out
 
 
+@_on_stream
 def sv_selftest_timeout(limit_cycles: int, stats=None, stream=None):
     lib = load()
     dev = torch.device("cuda", torch.cuda.current_device())
@@ -745,6 +820,7 @@ def sv_selftest_timeout(limit_cycles: int, stats=None, stream=None):
     return stats
 
 
+@_on_stream
 def sv_selftest_exp2(lo: float, hi: float, n: int, stream=None):
     lib = load()
     dev = torch.device("cuda", torch.cuda.current_device())
@@ -753,6 +829,7 @@ def sv_selftest_exp2(lo: float, hi: float, n: int, stream=None):
     return out
 
 
+@_on_stream
 def sv_selftest_exp2_all(lo: float, hi: float, stream=None):
     """Largest relative errors (fast, float-float) of the library's exponentials over every
     float32 input in [lo, hi], and the number of inputs evaluated."""

@@ -92,6 +92,7 @@ SIGNATURES = {
     "sv_kv_attend": (c_int, [c_kv, c_bt, c_vp, c_i64, c_i64, c_int, c_f32, c_vp, c_vp, c_int, c_vp, c_i64, c_i64, c_vp,
                              c_vp, c_vp, c_size, c_vp]),
     "sv_kv_commit": (c_int, [c_kv, c_bt, c_int, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "sv_stream_capture_id": (ctypes.c_uint64, [c_vp]),
     "sv_set_profile_events": (None, [c_vp, c_vp]),
     "sv_selftest_timeout": (c_int, [c_i64, c_vp, c_vp]),
     "sv_selftest_exp2": (c_int, [c_f64, c_f64, c_i64, c_vp, c_vp]),

@@ -210,6 +210,16 @@ extern "C" const char *sv_status_string(sv_status s) {
 
 extern "C" int sv_version(void) { return 100; }   // 0.1.0
 
+extern "C" uint64_t sv_stream_capture_id(sv_stream_t stream) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &st, &id) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return st == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 extern "C" void sv_set_profile_events(void *begin, void *end) {
     t_prof_begin = static_cast<cudaEvent_t>(begin);
     t_prof_end = static_cast<cudaEvent_t>(end);
