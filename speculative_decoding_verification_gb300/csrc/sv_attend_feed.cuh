@@ -95,12 +95,16 @@ __device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
     return d;
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(f32x2 x) {
-    float lo, hi;
-    uint32_t w;
-    f2_unpack(x, lo, hi);
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-    return w;
+// Two weights as bf16 pairs: the upper parts are cut off, the lower ones are the rounded rest, 16 bits in all (within 2^-16).
+// Both parts of a weight above 0 are above 0 (to 2^-102; the rest is taken from hi (1 - 2^-24), one instruction as it is from
+// hi): an infinite value times the two then adds up to that infinity.  With a rounded upper part the lower one is 0 or negative for
+// half of the weights, and the sum was NaN.
+__device__ __forceinline__ void weight_parts(f32x2 e, uint32_t &hi, uint32_t &lo) {
+    float a, b;
+    f2_unpack(e, a, b);
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    f2_unpack(f2_fma(f2_from_bf16x2(hi), f2_pack(-0x1.fffffep-1f, -0x1.fffffep-1f), e), a, b);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b), "f"(a));
 }
 
 // Values of a tile with hidden tokens, by 128 threads: thread t looks at token t.  A token whose values are not all finite becomes

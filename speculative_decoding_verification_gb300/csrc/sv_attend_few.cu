@@ -240,8 +240,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                         const int r = q * 8 + j * 2;
                         const f32x2 e = f2_ex2(f2_pack(x[r], x[r + 1]));
                         l[r / 2] = f2_add(l[r / 2], e);
-                        hi[j] = bf16_pair(e);
-                        lo[j] = bf16_pair(f2_fma(f2_from_bf16x2(hi[j]), f2_pack(-1.0f, -1.0f), e));
+                        weight_parts(e, hi[j], lo[j]);
                     }
                     sts128(prow + ((q ^ (t & 7)) << 4), hi);
                     sts128(prow + (((q + 4) ^ (t & 7)) << 4), lo);

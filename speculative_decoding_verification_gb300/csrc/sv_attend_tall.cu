@@ -9,7 +9,7 @@
 // is one row tile whose even key tiles go to one stream and odd ones to the other, each with its own maximum, sum and
 // output, added at the piece's end.  Either way one stream's products run while the other's softmax does.
 // Tensor memory (512 columns): scores 2 x 128, the weights over the scores they came from, outputs 2 x 128.
-// Weights.  A weight enters the product with V as two bf16 parts, its rounding and what that left (16 bits in all): one
+// Weights.  A weight enters the product with V as two bf16 parts, its upper bits and the rounded rest (16 bits in all): one
 // part alone is off by 2^-8, as much as the rounding of the output.
 //
 // What bounds it: a stream's softmax (1,600 cycles a tile of 128 x 128) and its products (1,536: 8 for the scores, 16 for the weighted
@@ -212,7 +212,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     }
                     const float shift = m_used == -INFINITY ? 0.0f : m_used * c;
                     const f32x2 c2 = f2_pack(c, c), s2 = f2_pack(-shift, -shift);
-                    const f32x2 minus1 = f2_pack(-1.0f, -1.0f);
                     f32x2 sum[2] = {f2_pack(l, 0.0f), f2_pack(0.0f, 0.0f)};
                     // A chunk's weights go where its scores were: upper parts, then lower ones.
                     uint32_t x[32];
@@ -226,8 +225,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                         for (int u = 0; u < 16; ++u) {
                             const f32x2 e = f2_ex2(f2_fma(f2_from_u32x2(x[2 * u], x[2 * u + 1]), c2, s2));
                             sum[u & 1] = f2_add(sum[u & 1], e);
-                            p[u] = bf16_pair(e);
-                            p[16 + u] = bf16_pair(f2_fma(f2_from_bf16x2(p[u]), minus1, e));
+                            weight_parts(e, p[u], p[16 + u]);
                         }
                         if (q < 3) tmem_ld32(colS + q * 32 + 32, x);
                         tmem_st32(colS + q * 32, p);

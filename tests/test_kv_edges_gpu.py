@@ -1,0 +1,66 @@
+"""GPU tests of attention at the edges of its inputs: infinite values that rows see, scales of either sign and none, scores near the
+ends of float32, blocks of all shapes in every kernel.  The kernels are named by what takes a call there: "few" for bf16 with up to 32
+packed rows a sequence and key head, "tall" for bf16 with more, "few32" for float32 with up to 8, "small32" up to 16, "f32" for more."""
+import numpy as np
+import pytest
+import torch
+
+from kv_helpers import Cache, check_attend, random_tree
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+# kernel, dtype, rows, heads, kv_heads, dim
+KERNELS = [("few", BF, 5, 8, 2, 128), ("few", BF, 3, 4, 4, 64), ("tall", BF, 40, 8, 2, 128), ("tall", BF, 150, 4, 2, 64),
+           ("few32", F32, 2, 8, 2, 64), ("few32", F32, 1, 4, 1, 128), ("small32", F32, 4, 8, 2, 80), ("f32", F32, 30, 8, 2, 64),
+           ("wide", BF, 2, 4, 2, 256), ("wide", BF, 30, 4, 2, 136)]
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import speculative_decoding_verification_gb300 as sv
+    sv.load()
+    return sv
+
+
+def randn(seed, *shape, dtype=F32):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+def block(c, seed, n, heads, kv, dim, dtype, size=2.0):
+    """Queries [B, n, heads, dim]; the block's keys and values go to the slots after each context."""
+    B = len(c.contexts)
+    for b in range(B):
+        c.put(b, c.contexts[b], randn(seed + 1 + b, n, kv, dim), randn(seed + 101 + b, n, kv, dim))
+    return randn(seed, B, n, heads, dim, dtype=dtype) * size
+
+
+def rows_of(B, n):
+    return [slice(b * n, b * n + n) for b in range(B)]
+
+
+@pytest.mark.parametrize("kernel,dtype,n,heads,kv,dim", KERNELS)
+@pytest.mark.parametrize("pre", [0, 384])
+def test_infinite_values_that_rows_see(sv, kernel, dtype, n, heads, kv, dim, pre):
+    """An infinite value reaches every row that sees it as that infinity, wherever its token lies; infinities of both signs
+    and NaN as NaN; the other elements stay those of the finite ones."""
+    ctx = [pre + 700, pre + 130]
+    c = Cache(n + dim, dtype, ctx, n, kv, dim, 16, groups=[(0, pre)] if pre else None)
+    q = block(c, 30, n, heads, kv, dim, dtype)
+    inf, page = float("inf"), 16
+    tokens = [pre + 3, pre + 127, pre + 128, pre + 129] + ([5, 300] if pre else [])
+    for b, cx in enumerate(ctx):
+        for t in tokens + [cx]:   # the last one is the block's first row
+            at = int(c.table[b, t // page]), t % page
+            c.v[at][:, 3] = inf
+            c.v[at][:, 4] = -inf
+            c.v[at][:, 5] = inf if t % 2 else -inf
+            c.v[at][:, 6] = float("nan")
+    out, lse = sv.sv_kv_attend(q, c.k, c.v, lse=True, **c.args, **c.group_args)
+    assert bool((out[..., 3] == inf).all()) and bool((out[..., 4] == -inf).all())
+    assert bool(out[..., 5:7].isnan().all()) and bool(torch.isfinite(lse).all())
+    keep = [d for d in range(dim) if d not in (3, 4, 5, 6)]
+    assert bool(torch.isfinite(out[..., keep]).all())
+    c.v[..., 3:7] = 0.0
+    out[..., 3:7] = 0.0
+    check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), dim ** -0.5, rows_of(2, n))
