@@ -605,8 +605,11 @@ sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *batch, const
  *
  *  n_layers, layer_stride   layer l of the cache starts l * layer_stride elements after k (after v).
  *  accept_len   dev int32 [B]; path dev int32 [B][n-1], rising node ids in 1..n-1.
- *  context_out  dev int32 [B] or NULL (not context_len itself): context_len[b] + 1 + accept_len[b].
- * batch->row_start and batch->parents are not used.  An accept_len outside [0, n-1] or a path that does not rise is
+ *  context_out  dev int32 [B] or NULL (not context_len itself): context_len[b] + 1 + accept_len[b], or context_len[b]
+ *               of an empty block.
+ * batch->row_start (with `rows`) gives each sequence's own number of rows, as in sv_kv_append; without it each has n.
+ * batch->parents is not used.  An accept_len or a path node that is no row of the sequence's block after row 0, a path that
+ * does not rise, or a slot past max_pages * page_size (of row 0 and the path; other rows' slots are not looked at) is
  * reported in stats; that sequence is left as it is, with context_out = context_len.
  * -------------------------------------------------------------------------------------- */
 sv_status sv_kv_commit(const sv_kv_cache *cache, const sv_kv_batch *batch, int n_layers, int64_t layer_stride,

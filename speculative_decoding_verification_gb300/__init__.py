@@ -788,10 +788,12 @@ def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, paren
 
 
 @_on_stream
-def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, context_out=None, stats=None, stream=None):
+def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, context_out=None, stats=None, stream=None,
+                 row_start=None):
     """sv_kv_commit: after sv_tree_verify, move the accepted path's keys and values to consecutive slots in every
     layer.  k_cache, v_cache [layers, pages, page_size, kv_heads, dim]; accept_len int32 [B] and path int32 [B, N]
-    as sv_tree_verify gives them.  Returns context_out int32 [B]: context_len + 1 + accept_len."""
+    as sv_tree_verify gives them.  row_start int32 [B+1]: the blocks were ragged, as in sv_kv_append (at most N + 1 rows a
+    sequence).  Returns context_out int32 [B]: context_len + 1 + accept_len, or context_len of an empty block."""
     lib = _abi.load_packed()
     dev, c_shape, strides, cache = _kv_cache(k_cache, v_cache, 5)
     B, N = path.shape
@@ -802,8 +804,9 @@ def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, co
     if context_out is not None and context_out.data_ptr() == ctx:
         raise ValueError("context_out must not be context_len")
     context_out = _out(context_out, "context_out", torch.int32, (B,), dev)
+    starts = 0 if row_start is None else _ints(row_start, "row_start", torch.int32, B + 1, dev)
     st = _stats(stats, dev).data_ptr() if stats is not None else 0
-    batch = _abi.KV_BATCH.pack(ctx, table, 0, 0, pitch, pages, B, N + 1, B * (N + 1))
+    batch = _abi.KV_BATCH.pack(ctx, table, starts, 0, pitch, pages, B, N + 1, B * (N + 1))
     code = _call(dev, stream, lib.sv_kv_commit, cache, batch, c_shape[0], strides[0], acc, nodes if N else 0, context_out.data_ptr(), st)
     if code:
         _abi.check("sv_kv_commit", code)

@@ -120,19 +120,22 @@ struct CommitArgs {
 
 // One block a (layer, sequence): 32 layers x 64 sequences of 8 heads of 128 take 9.1 us, 0.94 of the measured copy bandwidth.  Thread t holds one 16-byte column of a slot.  Slot path[j] moves to
 // slot 1 + j; the path rises, so path[j'] > 1 + j for j' > j and moves in order of j never overwrite
-// a slot that a later move reads.
+// a slot that a later move reads.  Only slots of the sequence's own rows are touched: a short block may end where its pages do,
+// and an empty one has no row 0 to keep.
 __global__ void __launch_bounds__(256) k_kv_commit(const CommitArgs a, int es) {
     __shared__ int64_t src[SV_MAX_TREE], dst[SV_MAX_TREE];
     const int b = blockIdx.x % a.bt.B, N = a.bt.n - 1;
     const int64_t layer = blockIdx.x / a.bt.B;
     const int acc = a.accept_len[b], ctx = a.bt.context_len[b];
     const int32_t *path = a.path + (int64_t)b * N;
-    bool bad = acc < 0 || acc > N || ctx < 0 || ctx + (int64_t)a.bt.n > (int64_t)a.bt.max_pages * a.c.page_size;
+    const SeqRows sr = seq_rows(a.bt, b);
+    const int64_t cap = (int64_t)a.bt.max_pages * a.c.page_size;
+    bool bad = !sr.ok || acc < 0 || acc > max(sr.n - 1, 0) || ctx < 0 || ctx + (int64_t)min(sr.n, 1) > cap;
     if (!bad) {
         const int32_t *table = a.bt.page_table + b * a.bt.table_pitch;
         for (int j = threadIdx.x; j < acc; j += 256) {
             const int p = path[j];
-            if (p > N || p <= (j ? path[j - 1] : 0) || p <= j) {
+            if (p >= sr.n || ctx + (int64_t)p >= cap || p <= (j ? path[j - 1] : 0) || p <= j) {
                 bad = true;
             } else {
                 src[j] = slot_offset(a.c, table, ctx + p);
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(256) k_kv_commit(const CommitArgs a, int es) {
     bad = __syncthreads_or(bad);
     if (layer == 0 && threadIdx.x == 0) {
         if (bad) report_error(a.stats, SV_ERR_INVALID_ARG, b);
-        if (a.context_out) a.context_out[b] = bad ? ctx : ctx + 1 + acc;
+        if (a.context_out) a.context_out[b] = bad || sr.n == 0 ? ctx : ctx + 1 + acc;
     }
     if (bad) return;
     const int vec = a.c.head_dim * es / 16, cols = vec * a.c.kv_heads;
