@@ -78,9 +78,10 @@ void profile_end(cudaStream_t s) {
     if (t_prof_end) cudaEventRecord(t_prof_end, s);
 }
 
-int prepare_kernel(const void *func, int threads, size_t smem_bytes) {
-    if (smem_bytes > 48 * 1024) {
-        if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes) != cudaSuccess)
+int prepare_kernel(const void *func, int threads, size_t smem_bytes, size_t most_bytes) {
+    const size_t opt_in = most_bytes > smem_bytes ? most_bytes : smem_bytes;
+    if (opt_in > 48 * 1024) {
+        if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)opt_in) != cudaSuccess)
             return 0;
     }
     int blocks = 0;

@@ -120,3 +120,27 @@ def test_threads_on_one_stream(sv):
     torch.cuda.synchronize()
     assert not errors
     assert all(call.same(x) for call, to in zip(calls, got) for x in to)
+
+
+def test_threads_with_other_head_widths(sv):
+    """The float32 kernel of few rows takes shared memory by the head width: two threads with widths 128 and 64, on streams of their
+    own, do not take it from each other."""
+    calls = [Call(sv, 8, F32, 2, 1, 2, 1, 128, 100), Call(sv, 9, F32, 2, 1, 2, 1, 64, 100)]
+    got, errors = [[], []], []
+
+    def work(call, to):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(3000):
+                    last = call.run()
+                torch.cuda.current_stream().synchronize()
+                to.append(last)
+        except Exception as e:   # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in zip(calls, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert all(call.same(x) for call, to in zip(calls, got) for x in to)
