@@ -474,6 +474,8 @@ sv_status sv_mirror_reuse(const int32_t *branches, const int32_t *accept_len,
  * must be 16-byte aligned and the strides and head_dim multiples of 16 bytes.  Any order of the axes works, and
  * keys and values may be interleaved in one allocation as long as they share the strides.
  *
+ * A page table holds at most 2^31 - 1025 slots (max_pages * page_size; more are refused).
+ *
  * Batch.  Rows of q, k, v and out are [row][head][element] with caller-given strides.  Without
  * row_start, sequence b has rows b*n..b*n+n-1; with it, rows row_start[b]..row_start[b+1]-1 (at most n
  * of them, none is allowed) and parents must be NULL.  context_len[b] tokens of sequence b are

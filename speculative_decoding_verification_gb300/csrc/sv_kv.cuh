@@ -35,6 +35,9 @@ inline bool strides16(int es, int64_t a, int64_t b = 0, int64_t c = 0) {
     return (a * es) % 16 == 0 && (b * es) % 16 == 0 && (c * es) % 16 == 0;
 }
 
+// Most slots of a page table: places up to a few tiles past the last slot are formed in 32 bits.
+constexpr int64_t kMaxSlots = INT32_MAX - 1024;
+
 inline bool kv_args_ok(const sv_kv_cache *c, const sv_kv_batch *b, bool block) {
     if (c == nullptr || b == nullptr || c->k == nullptr || c->v == nullptr) return false;
     if (c->dtype != SV_F32 && c->dtype != SV_BF16) return false;
@@ -47,7 +50,7 @@ inline bool kv_args_ok(const sv_kv_cache *c, const sv_kv_batch *b, bool block) {
     if (b->context_len == nullptr || b->page_table == nullptr || b->B < 1 || b->n < 1 || b->max_pages < 1 ||
         b->table_pitch < b->max_pages)
         return false;
-    if ((int64_t)b->max_pages * c->page_size > INT32_MAX || (b->row_start == nullptr && (int64_t)b->B * b->n > INT32_MAX))
+    if ((int64_t)b->max_pages * c->page_size > kMaxSlots || (b->row_start == nullptr && (int64_t)b->B * b->n > INT32_MAX))
         return false;
     if (block) {
         if (b->rows < 0 || (b->row_start == nullptr && b->rows != b->B * b->n)) return false;
