@@ -589,7 +589,10 @@ sv_status sv_kv_append(const sv_kv_cache *cache, const sv_kv_batch *batch, const
  *  workspace    dev, >= sv_kv_attend_workspace_size(rows, q_heads, head_dim, B, n_groups) bytes, 256-byte aligned.
  * Results do not change from run to run: partial sums are joined in a fixed order.
  * Returns SV_ERR_INVALID_ARG as sv_kv_append, and for a q_heads that kv_heads does not divide, a scale that is not
- * finite, or n_groups > B.
+ * finite, n_groups > B, or sizes past these limits: rows * q_heads at most 2^30, B * kv_heads below 2^31, and the product of
+ * the rows that meet the same tokens (a block's n, with groups all rows; times q_heads / kv_heads) with the page table's
+ * max_pages * page_size slots below about 2^44 (a million rows of 8 heads over two million tokens).  The sum over
+ * sequences and heads has no limit.
  * -------------------------------------------------------------------------------------- */
 size_t sv_kv_attend_workspace_size(int64_t rows, int q_heads, int head_dim, int B, int n_groups);
 

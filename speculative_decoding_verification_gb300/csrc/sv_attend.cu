@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     Piece p;
     for (int first = 1;; first = 0) {
         const bool more = w.next(a, p);
-        if (first && tid == 0) leave_tail(a, p, more, w.total);
+        if (first && tid == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more, blockIdx.x);
         if (!more) break;
         const int m0 = p.t * TM, h = p.h;
         const int32_t *table = a.bt.page_table + p.g.table * a.bt.table_pitch;
@@ -374,33 +374,6 @@ __global__ void __launch_bounds__(256) k_attend_join_tails(const AttendArgs a) {
 // (sequence, key head); its segments are looked up once, its rows' pieces by a lane each.
 constexpr int kJoinRows = 8;
 
-struct JoinSeg {
-    Seg g;
-    Ranges r;
-    int first;   // the key head's place
-};
-
-__device__ __forceinline__ void join_seg(const AttendArgs &a, const AttendGeo &geo, int s, int h, JoinSeg *j) {
-    j->r = ranges_of(geo.seg_off[geo.s1 - geo.s0], geo);
-    j->g = seg_of(a, geo, s, false);
-    j->first = geo.seg_off[s - geo.s0] + units_before(a, geo, j->g, j->g.tiles_m) * h;
-}
-
-// The unit with row tile t: its tiles and the blocks [c0, c1] that may hold pieces of it; c1 < c0: none.
-struct JoinUnit {
-    int at, cost, tiles, c0, c1;
-};
-
-__device__ __forceinline__ JoinUnit join_unit(const AttendArgs &a, const AttendGeo &geo, const JoinSeg &j, int t) {
-    JoinUnit u{0, 1, seg_tiles(a, geo, j.g, t), 0, -1};
-    if (u.tiles <= 0 || j.r.parts == 0) return u;
-    u.at = j.first + units_before(a, geo, j.g, t) + geo.unit_cost;
-    u.cost = tile_cost(geo, j.g, t);
-    u.c0 = block_of_place(j.r, u.at);
-    u.c1 = block_of_place(j.r, u.at + (u.tiles - 1) * u.cost);
-    return u;
-}
-
 template <int ES>
 __global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a, const AttendGeo prefix, const AttendGeo own) {
     __shared__ JoinSeg sj[2];
@@ -409,8 +382,8 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendArgs a, const A
     const int h = blockIdx.x % a.c.kv_heads, unit = blockIdx.x / a.c.kv_heads;
     const bool ragged = a.bt.row_start != nullptr;   // then a block takes the heads of one row
     const int b = ragged ? row_sequence(a.bt, unit) : unit;
-    if (threadIdx.x == 0) join_seg(a, own, a.n_groups + b, h, &sj[1]);
-    if (threadIdx.x == 32) join_seg(a, prefix, group_of(a, b), h, &sj[0]);
+    if (threadIdx.x == 0) sj[1] = join_seg(a, own, a.n_groups + b, h);
+    if (threadIdx.x == 32) sj[0] = join_seg(a, prefix, group_of(a, b), h);
     __syncthreads();
     const JoinSeg &jo = sj[1], &jp = sj[0];
     const int start = ragged ? (unit - jo.g.r0) * a.G : blockIdx.y * kJoinRows;
@@ -455,10 +428,9 @@ template <int ES, int DP, int TM>
 static cudaError_t run_f32(AttendArgs &a, cudaStream_t stream) {
     using S = F32Shape<ES, DP, TM>;
     if (prepare_kernel((const void *)k_attend_f32<ES, DP, TM>, kAttThreads, S::BYTES) < 1) return cudaErrorInvalidConfiguration;
-    a.geo.TM = TM;
-    a.geo.TK = S::TK;
-    a.geo.tile_cost = a.geo.tall_cost = 1;
-    a.geo.unit_cost = 0;
+    constexpr AttendTiles tiles = tiles_f32(TM, DP);
+    static_assert(tiles.TK == S::TK, "the cutting's key tiles are the kernel's");
+    a.geo.set(tiles);
     k_attend_f32<ES, DP, TM><<<a.geo.blocks, kAttThreads, S::BYTES, stream>>>(a);
     return cudaGetLastError();
 }
@@ -486,7 +458,7 @@ static AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, in
     Carver cv;
     const size_t slots = attend_slots(rows, q_heads, n_groups > 0, true, kAttMaxTile, kAttBlocks) +
                          (n_groups > 0 ? (size_t)kFewRows * kAttBlocks : 0);
-    p.off_seg = cv.take<int>((size_t)n_groups + B + 2);
+    p.off_seg = cv.take<long long>((size_t)n_groups + B + 2);
     p.off_tails = cv.take<AttendTail>(2 * kAttBlocks);
     p.off_ml = cv.take<float2>(slots);
     p.off_part = cv.take<float>(slots * head_dim);
@@ -518,6 +490,14 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
         !strides16(es, out_row_stride, out_head_stride) || (int64_t)batch->rows * q_heads > (1 << 30) ||
         (int64_t)batch->B * cache->kv_heads > INT32_MAX)
         return SV_ERR_INVALID_ARG;
+    // Rows that meet the same tokens, and the tiles they are cut into (few rows make one row tile, which always fits).
+    const bool fma = es == 4 || cache->head_dim > 128;
+    const int64_t G = q_heads / cache->kv_heads, packed = batch->n * G;
+    const bool few = packed <= (fma ? kSmallRows : kFewRows);
+    const AttendTiles large = fma ? tiles_f32(64, cache->head_dim > 128 ? 256 : 128) : kTilesTall;
+    if ((!few || n_groups > 0) &&
+        !tiles_fit(large, (n_groups > 0 || batch->rows < batch->n ? batch->rows : batch->n) * G, (int64_t)batch->max_pages * cache->page_size))
+        return SV_ERR_INVALID_ARG;
     const AttendPlan pl = plan_attend(batch->rows, q_heads, cache->head_dim, batch->B, n_groups);
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.bytes) return SV_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -547,7 +527,7 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     a.tails = reinterpret_cast<AttendTail *>(w + pl.off_tails);
     a.part_ml = reinterpret_cast<float2 *>(w + pl.off_ml);
     a.part = reinterpret_cast<float *>(w + pl.off_part);
-    int *seg = reinterpret_cast<int *>(w + pl.off_seg);
+    long long *seg = reinterpret_cast<long long *>(w + pl.off_seg);
     const int blocks = di.sms < kAttBlocks ? di.sms : kAttBlocks;
     const AttendGeo all{0, n_groups + batch->B, 0, 0, blocks, 1, 1, 0, seg, 0};
     AttendGeo prefix = all, own = all;
@@ -559,9 +539,6 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     // launch: 64 x 16 float32 rows over 1.9-3.5k own tokens take 676 us, in the prefixes' tiles of 64 rows 2,230.  On the tensor cores
     // 64 x 6 rows behind 32k tokens would take 266 us in one launch instead of 293, but twice as long where own tokens outweigh the
     // prefix, and the lengths are on the device.
-    const bool fma = es == 4 || cache->head_dim > 128;
-    const int64_t packed = (int64_t)batch->n * a.G;
-    const bool few = packed <= (fma ? kSmallRows : kFewRows);
     a.geo = all;
     if (!few || n_groups > 0) {
         if (few) a.geo.s1 = n_groups;

@@ -13,6 +13,9 @@
 // maximum, sum and weighted values in the workspace, and k_attend_join adds a row's pieces in order.  A unit
 // that is one piece and the only one of its rows writes its output itself.
 //
+// Places are 64 bits wide; a key head's cost within a segment fits 31 (the entry point refuses what could pass that), so that a walk
+// divides 32-bit numbers only.
+//
 // Everything is derived from device arrays inside the call; the host knows bounds only.
 #pragma once
 
@@ -22,13 +25,25 @@ namespace sv {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// What the cutting has in common with its test on the host.
+#define SV_HD __host__ __device__ __forceinline__
+
+// Row and key tiles of a kernel and what they cost: a key tile, one for more than TM / 2 rows, setting a unit up and writing it out.
+struct AttendTiles {
+    int TM, TK, tile_cost, tall_cost, unit_cost;
+};
+constexpr AttendTiles kTilesTall{256, 128, 2, 3, 8};   // of up to 128 rows: the streams take one row tile's key tiles in turn
+constexpr AttendTiles kTilesFew{32, 128, 1, 1, 2};        // setting a piece up and writing it out take about two tiles
+SV_HD constexpr AttendTiles tiles_few32(int rows) { return {rows, 64, 1, 1, 1}; }
+SV_HD constexpr AttendTiles tiles_f32(int rows, int padded_dim) { return {rows, padded_dim == 256 ? 32 : 64, 1, 1, 0}; }
+
 // A unit cut by the ranges of several blocks, left by the block that ends it (only its first piece can): without prefixes
 // these are all that has to be joined.
 struct AttendTail {
     long long slot;         // of the first piece; the next ones follow TM slots apart
     int c0, pieces;         // the first piece's block; blocks up to the last's (0: none)
-    int at, cost, tiles;    // place of the unit's first tile, cost of a tile, tiles
-    int total;              // cost of the launch
+    long long at, total;    // place of the unit's first tile, cost of the launch
+    int cost, tiles;        // of a tile; tiles
     int r0, m0, vr, h;
 };
 
@@ -36,9 +51,23 @@ struct AttendTail {
 struct AttendGeo {
     int s0, s1, TM, TK, blocks;
     int tile_cost, tall_cost, unit_cost;   // of a key tile, of one for more than TM / 2 rows, of a unit
-    int *seg_off;         // [s1 - s0 + 1] place of each segment, in the unit order
+    long long *seg_off;   // [s1 - s0 + 1] place of each segment, in the unit order
     size_t slot0;         // its first workspace slot
+
+    void set(const AttendTiles &t) {
+        TM = t.TM;
+        TK = t.TK;
+        tile_cost = t.tile_cost;
+        tall_cost = t.tall_cost;
+        unit_cost = t.unit_cost;
+    }
 };
+
+// Whether a key head's cost fits 31 bits for blocks of up to `rows` packed rows over `slots` tokens.
+SV_HD bool tiles_fit(const AttendTiles &t, int64_t rows, int64_t slots) {
+    const int64_t units = (rows + t.TM - 1) / t.TM, most = t.unit_cost + (slots + t.TK - 1) / t.TK * t.tall_cost;
+    return units * most <= INT32_MAX - 1024;
+}
 
 struct AttendArgs {
     KvCache c;
@@ -75,7 +104,7 @@ struct Seg {
 };
 
 // The group of sequence b: the last g with group_start[g] <= b.
-__device__ __forceinline__ int group_of(const AttendArgs &a, int b) {
+SV_HD int group_of(const AttendArgs &a, int b) {
     int lo = 0, hi = a.n_groups;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -85,10 +114,10 @@ __device__ __forceinline__ int group_of(const AttendArgs &a, int b) {
     return lo;
 }
 
-__device__ __forceinline__ int clamp_int(long long x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : (int)x; }
+SV_HD int clamp_int(long long x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : (int)x; }
 
 // Segment s, with every device value clamped to what the arrays hold.  `check` reports what had to be.
-__device__ __forceinline__ Seg seg_of(const AttendArgs &a, const AttendGeo &geo, int s, bool check) {
+SV_HD Seg seg_of(const AttendArgs &a, const AttendGeo &geo, int s, bool check) {
     Seg g;
     const int cap = a.bt.max_pages * a.c.page_size;
     if (s < a.n_groups) {
@@ -106,9 +135,11 @@ __device__ __forceinline__ Seg seg_of(const AttendArgs &a, const AttendGeo &geo,
         g.end = clamp_int(len, 0, cap);
         g.ctx = g.end;
         g.chain = false;
+#ifdef __CUDA_ARCH__
         if (check && (g.end != len || a.group_start[s] != b0 || a.group_start[s + 1] != b1 || (s == 0 && b0 != 0) ||
                       (s == a.n_groups - 1 && b1 != a.bt.B)))
             report_error(a.stats, SV_ERR_INVALID_ARG, b0);
+#endif
     } else {
         const int b = s - a.n_groups;
         const SeqRows sr = seq_rows(a.bt, b);
@@ -121,8 +152,10 @@ __device__ __forceinline__ Seg seg_of(const AttendArgs &a, const AttendGeo &geo,
         g.key0 = clamp_int(start, 0, g.ctx);
         g.end = clamp_int((long long)g.ctx + sr.n, 0, cap);
         g.chain = a.bt.parents == nullptr;
+#ifdef __CUDA_ARCH__
         if (check && (!sr.ok || g.ctx != ctx || g.key0 != start || (long long)g.ctx + sr.n > cap))
             report_error(a.stats, SV_ERR_INVALID_ARG, b);
+#endif
     }
     g.packed = g.n * a.G;
     g.tiles_m = (g.packed + geo.TM - 1) / geo.TM;
@@ -130,27 +163,27 @@ __device__ __forceinline__ Seg seg_of(const AttendArgs &a, const AttendGeo &geo,
 }
 
 // One past the last token that row tile t of the segment sees, and its tiles of keys.
-__device__ __forceinline__ int seg_end(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+SV_HD int seg_end(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
     if (!g.chain) return g.end;
     const int last = min((t + 1) * geo.TM, g.packed) - 1;
     return min(g.ctx + last / a.G + 1, g.end);
 }
 
-__device__ __forceinline__ int seg_tiles(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+SV_HD int seg_tiles(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
     return (seg_end(a, geo, g, t) - g.key0 + geo.TK - 1) / geo.TK;
 }
 
 // Cost of a key tile of row tile t, and of the unit.
-__device__ __forceinline__ int tile_cost(const AttendGeo &geo, const Seg &g, int t) {
+SV_HD int tile_cost(const AttendGeo &geo, const Seg &g, int t) {
     return 2 * min(geo.TM, g.packed - t * geo.TM) > geo.TM ? geo.tall_cost : geo.tile_cost;
 }
-__device__ __forceinline__ int unit_span(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+SV_HD int unit_span(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
     const int kt = seg_tiles(a, geo, g, t);
     return kt > 0 ? geo.unit_cost + kt * tile_cost(geo, g, t) : 0;
 }
 
 // Place of row tile t among a key head's units (t = tiles_m: the cost of all).
-__device__ __forceinline__ int units_before(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+SV_HD int units_before(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
     if (t <= 0) return 0;
     if (!g.chain) return (t - 1) * unit_span(a, geo, g, 0) + unit_span(a, geo, g, t - 1);   // all but the last are full
     int n = 0;
@@ -159,73 +192,99 @@ __device__ __forceinline__ int units_before(const AttendArgs &a, const AttendGeo
 }
 
 // First workspace slot of unit (h, t) of a segment.
-__device__ __forceinline__ size_t unit_slot(const AttendArgs &a, const AttendGeo &geo, const Seg &g, bool prefix, int h, int t) {
+SV_HD size_t unit_slot(const AttendArgs &a, const AttendGeo &geo, const Seg &g, bool prefix, int h, int t) {
     const size_t own = geo.s0 < a.n_groups && !prefix ? (size_t)a.bt.rows * a.q_heads : 0;
     return geo.slot0 + own + (size_t)g.r0 * a.q_heads + (size_t)h * g.packed + (size_t)t * geo.TM;
 }
 
 // Ranges of equal cost, the first `more` one longer, of as many blocks as there is a tile's cost for each.
 struct Ranges {
-    int parts, each, more;
+    long long each;
+    int parts, more;
 };
 
-__device__ __forceinline__ Ranges ranges_of(int total, const AttendGeo &geo) {
-    Ranges r;
-    r.parts = total > 0 ? max(1, min(total / geo.tile_cost, geo.blocks)) : 0;
-    r.each = r.parts > 0 ? total / r.parts : 0;
-    r.more = total - r.each * r.parts;
+// a / b, both below 2^31 as a rule.
+SV_HD long long quotient(long long a, long long b) {
+    return ((a | b) >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+SV_HD Ranges ranges_of(long long total, const AttendGeo &geo) {
+    Ranges r{0, 0, 0};
+    if (total <= 0) return r;
+    r.parts = total >= (long long)geo.blocks * geo.tile_cost ? geo.blocks : max(1, (int)total / geo.tile_cost);
+    r.each = quotient(total, r.parts);
+    r.more = (int)(total - r.each * r.parts);
     return r;
 }
 
-__device__ __forceinline__ int range_start(const Ranges &r, int c) { return c * r.each + min(c, r.more); }
+SV_HD long long range_start(const Ranges &r, int c) { return c * r.each + min(c, r.more); }
 
 // The block whose range holds place x.
-__device__ __forceinline__ int block_of_place(const Ranges &r, int x) {
-    const int split = r.more * (r.each + 1);
-    return x < split ? x / (r.each + 1) : r.more + (x - split) / r.each;
+SV_HD int block_of_place(const Ranges &r, long long x) {
+    const long long split = r.more * (r.each + 1);
+    return x < split ? (int)quotient(x, r.each + 1) : r.more + (int)quotient(x - split, r.each);
 }
 
 // First of a unit's tiles (the first at place `at`, `cost` each) at or after place x.
-__device__ __forceinline__ int tile_from(int at, int cost, int tiles, int x) {
+SV_HD int tile_from(int at, int cost, int tiles, int x) {
     return x <= at ? 0 : min(tiles, (x - at + cost - 1) / cost);
 }
 // Whether block c holds any.
-__device__ __forceinline__ bool block_has(const Ranges &r, int c, int at, int cost, int tiles) {
-    return tile_from(at, cost, tiles, range_start(r, c)) < tile_from(at, cost, tiles, range_start(r, c + 1));
+SV_HD bool block_has(const Ranges &r, int c, long long at, int cost, int tiles) {
+    const long long span = (long long)tiles * cost, from = range_start(r, c) - at, to = range_start(r, c + 1) - at;
+    return tile_from(0, cost, tiles, (int)(from < 0 ? 0 : from > span ? span : from)) <
+           tile_from(0, cost, tiles, (int)(to < 0 ? 0 : to > span ? span : to));
 }
 
 // A row's output is complete in its own piece when no prefix adds to it.
-__device__ __forceinline__ bool seg_alone(const Seg &g) { return g.key0 == 0; }
+SV_HD bool seg_alone(const Seg &g) { return g.key0 == 0; }
 
 struct Piece {
     Seg g;
     int seg, h, t;      // unit
     int vr;             // packed rows of the unit, the first at t * TM
     int k0, k1, kt;     // tiles of keys [k0, k1) of kt
-    int at, cost;       // place of the unit's first tile, cost of a tile
+    int at, cost;       // place of the unit's first tile from its key head's, cost of a tile
     int end;            // one past the last token the unit sees
 };
 
-// Walks the pieces of one block's range [pos, stop) of places.
+// Walks the pieces of one block's range of places, which ends at `stop`.
 struct Walk {
-    int pos, stop, seg_start, per_head, total, s;
+    long long head_at, stop, total;   // the key head's place; cost of the launch
+    int pos;                          // place from there
+    int per_head, h, s;
     Seg g;
 
-    __device__ __forceinline__ bool next(const AttendArgs &a, Piece &p) {
-        while (pos < stop) {
-            while (pos >= seg_start + per_head * a.c.kv_heads) {
-                seg_start += per_head * a.c.kv_heads;
-                ++s;
-                g = seg_of(a, a.geo, s, false);
-                per_head = units_before(a, a.geo, g, g.tiles_m);
+    // Takes segment `seg`, whose place is `at`, up at place `first` of it (n its key heads' number).
+    SV_HD void begin(const Seg &sg, int seg, int per, long long at, long long first) {
+        s = seg;
+        g = sg;
+        per_head = per;
+        h = (int)quotient(first - at, per);
+        head_at = at + (long long)h * per;
+        pos = (int)(first - head_at);
+    }
+
+    SV_HD bool next(const AttendArgs &a, Piece &p) {
+        while (head_at + pos < stop) {
+            if (pos >= per_head) {   // the next key head, or the next segment's first
+                head_at += per_head;
+                pos = 0;
+                if (per_head == 0 || ++h == a.c.kv_heads) {
+                    h = 0;
+                    ++s;
+                    g = seg_of(a, a.geo, s, false);
+                    per_head = units_before(a, a.geo, g, g.tiles_m);
+                }
+                continue;
             }
-            p.h = (pos - seg_start) / per_head;
-            const int head = seg_start + p.h * per_head;   // the key head's place
+            const int lim = stop - head_at < per_head ? (int)(stop - head_at) : per_head;
+            p.h = h;
             p.t = 0;
-            int unit = head, span = unit_span(a, a.geo, g, 0);
+            int unit = 0, span = unit_span(a, a.geo, g, 0);
             if (!g.chain) {
-                p.t = min((pos - head) / span, g.tiles_m - 1);
-                unit += p.t * span;
+                p.t = min(pos / span, g.tiles_m - 1);
+                unit = p.t * span;
                 span = unit_span(a, a.geo, g, p.t);
             } else {
                 while (pos >= unit + span) {
@@ -237,8 +296,8 @@ struct Walk {
             p.cost = tile_cost(a.geo, g, p.t);
             p.at = unit + a.geo.unit_cost;
             p.k0 = tile_from(p.at, p.cost, p.kt, pos);
-            p.k1 = tile_from(p.at, p.cost, p.kt, stop);
-            pos = min(stop, unit + span);
+            p.k1 = tile_from(p.at, p.cost, p.kt, lim);
+            pos = min(lim, unit + span);
             if (p.k0 >= p.k1) continue;   // the range holds none of the unit's tiles
             p.g = g;
             p.seg = s;
@@ -250,28 +309,59 @@ struct Walk {
     }
 };
 
-// Block c's tail, from its first piece p (`more` false: it has none).
-__device__ __forceinline__ void leave_tail(const AttendArgs &a, const Piece &p, bool more, int total) {
+// Block c's tail, from the walk's first piece p (`more` false: it has none).
+SV_HD AttendTail tail_of(const AttendArgs &a, const Walk &w, const Piece &p, bool more, int c) {
     AttendTail t{};
     if (more && p.k0 > 0 && p.k1 == p.kt) {
-        t.c0 = block_of_place(ranges_of(total, a.geo), p.at);
-        t.pieces = (int)blockIdx.x - t.c0 + 1;
+        t.at = w.head_at + p.at;
+        t.c0 = block_of_place(ranges_of(w.total, a.geo), t.at);
+        t.pieces = c - t.c0 + 1;
         t.slot = (long long)(unit_slot(a, a.geo, p.g, p.seg < a.n_groups, p.h, p.t) + (size_t)t.c0 * a.geo.TM);
-        t.at = p.at;
         t.cost = p.cost;
         t.tiles = p.kt;
-        t.total = total;
+        t.total = w.total;
         t.r0 = p.g.r0;
         t.m0 = p.t * a.geo.TM;
         t.vr = p.vr;
         t.h = p.h;
     }
-    a.tails[blockIdx.x] = t;
+    return t;
+}
+
+// The join's view of a segment: its ranges and the key head's place.
+struct JoinSeg {
+    Seg g;
+    Ranges r;
+    long long first;
+};
+
+SV_HD JoinSeg join_seg(const AttendArgs &a, const AttendGeo &geo, int s, int h) {
+    JoinSeg j;
+    j.r = ranges_of(geo.seg_off[geo.s1 - geo.s0], geo);
+    j.g = seg_of(a, geo, s, false);
+    j.first = geo.seg_off[s - geo.s0] + (long long)units_before(a, geo, j.g, j.g.tiles_m) * h;
+    return j;
+}
+
+// The unit with row tile t: its tiles and the blocks [c0, c1] that may hold pieces of it; c1 < c0: none.
+struct JoinUnit {
+    long long at;
+    int cost, tiles, c0, c1;
+};
+
+SV_HD JoinUnit join_unit(const AttendArgs &a, const AttendGeo &geo, const JoinSeg &j, int t) {
+    JoinUnit u{0, 1, seg_tiles(a, geo, j.g, t), 0, -1};
+    if (u.tiles <= 0 || j.r.parts == 0) return u;
+    u.at = j.first + units_before(a, geo, j.g, t) + geo.unit_cost;
+    u.cost = tile_cost(geo, j.g, t);
+    u.c0 = block_of_place(j.r, u.at);
+    u.c1 = block_of_place(j.r, u.at + (long long)(u.tiles - 1) * u.cost);
+    return u;
 }
 
 // Block-wide: the total cost and, for this block's range, where its walk starts.  Each thread takes a
 // run of consecutive segments; warp_sum has THREADS / 32 places.  Block 0 leaves the segments' places for the join and reports bad
-// input, a total past 2^30 among it (nothing is computed then).
+// input.
 template <int THREADS>
 __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long long *warp_sum) {
     const AttendGeo &geo = a.geo;
@@ -295,39 +385,32 @@ __device__ __forceinline__ void walk_start(const AttendArgs &a, Walk *w, long lo
     }
     if (lane == 31) warp_sum[wp] = inc;
     __syncthreads();
-    long long before = inc - mine, sum = 0;
+    long long before = inc - mine, total = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
         if (i < wp) before += warp_sum[i];
-        sum += warp_sum[i];
+        total += warp_sum[i];
     }
-    if (sum > 1 << 30) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.stats, SV_ERR_INVALID_ARG, -1);
-        sum = 0;
-    }
-    const int total = (int)sum;
     const Ranges r = ranges_of(total, geo);
-    const int c = blockIdx.x, pos = c < r.parts ? range_start(r, c) : total, stop = c < r.parts ? range_start(r, c + 1) : total;
+    const int c = blockIdx.x;
+    const long long pos = c < r.parts ? range_start(r, c) : total, stop = c < r.parts ? range_start(r, c + 1) : total;
     if (threadIdx.x == 0) {
         w->total = total;
-        if (pos >= stop) w->pos = w->stop = 0;
+        w->stop = stop;
+        if (pos >= stop) {   // nothing to walk
+            w->head_at = stop;
+            w->pos = 0;
+        }
     }
     if (blockIdx.x == 0 || (pos < stop && pos >= before && pos < before + mine)) {
-        int at = total > 0 ? (int)before : 0;
+        long long at = before;
         for (int s = s0; s < s1; ++s) {
             if (each > 1) {   // with one segment a thread, g and per are still those
                 g = seg_of(a, geo, geo.s0 + s, false);
                 per = units_before(a, geo, g, g.tiles_m);
             }
-            const int n = total > 0 ? per * a.c.kv_heads : 0;
-            if (pos < stop && pos >= at && pos < at + n) {
-                w->pos = pos;
-                w->stop = stop;
-                w->s = geo.s0 + s;
-                w->seg_start = at;
-                w->g = g;
-                w->per_head = per;
-            }
+            const long long n = (long long)per * a.c.kv_heads;
+            if (pos < stop && pos >= at && pos < at + n) w->begin(g, geo.s0 + s, per, at, pos);
             if (blockIdx.x == 0) {
                 geo.seg_off[s] = at;
                 if (s == NS - 1) geo.seg_off[NS] = at + n;

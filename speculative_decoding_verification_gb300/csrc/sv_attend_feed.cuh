@@ -292,7 +292,7 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
     for (int it = 0;; ++it) {
         Piece p;
         const bool more = w.next(a, p);
-        if (it == 0 && lane == 0) leave_tail(a, p, more, w.total);
+        if (it == 0 && lane == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more, blockIdx.x);
         wait_phase(fd, &fd->pd_empty[it % kRing], ((it / kRing) & 1) ^ 1, a.stats);
         PieceInfo *pi = &fd->pd[it % kRing];
         const bool own = more && p.seg >= a.n_groups, tree = own && a.bt.parents != nullptr;

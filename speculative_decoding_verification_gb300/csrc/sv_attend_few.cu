@@ -476,10 +476,8 @@ cudaError_t run_few(AttendArgs &a, bool negate, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attend_few(AttendArgs &a, cudaStream_t stream) {
-    a.geo.TM = NR;
-    a.geo.TK = kTcKeys;
-    a.geo.tile_cost = a.geo.tall_cost = 1;
-    a.geo.unit_cost = 2;   // setting a piece up and writing it out take about two tiles
+    static_assert(kTilesFew.TM == NR && kTilesFew.TK == kTcKeys, "the cutting's tiles are the kernel's");
+    a.geo.set(kTilesFew);
     AttendArgs t = a;
     // The maximum is taken after the scale; a negative scale negates the queries in the product, and zero stays zero.
     const bool negate = a.scale_log2 < 0.0f;

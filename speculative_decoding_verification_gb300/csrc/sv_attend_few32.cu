@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
     Piece p;
     for (int first = 1;; first = 0) {
         const bool more = w.next(a, p);
-        if (first && tid == 0) leave_tail(a, p, more, w.total);
+        if (first && tid == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more, blockIdx.x);
         if (!more) break;
         const int h = p.h;
         const int32_t *table = a.bt.page_table + p.g.table * a.bt.table_pitch;
@@ -249,10 +249,7 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
 
 template <int R>
 cudaError_t run_few32(AttendArgs &a, cudaStream_t stream) {
-    a.geo.TM = R;
-    a.geo.TK = 64;
-    a.geo.tile_cost = a.geo.tall_cost = 1;
-    a.geo.unit_cost = 1;
+    a.geo.set(tiles_few32(R));
     constexpr size_t each = (size_t)kWarps32 * 32 * 4;   // bytes an element of width
     const size_t bytes = each * a.c.head_dim;
     const int resident = prepare_kernel((const void *)k_attend_few32<R>, kThreads32, bytes, each * kMaxDim32);

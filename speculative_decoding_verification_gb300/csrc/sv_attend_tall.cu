@@ -487,11 +487,8 @@ cudaError_t run_tall(AttendArgs &a, bool negate, cudaStream_t stream) {
     constexpr size_t bytes = TallShape<DP>::OFF_MISC + sizeof(TallShared);
     static_assert(bytes <= 232448, "shared memory of a block");
     if (prepare_kernel((const void *)k_attend_tall<DP>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
-    a.geo.TM = kTallRows;
-    a.geo.TK = kTcKeys;
-    a.geo.tile_cost = 2;   // one row tile, the streams taking its key tiles in turn
-    a.geo.tall_cost = 3;
-    a.geo.unit_cost = 8;   // setting a piece up and writing it out
+    static_assert(kTilesTall.TM == kTallRows && kTilesTall.TK == kTcKeys, "the cutting's tiles are the kernel's");
+    a.geo.set(kTilesTall);
     k_attend_tall<DP><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, tc_args(a.c, mma_shape(128, false, false, negate, false)));
     return cudaGetLastError();
 }

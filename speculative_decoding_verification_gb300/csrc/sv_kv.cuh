@@ -66,7 +66,7 @@ struct SeqRows {
     bool ok;
 };
 
-__device__ __forceinline__ SeqRows seq_rows(const KvBatch &bt, int b) {
+__host__ __device__ __forceinline__ SeqRows seq_rows(const KvBatch &bt, int b) {
     if (bt.row_start == nullptr) return {b * bt.n, bt.n, true};
     const int r0 = bt.row_start[b], r1 = bt.row_start[b + 1];
     if (r0 < 0 || r1 < r0 || r1 > bt.rows || r1 - r0 > bt.n) return {0, 0, false};

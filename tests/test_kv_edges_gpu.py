@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv_helpers import Cache, check_attend, random_tree
+from kv_helpers import U32, Cache, check_attend, random_tree
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -64,3 +64,26 @@ def test_infinite_values_that_rows_see(sv, kernel, dtype, n, heads, kv, dim, pre
     c.v[..., 3:7] = 0.0
     out[..., 3:7] = 0.0
     check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), dim ** -0.5, rows_of(2, n))
+
+
+def test_costs_past_30_bits(sv):
+    """32,768 rows of two million cached tokens each, which all lie in one page: 1.07e9 key tiles.  32 repeats of a page weigh as the
+    page itself, with log(32) more in the log-sum-exp.  A warp adds up to 2^18 weighted values in a row; roundings of alternating
+    sign leave about sqrt(2^18) u32 = 2^-15 of the largest value, and a lane's 2^15 weights sqrt(2^15) u32 = 2^-16.5 of their sum.
+    Eight times that is allowed."""
+    B, H, page, reps, dim = 1024, 32, 1 << 16, 32, 4
+    k, v = randn(1, 1, page, H, dim), randn(2, 1, page, H, dim)
+    q = randn(3, B, 1, H, dim)
+    ctx = torch.full((B,), reps * page, dtype=torch.int32).cuda()
+    table = torch.zeros((B, reps + 1), dtype=torch.int32).cuda()
+    st = sv.new_stats("cuda")
+    k[0, 0], v[0, 0] = k[0, 1], v[0, 1]   # the rows' own token is the first slot of the page, once more
+    out, lse = sv.sv_kv_attend(q, k, v, ctx, table, lse=True, stats=st)
+    assert sv.read_stats(st)["status"] == 0
+    for b in (0, 1, 511, 1022, 1023):
+        s = torch.einsum("hd,thd->ht", q[b, 0].double(), k[0].double()) * dim ** -0.5
+        w = s.exp() * reps
+        w[:, 0] *= 1 + 1 / reps
+        want = torch.einsum("ht,thd->hd", w, v[0].double()) / w.sum(1, keepdim=True)
+        assert float((out[b, 0] - want).abs().max()) <= 2.0 ** -12 * float(v.abs().max())
+        assert float((lse[b, 0] - w.sum(1).log()).abs().max()) <= 2.0 ** -13.5 + 16 * U32

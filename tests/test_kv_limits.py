@@ -27,3 +27,17 @@ def test_slots_of_a_page_table(sv, page):
     most = (2**31 - 1 - 1024) // page
     assert attend(sv, size=page, mp=most, pitch=most) == WORKSPACE
     assert attend(sv, size=page, mp=most + 1, pitch=most + 1) == INVALID
+
+
+def test_rows_that_meet_the_same_tokens(sv):
+    """A key head's cost within a block or a prefix is kept below 2^31: rows times tokens past that are refused, whole batches are not."""
+    big = dict(size=1 << 16, B=1, n=1 << 20, rows=1 << 20, kv=1)
+    assert attend(sv, 8, mp=32, pitch=32, **big) == WORKSPACE            # a million rows of 8 heads over two million tokens
+    assert attend(sv, 8, mp=64, pitch=64, **big) == INVALID
+    many = dict(size=1 << 16, mp=64, pitch=64, B=1 << 14, n=64, rows=1 << 20, kv=1)
+    assert attend(sv, 8, **many) == WORKSPACE                            # the same rows in blocks of 64
+    assert attend(sv, 8, groups=1, **many) == INVALID                    # but not over one prefix
+    few = dict(size=1 << 16, mp=30000, pitch=30000, B=1 << 14, n=4, rows=1 << 16, kv=1)
+    assert attend(sv, 8, **few) == WORKSPACE
+    assert attend(sv, 1 << 15, n=2, rows=1 << 15, B=1 << 14, kv=1) == WORKSPACE   # rows * q_heads = 2^30
+    assert attend(sv, 1 << 15, n=3, rows=3 << 14, B=1 << 14, kv=1) == INVALID
