@@ -583,7 +583,8 @@ sv_status sv_kv_append(const sv_kv_cache *cache, const sv_kv_batch *batch, const
  * Tokens that a row does not see cannot reach it, whatever their keys and values hold (infinities and NaN
  * included); slots past the block are not read.
  *
- *  q, out       dev, strides in elements, 16-byte aligned; out must not overlap q.
+ *  q, out       dev, strides in elements, 16-byte aligned; out must not overlap q (refused where the two have one row
+ *               stride or the same base; interleaved in one allocation is fine).
  *  group_start  dev int32 [n_groups + 1], prefix_len dev int32 [n_groups]; NULL with n_groups 0.
  *  lse          dev float [rows][q_heads] or NULL.
  *  workspace    dev, >= sv_kv_attend_workspace_size(rows, q_heads, head_dim, B, n_groups) bytes, 256-byte aligned.
@@ -591,8 +592,8 @@ sv_status sv_kv_append(const sv_kv_cache *cache, const sv_kv_batch *batch, const
  * Returns SV_ERR_INVALID_ARG as sv_kv_append, and for a q_heads that kv_heads does not divide, a scale that is not
  * finite, n_groups > B, or sizes past these limits: rows * q_heads at most 2^30, B * kv_heads below 2^31, and the product of
  * the rows that meet the same tokens (a block's n, with groups all rows; times q_heads / kv_heads) with the page table's
- * max_pages * page_size slots below about 2^44 (a million rows of 8 heads over two million tokens).  The sum over
- * sequences and heads has no limit.
+ * max_pages * page_size slots: 2^42 always fits (half a million rows of 8 heads over a million tokens), 2^44 for bf16 heads up to
+ * 128 wide.  The sum over sequences and heads has no limit.
  * -------------------------------------------------------------------------------------- */
 size_t sv_kv_attend_workspace_size(int64_t rows, int q_heads, int head_dim, int B, int n_groups);
 

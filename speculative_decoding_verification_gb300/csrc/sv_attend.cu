@@ -500,6 +500,10 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
         return SV_ERR_INVALID_ARG;
     const AttendPlan pl = plan_attend(batch->rows, q_heads, cache->head_dim, batch->B, n_groups);
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.bytes) return SV_ERR_WORKSPACE;
+    const int64_t width = (int64_t)cache->head_dim * es;
+    if (overlap({q, q_row_stride * es, q_head_stride * es, batch->rows, q_heads, width},
+                {out, out_row_stride * es, out_head_stride * es, batch->rows, q_heads, width}))
+        return SV_ERR_INVALID_ARG;   // other blocks still read q
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (!on_current_device(s, cache->k, q)) return SV_ERR_INVALID_ARG;
     DeviceInfo di;

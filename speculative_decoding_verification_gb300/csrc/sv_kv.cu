@@ -207,6 +207,9 @@ static bool rope_ok(const float *inv_freq, int rotary_dim, int style, int head_d
     return rotary_dim == 0 || inv_freq != nullptr;
 }
 
+// A rotation in place is fine, one onto other rows that are still read is not.
+static bool turns_onto(const RowsView &x, const RowsView &out) { return !same_place(x, out) && overlap(x, out); }
+
 extern "C" sv_status sv_rope(const void *x, int64_t x_row_stride, int64_t x_head_stride, void *out,
                              int64_t out_row_stride, int64_t out_head_stride, sv_dtype dtype, int64_t rows, int heads,
                              int head_dim, const int32_t *positions, const float *inv_freq, int rotary_dim, int style,
@@ -217,9 +220,12 @@ extern "C" sv_status sv_rope(const void *x, int64_t x_row_stride, int64_t x_head
         return SV_ERR_INVALID_ARG;
     if (rows == 0) return SV_OK;
     if (x == nullptr || out == nullptr || positions == nullptr) return SV_ERR_INVALID_ARG;
+    const int es = elem_size(dtype);
+    if (turns_onto({x, x_row_stride * es, x_head_stride * es, rows, heads, (int64_t)head_dim * es},
+                   {out, out_row_stride * es, out_head_stride * es, rows, heads, (int64_t)head_dim * es}))
+        return SV_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (!on_current_device(s, x, out)) return SV_ERR_INVALID_ARG;
-    const int es = elem_size(dtype);
     RopeArgs a{static_cast<const char *>(x), static_cast<char *>(out), x_row_stride * es, x_head_stride * es,
                out_row_stride * es, out_head_stride * es, positions, inv_freq, {heads, head_dim, rotary_dim / 2, style},
                magnitude, backward ? -1.0f : 1.0f};
@@ -249,6 +255,10 @@ extern "C" sv_status sv_kv_append(const sv_kv_cache *cache, const sv_kv_batch *b
         !strides16(es, k_row_stride, k_head_stride) || !strides16(es, v_row_stride, v_head_stride))
         return SV_ERR_INVALID_ARG;
     if (q != nullptr && (!strides16(es, q_row_stride, q_head_stride) || !strides16(es, q_out_row_stride, q_out_head_stride)))
+        return SV_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)cache->head_dim * es;
+    if (q != nullptr && turns_onto({q, q_row_stride * es, q_head_stride * es, batch->rows, q_heads, width},
+                                   {q_out, q_out_row_stride * es, q_out_head_stride * es, batch->rows, q_heads, width}))
         return SV_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (!on_current_device(s, cache->k, k)) return SV_ERR_INVALID_ARG;

@@ -38,6 +38,45 @@ inline bool strides16(int es, int64_t a, int64_t b = 0, int64_t c = 0) {
 // Most slots of a page table: places up to a few tiles past the last slot are formed in 32 bits.
 constexpr int64_t kMaxSlots = INT32_MAX - 1024;
 
+// An array [rows][heads] of `width` bytes each, strides in bytes.
+struct RowsView {
+    const void *base;
+    int64_t row, head, rows, heads, width;
+};
+
+inline bool same_place(const RowsView &a, const RowsView &b) {
+    return a.base == b.base && (a.rows <= 1 || a.row == b.row) && (a.heads <= 1 || a.head == b.head);
+}
+
+// Whether some byte belongs to both.  Exact for arrays of one row stride (views of one projection interleave without sharing); of arrays
+// with different row strides only those that start at one address are said to.
+inline bool overlap(RowsView a, RowsView b) {
+    if (a.rows < 1 || b.rows < 1) return false;
+    if (a.base == b.base) return true;
+    auto low = [](const RowsView &v) { return (v.row < 0 ? (v.rows - 1) * v.row : 0) + (v.head < 0 ? (v.heads - 1) * v.head : 0); };
+    auto high = [](const RowsView &v) { return (v.row > 0 ? (v.rows - 1) * v.row : 0) + (v.head > 0 ? (v.heads - 1) * v.head : 0) + v.width; };
+    const int64_t d = (int64_t)((intptr_t)b.base - (intptr_t)a.base);   // b from a
+    if (high(a) <= d + low(b) || d + high(b) <= low(a)) return false;
+    if (a.rows == 1) a.row = b.row;
+    if (b.rows == 1) b.row = a.row;
+    if (a.row != b.row) return false;
+    // Row r of a and row r + s of b, -a.rows < s < b.rows, are s row strides apart: looks for the s that brings two heads nearest.
+    auto meets = [&](int64_t apart) {   // b's head from a's, in one row
+        if (a.row == 0) return apart < b.width && -apart < a.width;
+        const int64_t q = -apart / a.row;
+        for (int64_t s = q - 1; s <= q + 1; ++s) {
+            const int64_t in = s < 1 - a.rows ? 1 - a.rows : s > b.rows - 1 ? b.rows - 1 : s, x = apart + in * a.row;
+            if (x < b.width && -x < a.width) return true;
+        }
+        return false;
+    };
+    const bool one = a.head == b.head;   // then only the heads' difference counts
+    for (int64_t i = 0; i < (one ? 1 : a.heads); ++i)
+        for (int64_t j = one ? 1 - a.heads : 0; j < b.heads; ++j)
+            if (meets(d + j * b.head - i * a.head)) return true;
+    return false;
+}
+
 inline bool kv_args_ok(const sv_kv_cache *c, const sv_kv_batch *b, bool block) {
     if (c == nullptr || b == nullptr || c->k == nullptr || c->v == nullptr) return false;
     if (c->dtype != SV_F32 && c->dtype != SV_BF16) return false;
