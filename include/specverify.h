@@ -647,12 +647,18 @@ void sv_set_profile_events(void *begin, void *end);
  * shows that the library's bounded waits return an error instead of hanging; no copy is in
  * flight and nothing faults.
  *
+ * sv_selftest_attend_stall: while limit_cycles > 0, sv_kv_attend called from this host thread runs its tensor-core
+ * kernels with one barrier that nothing completes, and their waits give up after limit_cycles SM clock cycles.  A block that
+ * meets it reports SV_ERR_TIMEOUT, waits for its copies and products in flight and ends with meaningless output; the
+ * context stays usable.  0 ends it.
+ *
  * sv_selftest_exp2: evaluates the library's fast base-2 exponential (the float32 tier) and
  * its float-float exponential on n inputs spread over [lo, hi] and writes their largest
  * relative errors against CUDA's double-precision exp2 to out[0] (fast) and out[1]
  * (float-float).  The bounds that certify float32 decisions rest on these errors.
  * -------------------------------------------------------------------------------------- */
 sv_status sv_selftest_timeout(int64_t limit_cycles, sv_stats *stats, sv_stream_t stream);
+void sv_selftest_attend_stall(int64_t limit_cycles);
 sv_status sv_selftest_exp2(double lo, double hi, int64_t n, double *out, sv_stream_t stream);
 
 /* sv_selftest_exp2_all: the same two errors over EVERY float32 input in [lo, hi] (lo >= -125,

@@ -466,9 +466,14 @@ static AttendPlan plan_attend(int64_t rows, int q_heads, int head_dim, int B, in
     return p;
 }
 
+// sv_selftest_attend_stall's setting of this host thread.
+static thread_local long long t_stall_limit = 0;
+
 }  // namespace sv
 
 using namespace sv;
+
+extern "C" void sv_selftest_attend_stall(int64_t limit_cycles) { t_stall_limit = limit_cycles; }
 
 extern "C" size_t sv_kv_attend_workspace_size(int64_t rows, int q_heads, int head_dim, int B, int n_groups) {
     if (rows < 0 || q_heads < 1 || head_dim < 1 || head_dim > SV_KV_MAX_HEAD_DIM || B < 1 || n_groups < 0) return 0;
@@ -528,6 +533,8 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     a.n_groups = n_groups;
     a.lse = lse;
     a.stats = stats;
+    a.wait_limit = t_stall_limit > 0 ? t_stall_limit : kWaitLimitCycles;
+    a.stuck_stage = t_stall_limit > 0 ? 2 : -1;
     a.tails = reinterpret_cast<AttendTail *>(w + pl.off_tails);
     a.part_ml = reinterpret_cast<float2 *>(w + pl.off_ml);
     a.part = reinterpret_cast<float *>(w + pl.off_part);

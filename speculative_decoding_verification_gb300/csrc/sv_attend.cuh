@@ -81,6 +81,8 @@ struct AttendArgs {
     int n_groups;
     float *lse;
     sv_stats *stats;
+    long long wait_limit; // cycles after which a wait inside a kernel gives up
+    int stuck_stage;      // a ring stage whose copies never count as complete (the self-test of such waits), or -1
     AttendGeo geo;        // of this launch
     // workspace
     struct AttendTail *tails;   // [blocks] the unit that a block ends and an earlier one began

@@ -23,8 +23,8 @@ struct PieceInfo {
     int table, key0, ctx, end;        // page table's sequence, tokens
     int k0, k1;                       // key tiles; k0 == k1: no more pieces
     uint32_t seq;                     // ring number of the first tile's keys
-    int own, tree, whole;             // own segment, tree mask, output complete here
     int box_tiles;                    // tiles before this one load as boxes, the others by rows
+    bool own, tree, whole;            // own segment, tree mask, output complete here
     uint8_t par[SV_MAX_TREE];         // a tree's parents (255: invalid)
 };
 
@@ -33,28 +33,34 @@ struct Feed {
     PieceInfo pd[kRing];
     uint32_t vflag[8][4];             // per stage: tokens whose values are not finite (tiles with hidden tokens only)
     uint32_t tmem;
-    int dead;                         // a wait gave up: nobody waits any more
+    int dead;                         // a wait gave up: nobody waits for data any more
+    long long limit;                  // cycles after which one does
+    uint32_t next[4];                 // a producer warp's next ring number, left at its end
 };
 
-// Waits for a phase.  Gives up for everybody after the library's limit: waits return at once from then on, the block
-// runs to its end with meaningless results and the error is reported.
-__device__ __forceinline__ void wait_phase(Feed *fd, uint64_t *bar, uint32_t parity, sv_stats *stats) {
-    if (mbar_try_wait(bar, parity)) return;
-    const long long t0 = clock64();
-    while (!mbar_try_wait_sleep(bar, parity, kSuspendHintNs)) {
-        if (*reinterpret_cast<volatile int *>(&fd->dead)) return;
-        if (clock64() - t0 > kWaitLimitCycles) {
-            *reinterpret_cast<volatile int *>(&fd->dead) = 1;
-            report_error(stats, SV_ERR_TIMEOUT, -1);
-            return;
+// Waits for a phase; false when it gave up, which one wait does after the limit and from then on every one whose phase has not
+// completed.  The block runs to its end with meaningless results: the producers stop, the products and the softmax go on over the
+// same pieces (its warps meet at barriers, which all have to reach), and feed_drain waits for the copies in flight.  Only descriptions of pieces are still waited for (`patient`): they come from the walk, which waits for nothing but
+// their readers, so that all warps see the same pieces to the last.  A tile then takes microseconds, and that wait's own limit of
+// many seconds is never met.
+template <bool patient = false>
+__device__ __forceinline__ bool wait_phase(Feed *fd, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long until = clock64() + (patient ? 8 * kWaitLimitCycles : fd->limit);
+    do {
+        if (!patient && *reinterpret_cast<volatile int *>(&fd->dead)) return false;
+        if (clock64() > until) {
+            *reinterpret_cast<volatile int *>(&fd->dead) = 1;   // reported at the block's end: less code at every wait
+            return false;
         }
-    }
+    } while (!mbar_try_wait_sleep(bar, parity, kSuspendHintNs));
+    return true;
 }
 
 // `readers`: warps that read a piece description.
-__device__ __forceinline__ void feed_init(Feed *fd, int readers) {
+__device__ __forceinline__ void feed_init(Feed *fd, const AttendArgs &a, int readers) {
     for (int i = 0; i < 8; ++i) {
-        mbar_init(&fd->kv_full[i], 64);
+        mbar_init(&fd->kv_full[i], i == a.stuck_stage ? 65 : 64);
         mbar_init(&fd->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -66,6 +72,30 @@ __device__ __forceinline__ void feed_init(Feed *fd, int readers) {
         mbar_init(&fd->pd_empty[i], readers);
     }
     fd->dead = 0;
+    fd->limit = a.wait_limit;
+    for (int i = 0; i < 4; ++i) fd->next[i] = i >> 1;
+}
+
+// After a wait gave up, by one thread when every warp is done: reports it and waits for the boxes that are still on their way to
+// shared memory, which the next block will use.  Ring number q is filled by two warps; one that had stopped is stood in for.  A
+// stage is filled again only after its last fill was complete, so only the last one counts.
+template <int STAGES>
+__device__ __noinline__ void feed_drain(Feed *fd, sv_stats *stats) {
+    report_error(stats, SV_ERR_TIMEOUT, -1);
+    const long long t0 = clock64();
+    const int end = (int)max(max(fd->next[0], fd->next[1]), max(fd->next[2], fd->next[3]));   // ring numbers begun are below
+    for (int last = end - 1; last >= 0 && last >= end - STAGES; --last) {
+        for (int q = last; q >= 0; q -= STAGES) {
+            const int pair = (q & 1) * 2;
+            const bool first = q < (int)fd->next[pair], second = q < (int)fd->next[pair + 1];
+            if (!first && !second) continue;
+            uint64_t *bar = &fd->kv_full[q % STAGES];
+            if (first != second) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 32;" ::"r"(smem_addr(bar)) : "memory");
+            while (!mbar_try_wait_sleep(bar, (q / STAGES) & 1, kSuspendHintNs) && clock64() - t0 <= fd->limit) {
+            }
+            break;
+        }
+    }
 }
 
 __device__ __forceinline__ bool not_finite16(uint4 w) {
@@ -158,10 +188,10 @@ __device__ __forceinline__ void feed_produce_as(const AttendArgs &a, const TcArg
     auto page_index = [&](int key) { return pshift >= 0 ? key >> pshift : key / psize; };
     uint32_t seq = kv, q_phases = 0;   // q_phases: a bit a query tile
     int qnext = 0;
+    bool on = true;                    // off once a wait gave up
     for (int it = 0;; ++it) {
         const PieceInfo *pi = &fd->pd[it % kRing];
-        wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
-        __syncwarp();
+        if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1))) break;
         const int k0 = pi->k0, k1 = pi->k1;
         if (k0 >= k1) break;
         const int vr = pi->vr, key0 = pi->key0, end = pi->end, h = pi->h, m0 = pi->m0, r0 = pi->r0, tab = pi->table;
@@ -175,13 +205,15 @@ __device__ __forceinline__ void feed_produce_as(const AttendArgs &a, const TcArg
         auto box_key = [&](int k) { return key0 + k * kTcKeys + row0 + lane * a2.box_rows; };
         auto box_page = [&](int k) { return k < k1 && by_box(k) && lane < boxes ? table[page_index(box_key(k))] : kNoPage; };
         int page = box_page(k0);
-        for (int k = k0; k < k1; ++k) {
+        for (int k = k0; k < k1 && on; ++k) {
             const int pg = page;
             page = box_page(k + 1);
             const uint32_t stage = seq % STAGES;
             const uint32_t tile = kv_base + stage * TILE + part;
-            wait_phase(fd, &fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1, a.stats);
-            __syncwarp();
+            // Products that gave a wait up free stages that are still being filled: nothing is copied any more from then on.
+            on = __all_sync(0xFFFFFFFFu, wait_phase(fd, &fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1) &&
+                                             !*reinterpret_cast<volatile int *>(&fd->dead));
+            if (!on) break;
             seq += 2;
             if (by_box(k)) {
                 const int key = box_key(k), slot = key - page_index(key) * psize;
@@ -246,8 +278,8 @@ __device__ __forceinline__ void feed_produce_as(const AttendArgs &a, const TcArg
             if (k == k0) {   // queries, a quarter of the tile a warp; after the first keys, which memory has to bring
                 for (int t = 0; t < (two ? 2 : 1); ++t) {
                     const int qs = two ? t : qnext;
-                    wait_phase(fd, &fd->q_empty[qs], ((q_phases >> qs) & 1) ^ 1, a.stats);
-                    __syncwarp();
+                    on = __all_sync(0xFFFFFFFFu, wait_phase(fd, &fd->q_empty[qs], ((q_phases >> qs) & 1) ^ 1));
+                    if (!on) break;
                     q_phases ^= 1u << qs;
                     const int m = t * QROWS + wl * (QROWS / 4) + lane;
                     int64_t off = -1;
@@ -274,7 +306,8 @@ __device__ __forceinline__ void feed_produce_as(const AttendArgs &a, const TcArg
         }
     }
     cp_async_commit();
-    cp_async_wait<0>();   // nothing is in flight when the block ends
+    cp_async_wait<0>();   // no row is in flight when the block ends; boxes are when a wait gave up
+    if (lane == 0) fd->next[wl] = seq;
 }
 
 // Two copies of the loop: with the code for split boxes in it, pages without them took 595 us instead of 545 (512 x 6 rows over 1-2k
@@ -293,7 +326,7 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
         Piece p;
         const bool more = w.next(a, p);
         if (it == 0 && lane == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more, blockIdx.x);
-        wait_phase(fd, &fd->pd_empty[it % kRing], ((it / kRing) & 1) ^ 1, a.stats);
+        if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_empty[it % kRing], ((it / kRing) & 1) ^ 1))) break;
         PieceInfo *pi = &fd->pd[it % kRing];
         const bool own = more && p.seg >= a.n_groups, tree = own && a.bt.parents != nullptr;
         if (more && tree) {

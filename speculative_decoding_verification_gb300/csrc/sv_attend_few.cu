@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         return;
     }
     if (tid == 0) {
-        feed_init(fd, kFewReaders);
+        feed_init(fd, a, kFewReaders);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i][0], 1);
             mbar_init(&ms->s_full[i][1], 1);
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + gr) : "memory"); };
         for (int it = 0;; ++it) {
             const PieceInfo *pi = &fd->pd[it % kRing];
-            wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
+            if (!wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1)) break;
             __syncwarp();
             const int k0 = pi->k0, k1 = pi->k1;
             if (k0 >= k1) break;
@@ -161,13 +161,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             for (int k = begin; k < k1; k += 2, ++u) {
                 const int buf = u & 1;
                 const uint32_t colS = base + (gr * 2 + buf) * 32;
-                wait_phase(fd, &ms->s_full[gr][buf], (u >> 1) & 1, a.stats);
+                wait_phase(fd, &ms->s_full[gr][buf], (u >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
                 const bool masked = key0 + (k + 1) * kTcKeys > ctx;
                 const uint32_t sees = masked ? rows_that_see(pi, key0 + k * kTcKeys + t, a.G, a.bt.n) : 0xFFFFFFFFu;
                 // the group's previous product has read the weights and written the output
-                if (u > 0) wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
+                if (u > 0) wait_phase(fd, &ms->p_done[gr], (u - 1) & 1);
                 __syncwarp();
                 tc_fence_after();
                 // The scores less their maxima (step 0); where one passes 2^8, and on the group's first tile, the scores as they are
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                     // Values that are not finite are replaced by zeros; they are added here for the rows that see them, with the
                     // weights that the product would have used.
                     const uint32_t vs = pi->seq + 2 * (k - k0) + 1, stage = vs % S::STAGES;
-                    wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
+                    wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1);
                     __syncwarp();
                     scan_values<DP>(sbase + S::OFF_KV + stage * S::TILE, t, fd->vflag[stage]);
                     group_sync();   // the flags and every token's weights are written
@@ -262,7 +262,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                             if (!((*reinterpret_cast<volatile uint32_t *>(&fd->vflag[stage][j >> 5]) >> (j & 31)) & 1u)) continue;
                             const int kk = key0 + k * kTcKeys + j;
                             const uint32_t sees = rows_that_see(pi, kk, a.G, a.bt.n);
+                            if (kk >= pi->end) continue;   // flags mean nothing after a wait gave up
                             const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, kk);
+                            if (off < 0) continue;
                             const float v = t < a.c.head_dim
                                                 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a.c.v + off + pi->h * a.c.head_b)[t] << 16)
                                                 : 0.0f;
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 const int i = lane / a.G, g = lane - i * a.G;
                 ms->to[ga][lane] = (int64_t)(r0 + i) * a.o_row + (int64_t)(qh0 + g) * a.o_head;
             }
-            wait_phase(fd, &ms->p_done[gr], (u - 1) & 1, a.stats);
+            wait_phase(fd, &ms->p_done[gr], (u - 1) & 1);
             end_sync();
             tc_fence_after();
             // Four rows at a time, the groups taking turns.  Rolled: a piece of one tile goes through all of this once, and the
@@ -377,8 +379,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             uint32_t late_seq = 0, late_u = 0;
             auto weigh = [&]() {
                 const uint32_t stage = late_seq % S::STAGES;
-                wait_phase(fd, &fd->kv_full[stage], (late_seq / S::STAGES) & 1, a.stats);
-                wait_phase(fd, &ms->p_full[late_gr], late_u & 1, a.stats);
+                wait_phase(fd, &fd->kv_full[stage], (late_seq / S::STAGES) & 1);
+                wait_phase(fd, &ms->p_full[late_gr], late_u & 1);
                 __syncwarp();
                 if (late_rows) fence_async_smem();
                 tc_fence_after();
@@ -393,18 +395,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 }
                 __syncwarp();
             };
-            // Waits for what the next scores need; the weighted sum does not wait for it too.
-            auto ready = [&](uint64_t *bar, uint32_t parity) {
+            // Before a wait for what the next scores need: the weighted sum does not wait for it too.
+            auto weigh_first = [&](uint64_t *bar, uint32_t parity) {
                 if (late && !__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) {
                     weigh();
                     late = 0;
                 }
-                wait_phase(fd, bar, parity, a.stats);
+            };
+            auto ready = [&](uint64_t *bar, uint32_t parity) {
+                weigh_first(bar, parity);
+                wait_phase(fd, bar, parity);
                 __syncwarp();
             };
             for (int it = 0;; ++it) {
                 const PieceInfo *pi = &fd->pd[it % kRing];
-                ready(&fd->pd_full[it % kRing], (it / kRing) & 1);
+                weigh_first(&fd->pd_full[it % kRing], (it / kRing) & 1);
+                if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1))) break;
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 if (nk <= 0) break;
                 const int rows_from = __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             }
             if (late) weigh();
             if (elect_one()) mma_commit(&ms->done);
-            wait_phase(fd, &ms->done, 0, a.stats);
+            wait_phase<true>(fd, &ms->done, 0);   // the products end by themselves
             __syncwarp();
         } else if (warp == 13) {
             feed_walk(a, a2, fd, ms->walk, lane);
@@ -457,6 +463,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && fd->dead) feed_drain<S::STAGES>(fd, a.stats);
     if (warp == 12) tmem_free(tmem, 256);
     pdl_wait();   // launched beside the prefixes' kernel: done only when that is, for the join waits for this one
 }

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
         return;
     }
     if (tid == 0) {
-        feed_init(fd, kTallReaders);
+        feed_init(fd, a, kTallReaders);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i], 1);
             mbar_init(&ms->p_half[i], 4);
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
         const float c = a.scale_log2;
         for (int it = 0;; ++it) {
             PieceInfo *pi = &fd->pd[it % kRing];
-            wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
+            if (!wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1)) break;
             const int k0 = pi->k0, k1 = pi->k1;
             if (k0 >= k1) break;
             __syncwarp();
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
             float m_used = -INFINITY, l = 0.0f;
             const int step = two ? 1 : 2, begin = two ? k0 : k0 + st;
             for (int k = begin; k < k1; k += step) {
-                wait_phase(fd, &ms->s_full[st], s_phase, a.stats);
+                wait_phase(fd, &ms->s_full[st], s_phase);
                 s_phase ^= 1;
                 __syncwarp();
                 const int first = key0 + k * kTcKeys;
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 const uint32_t vs = seq + 2 * (k - k0) + 1, vstage = vs % S::STAGES;
                 if (own && masked) {
                     if (!two || st == 0) {
-                        wait_phase(fd, &fd->kv_full[vstage], (vs / S::STAGES) & 1, a.stats);
+                        wait_phase(fd, &fd->kv_full[vstage], (vs / S::STAGES) & 1);
                         __syncwarp();
                         scan_values<DP>(smem_addr(smem) + S::OFF_KV + vstage * S::TILE, row, fd->vflag[vstage]);
                     }
@@ -255,7 +255,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                                 tc_wait_ld();
                                 const float w = j & 1 ? bf16_hi(pw) + bf16_hi(rw) : bf16_lo(pw) + bf16_lo(rw);
                                 const bool sees = (mine >> b) & 1u;
+                                if (first + j >= end) continue;   // flags mean nothing after a wait gave up
                                 const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, first + j);
+                                if (off < 0) continue;
                                 const char *v = a.c.v + off + pi->h * a.c.head_b;
 #pragma unroll 1
                                 for (int d = 0; d < a.c.head_dim; d += 32) {
@@ -297,14 +299,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 l_all = st == 0 ? l * mine + o.y * other : o.y * other + l * mine;
                 f0 = st == 0 ? mine : other;
                 f1 = st == 0 ? other : mine;
-                wait_phase(fd, &ms->o_full[0], o_phases & 1, a.stats);
+                wait_phase(fd, &ms->o_full[0], o_phases & 1);
                 o_phases ^= 1;
                 if (has1) {
-                    wait_phase(fd, &ms->o_full[1], (o_phases >> 1) & 1, a.stats);
+                    wait_phase(fd, &ms->o_full[1], (o_phases >> 1) & 1);
                     o_phases ^= 2;
                 }
             } else {
-                wait_phase(fd, &ms->o_full[st], (o_phases >> st) & 1, a.stats);
+                wait_phase(fd, &ms->o_full[st], (o_phases >> st) & 1);
                 o_phases ^= 3;   // the other stream's warps see that one
             }
             __syncwarp();
@@ -381,8 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
             int qnext = 0;
             for (int it = 0;; ++it) {
                 const PieceInfo *pi = &fd->pd[it % kRing];
-                wait_phase(fd, &fd->pd_full[it % kRing], (it / kRing) & 1, a.stats);
-                __syncwarp();
+                if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1))) break;
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 const bool two = __shfl_sync(0xFFFFFFFFu, pi->vr, 0) > 128;
                 if (nk <= 0) break;
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 const int jobs = two ? 2 * nk : nk, shift = two ? 1 : 0;
                 for (int t = 0; t < (two ? 2 : 1); ++t) {
                     const int qs = two ? t : qnext;
-                    wait_phase(fd, &fd->q_full[qs], (q_phases >> qs) & 1, a.stats);
+                    wait_phase(fd, &fd->q_full[qs], (q_phases >> qs) & 1);
                     q_phases ^= 1u << qs;
                 }
                 __syncwarp();
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 auto keys_bar = [&](int n) { return &fd->kv_full[(seq + 2 * (n >> shift)) % S::STAGES]; };
                 auto keys_phase = [&](int n) { return ((seq + 2 * (n >> shift)) / S::STAGES) & 1; };
                 auto keys_wait = [&](int n) {
-                    wait_phase(fd, keys_bar(n), keys_phase(n), a.stats);
+                    wait_phase(fd, keys_bar(n), keys_phase(n));
                     __syncwarp();
                     if ((n >> shift) >= rows_from) fence_async_smem();
                     tc_fence_after();
@@ -436,12 +437,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                     const bool next = n + 2 < jobs;
                     bool ready = next && __all_sync(0xFFFFFFFFu, mbar_test_wait(keys_bar(n + 2), keys_phase(n + 2)));
                     if (ready && ((n + 2) >> shift) >= rows_from) fence_async_smem();
-                    wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1, a.stats);
+                    wait_phase(fd, &fd->kv_full[stage], (vs / S::STAGES) & 1);
                     // Half of the tokens at a time, so that one half's products run while the other's weights are made; of each
                     // the weights' upper parts, then the lower ones.
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        wait_phase(fd, half ? &ms->p_full[s] : &ms->p_half[s], phase, a.stats);
+                        wait_phase(fd, half ? &ms->p_full[s] : &ms->p_half[s], phase);
                         __syncwarp();
                         if (half == 0 && tile >= rows_from) fence_async_smem();
                         tc_fence_after();
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 seq += 2 * nk;
             }
             if (elect_one()) mma_commit(&ms->done);
-            wait_phase(fd, &ms->done, 0, a.stats);
+            wait_phase<true>(fd, &ms->done, 0);   // the products end by themselves
             __syncwarp();
         } else if (warp == 13) {
             // ------------------------------------------------------------ the walk
@@ -479,6 +480,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && fd->dead) feed_drain<S::STAGES>(fd, a.stats);
     if (warp == 12) tmem_free(tmem, 512);
 }
 

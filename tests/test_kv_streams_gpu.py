@@ -144,3 +144,33 @@ def test_threads_with_other_head_widths(sv):
         t.join()
     assert not errors
     assert all(call.same(x) for call, to in zip(calls, got) for x in to)
+
+
+@pytest.mark.parametrize("B,n,heads,kv,dim,longest,pre", [(7, 4, 8, 2, 128, 3000, 0), (9, 3, 4, 4, 64, 2500, 0), (5, 40, 8, 2, 128, 2000, 0),
+                                                          (4, 150, 4, 2, 64, 1500, 0), (60, 4, 16, 8, 128, 1700, 1152),
+                                                          (160, 1, 8, 8, 64, 500, 0)])
+def test_waits_that_give_up(sv, B, n, heads, kv, dim, longest, pre):
+    """A barrier that nothing completes: the waits give up, the call ends with a report, and calls after it are as before it."""
+    g = torch.Generator().manual_seed(n)
+    ctx = [longest - 5 * (b % 40) for b in range(B)]
+    c = Cache(B, BF, ctx, n, kv, dim, 16, groups=[(0, pre)] if pre else None)
+    for b in range(B):
+        c.put(b, ctx[b], torch.randn((n, kv, dim), generator=g), torch.randn((n, kv, dim), generator=g))
+    q = torch.randn((B, n, heads, dim), generator=g).to(BF).cuda()
+
+    def run():
+        st = sv.new_stats("cuda")
+        out, lse = sv.sv_kv_attend(q, c.k, c.v, lse=True, stats=st, **c.args, **c.group_args)
+        return out, lse, sv.read_stats(st)["status"]
+    out, lse, status = run()
+    assert status == 0
+    lib = sv.load()
+    for limit in (2_000_000, 200_000):   # about 1 and 0.1 ms
+        lib.sv_selftest_attend_stall(limit)
+        try:
+            assert run()[2] == 4   # timed out
+        finally:
+            lib.sv_selftest_attend_stall(0)
+        for _ in range(3):
+            again = run()
+            assert again[2] == 0 and torch.equal(again[0], out) and torch.equal(again[1], lse)
