@@ -16,6 +16,8 @@
 // sum, 64 cycles each) follow one another; the two streams together take 4,060 cycles for a pair of tiles, against 3,077 for the
 // products alone.  64 x 6 rows of 32 heads over a prefix of 32,768 tokens: 213 us, 62% of tensor cycles.  One warp issues for both
 // streams: with a warp a stream their products interleave and each ends later (355 us for the call against 300).
+#include <float.h>
+
 #include "sv_attend_feed.cuh"
 
 namespace sv {
@@ -500,9 +502,9 @@ cudaError_t run_tall(AttendArgs &a, bool negate, cudaStream_t stream) {
 cudaError_t launch_attend_tall(AttendArgs &a, cudaStream_t stream) {
     AttendArgs t = a;
     // The maximum is taken of q.k before the scale, so the scale has to be positive: a negative one negates the queries in the
-    // product, and zero becomes a number too small to tell weights apart.
+    // product, and zero becomes the smallest normal number, which tells weights apart only where q.k passes 10^36.
     const bool negate = a.scale_log2 < 0.0f;
-    t.scale_log2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    t.scale_log2 = fmaxf(fabsf(a.scale_log2), FLT_MIN);
     const cudaError_t e = a.c.head_dim <= 64 ? run_tall<64>(t, negate, stream) : run_tall<128>(t, negate, stream);
     a.geo = t.geo;
     return e;

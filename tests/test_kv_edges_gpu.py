@@ -66,6 +66,18 @@ def test_infinite_values_that_rows_see(sv, kernel, dtype, n, heads, kv, dim, pre
     check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), dim ** -0.5, rows_of(2, n))
 
 
+@pytest.mark.parametrize("kernel,dtype,n,heads,kv,dim", KERNELS)
+@pytest.mark.parametrize("size,scale", [(1.0, 0.0), (1e16, 0.0), (1e16, 1e-33), (1e16, -1e-34)])
+def test_small_scales_of_large_products(sv, kernel, dtype, n, heads, kv, dim, size, scale):
+    """Scores are scale times q.k, however small the one and large the other."""
+    ctx = [300, 40]
+    c = Cache(dim, dtype, ctx, n, kv, dim, 16)
+    q = block(c, 50, n, heads, kv, dim, dtype, size)
+    c.k.mul_(size)
+    out, lse = sv.sv_kv_attend(q, c.k, c.v, lse=True, scale=scale, **c.args)
+    check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), scale, rows_of(2, n))
+
+
 def test_costs_past_30_bits(sv):
     """32,768 rows of two million cached tokens each, which all lie in one page: 1.07e9 key tiles.  32 repeats of a page weigh as the
     page itself, with log(32) more in the log-sum-exp.  A warp adds up to 2^18 weighted values in a row; roundings of alternating
