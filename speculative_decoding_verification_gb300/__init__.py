@@ -686,6 +686,8 @@ def _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
         n = shape[1]
         rows = B * n
         if parents is not None:
+            if parents.dim() == 2 and parents.shape[1] != n - 1:   # would be read with the wrong row length
+                raise ValueError(f"parents must be [B, n - 1] = [{B}, {n - 1}], got {list(parents.shape)}")
             par = _ints(parents, "parents", torch.int32, B * (n - 1), dev)
     else:
         if len(shape) != 3:

@@ -41,3 +41,20 @@ def test_rows_that_meet_the_same_tokens(sv):
     assert attend(sv, 8, **few) == WORKSPACE
     assert attend(sv, 1 << 15, n=2, rows=1 << 15, B=1 << 14, kv=1) == WORKSPACE   # rows * q_heads = 2^30
     assert attend(sv, 1 << 15, n=3, rows=3 << 14, B=1 << 14, kv=1) == INVALID
+
+
+def test_parents_of_another_block_size(sv):
+    """parents [B, m] of trees with other numbers of rows than the block's would be read with the wrong row length."""
+    import types
+
+    import torch
+    host, i32 = types.SimpleNamespace(index=-1), dict(dtype=torch.int32)
+    ctx, table = torch.zeros(3, **i32), torch.zeros(3, 5, **i32)
+
+    def batch(*shape):
+        return sv._kv_batch(host, ctx, table, (3, 4, 8, 64), None, torch.zeros(shape, **i32), None)
+    for shape in ((3, 3), (5, 3), (9,), (20,)):   # as many trees or more; flat arrays hold at least the elements
+        assert batch(*shape)[:2] == (3, 12)
+    for shape in ((3, 4), (3, 2), (9, 1), (12, 4)):
+        with pytest.raises(ValueError, match="parents must be"):
+            batch(*shape)
