@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     Piece p;
     for (int first = 1;; first = 0) {
         const bool more = w.next(a, p);
-        if (first && tid == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more, blockIdx.x);
+        if (first && tid == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more);
         if (!more) break;
         const int m0 = p.t * TM, h = p.h;
         const int32_t *table = a.bt.page_table + p.g.table * a.bt.table_pitch;
@@ -362,11 +362,12 @@ __global__ void __launch_bounds__(256) k_attend_join_tails(const AttendArgs a) {
     pdl_wait();
     const AttendTail t = a.tails[blockIdx.x];
     const int lane = threadIdx.x & 31, m = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (m >= t.vr || t.pieces == 0) return;
+    if (m >= t.vr || t.tiles == 0) return;
     const int i = (t.m0 + m) / a.G, g = t.m0 + m - i * a.G;
     const Ranges r = ranges_of(t.total, a.geo);
-    join_row<ES>(a, t.r0 + i, t.h * a.G + g, t.pieces, lane, [&](int p) {
-        return block_has(r, t.c0 + p, t.at, t.cost, t.tiles) ? (size_t)t.slot + m + (size_t)p * a.geo.TM : kNoSlot;
+    const int c0 = block_of_place(r, t.at);
+    join_row<ES>(a, t.r0 + i, t.h * a.G + g, (int)blockIdx.x - c0 + 1, lane, [&](int p) {
+        return block_has(r, c0 + p, t.at, t.cost, t.tiles) ? (size_t)t.slot + m + (size_t)(c0 + p) * a.geo.TM : kNoSlot;
     });
 }
 

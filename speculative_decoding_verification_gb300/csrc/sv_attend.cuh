@@ -38,12 +38,11 @@ SV_HD constexpr AttendTiles tiles_few32(int rows) { return {rows, 64, 1, 1, 1}; 
 SV_HD constexpr AttendTiles tiles_f32(int rows, int padded_dim) { return {rows, padded_dim == 256 ? 32 : 64, 1, 1, 0}; }
 
 // A unit cut by the ranges of several blocks, left by the block that ends it (only its first piece can): without prefixes
-// these are all that has to be joined.
+// these are all that has to be joined.  The block that begins it is that of place `at`.
 struct AttendTail {
-    long long slot;         // of the first piece; the next ones follow TM slots apart
-    int c0, pieces;         // the first piece's block; blocks up to the last's (0: none)
+    long long slot;         // of the unit; block c's piece is c * TM further
     long long at, total;    // place of the unit's first tile, cost of the launch
-    int cost, tiles;        // of a tile; tiles
+    int cost, tiles;        // of a tile; tiles (0: no such unit)
     int r0, m0, vr, h;
 };
 
@@ -205,9 +204,10 @@ struct Ranges {
     int parts, more;
 };
 
-// a / b, both below 2^31 as a rule.
+// a / b, both below 2^31 as a rule.  The wide division is kept out of the kernels' code, whose size costs them speed.
+__host__ __device__ __noinline__ static long long quotient_wide(long long a, long long b) { return a / b; }
 SV_HD long long quotient(long long a, long long b) {
-    return ((a | b) >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+    return ((a | b) >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : quotient_wide(a, b);
 }
 
 SV_HD Ranges ranges_of(long long total, const AttendGeo &geo) {
@@ -311,14 +311,12 @@ struct Walk {
     }
 };
 
-// Block c's tail, from the walk's first piece p (`more` false: it has none).
-SV_HD AttendTail tail_of(const AttendArgs &a, const Walk &w, const Piece &p, bool more, int c) {
+// A block's tail, from the walk's first piece p (`more` false: it has none).
+SV_HD AttendTail tail_of(const AttendArgs &a, const Walk &w, const Piece &p, bool more) {
     AttendTail t{};
     if (more && p.k0 > 0 && p.k1 == p.kt) {
         t.at = w.head_at + p.at;
-        t.c0 = block_of_place(ranges_of(w.total, a.geo), t.at);
-        t.pieces = c - t.c0 + 1;
-        t.slot = (long long)(unit_slot(a, a.geo, p.g, p.seg < a.n_groups, p.h, p.t) + (size_t)t.c0 * a.geo.TM);
+        t.slot = (long long)unit_slot(a, a.geo, p.g, p.seg < a.n_groups, p.h, p.t);
         t.cost = p.cost;
         t.tiles = p.kt;
         t.total = w.total;

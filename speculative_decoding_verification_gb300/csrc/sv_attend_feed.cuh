@@ -325,7 +325,7 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
     for (int it = 0;; ++it) {
         Piece p;
         const bool more = w.next(a, p);
-        if (it == 0 && lane == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more, blockIdx.x);
+        if (it == 0 && lane == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more);
         if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_empty[it % kRing], ((it / kRing) & 1) ^ 1))) break;
         PieceInfo *pi = &fd->pd[it % kRing];
         const bool own = more && p.seg >= a.n_groups, tree = own && a.bt.parents != nullptr;

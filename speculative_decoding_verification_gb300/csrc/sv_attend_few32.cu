@@ -51,12 +51,13 @@ template <int R>
 __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs a) {
     constexpr int KB = 32 / R;   // tokens of a batch
     __shared__ Walk s_walk;
+    __shared__ Piece s_piece;
+    __shared__ bool s_more;
     __shared__ long long warp_sum[kWarps32];
     extern __shared__ __align__(16) float4 ring[];   // [warp][2][8 tokens][keys, values][D / 4]; at a piece's end [warp][R][D / 4]
     __shared__ float s_m[kWarps32][R], s_l[kWarps32][R];
     walk_start<kThreads32>(a, &s_walk, warp_sum);
     pdl_trigger();
-    Walk w = s_walk;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
     const int D = a.c.head_dim, D4 = D / 4, psize = a.c.page_size;
     const int row = lane % R, slot = lane / R;   // this lane's score of a batch: row, token
@@ -72,11 +73,14 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
         place[i] = c < chunks ? j + 8 * 16 * (c - j * D4) : -1;
     }
     const int step_pages = 64 / psize, step_slots = 64 - step_pages * psize;   // a tile further in the page table
-    Piece p;
     for (int first = 1;; first = 0) {
-        const bool more = w.next(a, p);
-        if (first && tid == 0) a.tails[blockIdx.x] = tail_of(a, w, p, more, blockIdx.x);
-        if (!more) break;
+        if (tid == 0) {
+            s_more = s_walk.next(a, s_piece);
+            if (first) a.tails[blockIdx.x] = tail_of(a, s_walk, s_piece, s_more);
+        }
+        __syncthreads();
+        if (!s_more) break;
+        const Piece p = s_piece;
         const int h = p.h;
         const int32_t *table = a.bt.page_table + p.g.table * a.bt.table_pitch;
         const bool tree = !p.g.chain && p.seg >= a.n_groups;

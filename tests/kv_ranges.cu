@@ -66,7 +66,7 @@ static long long check_launch(AttendArgs a, const AttendTiles &tiles, int s0, in
         Piece p;
         for (bool first = true, more = true; more; first = false) {
             more = w.next(a, p);
-            if (first) tails[c] = tail_of(a, w, p, more, c);
+            if (first) tails[c] = tail_of(a, w, p, more);
             if (!more) break;
             CHECK(p.k0 >= 0 && p.k0 < p.k1 && p.k1 <= p.kt && p.vr > 0 && p.vr <= geo.TM, "block %d", c);
             const size_t slot = unit_slot(a, geo, p.g, p.seg < a.n_groups, p.h, p.t) + (size_t)c * geo.TM;
@@ -108,15 +108,15 @@ static long long check_launch(AttendArgs a, const AttendTiles &tiles, int s0, in
                 CHECK(i == v.size(), "pieces");
                 if (v.size() > 1) {   // its tail
                     const AttendTail &q = tails[v.back().block];
-                    CHECK(q.pieces == u.c1 - u.c0 + 1 && q.c0 == u.c0 && q.at == u.at && q.total == total && q.tiles == kt, "tail");
+                    CHECK(block_of_place(ranges_of(q.total, geo), q.at) == u.c0 && q.at == u.at && q.total == total && q.tiles == kt, "tail");
                     CHECK(q.r0 == g.r0 && q.m0 == t * geo.TM && q.vr == vr && q.h == h, "tail's rows");
-                    for (const Part &x : v) CHECK((size_t)q.slot + (size_t)(x.block - q.c0) * geo.TM == x.slot, "tail's slots");
+                    for (const Part &x : v) CHECK((size_t)q.slot + (size_t)x.block * geo.TM == x.slot, "tail's slots");
                     ++n_tails;
                 }
             }
         }
     }
-    for (const AttendTail &q : tails) n_tails -= q.pieces > 0;
+    for (const AttendTail &q : tails) n_tails -= q.tiles > 0;
     CHECK(n_tails == 0, "tails of nothing");
     for (auto &v : parts) units -= !v.second.empty();
     CHECK(units == 0, "pieces of nothing");
