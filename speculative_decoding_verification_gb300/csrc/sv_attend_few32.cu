@@ -18,7 +18,7 @@ namespace sv {
 
 namespace {
 
-constexpr int kThreads32 = 256, kWarps32 = 8, kMaxDim32 = 128;
+constexpr int kThreads32 = 256, kWarps32 = 8;
 
 // Sum of x[0..31] over the warp's lanes: lane i gets that of x[i].
 __device__ __forceinline__ float sum_lanes(float (&x)[32], int lane) {
@@ -254,9 +254,8 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
 template <int R>
 cudaError_t run_few32(AttendArgs &a, cudaStream_t stream) {
     a.geo.set(tiles_few32(R));
-    constexpr size_t each = (size_t)kWarps32 * 32 * 4;   // bytes an element of width
-    const size_t bytes = each * a.c.head_dim;
-    const int resident = prepare_kernel((const void *)k_attend_few32<R>, kThreads32, bytes, each * kMaxDim32);
+    const size_t bytes = (size_t)kWarps32 * 32 * a.c.head_dim * 4;
+    const int resident = prepare_kernel((const void *)k_attend_few32<R>, kThreads32, bytes);
     if (resident < 1) return cudaErrorInvalidConfiguration;
     a.geo.blocks *= resident < 2 ? 1 : 2;
     k_attend_few32<R><<<a.geo.blocks, kThreads32, bytes, stream>>>(a);

@@ -78,12 +78,17 @@ void profile_end(cudaStream_t s) {
     if (t_prof_end) cudaEventRecord(t_prof_end, s);
 }
 
-int prepare_kernel(const void *func, int threads, size_t smem_bytes, size_t most_bytes) {
-    const size_t opt_in = most_bytes > smem_bytes ? most_bytes : smem_bytes;
-    if (opt_in > 48 * 1024) {
-        if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)opt_in) != cudaSuccess)
-            return 0;
-    }
+cudaError_t opt_in_smem(const void *func, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    std::lock_guard<std::mutex> lk(g_mu);
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, func);
+    if (e != cudaSuccess || (size_t)at.maxDynamicSharedSizeBytes >= bytes) return e;
+    return cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+int prepare_kernel(const void *func, int threads, size_t smem_bytes) {
+    if (opt_in_smem(func, smem_bytes) != cudaSuccess) return 0;
     int blocks = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, func, threads, smem_bytes) != cudaSuccess) return 0;
     return blocks;

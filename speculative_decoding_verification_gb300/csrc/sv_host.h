@@ -23,10 +23,12 @@ bool device_info(DeviceInfo &out);
 void profile_begin(cudaStream_t s);
 void profile_end(cudaStream_t s);
 
-// Opt a kernel into dynamic shared memory and return its resident blocks per SM with `smem_bytes`.  The opt-in is the kernel's,
-// not the launch's: one whose launches differ gives the most any of them takes, so that a thread that is about to launch with
-// more never finds the limit lowered by another.
-int prepare_kernel(const void *func, int threads, size_t smem_bytes, size_t most_bytes = 0);
+// Opt a kernel into `bytes` of dynamic shared memory.  The opt-in is the kernel's, not the launch's: it only ever grows, so that a
+// thread that is about to launch with more never finds it lowered by another.
+cudaError_t opt_in_smem(const void *func, size_t bytes);
+
+// The same, and the kernel's resident blocks per SM with that much (0 on a CUDA error).
+int prepare_kernel(const void *func, int threads, size_t smem_bytes);
 
 inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 

@@ -746,10 +746,8 @@ inline int topn_ring_stages(int n_vec, int S) {
 template <class Args>
 cudaError_t launch_row_clusters(void (*kern)(Args), const Args &args, long long n_rows, int S, size_t smem,
                                 cudaStream_t stream) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(n_rows * S));
     cfg.blockDim = dim3(kThreads);

@@ -174,3 +174,29 @@ def test_waits_that_give_up(sv, B, n, heads, kv, dim, longest, pre):
         for _ in range(3):
             again = run()
             assert again[2] == 0 and torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+def test_threads_with_other_vocabularies(sv):
+    """The same for the top-N kernels, whose shared memory goes by the row length and the count."""
+    cases = [(torch.randn(4, 128256, device="cuda"), 64), (torch.randn(4, 20000, device="cuda"), 8), (torch.randn(300, 50000, device="cuda"), 700),
+             (torch.randn(2, 4000, device="cuda"), 3)]
+    want = [sv.sv_topk_rows(x, n)[:2] for x, n in cases]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in cases], []
+
+    def work(x, n, to):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(1500):
+                    last = sv.sv_topk_rows(x, n)[:2]
+                torch.cuda.current_stream().synchronize()
+                to.append(last)
+        except Exception as e:   # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(x, n, to)) for (x, n), to in zip(cases, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert all(torch.equal(a, b) for w, to in zip(want, got) for x in to for a, b in zip(x, w))
