@@ -78,6 +78,66 @@ def test_small_scales_of_large_products(sv, kernel, dtype, n, heads, kv, dim, si
     check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), scale, rows_of(2, n))
 
 
+@pytest.mark.parametrize("kernel,dtype,n,heads,kv,dim", KERNELS)
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 0.37])
+@pytest.mark.parametrize("pre", [0, 272])
+def test_scales_of_either_sign(sv, kernel, dtype, n, heads, kv, dim, scale, pre):
+    """Every kernel, alone and with a prefix (few rows then go beside the kernel that takes the prefix), chains and trees."""
+    ctx = [pre + 410, pre + 3, pre + 128]
+    c = Cache(n + kv, dtype, ctx, n, kv, dim, 16, groups=[(0, pre)] if pre else None)
+    q = block(c, 60, n, heads, kv, dim, dtype)
+    par = random_tree(c.rng, 3, n) if 1 < n <= 129 else None
+    for parents in (None, par) if par is not None else (None,):
+        kw = {} if parents is None else dict(parents=parents.cuda())
+        out, lse = sv.sv_kv_attend(q, c.k, c.v, lse=True, scale=scale, **kw, **c.args, **c.group_args)
+        check_attend(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), scale, rows_of(3, n), parents)
+
+
+@pytest.mark.parametrize("kernel,dtype,n,heads,kv,dim", KERNELS)
+@pytest.mark.parametrize("pre", [0, 256])
+def test_ragged_in_every_kernel(sv, kernel, dtype, n, heads, kv, dim, pre):
+    """Ragged blocks up to each kernel's rows, over contexts whose units several blocks share; with max_rows left out the number of
+    all rows decides on the kernel."""
+    lens = [n, 0, 1, (n + 1) // 2, n, 0, 1, n]
+    ctx = [pre + x for x in (1900, 40, 700, 3, 128, 0, 2500, 1030)]
+    starts = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    c = Cache(n + dim, dtype, ctx, n, kv, dim, 16, groups=[(0, pre), (5, pre)] if pre else None)
+    q = randn(70, starts[-1], heads, dim, dtype=dtype) * 2
+    for b, m in enumerate(lens):
+        if m:
+            c.put(b, ctx[b], randn(71 + b, m, kv, dim), randn(171 + b, m, kv, dim))
+    rows = [slice(starts[b], starts[b + 1]) for b in range(len(lens))]
+    kw = dict(row_start=torch.tensor(starts, dtype=torch.int32).cuda(), **c.args, **c.group_args)
+    for most in (n, None):
+        st = sv.new_stats("cuda")
+        out, lse = sv.sv_kv_attend(q, c.k, c.v, max_rows=most, lse=True, stats=st, **kw)
+        assert sv.read_stats(st)["status"] == 0
+        check_attend(c, q, out, lse, dim ** -0.5, rows)
+        assert torch.equal(out, sv.sv_kv_attend(q, c.k, c.v, max_rows=most, **kw)[0])
+
+
+@pytest.mark.parametrize("dtype,dim,heads,kv", [(BF, 128, 4, 2), (BF, 64, 4, 1), (F32, 64, 4, 2), (BF, 160, 2, 2)])
+@pytest.mark.parametrize("ctx", [[0, 0], [0, 900], [1111, 64]])
+def test_long_prompts(sv, dtype, dim, heads, kv, ctx):
+    """Prompts of 1,300 and 700 rows in one ragged call, each row over all rows before it; a sample of rows is checked, among them the
+    first and last of row tiles."""
+    lens = [1300, 700]
+    c = Cache(dim, dtype, ctx, 1300, kv, dim, 32)
+    q = randn(80, 2000, heads, dim, dtype=dtype) * 2
+    for b, first in ((0, 0), (1, 1300)):
+        c.put(b, ctx[b], randn(81 + b, lens[b], kv, dim), randn(91 + b, lens[b], kv, dim))
+    out, lse = sv.sv_kv_attend(q, c.k, c.v, row_start=torch.tensor([0, 1300, 2000], dtype=torch.int32).cuda(), max_rows=1300, lse=True, **c.args)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    for b, first in ((0, 0), (1, 1300)):
+        for i in sorted({0, 1, 63, 64, 127, 128, 255, 256, 383, 511, 512, lens[b] // 2 + 1, lens[b] - 2, lens[b] - 1}):
+            at = Cache.__new__(Cache)   # the same cache with the rows before i as its context
+            at.k, at.v, at.table, at.contexts = c.k, c.v, c.table, list(ctx)
+            at.contexts[b] += i
+            r = [slice(0, 0)] * 2
+            r[b] = slice(first + i, first + i + 1)
+            check_attend(at, q, out, lse, dim ** -0.5, r)
+
+
 def test_costs_past_30_bits(sv):
     """32,768 rows of two million cached tokens each, which all lie in one page: 1.07e9 key tiles.  32 repeats of a page weigh as the
     page itself, with log(32) more in the log-sum-exp.  A warp adds up to 2^18 weighted values in a row; roundings of alternating

@@ -58,3 +58,15 @@ def test_parents_of_another_block_size(sv):
     for shape in ((3, 4), (3, 2), (9, 1), (12, 4)):
         with pytest.raises(ValueError, match="parents must be"):
             batch(*shape)
+
+
+def test_packed_structures(sv):
+    """The bytes that the binding passes are those of the structures."""
+    import ctypes
+
+    from speculative_decoding_verification_gb300._abi import KV_BATCH, KV_CACHE, SvKvBatch, SvKvCache
+    cache = (1 << 40, 3 << 41, 5 << 33, 7 << 32, -9, 11, 13, 17, 19, 1)
+    batch = (1 << 40, 3 << 41, 5 << 42, 7 << 43, 9 << 33, 11, 13, 17, 2**31 - 1)
+    for packed, cls, values in ((KV_CACHE, SvKvCache, cache), (KV_BATCH, SvKvBatch, batch)):
+        assert packed.size == ctypes.sizeof(cls)
+        assert packed.pack(*values) == bytes(cls(*values))
