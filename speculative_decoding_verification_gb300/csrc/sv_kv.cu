@@ -122,7 +122,7 @@ struct CommitArgs {
 // slot 1 + j; the path rises, so path[j'] > 1 + j for j' > j and moves in order of j never overwrite
 // a slot that a later move reads.  Only slots of the sequence's own rows are touched: a short block may end where its pages do,
 // and an empty one has no row 0 to keep.
-__global__ void __launch_bounds__(256) k_kv_commit(const CommitArgs a, int es) {
+__global__ void __launch_bounds__(256, 8) k_kv_commit(const CommitArgs a, int es) {
     __shared__ int64_t src[SV_MAX_TREE], dst[SV_MAX_TREE];
     const int b = blockIdx.x % a.bt.B, N = a.bt.n - 1;
     const int64_t layer = blockIdx.x / a.bt.B;
