@@ -581,13 +581,21 @@ sv_status sv_kv_append(const sv_kv_cache *cache, const sv_kv_batch *batch, const
  * and prefix_len[g] is at most the context_len of each of its sequences.
  *
  * Tokens that a row does not see cannot reach it, whatever their keys and values hold (infinities and NaN
- * included); slots past the block are not read.
+ * included); slots past the block are not read.  Infinite values that it sees add up as in exact arithmetic (NaN is possible
+ * where their weight is below 2^-100 of the row's largest).
+ *
+ * Arithmetic.  Scores, their maxima, the sums of weights and values and lse are float32.  In bf16 with heads up to 128 wide, a weight
+ * enters its product with the values as two bf16 parts that hold it within 2^-16 (float32 and wider heads: float32 throughout), and
+ * |scale q.k| stays below 2^30.  Outputs are rounded once.
  *
  *  q, out       dev, strides in elements, 16-byte aligned; out must not overlap q (refused where the two have one row
  *               stride or the same base; interleaved in one allocation is fine).
  *  group_start  dev int32 [n_groups + 1], prefix_len dev int32 [n_groups]; NULL with n_groups 0.
  *  lse          dev float [rows][q_heads] or NULL.
- *  workspace    dev, >= sv_kv_attend_workspace_size(rows, q_heads, head_dim, B, n_groups) bytes, 256-byte aligned.
+ *  workspace    dev, >= sv_kv_attend_workspace_size(rows, q_heads, head_dim, B, n_groups) bytes, 256-byte aligned; no call that may
+ *               run at the same time uses it (a captured call's is its graph's: sv_stream_capture_id).
+ * Groups that do not rise from 0 to B and prefixes that are negative or longer than a context are reported in stats, as the other
+ * checks of device arrays are.
  * Results do not change from run to run: partial sums are joined in a fixed order.
  * Returns SV_ERR_INVALID_ARG as sv_kv_append, and for a q_heads that kv_heads does not divide, a scale that is not
  * finite, n_groups > B, or sizes past these limits: rows * q_heads at most 2^30, B * kv_heads below 2^31, and the product of

@@ -115,7 +115,7 @@ def _current_raw_stream(index):
 
 def _capture_id(index, raw):
     """The capture that `raw`, the current stream of device `index`, belongs to; 0 for none."""
-    if torch._C._cuda_getDevice() == index and not torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_getDevice() == index and not torch._C._cuda_isCurrentStreamCapturing():
         return 0
     return load().sv_stream_capture_id(raw)
 
@@ -133,7 +133,7 @@ class Workspace:
         self._captured = {}               # (device, stream, capture) -> buffers, the largest last
 
     def get(self, nbytes: int, device) -> torch.Tensor:
-        index = torch.device(device).index
+        index = device.index if type(device) is torch.device else torch.device(device).index
         if index is None:
             index = torch.cuda.current_device()
         raw = _current_raw_stream(index)
@@ -751,7 +751,8 @@ def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, paren
     q [B, n, heads, dim] (or [rows, heads, dim] with row_start); the other arguments as sv_kv_append's.  scale defaults to
     dim ** -0.5.  group_start int32 [G+1] and prefix_len int32 [G]: the sequences of a group share their first
     prefix_len tokens, which are read once for all of them.  lse: True, or a float32 tensor of q's shape without
-    the last axis.  Returns (out, lse or None)."""
+    the last axis.  out must not overlap q.  With row_start, max_rows picks the kernel: left out, all rows count as one
+    block's, which is right and may be slower.  Returns (out, lse or None)."""
     lib = _abi.load_packed()
     dev, c_shape, _, cache = _kv_cache(k_cache, v_cache, 4)
     shape, (q_row, q_head) = q.shape, _heads(q, "q", k_cache)

@@ -544,12 +544,13 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     const AttendGeo all{0, n_groups + batch->B, 0, 0, blocks, 1, 1, 0, seg, 0};
     AttendGeo prefix = all, own = all;
     cudaError_t e = cudaSuccess;
-    // bf16 heads up to 128 wide go to the tensor cores; wider ones do not fit their tiles' shared memory.  Where a sequence's own
+    // bf16 heads up to 128 wide go to the tensor cores; wider ones have float32 arithmetic only (two outputs of 256 columns would fill
+    // the tall kernel's tensor memory, and no other form is built).  Where a sequence's own
     // tokens meet few packed rows they have a kernel of their own: up to 32 rows on the tensor cores, with the tokens along the
-    // tile's rows (512 x 6 rows over 1-2k tokens: 523 us, against 1,040 in the tall kernel); up to 8 in float32 by warps (64 single
-    // tokens of 4 rows: 111 us, against 360 in tiles); up to 16 otherwise in tiles of 16 rows.  Beside prefixes too, in a second
+    // tile's rows (512 x 6 rows over 1-2k tokens: 525 us, against 1,040 in the tall kernel); up to 8 in float32 by warps (64 single
+    // tokens of 4 rows: 112 us, against 360 in tiles); up to 16 otherwise in tiles of 16 rows.  Beside prefixes too, in a second
     // launch: 64 x 16 float32 rows over 1.9-3.5k own tokens take 676 us, in the prefixes' tiles of 64 rows 2,230.  On the tensor cores
-    // 64 x 6 rows behind 32k tokens would take 266 us in one launch instead of 293, but twice as long where own tokens outweigh the
+    // 64 x 6 rows behind 32k tokens would take 266 us in one launch instead of 291, but twice as long where own tokens outweigh the
     // prefix, and the lengths are on the device.
     a.geo = all;
     if (!few || n_groups > 0) {

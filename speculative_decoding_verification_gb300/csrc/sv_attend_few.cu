@@ -18,7 +18,7 @@
 //
 // What bounds it: memory.  A tile is 64 KB (heads of 128), 2800 cycles of an SM's share of the measured copy bandwidth; its
 // products take about 700 and its softmax about 1300, which the two groups share.  512 sequences x 6 rows, 8 key heads, 1,024 to
-// 2,048 tokens: 523 us, 6.3 TB/s or 0.93 of the measured copy bandwidth (the tall kernel: 1,040 us).
+// 2,048 tokens: 525 us, 6.3 TB/s or 0.92 of the measured copy bandwidth (the tall kernel: 1,040 us).
 #include "sv_attend_feed.cuh"
 
 namespace sv {

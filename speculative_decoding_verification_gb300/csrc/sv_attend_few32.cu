@@ -7,9 +7,12 @@
 // (31 shuffles, after which lane j R + r has that of token j and row r), each lane does one exponential, and the weights are handed
 // round for the weighted sum.  Warps keep maxima, sums and outputs of their own and are added at the piece's end.
 //
-// What bounds it: issue slots as much as memory (725 instructions a warp and 8 tokens of 4 rows, 62% of slots used).  64 sequences of
-// up to 8,192 tokens, 3 key heads of 80, 4 rows: 111 us, 4.6 TB/s or 0.68 of the measured copy bandwidth.  With the tiles held in
-// registers instead of copied ahead 176 us, in the kernel for any number of rows 360 us.
+// What bounds it: latency of 16 warps an SM, between memory (66% of its peak) and issue slots (51%; 710 instructions a warp and 8
+// tokens of 4 rows).  64 sequences of up to 8,192 tokens, 3 key heads of 80, 4 rows: 112 us, 4.6 TB/s or 0.68 of the measured copy
+// bandwidth.  With the tiles held in registers instead of copied ahead 176 us, in the kernel for any number of rows 360 us.  One
+// thread walks the pieces and leaves them in shared memory: with the walk in every thread's registers 118 us.  The form for 8 rows
+// spills 24 bytes.  From width 116 on the ring leaves room for one block an SM, which costs nothing: 8 key heads of 128 take 355 us, 6.2
+// TB/s or 0.91 of the copy bandwidth, of 112 (two blocks) 356 us, 5.4 TB/s or 0.79.
 #include <type_traits>
 
 #include "sv_attend.cuh"

@@ -1,4 +1,4 @@
-// sv_tc.cuh — the tensor-core instructions of sm_103a that sv_attend_tc.cu uses: tcgen05.mma with operands in shared or
+// sv_tc.cuh — the tensor-core instructions of sm_103a that sv_kv_attend's kernels use: tcgen05.mma with operands in shared or
 // tensor memory, its completion barriers, and the moves between registers and tensor memory.
 #pragma once
 
