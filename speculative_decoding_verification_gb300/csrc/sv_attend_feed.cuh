@@ -40,9 +40,10 @@ struct Feed {
 
 // Waits for a phase; false when it gave up, which one wait does after the limit and from then on every one whose phase has not
 // completed.  The block runs to its end with meaningless results: the producers stop, the products and the softmax go on over the
-// same pieces (its warps meet at barriers, which all have to reach), and feed_drain waits for the copies in flight.  Only descriptions of pieces are still waited for (`patient`): they come from the walk, which waits for nothing but
-// their readers, so that all warps see the same pieces to the last.  A tile then takes microseconds, and that wait's own limit of
-// many seconds is never met.
+// same pieces (its warps meet at barriers, which all have to reach), and feed_drain waits for the copies in flight.  Only
+// descriptions of pieces are still waited for (`patient`): they come from the walk, which waits for nothing but their readers, so
+// that all warps see the same pieces to the last.  A tile then takes microseconds, and that wait's own limit of many seconds is
+// never met.
 template <bool patient = false>
 __device__ __forceinline__ bool wait_phase(Feed *fd, uint64_t *bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;

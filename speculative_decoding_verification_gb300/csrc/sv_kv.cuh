@@ -2,6 +2,8 @@
 // block's rows and depths, and the rotation of a position's pairs.
 #pragma once
 
+#include <utility>
+
 #include "sv_device.cuh"
 #include "sv_host.h"
 
@@ -49,7 +51,7 @@ inline bool same_place(const RowsView &a, const RowsView &b) {
 }
 
 // Whether some byte belongs to both.  Exact for arrays of one row stride (views of one projection interleave without sharing); of arrays
-// with different row strides only those that start at one address are said to.
+// with different row strides, or of thousands of heads with different head strides, only those that start at one address are said to.
 inline bool overlap(RowsView a, RowsView b) {
     if (a.rows < 1 || b.rows < 1) return false;
     if (a.base == b.base) return true;
@@ -60,6 +62,14 @@ inline bool overlap(RowsView a, RowsView b) {
     if (a.rows == 1) a.row = b.row;
     if (b.rows == 1) b.row = a.row;
     if (a.row != b.row) return false;
+    const bool one = a.head == b.head;
+    if (one && a.heads + b.heads > a.rows + b.rows) {   // rows and heads are alike: the longer axis is solved for, the shorter walked
+        std::swap(a.row, a.head);
+        std::swap(a.rows, a.heads);
+        std::swap(b.row, b.head);
+        std::swap(b.rows, b.heads);
+    }
+    if (!one && a.heads * b.heads > 1 << 20) return false;
     // Row r of a and row r + s of b, -a.rows < s < b.rows, are s row strides apart: looks for the s that brings two heads nearest.
     auto meets = [&](int64_t apart) {   // b's head from a's, in one row
         if (a.row == 0) return apart < b.width && -apart < a.width;
@@ -70,8 +80,7 @@ inline bool overlap(RowsView a, RowsView b) {
         }
         return false;
     };
-    const bool one = a.head == b.head;   // then only the heads' difference counts
-    for (int64_t i = 0; i < (one ? 1 : a.heads); ++i)
+    for (int64_t i = 0; i < (one ? 1 : a.heads); ++i)   // with one head stride only the heads' difference counts
         for (int64_t j = one ? 1 - a.heads : 0; j < b.heads; ++j)
             if (meets(d + j * b.head - i * a.head)) return true;
     return false;

@@ -54,6 +54,10 @@ int main() {
             want.append(bool(places(0, ar, ah, ra, ha, width) & places(off, br, bh, rb, heads, width)))
     lines += ["128 32 3 4 32 0 256 32 3 4", "128 32 0 4 32 0 128 32 0 4"]
     want += [True, False]
+    many = 1 << 28   # heads: the answer may not take long
+    lines += [f"0 32 1 {many} 32 {32 * many - 32} 0 32 1 {many}", f"0 32 1 {many} 32 {32 * many} 0 32 1 {many}",
+              f"0 64 1 {many} 32 32 0 64 1 {many}", f"0 64 1 {many} 32 64 0 32 1 {many}"]
+    want += [True, False, False, False]
     got = subprocess.run([str(exe)], input="\n".join(lines), capture_output=True, text=True).stdout
     assert len(got) == len(want)
     wrong = [(x, w) for x, g, w in zip(lines, got, want) if (g == "1") != w]
