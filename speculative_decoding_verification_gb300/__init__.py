@@ -743,6 +743,11 @@ def sv_kv_append(k, v, k_cache, v_cache, context_len, page_table, q=None, q_out=
     return q_out
 
 
+@functools.lru_cache(maxsize=1024)
+def _attend_ws_bytes(rows, heads, dim, B, groups):
+    return load().sv_kv_attend_workspace_size(rows, heads, dim, B, groups)
+
+
 @_on_stream
 def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, parents=None, row_start=None, max_rows=None,
                  group_start=None, prefix_len=None, out=None, lse=False, stats=None, workspace=None, stream=None):
@@ -781,7 +786,7 @@ def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, paren
     st = _stats(stats, dev).data_ptr() if stats is not None else 0
     if rows == 0:
         return out, lse
-    ws = (workspace or _default_ws).get(load().sv_kv_attend_workspace_size(rows, heads, dim, B, groups), dev)
+    ws = (workspace or _default_ws).get(_attend_ws_bytes(rows, heads, dim, B, groups), dev)
     code = _call(dev, stream, lib.sv_kv_attend, cache, batch, q.data_ptr(), q_row, q_head, heads,
                  dim ** -0.5 if scale is None else scale, starts, lens, groups, out.data_ptr(), o_row, o_head,
                  lse.data_ptr() if lse is not None else 0, st, ws.data_ptr(), ws.numel())

@@ -80,11 +80,30 @@ void profile_end(cudaStream_t s) {
 
 cudaError_t opt_in_smem(const void *func, size_t bytes) {
     if (bytes <= 48 * 1024) return cudaSuccess;
+    struct OptIn {
+        const void *func;
+        int device;
+        size_t bytes;
+    };
+    static OptIn known[128];   // asking the driver each time costs a short call 1 us
+    static int n_known = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lk(g_mu);
-    cudaFuncAttributes at;
-    const cudaError_t e = cudaFuncGetAttributes(&at, func);
-    if (e != cudaSuccess || (size_t)at.maxDynamicSharedSizeBytes >= bytes) return e;
-    return cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    OptIn *at = nullptr;
+    for (int i = 0; i < n_known && at == nullptr; ++i)
+        if (known[i].func == func && known[i].device == dev) at = &known[i];
+    if (at != nullptr && at->bytes >= bytes) return cudaSuccess;
+    if (at == nullptr) {
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, func);
+        if (e != cudaSuccess || (size_t)attr.maxDynamicSharedSizeBytes >= bytes) return e;
+        if (n_known < 128) *(at = &known[n_known++]) = {func, dev, 0};
+    }
+    e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && at != nullptr) at->bytes = bytes;
+    return e;
 }
 
 int prepare_kernel(const void *func, int threads, size_t smem_bytes) {
