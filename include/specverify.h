@@ -70,7 +70,8 @@ typedef enum sv_status {
     SV_ERR_NONFINITE = 3,    /* device: a row holds NaN, or its maximum is not finite */
     SV_ERR_TIMEOUT = 4,      /* device: a bounded wait on a shared-memory copy gave up */
     SV_ERR_WORKSPACE = 5,    /* workspace pointer null/misaligned or smaller than required */
-    SV_ERR_BAD_TOKEN = 6     /* device: a token id outside [0, V) */
+    SV_ERR_BAD_TOKEN = 6,    /* device: a token id outside [0, V) */
+    SV_ERR_NO_PAGE = 7       /* device: a pool has no free page left */
 } sv_status;
 
 typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
@@ -629,6 +630,134 @@ sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *batch, const
 sv_status sv_kv_commit(const sv_kv_cache *cache, const sv_kv_batch *batch, int n_layers, int64_t layer_stride,
                        const int32_t *accept_len, const int32_t *path, int32_t *context_out, sv_stats *stats,
                        sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * The cache held in 8 bits (no counterpart on the pages).
+ * k and v hold codes, e4m3 numbers (1 byte: sign, 4 bits of exponent, 3 of fraction; largest 448; 0x7F and 0xFF are NaN), laid out
+ * as sv_kv_cache's elements are.  A page has one scale for each key head, for keys and values apart: byte e at
+ * k_scale + page * scale_page_stride + head * scale_head_stride stands for 2^(e - 127), 255 for NaN.  An element is its code times
+ * its page's and head's scale.  head_dim is a multiple of 16, k and v are 16-byte aligned and the code strides multiples of 16;
+ * scales may lie anywhere.
+ *
+ * A page that sv_kv_append8 or sv_kv_commit8 writes belongs to one sequence alone (sv_kv_fork sees to that): its scale may change.
+ * -------------------------------------------------------------------------------------- */
+typedef struct sv_kv_cache8 {
+    void *k, *v;                                     /* dev, codes */
+    uint8_t *k_scale, *v_scale;                      /* dev */
+    int64_t page_stride, slot_stride, head_stride;   /* bytes */
+    int64_t scale_page_stride, scale_head_stride;    /* bytes */
+    int32_t n_pages, page_size, kv_heads, head_dim;
+} sv_kv_cache8;
+
+/* ----------------------------------------------------------------------------------------
+ * sv_kv_append8 — sv_kv_append to a cache held in 8 bits (no counterpart on the pages).  q, k, v and q_out have type dtype; the
+ * other arguments are sv_kv_append's.
+ * Let a be the largest |x| of the finite elements that the block brings to a page and key head (keys after the rotation, in float32), and E
+ * the smallest integer >= -120 with a <= 448 * 2^E.  A page that holds no cached token yet gets the scale 2^E; one that does gets the
+ * larger of 2^E and its own, and where that is larger, the codes of its cached tokens are rounded to it (to nearest, ties to even).
+ * An element x becomes x / scale, rounded once to nearest, ties to even; infinities and NaN become NaN.
+ * Slots of a page behind the block are left as they are.
+ * -------------------------------------------------------------------------------------- */
+sv_status sv_kv_append8(const sv_kv_cache8 *cache, const sv_kv_batch *batch, sv_dtype dtype, const void *q, int64_t q_row_stride,
+                        int64_t q_head_stride, void *q_out, int64_t q_out_row_stride, int64_t q_out_head_stride,
+                        int q_heads, const void *k, int64_t k_row_stride, int64_t k_head_stride, const void *v,
+                        int64_t v_row_stride, int64_t v_head_stride, const float *inv_freq, int rotary_dim, int style,
+                        float magnitude, sv_stats *stats, sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * sv_kv_attend8 — sv_kv_attend over a cache held in 8 bits (no counterpart on the pages).  q and out have type dtype; the other
+ * arguments, shared prefixes, masks, limits and the workspace (sv_kv_attend_workspace_size) are sv_kv_attend's.
+ * The result is that of sv_kv_attend over a cache of type dtype that holds the elements' values (rounded to bf16 with dtype SV_BF16,
+ * which is exact for scales of 2^-124 and above).
+ * -------------------------------------------------------------------------------------- */
+sv_status sv_kv_attend8(const sv_kv_cache8 *cache, const sv_kv_batch *batch, sv_dtype dtype, const void *q, int64_t q_row_stride,
+                        int64_t q_head_stride, int q_heads, float scale, const int32_t *group_start,
+                        const int32_t *prefix_len, int n_groups, void *out, int64_t out_row_stride,
+                        int64_t out_head_stride, float *lse, sv_stats *stats, void *workspace,
+                        size_t workspace_bytes, sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * sv_kv_commit8 — sv_kv_commit in a cache held in 8 bits (no counterpart on the pages); the other arguments are sv_kv_commit's.
+ * A page that accepted tokens move to (or stay in) gets, in each layer and key head, the largest of its own scale and those of the pages
+ * that they come from; its tokens up to row 0's and the accepted ones are rounded to it.  Other slots of the page keep
+ * their codes: they hold no tokens any more.
+ *  scale_layer_stride   layer l's scales start l * scale_layer_stride bytes after k_scale (after v_scale).
+ * -------------------------------------------------------------------------------------- */
+sv_status sv_kv_commit8(const sv_kv_cache8 *cache, const sv_kv_batch *batch, int n_layers, int64_t layer_stride,
+                        int64_t scale_layer_stride, const int32_t *accept_len, const int32_t *path, int32_t *context_out,
+                        sv_stats *stats, sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * Pages of a cache (no counterpart on the pages): which sequences hold which, for caches of any element type and any number of
+ * layers.
+ *
+ * refs[p] counts who holds page p: each entry of a page table that names it, and whoever else the caller counts (a prompt kept for later
+ * requests, say); 0 means free.  Entries of a page table below 0 name no page.
+ *
+ * A pool describes the layers' pages in bytes: slot `place`, head h of page p in layer l starts
+ * l * layer_stride + p * page_stride + place * slot_stride + h * head_stride bytes after k (after v) and is head_bytes long.
+ * Bases are 16-byte aligned, strides and head_bytes multiples of 16.  k_scale and v_scale are NULL but for a cache held
+ * in 8 bits, whose scales have strides of their own, in bytes.
+ * -------------------------------------------------------------------------------------- */
+typedef struct sv_kv_pool {
+    void *k, *v;                                                              /* dev */
+    uint8_t *k_scale, *v_scale;                                               /* dev or NULL */
+    int64_t layer_stride, page_stride, slot_stride, head_stride, head_bytes;
+    int64_t scale_layer_stride, scale_page_stride, scale_head_stride;
+    int32_t n_layers, n_pages, page_size, kv_heads;
+} sv_kv_pool;
+
+/* ----------------------------------------------------------------------------------------
+ * sv_kv_fork — a new batch of N sequences from an old one of B (no counterpart on the pages; Mirror-SD notes §3.2 continue one
+ * context in several branches, whose shared tokens this keeps once): sequence j of the new continues old
+ * sequence src[j] (several may continue one: beams, drafted branches), and is empty where src[j] is -1.  Old sequences that none continues
+ * are dropped.  With c = context_len[src[j]]:
+ *   - entries below c / page_size name the old sequence's pages, which are shared: nothing of them is copied;
+ *   - where the last tokens fill a page in part, it stays with the first new sequence if nobody else holds it then; every
+ *     other one gets a page of its own, to which the c % page_size tokens (and their page's scales) are copied in all layers;
+ *   - the entries up to slot c + reserve are given pages, the others of the max_pages are -1.
+ * refs_out counts the pages' holders from then on: refs, less the old table's entries, plus the new one's.
+ * New pages are the free ones of the lowest number, in order of sequences and entries.  A page freed by the call may be given out by it.
+ * Slots of pages that a copy does not fill keep their bytes.
+ *
+ *  context_len  dev int32 [B]; page_table dev int32 [B][table_pitch], max_pages used.
+ *  src          dev int32 [N].
+ *  refs         dev int32 [n_pages]; refs_out dev int32 [n_pages], refs itself or no part of it.
+ *  table_out    dev int32 [N][table_out_pitch], max_pages used; context_out dev int32 [N]: neither overlaps an input.
+ *  workspace    dev, >= sv_kv_fork_workspace_size(n_pages, N) bytes, 256-byte aligned, as other calls'.
+ * Device-side checks, in stats: SV_ERR_INVALID_ARG with the sequence for a src outside [-1, B), a context_len that is negative or, with
+ * reserve, passes max_pages * page_size (both treated as -1), a page id >= n_pages, or a token's entry that names no page; with the page for
+ * refs below its holders.  SV_ERR_NO_PAGE with the new sequence where no page is free: its entry is then -1, and what it would have
+ * held is lost with it.  Nothing is read or written out of range for any of these.
+ * Returns SV_ERR_INVALID_ARG for null pointers, sizes below 1, reserve < 0, misaligned bases or strides, B * max_pages or
+ * N * max_pages or N * n_layers above 2^31 - 1, or outputs that overlap inputs.
+ * -------------------------------------------------------------------------------------- */
+size_t sv_kv_fork_workspace_size(int n_pages, int N);
+
+sv_status sv_kv_fork(const sv_kv_pool *pool, const int32_t *refs, const int32_t *context_len, const int32_t *page_table,
+                     int64_t table_pitch, int max_pages, int B, const int32_t *src, int N, int reserve, int32_t *refs_out,
+                     int32_t *table_out, int64_t table_out_pitch, int32_t *context_out, sv_stats *stats, void *workspace,
+                     size_t workspace_bytes, sv_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * sv_kv_compact — moves the pages that are held to the front of the pool (no counterpart on the pages).  With L pages held, the
+ * k-th lowest of them with a number of L or more moves, in all layers, to the k-th lowest free number below L; the others stay.
+ *
+ *  page_table   dev int32 [B][table_pitch], max_pages used, or NULL with B 0 (more tables: call again with their entries in one).
+ *  table_out    as page_table with the new numbers (entries below 0 stay); it may be page_table itself with the same pitch.
+ *  refs, refs_out   as in sv_kv_fork.
+ *  moved_to     dev int32 [n_pages] or NULL: each page's new number, -1 for a free one (for names that are kept elsewhere).
+ *  live         dev int32 [1]: L.
+ *  workspace    dev, >= sv_kv_compact_workspace_size(n_pages) bytes, 256-byte aligned, as other calls'.
+ * An entry that names a free page or none of the pool's stays as it is and is reported in stats (SV_ERR_INVALID_ARG with the
+ * sequence), as refs below 0 are (with the page; they count as free).
+ * Returns SV_ERR_INVALID_ARG as sv_kv_fork.
+ * -------------------------------------------------------------------------------------- */
+size_t sv_kv_compact_workspace_size(int n_pages);
+
+sv_status sv_kv_compact(const sv_kv_pool *pool, const int32_t *refs, const int32_t *page_table, int64_t table_pitch, int max_pages,
+                        int B, int32_t *refs_out, int32_t *table_out, int64_t table_out_pitch, int32_t *moved_to, int32_t *live,
+                        sv_stats *stats, void *workspace, size_t workspace_bytes, sv_stream_t stream);
 
 /* ----------------------------------------------------------------------------------------
  * sv_stream_capture_id — the id of the CUDA graph capture that a stream takes part in, 0 for none

@@ -114,3 +114,113 @@ def commit(k_cache, v_cache, context, page_table, accept_len, path):
         for j in range(accept_len):
             c[:, page[context + 1 + j], place[context + 1 + j]] = moved[:, j]
     return context + 1 + accept_len
+
+
+# ---- the cache held in 8 bits --------------------------------------------------------------------------------------------------
+
+def e4m3_grid(x):
+    """x rounded to the nearest e4m3 number, ties to the even one; |x| at most 448 but for infinities, which become NaN."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        step = np.exp2(np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -6))) - 3)
+        y = np.round(x / step) * step   # half to even
+    return np.where(np.isfinite(x), y, np.nan)
+
+
+def scale_exponent(most):
+    """The smallest exponent, -120 at least, of a power of two that keeps `most` within 448."""
+    m, e = np.frexp(np.asarray(most, np.float64) / 448.0)
+    return np.where(np.asarray(most) > 0, np.maximum(e - (m == 0.5), -120), -120).astype(np.int64)
+
+
+def append8(codes, exps, x, context, page_table):
+    """One sequence's block x [n, heads, dim], rotated already, into codes [pages, size, heads, dim] (as the e4m3 numbers they are) and the
+    exponents of the scales [pages, heads], both in place."""
+    n, size = len(x), codes.shape[1]
+    i = 0
+    while i < n:
+        page, place = int(page_table[(context + i) // size]), (context + i) % size
+        m = min(n - i, size - place)
+        part = x[i:i + m]
+        e = scale_exponent(np.where(np.isfinite(part), np.abs(part), 0.0).max((0, 2)))
+        if place:
+            e = np.maximum(e, exps[page])
+            codes[page, :place] = e4m3_grid(codes[page, :place] * np.exp2(exps[page] - e)[:, None])
+        exps[page] = e
+        codes[page, place:place + m] = e4m3_grid(part * np.exp2(-e)[:, None])
+        i += m
+
+
+def commit8(codes, exps, context, page_table, accept_len, path):
+    """One sequence: the accepted path in codes [layers, pages, size, heads, dim], exps [layers, pages, heads], in place."""
+    size = codes.shape[2]
+
+    def at(slot):
+        return int(page_table[slot // size]), slot % size
+    j = 0
+    while j < accept_len:
+        page, place = at(context + 1 + j)
+        m = min(accept_len - j, size - place)
+        src = [at(context + int(p)) for p in path[j:j + m]]
+        e = np.max([exps[:, page]] + [exps[:, p] for p, _ in src], 0)
+        came = [e4m3_grid(codes[:, p, o] * np.exp2(exps[:, p] - e)[..., None]) for p, o in src]
+        codes[:, page, :place] = e4m3_grid(codes[:, page, :place] * np.exp2(exps[:, page] - e)[:, None, :, None])
+        exps[:, page] = e
+        for k, c in enumerate(came):
+            codes[:, page, place + k] = c
+        j += m
+    return context + 1 + accept_len
+
+
+# ---- pages ---------------------------------------------------------------------------------------------------------------------
+
+def fork(refs, context, table, src, reserve, size):
+    """(table, context, refs, copies) of the new batch: copies (from, to, tokens)."""
+    refs, width = [int(r) for r in refs], len(table[0])
+    for row in table:
+        for p in row:
+            if p >= 0:
+                refs[p] -= 1
+    rows, ctx, keeps = [], [], set()
+    for b in src:
+        c = int(context[b]) if b >= 0 else 0
+        ctx.append(c)
+        rows.append([int(p) for p in table[b][:c // size]] if b >= 0 else [])
+        for p in rows[-1]:
+            refs[p] += 1
+    for j, b in enumerate(src):
+        if b >= 0 and ctx[j] % size and refs[table[b][ctx[j] // size]] == 0:
+            refs[table[b][ctx[j] // size]] = 1
+            keeps.add(j)
+    free = [p for p, r in enumerate(refs) if r == 0]
+    copies = []
+    for j, b in enumerate(src):
+        if b < 0:
+            rows[j] = [-1] * width
+            continue
+        if j in keeps:
+            rows[j].append(int(table[b][ctx[j] // size]))
+        while len(rows[j]) * size < ctx[j] + reserve:
+            p = free.pop(0) if free else -1
+            if len(rows[j]) == ctx[j] // size and ctx[j] % size and p >= 0:
+                copies.append((int(table[b][ctx[j] // size]), p, ctx[j] % size))
+            rows[j].append(p)
+            if p >= 0:
+                refs[p] = 1
+        rows[j] += [-1] * (width - len(rows[j]))
+    return rows, ctx, refs, copies
+
+
+def compact(refs):
+    """(new number of each page, -1 for a free one; refs; pages held)."""
+    refs = [int(r) for r in refs]
+    held = [p for p, r in enumerate(refs) if r > 0]
+    live = len(held)
+    holes = iter([p for p in range(live) if refs[p] <= 0])
+    to = [-1] * len(refs)
+    for p in held:
+        to[p] = p if p < live else next(holes)
+    after = [0] * len(refs)
+    for p in held:
+        after[to[p]] = refs[p]
+    return to, after, live

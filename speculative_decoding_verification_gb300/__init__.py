@@ -21,6 +21,7 @@ from ._abi import (DBG, SV_BF16, SV_F32, SV_MAX_K, STATS_BYTES, STATS_FIELDS, Sv
 
 __all__ = ["sv_verify", "sv_saguaro_sample", "sv_fanout", "sv_cache_keys", "sv_cache_lookup", "sv_topk_rows",
            "sv_mirror_reuse", "sv_rope_frequencies", "sv_rope", "sv_kv_append", "sv_kv_attend", "sv_kv_commit",
+           "sv_kv_append8", "sv_kv_attend8", "sv_kv_commit8", "sv_kv_fork", "sv_kv_compact",
            "sv_selftest_timeout", "sv_selftest_exp2", "read_stats", "load", "status_string",
            "SvError", "Workspace"]
 
@@ -647,9 +648,9 @@ def sv_rope(x, positions, inv_freq, style="half", magnitude=1.0, backward=False,
     return out
 
 
-def _kv_cache(k_cache, v_cache, dims):
-    """(device, shape, strides, packed sv_kv_cache) of paged tensors [pages, page_size, kv_heads, dim] (with a leading layer axis
-    where dims is 5): one shape, dtype, device and set of strides for keys and values."""
+def _paged(k_cache, v_cache, dims):
+    """(device, shape, strides) of paged tensors [pages, page_size, kv_heads, dim] (with a leading layer axis where dims is 5): one shape,
+    dtype, device and set of strides for keys and values."""
     dev = _cuda(k_cache, "k_cache")
     shape, st = k_cache.shape, k_cache.stride()
     if len(shape) != dims:
@@ -662,16 +663,27 @@ def _kv_cache(k_cache, v_cache, dims):
         raise ValueError("k_cache and v_cache must be on one device")
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError("k_cache: the last axis must be contiguous")
+    return dev, shape, st
+
+
+def _kv_cache(k_cache, v_cache, dims):
+    """_paged's, and the packed sv_kv_cache."""
+    dev, shape, st = _paged(k_cache, v_cache, dims)
     return dev, shape, st, _abi.KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), st[-4], st[-3], st[-2], shape[-4], shape[-3],
                                               shape[-2], shape[-1], _dtype_code(k_cache))
 
 
-def _page_table(page_table, B, dev):
+def _on_device(t, name, dev):
+    if t.get_device() != dev.index:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _page_table(page_table, B, dev, name="page_table"):
     """(address, pitch, pages, B) of a page table, checked."""
     shape, st = page_table.shape, page_table.stride()
     if len(shape) != 2 or (B is not None and shape[0] != B) or page_table.dtype is not torch.int32 or \
             page_table.get_device() != dev.index or (st[1] != 1 and shape[1] > 1):
-        raise ValueError(f"page_table must be an int32 [{'B' if B is None else B}, pages] tensor on {dev} with contiguous rows")
+        raise ValueError(f"{name} must be an int32 [{'B' if B is None else B}, pages] tensor on {dev} with contiguous rows")
     return page_table.data_ptr(), st[0], shape[1], shape[0]
 
 
@@ -700,6 +712,39 @@ def _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
     return B, rows, _abi.KV_BATCH.pack(ctx, table, starts, par, pitch, pages, B, max(n, 1), rows)
 
 
+def _append(fn, dev, c_shape, cache, dtype, like, k, v, context_len, page_table, q, q_out, inv_freq, style, magnitude, parents, row_start,
+            max_rows, stats, stream):
+    """The body of sv_kv_append and sv_kv_append8; k, v and q are of the type of `like` and on its device."""
+    shape, (k_row, k_head), (v_row, v_head) = k.shape, _heads(k, "k", like), _heads(v, "v", like)
+    if v.shape != shape or shape[-2:] != c_shape[-2:]:
+        raise ValueError("k and v must share a shape that ends in the cache's [kv_heads, dim]")
+    _, rows, batch = _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
+    freq = rotary = 0
+    if inv_freq is not None:
+        freq, rotary = _ints(inv_freq, "inv_freq", torch.float32, 1, dev), 2 * inv_freq.numel()
+    q_row = q_head = o_row = o_head = heads = q_ptr = o_ptr = 0
+    if q is not None:
+        q_shape, (q_row, q_head) = q.shape, _heads(q, "q", like)
+        if q_shape[:-2] != shape[:-2] or q_shape[-1] != shape[-1]:
+            raise ValueError("q must have the rows and head width of k")
+        if q_out is None:
+            q_out = torch.empty(q_shape, dtype=q.dtype, device=dev)
+        o_row, o_head = _heads(q_out, "q_out", like)
+        if q_out.shape != q_shape:
+            raise ValueError(f"q_out must have shape {tuple(q_shape)}")
+        heads, q_ptr, o_ptr = q_shape[-2], q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = _stats(stats, dev).data_ptr() if stats is not None else 0
+    if rows == 0:
+        return q_out
+    code = _call(dev, stream, fn, cache, batch, *dtype, q_ptr, q_row, q_head, o_ptr, o_row, o_head, heads, k.data_ptr(), k_row,
+                 k_head, v.data_ptr(), v_row, v_head, freq, rotary, _style(style), magnitude, st)
+    if code:
+        _abi.check(fn.__name__, code)
+    return q_out
+
+
 @_on_stream
 def sv_kv_append(k, v, k_cache, v_cache, context_len, page_table, q=None, q_out=None, inv_freq=None, style="half",
                  magnitude=1.0, parents=None, row_start=None, max_rows=None, stats=None, stream=None):
@@ -713,39 +758,51 @@ def sv_kv_append(k, v, k_cache, v_cache, context_len, page_table, q=None, q_out=
     stats where one is passed (new_stats)."""
     lib = _abi.load_packed()
     dev, c_shape, _, cache = _kv_cache(k_cache, v_cache, 4)
-    shape, (k_row, k_head), (v_row, v_head) = k.shape, _heads(k, "k", k_cache), _heads(v, "v", k_cache)
-    if v.shape != shape or shape[-2:] != c_shape[-2:]:
-        raise ValueError("k and v must share a shape that ends in the cache's [kv_heads, dim]")
-    _, rows, batch = _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
-    freq = rotary = 0
-    if inv_freq is not None:
-        freq, rotary = _ints(inv_freq, "inv_freq", torch.float32, 1, dev), 2 * inv_freq.numel()
-    q_row = q_head = o_row = o_head = heads = q_ptr = o_ptr = 0
-    if q is not None:
-        q_shape, (q_row, q_head) = q.shape, _heads(q, "q", k_cache)
-        if q_shape[:-2] != shape[:-2] or q_shape[-1] != shape[-1]:
-            raise ValueError("q must have the rows and head width of k")
-        if q_out is None:
-            q_out = torch.empty(q_shape, dtype=q.dtype, device=dev)
-        o_row, o_head = _heads(q_out, "q_out", k_cache)
-        if q_out.shape != q_shape:
-            raise ValueError(f"q_out must have shape {tuple(q_shape)}")
-        heads, q_ptr, o_ptr = q_shape[-2], q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    st = _stats(stats, dev).data_ptr() if stats is not None else 0
-    if rows == 0:
-        return q_out
-    code = _call(dev, stream, lib.sv_kv_append, cache, batch, q_ptr, q_row, q_head, o_ptr, o_row, o_head, heads, k.data_ptr(), k_row,
-                 k_head, v.data_ptr(), v_row, v_head, freq, rotary, _style(style), magnitude, st)
-    if code:
-        _abi.check("sv_kv_append", code)
-    return q_out
+    return _append(lib.sv_kv_append, dev, c_shape, cache, (), k_cache, k, v, context_len, page_table, q, q_out, inv_freq, style, magnitude,
+                   parents, row_start, max_rows, stats, stream)
 
 
 @functools.lru_cache(maxsize=1024)
 def _attend_ws_bytes(rows, heads, dim, B, groups):
     return load().sv_kv_attend_workspace_size(rows, heads, dim, B, groups)
+
+
+def _attend(fn, dev, c_shape, cache, dtype, like, q, context_len, page_table, scale, parents, row_start, max_rows, group_start, prefix_len, out,
+            lse, stats, workspace, stream):
+    """The body of sv_kv_attend and sv_kv_attend8; q and out are of the type of `like` and on its device."""
+    shape, (q_row, q_head) = q.shape, _heads(q, "q", like)
+    heads, dim = shape[-2], shape[-1]
+    if dim != c_shape[-1]:
+        raise ValueError("q must have the cache's head width")
+    B, rows, batch = _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
+    groups = starts = lens = 0
+    if (group_start is None) != (prefix_len is None):
+        raise ValueError("group_start and prefix_len come together")
+    if prefix_len is not None:
+        groups = prefix_len.numel()
+        lens = _ints(prefix_len, "prefix_len", torch.int32, 1, dev)
+        starts = _ints(group_start, "group_start", torch.int32, groups + 1, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    o_row, o_head = _heads(out, "out", like)
+    if out.shape != shape:
+        raise ValueError(f"out must have shape {tuple(shape)}")
+    if lse is True:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    else:
+        _opt(lse, "lse", torch.float32, rows * heads, dev)
+    st = _stats(stats, dev).data_ptr() if stats is not None else 0
+    if rows == 0:
+        return out, lse
+    ws = (workspace or _default_ws).get(_attend_ws_bytes(rows, heads, dim, B, groups), dev)
+    code = _call(dev, stream, fn, cache, batch, *dtype, q.data_ptr(), q_row, q_head, heads,
+                 dim ** -0.5 if scale is None else scale, starts, lens, groups, out.data_ptr(), o_row, o_head,
+                 lse.data_ptr() if lse is not None else 0, st, ws.data_ptr(), ws.numel())
+    if code:
+        _abi.check(fn.__name__, code)
+    return out, lse
 
 
 @_on_stream
@@ -760,50 +817,12 @@ def sv_kv_attend(q, k_cache, v_cache, context_len, page_table, scale=None, paren
     block's, which is right and may be slower.  Returns (out, lse or None)."""
     lib = _abi.load_packed()
     dev, c_shape, _, cache = _kv_cache(k_cache, v_cache, 4)
-    shape, (q_row, q_head) = q.shape, _heads(q, "q", k_cache)
-    heads, dim = shape[-2], shape[-1]
-    if dim != c_shape[-1]:
-        raise ValueError("q must have the cache's head width")
-    B, rows, batch = _kv_batch(dev, context_len, page_table, shape, row_start, parents, max_rows)
-    groups = starts = lens = 0
-    if (group_start is None) != (prefix_len is None):
-        raise ValueError("group_start and prefix_len come together")
-    if prefix_len is not None:
-        groups = prefix_len.numel()
-        lens = _ints(prefix_len, "prefix_len", torch.int32, 1, dev)
-        starts = _ints(group_start, "group_start", torch.int32, groups + 1, dev)
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=dev)
-    o_row, o_head = _heads(out, "out", k_cache)
-    if out.shape != shape:
-        raise ValueError(f"out must have shape {tuple(shape)}")
-    if lse is True:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    elif lse is False:
-        lse = None
-    else:
-        _opt(lse, "lse", torch.float32, rows * heads, dev)
-    st = _stats(stats, dev).data_ptr() if stats is not None else 0
-    if rows == 0:
-        return out, lse
-    ws = (workspace or _default_ws).get(_attend_ws_bytes(rows, heads, dim, B, groups), dev)
-    code = _call(dev, stream, lib.sv_kv_attend, cache, batch, q.data_ptr(), q_row, q_head, heads,
-                 dim ** -0.5 if scale is None else scale, starts, lens, groups, out.data_ptr(), o_row, o_head,
-                 lse.data_ptr() if lse is not None else 0, st, ws.data_ptr(), ws.numel())
-    if code:
-        _abi.check("sv_kv_attend", code)
-    return out, lse
+    return _attend(lib.sv_kv_attend, dev, c_shape, cache, (), k_cache, q, context_len, page_table, scale, parents, row_start, max_rows,
+                   group_start, prefix_len, out, lse, stats, workspace, stream)
 
 
-@_on_stream
-def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, context_out=None, stats=None, stream=None,
-                 row_start=None):
-    """sv_kv_commit: after sv_tree_verify, move the accepted path's keys and values to consecutive slots in every
-    layer.  k_cache, v_cache [layers, pages, page_size, kv_heads, dim]; accept_len int32 [B] and path int32 [B, N]
-    as sv_tree_verify gives them.  row_start int32 [B+1]: the blocks were ragged, as in sv_kv_append (at most N + 1 rows a
-    sequence).  Returns context_out int32 [B]: context_len + 1 + accept_len, or context_len of an empty block."""
-    lib = _abi.load_packed()
-    dev, c_shape, strides, cache = _kv_cache(k_cache, v_cache, 5)
+def _commit(fn, dev, cache, layers, context_len, page_table, accept_len, path, context_out, stats, stream, row_start):
+    """The body of sv_kv_commit and sv_kv_commit8; layers: their number and strides."""
     B, N = path.shape
     table, pitch, pages, _ = _page_table(page_table, B, dev)
     ctx = _ints(context_len, "context_len", torch.int32, B, dev)
@@ -815,10 +834,180 @@ def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, co
     starts = 0 if row_start is None else _ints(row_start, "row_start", torch.int32, B + 1, dev)
     st = _stats(stats, dev).data_ptr() if stats is not None else 0
     batch = _abi.KV_BATCH.pack(ctx, table, starts, 0, pitch, pages, B, N + 1, B * (N + 1))
-    code = _call(dev, stream, lib.sv_kv_commit, cache, batch, c_shape[0], strides[0], acc, nodes if N else 0, context_out.data_ptr(), st)
+    code = _call(dev, stream, fn, cache, batch, *layers, acc, nodes if N else 0, context_out.data_ptr(), st)
     if code:
-        _abi.check("sv_kv_commit", code)
+        _abi.check(fn.__name__, code)
     return context_out
+
+
+@_on_stream
+def sv_kv_commit(k_cache, v_cache, context_len, page_table, accept_len, path, context_out=None, stats=None, stream=None,
+                 row_start=None):
+    """sv_kv_commit: after sv_tree_verify, move the accepted path's keys and values to consecutive slots in every
+    layer.  k_cache, v_cache [layers, pages, page_size, kv_heads, dim]; accept_len int32 [B] and path int32 [B, N]
+    as sv_tree_verify gives them.  row_start int32 [B+1]: the blocks were ragged, as in sv_kv_append (at most N + 1 rows a
+    sequence).  Returns context_out int32 [B]: context_len + 1 + accept_len, or context_len of an empty block."""
+    lib = _abi.load_packed()
+    dev, c_shape, strides, cache = _kv_cache(k_cache, v_cache, 5)
+    return _commit(lib.sv_kv_commit, dev, cache, (c_shape[0], strides[0]), context_len, page_table, accept_len, path, context_out, stats, stream,
+                   row_start)
+
+
+def _cache8(k_cache, v_cache, k_scale, v_scale, dims):
+    """(device, shape, strides, strides of the scales) of a cache held in 8 bits: codes [pages, page_size, kv_heads, dim], scales [pages,
+    kv_heads] (with a leading layer axis each where dims is 5), one set of strides for keys and values."""
+    dev, shape, st = _paged(k_cache, v_cache, dims)
+    if k_cache.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"k_cache and v_cache must be torch.float8_e4m3fn, got {k_cache.dtype}")
+    return dev, shape, st, _scales(k_scale, v_scale, shape, dev)
+
+
+def _scales(k_scale, v_scale, shape, dev):
+    want, st = shape[:-3] + shape[-2:-1], k_scale.stride()
+    if k_scale.dtype not in (torch.uint8, torch.float8_e8m0fnu) or v_scale.dtype is not k_scale.dtype:
+        raise TypeError("k_scale and v_scale must both be torch.float8_e8m0fnu or torch.uint8 (biased exponents)")
+    if k_scale.shape != want or v_scale.shape != want or v_scale.stride() != st:
+        raise ValueError(f"k_scale and v_scale must have shape {tuple(want)} and one set of strides")
+    if k_scale.get_device() != dev.index or v_scale.get_device() != dev.index:
+        raise ValueError(f"k_scale and v_scale must be on {dev}")
+    return st
+
+
+def _pack8(k_cache, v_cache, k_scale, v_scale, shape, st, sst):
+    return _abi.KV_CACHE8.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), st[-4], st[-3], st[-2], sst[-2],
+                               sst[-1], shape[-4], shape[-3], shape[-2], shape[-1])
+
+
+@_on_stream
+def sv_kv_append8(k, v, k_cache, v_cache, k_scale, v_scale, context_len, page_table, q=None, q_out=None, inv_freq=None, style="half",
+                  magnitude=1.0, parents=None, row_start=None, max_rows=None, stats=None, stream=None):
+    """sv_kv_append8: sv_kv_append to a cache held in 8 bits.
+
+    k_cache, v_cache float8_e4m3fn [pages, page_size, kv_heads, dim]; k_scale, v_scale float8_e8m0fnu (or uint8, the same
+    bytes) [pages, kv_heads].  The other arguments are sv_kv_append's; k, v and q are float32 or bfloat16.  A page that the
+    block writes belongs to one sequence alone: its scale may grow, and its earlier codes are then rounded to it."""
+    lib = _abi.load_packed()
+    dev, c_shape, st, sst = _cache8(k_cache, v_cache, k_scale, v_scale, 4)
+    _on_device(k, "k", dev)
+    return _append(lib.sv_kv_append8, dev, c_shape, _pack8(k_cache, v_cache, k_scale, v_scale, c_shape, st, sst), (_dtype_code(k),), k, k, v,
+                   context_len, page_table, q, q_out, inv_freq, style, magnitude, parents, row_start, max_rows, stats, stream)
+
+
+@_on_stream
+def sv_kv_attend8(q, k_cache, v_cache, k_scale, v_scale, context_len, page_table, scale=None, parents=None, row_start=None, max_rows=None,
+                  group_start=None, prefix_len=None, out=None, lse=False, stats=None, workspace=None, stream=None):
+    """sv_kv_attend8: sv_kv_attend over a cache held in 8 bits (arrays as sv_kv_append8's; the other arguments as
+    sv_kv_attend's; q and out are float32 or bfloat16).  Returns (out, lse or None)."""
+    lib = _abi.load_packed()
+    dev, c_shape, st, sst = _cache8(k_cache, v_cache, k_scale, v_scale, 4)
+    _on_device(q, "q", dev)
+    return _attend(lib.sv_kv_attend8, dev, c_shape, _pack8(k_cache, v_cache, k_scale, v_scale, c_shape, st, sst), (_dtype_code(q),), q, q,
+                   context_len, page_table, scale, parents, row_start, max_rows, group_start, prefix_len, out, lse, stats, workspace, stream)
+
+
+@_on_stream
+def sv_kv_commit8(k_cache, v_cache, k_scale, v_scale, context_len, page_table, accept_len, path, context_out=None, stats=None, stream=None,
+                  row_start=None):
+    """sv_kv_commit8: sv_kv_commit in a cache held in 8 bits: k_cache, v_cache float8_e4m3fn [layers, pages, page_size, kv_heads, dim],
+    k_scale, v_scale [layers, pages, kv_heads] as sv_kv_append8's.  Returns context_out."""
+    lib = _abi.load_packed()
+    dev, c_shape, st, sst = _cache8(k_cache, v_cache, k_scale, v_scale, 5)
+    return _commit(lib.sv_kv_commit8, dev, _pack8(k_cache, v_cache, k_scale, v_scale, c_shape, st, sst), (c_shape[0], st[0], sst[0]),
+                   context_len, page_table, accept_len, path, context_out, stats, stream, row_start)
+
+
+def _kv_pool(k_cache, v_cache, k_scale, v_scale):
+    """(device, pages, packed sv_kv_pool) of caches [layers, pages, page_size, kv_heads, dim] of any element type."""
+    dev, shape, st = _paged(k_cache, v_cache, 5)
+    es = k_cache.element_size()
+    scale_at, sst = (0, 0), (0, 0, 0)
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale come together")
+    if k_scale is not None:
+        sst = _scales(k_scale, v_scale, shape, dev)
+        scale_at = k_scale.data_ptr(), v_scale.data_ptr()
+    elif es == 1:
+        raise ValueError("a cache held in 8 bits has scales: pass k_scale and v_scale")
+    return dev, shape[1], _abi.KV_POOL.pack(k_cache.data_ptr(), v_cache.data_ptr(), *scale_at, st[0] * es, st[1] * es, st[2] * es, st[3] * es,
+                                            shape[4] * es, *sst, shape[0], shape[1], shape[2], shape[3])
+
+
+def _table_out(table_out, shape, dev, name="table_out"):
+    """table_out or a new one, (address, pitch) of its rows."""
+    if table_out is None:
+        table_out = torch.empty(shape, dtype=torch.int32, device=dev)
+    at, pitch, pages, _ = _page_table(table_out, shape[0], dev, name)
+    if pages != shape[1]:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return table_out, at, pitch
+
+
+@functools.lru_cache(maxsize=1024)
+def _fork_ws_bytes(pages, n):
+    return load().sv_kv_fork_workspace_size(pages, n)
+
+
+@functools.lru_cache(maxsize=1024)
+def _compact_ws_bytes(pages):
+    return load().sv_kv_compact_workspace_size(pages)
+
+
+@_on_stream
+def sv_kv_fork(k_cache, v_cache, page_refs, context_len, page_table, src, reserve=0, k_scale=None, v_scale=None, refs_out=None, table_out=None,
+               context_out=None, stats=None, workspace=None, stream=None):
+    """sv_kv_fork: a new batch whose sequence j continues sequence src[j] of the old one (-1: an empty sequence).
+
+    k_cache, v_cache [layers, pages, page_size, kv_heads, dim] of any type (with k_scale, v_scale [layers, pages, kv_heads] where
+    they are held in 8 bits); page_refs int32 [pages]: holders of each page, 0 free; context_len int32 [B]; page_table int32 [B,
+    max_pages], -1 where an entry names no page; src int32 [N].  Full pages are shared, a partly filled one is copied for all but its
+    first new sequence, entries up to slot context + reserve are given free pages.  refs_out may be page_refs.
+    Returns (table_out [N, max_pages], context_out [N], refs_out [pages])."""
+    lib = _abi.load_packed()
+    dev, pages, pool = _kv_pool(k_cache, v_cache, k_scale, v_scale)
+    table, pitch, width, B = _page_table(page_table, None, dev)
+    ctx = _ints(context_len, "context_len", torch.int32, B, dev)
+    refs = _ints(page_refs, "page_refs", torch.int32, pages, dev)
+    N = src.numel()
+    of = _ints(src, "src", torch.int32, N, dev)
+    table_out, to, to_pitch = _table_out(table_out, (N, width), dev)
+    context_out = _out(context_out, "context_out", torch.int32, (N,), dev)
+    refs_out = _out(refs_out, "refs_out", torch.int32, (pages,), dev)
+    st = _stats(stats, dev).data_ptr() if stats is not None else 0
+    ws = (workspace or _default_ws).get(_fork_ws_bytes(pages, N), dev)
+    code = _call(dev, stream, lib.sv_kv_fork, pool, refs, ctx, table, pitch, width, B, of, N, int(reserve), refs_out.data_ptr(), to, to_pitch,
+                 context_out.data_ptr(), st, ws.data_ptr(), ws.numel())
+    if code:
+        _abi.check("sv_kv_fork", code)
+    return table_out, context_out, refs_out
+
+
+@_on_stream
+def sv_kv_compact(k_cache, v_cache, page_refs, page_table=None, k_scale=None, v_scale=None, refs_out=None, table_out=None, moved_to=None,
+                  live=None, stats=None, workspace=None, stream=None):
+    """sv_kv_compact: the pages that are held move to the pool's front, in every layer.
+
+    Caches, scales and page_refs as sv_kv_fork's; page_table int32 [B, max_pages] or None; refs_out may be page_refs and table_out
+    page_table.  moved_to int32 [pages] or None takes each page's new number (-1: it was free).
+    Returns (table_out or None, refs_out, live int32 [1])."""
+    lib = _abi.load_packed()
+    dev, pages, pool = _kv_pool(k_cache, v_cache, k_scale, v_scale)
+    table = pitch = width = B = to = to_pitch = 0
+    if page_table is not None:
+        table, pitch, width, B = _page_table(page_table, None, dev)
+        table_out, to, to_pitch = _table_out(table_out, (B, width), dev)
+    elif table_out is not None:
+        raise ValueError("table_out without page_table")
+    refs = _ints(page_refs, "page_refs", torch.int32, pages, dev)
+    refs_out = _out(refs_out, "refs_out", torch.int32, (pages,), dev)
+    moved = 0 if moved_to is None else _ints(moved_to, "moved_to", torch.int32, pages, dev)
+    live = _out(live, "live", torch.int32, (1,), dev)
+    st = _stats(stats, dev).data_ptr() if stats is not None else 0
+    ws = (workspace or _default_ws).get(_compact_ws_bytes(pages), dev)
+    code = _call(dev, stream, lib.sv_kv_compact, pool, refs, table, pitch, width, B, refs_out.data_ptr(), to, to_pitch, moved, live.data_ptr(),
+                 st, ws.data_ptr(), ws.numel())
+    if code:
+        _abi.check("sv_kv_compact", code)
+    return table_out, refs_out, live
 
 
 @_on_stream

@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 c_int, c_i32p, c_i64, c_f32, c_f64 = ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_double
 c_vp, c_size = ctypes.c_void_p, ctypes.c_size_t
 
-SV_OK, SV_ERR_INVALID_ARG, SV_ERR_CUDA, SV_ERR_NONFINITE, SV_ERR_TIMEOUT, SV_ERR_WORKSPACE, SV_ERR_BAD_TOKEN = range(7)
+SV_OK, SV_ERR_INVALID_ARG, SV_ERR_CUDA, SV_ERR_NONFINITE, SV_ERR_TIMEOUT, SV_ERR_WORKSPACE, SV_ERR_BAD_TOKEN, SV_ERR_NO_PAGE = range(8)
 SV_F32, SV_BF16 = 0, 1
 SV_DEBUG_FIELDS = 8
 SV_MAX_K = 32
@@ -46,10 +46,26 @@ class SvKvBatch(ctypes.Structure):
                 ("B", ctypes.c_int32), ("n", ctypes.c_int32), ("rows", ctypes.c_int32)]
 
 
+class SvKvCache8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class SvKvPool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("head_bytes", ctypes.c_int64), ("scale_layer_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64), ("n_layers", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32)]
+
+
 STATS_FIELDS = [f for f, _ in SvStats._fields_]
 STATS_BYTES = ctypes.sizeof(SvStats)
 
 c_kv, c_bt = ctypes.POINTER(SvKvCache), ctypes.POINTER(SvKvBatch)
+c_kv8, c_pool = ctypes.POINTER(SvKvCache8), ctypes.POINTER(SvKvPool)
 
 # name -> (restype, argtypes); the order follows the header.
 SIGNATURES = {
@@ -92,6 +108,17 @@ SIGNATURES = {
     "sv_kv_attend": (c_int, [c_kv, c_bt, c_vp, c_i64, c_i64, c_int, c_f32, c_vp, c_vp, c_int, c_vp, c_i64, c_i64, c_vp,
                              c_vp, c_vp, c_size, c_vp]),
     "sv_kv_commit": (c_int, [c_kv, c_bt, c_int, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "sv_kv_append8": (c_int, [c_kv8, c_bt, c_int, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_int, c_vp, c_i64, c_i64, c_vp,
+                              c_i64, c_i64, c_vp, c_int, c_int, c_f32, c_vp, c_vp]),
+    "sv_kv_attend8": (c_int, [c_kv8, c_bt, c_int, c_vp, c_i64, c_i64, c_int, c_f32, c_vp, c_vp, c_int, c_vp, c_i64, c_i64,
+                              c_vp, c_vp, c_vp, c_size, c_vp]),
+    "sv_kv_commit8": (c_int, [c_kv8, c_bt, c_int, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "sv_kv_fork_workspace_size": (c_size, [c_int, c_int]),
+    "sv_kv_fork": (c_int, [c_pool, c_vp, c_vp, c_vp, c_i64, c_int, c_int, c_vp, c_int, c_int, c_vp, c_vp, c_i64, c_vp, c_vp,
+                           c_vp, c_size, c_vp]),
+    "sv_kv_compact_workspace_size": (c_size, [c_int]),
+    "sv_kv_compact": (c_int, [c_pool, c_vp, c_vp, c_i64, c_int, c_int, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_size,
+                              c_vp]),
     "sv_stream_capture_id": (ctypes.c_uint64, [c_vp]),
     "sv_set_profile_events": (None, [c_vp, c_vp]),
     "sv_selftest_timeout": (c_int, [c_i64, c_vp, c_vp]),
@@ -100,24 +127,27 @@ SIGNATURES = {
     "sv_selftest_exp2_all": (c_int, [c_f32, c_f32, c_vp, c_vp]),
 }
 
-# The structures as bytes, in the layout of SvKvCache and SvKvBatch: packing one takes a fifth of the time of filling a ctypes
-# structure.
+# The structures as bytes, in the layout of SvKvCache, SvKvCache8, SvKvPool and SvKvBatch: packing one takes a fifth of the time of
+# filling a ctypes structure.
 KV_CACHE = struct.Struct("PPqqqiiiii4x")
+KV_CACHE8 = struct.Struct("PPPPqqqqqiiii")
+KV_POOL = struct.Struct("PPPPqqqqqqqqiiii")
 KV_BATCH = struct.Struct("PPPPqiiii")
 _packed = None
 
 
 def load_packed():
-    """The library with the structures of sv_kv_append, sv_kv_attend and sv_kv_commit passed as KV_CACHE / KV_BATCH bytes."""
+    """The library with the structures of the cache's calls passed as bytes (KV_CACHE, KV_CACHE8, KV_POOL, KV_BATCH)."""
     global _packed
     if _packed is None:
         load()
         lib = ctypes.CDLL(LIB_PATH)
-        for name in ("sv_kv_append", "sv_kv_attend", "sv_kv_commit"):
+        for name in ("sv_kv_append", "sv_kv_attend", "sv_kv_commit", "sv_kv_append8", "sv_kv_attend8", "sv_kv_commit8", "sv_kv_fork",
+                     "sv_kv_compact"):
             res, args = SIGNATURES[name]
             fn = getattr(lib, name)
             fn.restype = res
-            fn.argtypes = [ctypes.c_char_p, ctypes.c_char_p] + args[2:]
+            fn.argtypes = [ctypes.c_char_p if a in (c_kv, c_kv8, c_pool, c_bt) else a for a in args]
         _packed = lib
     return _packed
 

@@ -8,10 +8,12 @@ namespace sv {
 
 constexpr int kAttThreads = 256;
 
-// Four consecutive elements in shared memory, as float32.
+// Four consecutive elements in shared memory, as float32 (ES 1: codes, without their scale).
 template <int ES>
 __device__ __forceinline__ float4 lds4(const char *p) {
-    if constexpr (ES == 4) {
+    if constexpr (ES == 1) {
+        return codes4(*reinterpret_cast<const uint32_t *>(p));
+    } else if constexpr (ES == 4) {
         return *reinterpret_cast<const float4 *>(p);
     } else {
         const uint2 w = *reinterpret_cast<const uint2 *>(p);
@@ -19,8 +21,9 @@ __device__ __forceinline__ float4 lds4(const char *p) {
     }
 }
 
-template <int ES, int DP, int TM>
+template <int ES, int DP, int TM, bool C8>
 struct F32Shape {
+    static constexpr int EC = C8 ? 1 : ES;                  // bytes of a cached element
     static constexpr int TK = DP == 256 ? 32 : 64;
     static constexpr int RG = TM / 4;                       // groups of four rows
     static constexpr int TPR = kAttThreads / RG;            // threads of a row group
@@ -28,24 +31,27 @@ struct F32Shape {
     static constexpr int CG = DP / 4;                       // groups of four columns
     static constexpr int KS = TPR > CG ? TPR / CG : 1;      // keys split over threads in the weighted sum
     static constexpr int NC = TPR > CG ? 1 : CG / TPR;      // column groups of a thread
-    static constexpr int ROW = DP * ES + 16;                // bytes of a key row, padded off the banks
+    static constexpr int ROW = DP * EC + 16;                // bytes of a key row, padded off the banks
     static constexpr int SP = TK + 4;                       // floats of a score row
     static constexpr int ANC = (SV_MAX_TREE + 32) / 32;
     static constexpr size_t OFF_K = (size_t)TM * DP * 4;
     static constexpr size_t OFF_V = OFF_K + 2 * (size_t)TK * ROW;
     static constexpr size_t OFF_S = OFF_V + 2 * (size_t)TK * ROW;
     static constexpr size_t OFF_M = OFF_S + (size_t)TM * SP * 4;
-    static constexpr size_t BYTES = OFF_M + (size_t)TM * 4 * (4 + ANC) + 64;
+    static constexpr size_t OFF_SCALE = OFF_M + (size_t)TM * 4 * (4 + ANC);   // [2][keys, values][TK]
+    static constexpr size_t BYTES = OFF_SCALE + (C8 ? 4 * (size_t)TK * 4 : 0) + 64;
 };
 
 // Scores, softmax and weighted sum in float32 FMA, a tile of TM packed rows by TK keys at a time.  Threads hold
 // 4 rows by NK keys of the scores and 4 rows by 4 NC columns of the output; keys and values are
 // double buffered with asynchronous copies.  For float32 with more rows than few32 takes and for bf16 heads wider than 128: the
 // FMA rate and, with few rows, the four block barriers a tile bound it.
-template <int ES, int DP, int TM>
+// C8: the cache is held in 8 bits.  Codes are copied as they are and become floats as they are read; a key's scale multiplies its
+// score, a value's its elements.
+template <int ES, int DP, int TM, bool C8>
 __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) {
-    using S = F32Shape<ES, DP, TM>;
-    constexpr int TK = S::TK;
+    using S = F32Shape<ES, DP, TM, C8>;
+    constexpr int TK = S::TK, EC = S::EC;
     extern __shared__ __align__(128) char smem[];
     __shared__ Walk s_walk;
     __shared__ long long warp_sum[kAttThreads / 32];
@@ -55,12 +61,13 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
     float *row_m = reinterpret_cast<float *>(smem + S::OFF_M), *row_l = row_m + TM, *row_a = row_l + TM;
     int *row_lim = reinterpret_cast<int *>(row_a + TM);
     uint32_t *row_anc = reinterpret_cast<uint32_t *>(row_lim + TM);
+    float *scale8 = reinterpret_cast<float *>(smem + S::OFF_SCALE);
 
     walk_start<kAttThreads>(a, &s_walk, warp_sum);
     pdl_trigger();
     Walk w = s_walk;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
-    const int D = a.c.head_dim, D4 = D / 4, chunks = D * ES / 16;
+    const int D = a.c.head_dim, D4 = D / 4, chunks = D * EC / 16;
     const int rg = tid / S::TPR, tx = tid % S::TPR;
     const int cx = tx % S::CG, ks = S::KS > 1 ? tx / S::CG : 0;
     Piece p;
@@ -76,6 +83,14 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
             if (lane < TK / 8 && first + lane < p.end) {
                 off = slot_offset(a.c, table, first + lane);
                 if (off < 0) report_error(a.stats, SV_ERR_INVALID_ARG, p.g.table);
+            }
+            if constexpr (C8) {
+                if (lane < TK / 8) {
+                    const int64_t at = off < 0 ? 0 : table[(first + lane) / a.c.page_size] * a.sc.page_b + h * a.sc.head_b;
+                    float *to = scale8 + buf * 2 * TK + wp * (TK / 8) + lane;
+                    to[0] = off < 0 ? 1.0f : scale_of(a.sc.k[at]);
+                    to[TK] = off < 0 ? 1.0f : scale_of(a.sc.v[at]);
+                }
             }
 #pragma unroll
             for (int r = 0; r < TK / 8; ++r) {
@@ -138,10 +153,18 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
                     for (int r = 0; r < 4; ++r) qv[r] = *reinterpret_cast<const float4 *>(sq + (rg * 4 + r) * DP + d * 4);
 #pragma unroll
                     for (int j = 0; j < S::NK; ++j) {
-                        const float4 kv = lds4<ES>(tk + (size_t)(tx + j * S::TPR) * S::ROW + d * 4 * ES);
+                        const float4 kv = lds4<EC>(tk + (size_t)(tx + j * S::TPR) * S::ROW + d * 4 * EC);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             s[r][j] = fmaf(qv[r].x, kv.x, fmaf(qv[r].y, kv.y, fmaf(qv[r].z, kv.z, fmaf(qv[r].w, kv.w, s[r][j]))));
+                    }
+                }
+                if constexpr (C8) {
+#pragma unroll
+                    for (int j = 0; j < S::NK; ++j) {
+                        const float f = scale8[buf * 2 * TK + tx + j * S::TPR];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) s[r][j] *= f;
                     }
                 }
 #pragma unroll
@@ -210,7 +233,11 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
                     for (int u = 0; u < 4; ++u) {
 #pragma unroll
                         for (int c = 0; c < S::NC; ++c) {
-                            const float4 v = lds4<ES>(tv + (size_t)(k4 + u) * S::ROW + (cx + c * S::TPR) * 4 * ES);
+                            float4 v = lds4<EC>(tv + (size_t)(k4 + u) * S::ROW + (cx + c * S::TPR) * 4 * EC);
+                            if constexpr (C8) {
+                                const float f = scale8[buf * 2 * TK + TK + k4 + u];
+                                v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                            }
 #pragma unroll
                             for (int r = 0; r < 4; ++r) {
                                 const float e = u == 0 ? pw[r].x : u == 1 ? pw[r].y : u == 2 ? pw[r].z : pw[r].w;
@@ -425,21 +452,23 @@ cudaError_t launch_attend_join(const AttendArgs &a, const AttendGeo &prefix, con
                    : launch_pdl(k_attend_join<2>, grid, dim3(256), 0, stream, a, prefix, own);
 }
 
-template <int ES, int DP, int TM>
+template <int ES, int DP, int TM, bool C8>
 static cudaError_t run_f32(AttendArgs &a, cudaStream_t stream) {
-    using S = F32Shape<ES, DP, TM>;
-    if (prepare_kernel((const void *)k_attend_f32<ES, DP, TM>, kAttThreads, S::BYTES) < 1) return cudaErrorInvalidConfiguration;
+    using S = F32Shape<ES, DP, TM, C8>;
+    if (prepare_kernel((const void *)k_attend_f32<ES, DP, TM, C8>, kAttThreads, S::BYTES) < 1) return cudaErrorInvalidConfiguration;
     constexpr AttendTiles tiles = tiles_f32(TM, DP);
     static_assert(tiles.TK == S::TK, "the cutting's key tiles are the kernel's");
     a.geo.set(tiles);
-    k_attend_f32<ES, DP, TM><<<a.geo.blocks, kAttThreads, S::BYTES, stream>>>(a);
+    k_attend_f32<ES, DP, TM, C8><<<a.geo.blocks, kAttThreads, S::BYTES, stream>>>(a);
     return cudaGetLastError();
 }
 
 // `small`: tiles of kSmallRows rows.
 cudaError_t launch_attend_f32(AttendArgs &a, int es, bool small, cudaStream_t stream) {
     const int D = a.c.head_dim;
-#define SV_ATT(ES, DP) (small ? run_f32<ES, DP, kSmallRows>(a, stream) : run_f32<ES, DP, 64>(a, stream))
+#define SV_ATT(ES, DP)                                                                                                       \
+    (a.sc.k ? (small ? run_f32<ES, DP, kSmallRows, true>(a, stream) : run_f32<ES, DP, 64, true>(a, stream))                   \
+            : (small ? run_f32<ES, DP, kSmallRows, false>(a, stream) : run_f32<ES, DP, 64, false>(a, stream)))
     if (es == 4) return D <= 64 ? SV_ATT(4, 64) : D <= 128 ? SV_ATT(4, 128) : SV_ATT(4, 256);
     return SV_ATT(2, 256);   // narrower bf16 heads go to the tensor cores
 #undef SV_ATT
@@ -481,44 +510,45 @@ extern "C" size_t sv_kv_attend_workspace_size(int64_t rows, int q_heads, int hea
     return plan_attend(rows, q_heads, head_dim, B, n_groups).bytes;
 }
 
-extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *batch, const void *q,
-                                  int64_t q_row_stride, int64_t q_head_stride, int q_heads, float scale,
-                                  const int32_t *group_start, const int32_t *prefix_len, int n_groups, void *out,
-                                  int64_t out_row_stride, int64_t out_head_stride, float *lse, sv_stats *stats,
-                                  void *workspace, size_t workspace_bytes, sv_stream_t stream) {
-    if (!kv_args_ok(cache, batch, true) || q_heads < 1 || q_heads % cache->kv_heads != 0 || !isfinite(scale))
-        return SV_ERR_INVALID_ARG;
+// Both entry points, once the cache and the batch are checked.
+static sv_status attend_call(const KvCache &c, const KvScale &sc, const sv_kv_batch *batch, sv_dtype dtype, const void *q,
+                             int64_t q_row_stride, int64_t q_head_stride, int q_heads, float scale, const int32_t *group_start,
+                             const int32_t *prefix_len, int n_groups, void *out, int64_t out_row_stride,
+                             int64_t out_head_stride, float *lse, sv_stats *stats, void *workspace, size_t workspace_bytes,
+                             sv_stream_t stream) {
+    if (q_heads < 1 || q_heads % c.kv_heads != 0 || !isfinite(scale)) return SV_ERR_INVALID_ARG;
     if (n_groups < 0 || n_groups > batch->B || (n_groups > 0 && (group_start == nullptr || prefix_len == nullptr)))
         return SV_ERR_INVALID_ARG;
-    const int es = elem_size((sv_dtype)cache->dtype);
+    const int es = elem_size(dtype);
     if (batch->rows > 0 && (q == nullptr || out == nullptr)) return SV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !strides16(es, q_row_stride, q_head_stride) ||
         !strides16(es, out_row_stride, out_head_stride) || (int64_t)batch->rows * q_heads > (1 << 30) ||
-        (int64_t)batch->B * cache->kv_heads > INT32_MAX)
+        (int64_t)batch->B * c.kv_heads > INT32_MAX)
         return SV_ERR_INVALID_ARG;
     // Rows that meet the same tokens, and the tiles they are cut into (few rows make one row tile, which always fits).
-    const bool fma = es == 4 || cache->head_dim > 128;
-    const int64_t G = q_heads / cache->kv_heads, packed = batch->n * G;
+    const bool fma = es == 4 || c.head_dim > 128 || sc.k != nullptr;
+    const int64_t G = q_heads / c.kv_heads, packed = batch->n * G;
     const bool few = packed <= (fma ? kSmallRows : kFewRows);
-    const AttendTiles large = fma ? tiles_f32(64, cache->head_dim > 128 ? 256 : 128) : kTilesTall;
+    const AttendTiles large = fma ? tiles_f32(64, c.head_dim > 128 ? 256 : 128) : kTilesTall;
     if ((!few || n_groups > 0) &&
-        !tiles_fit(large, (n_groups > 0 || batch->rows < batch->n ? batch->rows : batch->n) * G, (int64_t)batch->max_pages * cache->page_size))
+        !tiles_fit(large, (n_groups > 0 || batch->rows < batch->n ? batch->rows : batch->n) * G, (int64_t)batch->max_pages * c.page_size))
         return SV_ERR_INVALID_ARG;
-    const AttendPlan pl = plan_attend(batch->rows, q_heads, cache->head_dim, batch->B, n_groups);
+    const AttendPlan pl = plan_attend(batch->rows, q_heads, c.head_dim, batch->B, n_groups);
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.bytes) return SV_ERR_WORKSPACE;
-    const int64_t width = (int64_t)cache->head_dim * es;
+    const int64_t width = (int64_t)c.head_dim * es;
     if (overlap({q, q_row_stride * es, q_head_stride * es, batch->rows, q_heads, width},
                 {out, out_row_stride * es, out_head_stride * es, batch->rows, q_heads, width}))
         return SV_ERR_INVALID_ARG;   // other blocks still read q
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!on_current_device(s, cache->k, q)) return SV_ERR_INVALID_ARG;
+    if (!on_current_device(s, c.k, q)) return SV_ERR_INVALID_ARG;
     DeviceInfo di;
     if (!device_info(di)) return SV_ERR_CUDA;
     if (stats && cudaMemsetAsync(stats, 0, sizeof(sv_stats), s) != cudaSuccess) return SV_ERR_CUDA;
     if (batch->rows == 0) return SV_OK;
     char *w = static_cast<char *>(workspace);
     AttendArgs a{};
-    a.c = kv_cache_of(*cache);
+    a.c = c;
+    a.sc = sc;
     a.bt = kv_batch_of(*batch);
     a.q = static_cast<const char *>(q);
     a.out = static_cast<char *>(out);
@@ -527,7 +557,7 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
     a.o_row = out_row_stride * es;
     a.o_head = out_head_stride * es;
     a.q_heads = q_heads;
-    a.G = q_heads / cache->kv_heads;
+    a.G = q_heads / c.kv_heads;
     a.scale_log2 = (float)((double)scale * 1.44269504088896340736);
     a.group_start = group_start;
     a.prefix_len = prefix_len;
@@ -566,10 +596,30 @@ extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *b
             a.geo.slot0 = attend_slots(batch->rows, q_heads, true, false, prefix.TM, blocks);
         }
         e = !fma ? launch_attend_few(a, s)
-            : es == 4 && cache->head_dim <= 128 && packed <= kFewRows32 ? launch_attend_few32(a, s)
+            : es == 4 && c.head_dim <= 128 && packed <= kFewRows32 && sc.k == nullptr ? launch_attend_few32(a, s)
                                                                          : launch_attend_f32(a, es, true, s);
         own = a.geo;
     }
     if (e == cudaSuccess) e = launch_attend_join(a, prefix, own, es, s);
     return cuda_status(e);
+}
+
+extern "C" sv_status sv_kv_attend(const sv_kv_cache *cache, const sv_kv_batch *batch, const void *q,
+                                  int64_t q_row_stride, int64_t q_head_stride, int q_heads, float scale,
+                                  const int32_t *group_start, const int32_t *prefix_len, int n_groups, void *out,
+                                  int64_t out_row_stride, int64_t out_head_stride, float *lse, sv_stats *stats,
+                                  void *workspace, size_t workspace_bytes, sv_stream_t stream) {
+    if (!kv_args_ok(cache, batch, true)) return SV_ERR_INVALID_ARG;
+    return attend_call(kv_cache_of(*cache), KvScale{}, batch, (sv_dtype)cache->dtype, q, q_row_stride, q_head_stride, q_heads, scale, group_start,
+                       prefix_len, n_groups, out, out_row_stride, out_head_stride, lse, stats, workspace, workspace_bytes, stream);
+}
+
+extern "C" sv_status sv_kv_attend8(const sv_kv_cache8 *cache, const sv_kv_batch *batch, sv_dtype dtype, const void *q,
+                                   int64_t q_row_stride, int64_t q_head_stride, int q_heads, float scale,
+                                   const int32_t *group_start, const int32_t *prefix_len, int n_groups, void *out,
+                                   int64_t out_row_stride, int64_t out_head_stride, float *lse, sv_stats *stats,
+                                   void *workspace, size_t workspace_bytes, sv_stream_t stream) {
+    if (!kv_args_ok(cache, batch, dtype, true)) return SV_ERR_INVALID_ARG;
+    return attend_call(kv_cache_of(*cache), kv_scale_of(*cache), batch, dtype, q, q_row_stride, q_head_stride, q_heads, scale, group_start,
+                       prefix_len, n_groups, out, out_row_stride, out_head_stride, lse, stats, workspace, workspace_bytes, stream);
 }

@@ -19,7 +19,7 @@
 // Everything is derived from device arrays inside the call; the host knows bounds only.
 #pragma once
 
-#include "sv_kv.cuh"
+#include "sv_code8.cuh"
 
 namespace sv {
 
@@ -70,6 +70,7 @@ SV_HD bool tiles_fit(const AttendTiles &t, int64_t rows, int64_t slots) {
 
 struct AttendArgs {
     KvCache c;
+    KvScale sc;                             // of a cache held in 8 bits (no pointers: of the type of q)
     KvBatch bt;
     const char *q;
     char *out;

@@ -229,6 +229,7 @@ extern "C" const char *sv_status_string(sv_status s) {
         case SV_ERR_TIMEOUT: return "bounded wait timed out";
         case SV_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         case SV_ERR_BAD_TOKEN: return "token id outside [0, V)";
+        case SV_ERR_NO_PAGE: return "no free page left in the pool";
     }
     return "unknown status";
 }

@@ -201,22 +201,13 @@ extern "C" sv_status sv_rope_frequencies(int rotary_dim, double base, int scalin
     return SV_OK;
 }
 
-static bool rope_ok(const float *inv_freq, int rotary_dim, int style, int head_dim) {
-    if (style != SV_ROPE_HALF && style != SV_ROPE_INTERLEAVED) return false;
-    if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > head_dim || rotary_dim > SV_KV_MAX_HEAD_DIM) return false;
-    return rotary_dim == 0 || inv_freq != nullptr;
-}
-
-// A rotation in place is fine, one onto other rows that are still read is not.
-static bool turns_onto(const RowsView &x, const RowsView &out) { return !same_place(x, out) && overlap(x, out); }
-
 extern "C" sv_status sv_rope(const void *x, int64_t x_row_stride, int64_t x_head_stride, void *out,
                              int64_t out_row_stride, int64_t out_head_stride, sv_dtype dtype, int64_t rows, int heads,
                              int head_dim, const int32_t *positions, const float *inv_freq, int rotary_dim, int style,
                              float magnitude, int backward, sv_stream_t stream) {
     if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
     if (rows < 0 || rows > INT32_MAX || heads < 1 || head_dim < 1 || rotary_dim < 2 ||
-        !rope_ok(inv_freq, rotary_dim, style, head_dim) || (int64_t)heads * head_dim > INT32_MAX)
+        !rope_args_ok(inv_freq, rotary_dim, style, head_dim) || (int64_t)heads * head_dim > INT32_MAX)
         return SV_ERR_INVALID_ARG;
     if (rows == 0) return SV_OK;
     if (x == nullptr || out == nullptr || positions == nullptr) return SV_ERR_INVALID_ARG;
@@ -246,7 +237,7 @@ extern "C" sv_status sv_kv_append(const sv_kv_cache *cache, const sv_kv_batch *b
                                   int64_t k_head_stride, const void *v, int64_t v_row_stride, int64_t v_head_stride,
                                   const float *inv_freq, int rotary_dim, int style, float magnitude, sv_stats *stats,
                                   sv_stream_t stream) {
-    if (!kv_args_ok(cache, batch, true) || !rope_ok(inv_freq, rotary_dim, style, cache->head_dim))
+    if (!kv_args_ok(cache, batch, true) || !rope_args_ok(inv_freq, rotary_dim, style, cache->head_dim))
         return SV_ERR_INVALID_ARG;
     if ((q == nullptr) != (q_out == nullptr) || (q != nullptr && q_heads < 1)) return SV_ERR_INVALID_ARG;
     const int es = elem_size((sv_dtype)cache->dtype);

@@ -107,6 +107,15 @@ inline bool kv_args_ok(const sv_kv_cache *c, const sv_kv_batch *b, bool block) {
     return true;
 }
 
+inline bool rope_args_ok(const float *inv_freq, int rotary_dim, int style, int head_dim) {
+    if (style != SV_ROPE_HALF && style != SV_ROPE_INTERLEAVED) return false;
+    if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > head_dim || rotary_dim > SV_KV_MAX_HEAD_DIM) return false;
+    return rotary_dim == 0 || inv_freq != nullptr;
+}
+
+// A rotation in place is fine, one onto other rows that are still read is not.
+inline bool turns_onto(const RowsView &x, const RowsView &out) { return !same_place(x, out) && overlap(x, out); }
+
 // Rows [r0, r0 + n) of sequence b; a row_start that falls, passes `rows` or holds more than n rows gives
 // none (ok = false).
 struct SeqRows {
