@@ -526,7 +526,7 @@ static sv_status attend_call(const KvCache &c, const KvScale &sc, const sv_kv_ba
         (int64_t)batch->B * c.kv_heads > INT32_MAX)
         return SV_ERR_INVALID_ARG;
     // Rows that meet the same tokens, and the tiles they are cut into (few rows make one row tile, which always fits).
-    const bool fma = es == 4 || c.head_dim > 128 || sc.k != nullptr;
+    const bool fma = es == 4 || c.head_dim > 128;
     const int64_t G = q_heads / c.kv_heads, packed = batch->n * G;
     const bool few = packed <= (fma ? kSmallRows : kFewRows);
     const AttendTiles large = fma ? tiles_f32(64, c.head_dim > 128 ? 256 : 128) : kTilesTall;

@@ -58,10 +58,10 @@ __device__ __forceinline__ bool wait_phase(Feed *fd, uint64_t *bar, uint32_t par
     return true;
 }
 
-// `readers`: warps that read a piece description.
-__device__ __forceinline__ void feed_init(Feed *fd, const AttendArgs &a, int readers) {
+// `readers`: warps that read a piece description; `fills`: arrivals that make a stage full.
+__device__ __forceinline__ void feed_init(Feed *fd, const AttendArgs &a, int readers, int fills) {
     for (int i = 0; i < 8; ++i) {
-        mbar_init(&fd->kv_full[i], i == a.stuck_stage ? 65 : 64);
+        mbar_init(&fd->kv_full[i], i == a.stuck_stage ? fills + 1 : fills);
         mbar_init(&fd->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {

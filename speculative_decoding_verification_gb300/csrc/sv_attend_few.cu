@@ -19,7 +19,7 @@
 // What bounds it: memory.  A tile is 64 KB (heads of 128), 2800 cycles of an SM's share of the measured copy bandwidth; its
 // products take about 700 and its softmax about 1300, which the two groups share.  512 sequences x 6 rows, 8 key heads, 1,024 to
 // 2,048 tokens: 525 us, 6.3 TB/s or 0.92 of the measured copy bandwidth (the tall kernel: 1,040 us).
-#include "sv_attend_feed.cuh"
+#include "sv_attend_feed8.cuh"
 
 namespace sv {
 
@@ -29,15 +29,18 @@ constexpr int NR = kFewRows;
 constexpr int kFewReaders = 13;       // warps that read a piece description
 constexpr float kNoMax = -1e30f;      // maximum of a row that has seen no token yet
 
-template <int DP>
+// C8: the cache is held in 8 bits.
+template <int DP, bool C8>
 struct FewShape {
     static constexpr int TILE = 128 * DP * 2;
-    static constexpr int STAGES = DP == 128 ? 5 : 8;
+    static constexpr int STAGES = DP == 64 ? 8 : C8 ? 4 : 5;
+    static constexpr int SLOTS = DP == 64 ? 8 : 5;                // of each ring of codes
     static constexpr int HALF = 128 * 128;
     static constexpr int OFF_P = 2 * NR * DP * 2;                 // after two query tiles
     static constexpr int PBUF = 128 * 4 * NR;                     // a group's weights: 128 tokens x (32 high + 32 low)
     static constexpr int OFF_KV = OFF_P + 2 * PBUF;
-    static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
+    static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
+    static constexpr int OFF_MISC = OFF_RAW + (C8 ? 2 * SLOTS * kRawTokens * DP : 0);
 };
 
 struct FewShared {
@@ -51,6 +54,10 @@ struct FewShared {
     alignas(16) float zero[NR];
     int64_t to[2][NR];                // where a row's output goes (the first's, where both groups work on the piece)
     alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end what the group's output is scaled by
+};
+
+struct FewShared8 : FewShared {
+    Feed8 f8;
 };
 
 // Element-wise reduction of x[0..31] over the warp's lanes: lane r gets that of x[r].
@@ -87,12 +94,13 @@ __device__ __forceinline__ uint32_t rows_that_see(const PieceInfo *pi, int key, 
     return rows;
 }
 
-template <int DP>
+template <int DP, bool C8>
 __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_constant__ AttendArgs a, const __grid_constant__ TcArgs a2) {
-    using S = FewShape<DP>;
+    using S = FewShape<DP, C8>;
     extern __shared__ __align__(1024) char smem[];
     FewShared *ms = reinterpret_cast<FewShared *>(smem + S::OFF_MISC);
     Feed *fd = &ms->fd;
+    Feed8 *f8 = C8 ? &static_cast<FewShared8 *>(ms)->f8 : nullptr;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
 
     if (smem_addr(smem) & 1023) {   // the swizzle goes by address bits
@@ -100,7 +108,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         return;
     }
     if (tid == 0) {
-        feed_init(fd, a, kFewReaders);
+        feed_init(fd, a, C8 ? kFewReaders + 2 : kFewReaders, C8 ? 2 : 64);
+        if (C8) feed8_init(f8, S::SLOTS);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i][0], 1);
             mbar_init(&ms->s_full[i][1], 1);
@@ -265,9 +274,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                             if (kk >= pi->end) continue;   // flags mean nothing after a wait gave up
                             const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, kk);
                             if (off < 0) continue;
-                            const float v = t < a.c.head_dim
-                                                ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a.c.v + off + pi->h * a.c.head_b)[t] << 16)
-                                                : 0.0f;
+                            const float v = t < a.c.head_dim ? cached_value<C8>(a, off, a.bt.page_table + pi->table * a.bt.table_pitch, kk, pi->h, t) : 0.0f;
                             const char *pj = smem + S::OFF_P + gr * S::PBUF + j * (4 * NR);
                             uint32_t o[32];
                             tmem_ld32(colO, o);
@@ -365,7 +372,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         }
     } else if (warp < 12) {
         regs_dec<kRegsOther>();
-        feed_produce<DP, S::STAGES, NR>(a, a2, fd, sbase, sbase + S::OFF_KV, warp - 8, lane);
+        if constexpr (C8) feed8_widen<DP, S::STAGES, NR, S::SLOTS>(a, fd, f8, sbase, sbase + S::OFF_KV, sbase + S::OFF_RAW, warp - 8, lane);
+        else feed_produce<DP, S::STAGES, NR>(a, a2, fd, sbase, sbase + S::OFF_KV, warp - 8, lane);
     } else {
         regs_dec<kRegsOther>();
         if (warp == 12) {   // the whole warp runs this, with uniform values
@@ -413,7 +421,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                 if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1))) break;
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 if (nk <= 0) break;
-                const int rows_from = __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
+                const int rows_from = C8 ? INT32_MAX   // the widening warps fence their tiles
+                                         : __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
                 if (nk == 1) rests ^= 1;
                 const int first = __shfl_sync(0xFFFFFFFFu, nk == 1 ? rests ^ 1 : 0, 0);   // uniform for the compiler too
@@ -458,25 +467,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
             __syncwarp();
         } else if (warp == 13) {
             feed_walk(a, a2, fd, ms->walk, lane);
+        } else if constexpr (C8) {
+            feed8_load<DP, S::SLOTS>(a, a2, fd, f8, sbase + S::OFF_RAW + (warp - 14) * (S::SLOTS * kRawTokens * DP), warp - 14, lane);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && fd->dead) feed_drain<S::STAGES>(fd, a.stats);
+    if (tid == 0 && fd->dead) {
+        if constexpr (C8) feed8_drain<S::SLOTS>(fd, f8, a.stats);
+        else feed_drain<S::STAGES>(fd, a.stats);
+    }
     if (warp == 12) tmem_free(tmem, 256);
     pdl_wait();   // launched beside the prefixes' kernel: done only when that is, for the join waits for this one
 }
 
-template <int DP>
+template <int DP, bool C8>
 cudaError_t run_few(AttendArgs &a, bool negate, cudaStream_t stream) {
-    constexpr size_t bytes = FewShape<DP>::OFF_MISC + sizeof(FewShared);
+    constexpr size_t bytes = FewShape<DP, C8>::OFF_MISC + (C8 ? sizeof(FewShared8) : sizeof(FewShared));
     static_assert(bytes <= 232448, "shared memory of a block");
-    if (prepare_kernel((const void *)k_attend_few<DP>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
-    const TcArgs t = tc_args(a.c, mma_shape(NR, false, false, false, negate));
+    if (prepare_kernel((const void *)k_attend_few<DP, C8>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
+    const uint32_t shape = mma_shape(NR, false, false, false, negate);
+    const TcArgs t = C8 ? tc_args8(a.c, DP, shape) : tc_args(a.c, shape);
     // After the prefixes' kernel of the same call, blocks start as that one's end: they need nothing of it.
-    if (a.geo.s0 > 0) return launch_pdl(k_attend_few<DP>, dim3(a.geo.blocks), dim3(kTcThreads), bytes, stream, a, t);
-    k_attend_few<DP><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, t);
+    if (a.geo.s0 > 0) return launch_pdl(k_attend_few<DP, C8>, dim3(a.geo.blocks), dim3(kTcThreads), bytes, stream, a, t);
+    k_attend_few<DP, C8><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, t);
     return cudaGetLastError();
 }
 
@@ -489,7 +504,8 @@ cudaError_t launch_attend_few(AttendArgs &a, cudaStream_t stream) {
     // The maximum is taken after the scale; a negative scale negates the queries in the product, and zero stays zero.
     const bool negate = a.scale_log2 < 0.0f;
     t.scale_log2 = fabsf(a.scale_log2);
-    return a.c.head_dim <= 64 ? run_few<64>(t, negate, stream) : run_few<128>(t, negate, stream);
+    if (a.sc.k) return a.c.head_dim <= 64 ? run_few<64, true>(t, negate, stream) : run_few<128, true>(t, negate, stream);
+    return a.c.head_dim <= 64 ? run_few<64, false>(t, negate, stream) : run_few<128, false>(t, negate, stream);
 }
 
 }  // namespace sv

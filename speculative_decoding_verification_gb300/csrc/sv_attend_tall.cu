@@ -18,7 +18,7 @@
 // streams: with a warp a stream their products interleave and each ends later (355 us for the call against 300).
 #include <float.h>
 
-#include "sv_attend_feed.cuh"
+#include "sv_attend_feed8.cuh"
 
 namespace sv {
 
@@ -28,13 +28,16 @@ constexpr int kTallRows = 256;
 constexpr int kTallReaders = 13;      // warps that read a piece description
 constexpr uint32_t kColS = 0, kColO = 256;
 
-template <int DP>
+// C8: the cache is held in 8 bits.
+template <int DP, bool C8>
 struct TallShape {
     static constexpr int TILE = 128 * DP * 2;              // bytes of 128 rows
-    static constexpr int STAGES = DP == 128 ? 5 : 8;
+    static constexpr int STAGES = DP == 64 ? 8 : C8 ? 4 : 5;
+    static constexpr int SLOTS = DP == 64 ? 8 : 3;         // of each ring of codes
     static constexpr int HALF = 128 * 128;                 // bytes of 128 rows of 64 elements
     static constexpr int OFF_KV = 2 * TILE;
-    static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
+    static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
+    static constexpr int OFF_MISC = OFF_RAW + (C8 ? 2 * SLOTS * kRawTokens * DP : 0);
 };
 
 struct TallShared {
@@ -49,6 +52,10 @@ struct TallShared {
     };
 };
 
+struct TallShared8 : TallShared {
+    Feed8 f8;
+};
+
 // Bits of the 128 tokens first .. first + 127 that a row of a tree sees, from its ancestor bits.
 __device__ __forceinline__ uint32_t anc_at(const uint32_t (&anc)[5], int k) {
     if (k < 0) return 0xFFFFFFFFu;   // cached tokens
@@ -59,12 +66,13 @@ __device__ __forceinline__ uint32_t anc_at(const uint32_t (&anc)[5], int k) {
     return w;
 }
 
-template <int DP>
+template <int DP, bool C8>
 __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_constant__ AttendArgs a, const __grid_constant__ TcArgs a2) {
-    using S = TallShape<DP>;
+    using S = TallShape<DP, C8>;
     extern __shared__ __align__(1024) char smem[];
     TallShared *ms = reinterpret_cast<TallShared *>(smem + S::OFF_MISC);
     Feed *fd = &ms->fd;
+    Feed8 *f8 = C8 ? &static_cast<TallShared8 *>(ms)->f8 : nullptr;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
 
     if (smem_addr(smem) & 1023) {   // the swizzle goes by address bits
@@ -72,7 +80,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
         return;
     }
     if (tid == 0) {
-        feed_init(fd, a, kTallReaders);
+        feed_init(fd, a, C8 ? kTallReaders + 2 : kTallReaders, C8 ? 2 : 64);
+        if (C8) feed8_init(f8, S::SLOTS);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i], 1);
             mbar_init(&ms->p_half[i], 4);
@@ -258,9 +267,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                                 const float w = j & 1 ? bf16_hi(pw) + bf16_hi(rw) : bf16_lo(pw) + bf16_lo(rw);
                                 const bool sees = (mine >> b) & 1u;
                                 if (first + j >= end) continue;   // flags mean nothing after a wait gave up
-                                const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, first + j);
+                                const int32_t *table = a.bt.page_table + pi->table * a.bt.table_pitch;
+                                const int64_t off = slot_offset(a.c, table, first + j);
                                 if (off < 0) continue;
-                                const char *v = a.c.v + off + pi->h * a.c.head_b;
 #pragma unroll 1
                                 for (int d = 0; d < a.c.head_dim; d += 32) {
                                     uint32_t o[32];
@@ -268,9 +277,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                                     tc_wait_ld();
 #pragma unroll
                                     for (int u = 0; u < 32; ++u) {
-                                        const float vv = d + u < a.c.head_dim
-                                                             ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(v)[d + u] << 16)
-                                                             : 0.0f;
+                                        const float vv = d + u < a.c.head_dim ? cached_value<C8>(a, off, table, first + j, pi->h, d + u) : 0.0f;
                                         if (sees) o[u] = __float_as_uint(__uint_as_float(o[u]) + w * vv);
                                     }
                                     tmem_st32(colO + d, o);
@@ -374,7 +381,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
     } else if (warp < 12) {
         regs_dec<kRegsOther>();
         // ---------------------------------------------------------------- producers
-        feed_produce<DP, S::STAGES, 128>(a, a2, fd, smem_addr(smem), smem_addr(smem) + S::OFF_KV, warp - 8, lane);
+        if constexpr (C8) feed8_widen<DP, S::STAGES, 128, S::SLOTS>(a, fd, f8, smem_addr(smem), smem_addr(smem) + S::OFF_KV, smem_addr(smem) + S::OFF_RAW, warp - 8, lane);
+        else feed_produce<DP, S::STAGES, 128>(a, a2, fd, smem_addr(smem), smem_addr(smem) + S::OFF_KV, warp - 8, lane);
     } else {
         regs_dec<kRegsOther>();
         if (warp == 12) {   // the whole warp runs this, with uniform values
@@ -389,7 +397,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
                 const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
                 const bool two = __shfl_sync(0xFFFFFFFFu, pi->vr, 0) > 128;
                 if (nk <= 0) break;
-                const int rows_from = __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
+                const int rows_from = C8 ? INT32_MAX   // the widening warps fence their tiles
+                                         : __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
                 if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
                 // Job n: stream n & 1, key tile n / 2 (two row tiles) or n.
                 const int jobs = two ? 2 * nk : nk, shift = two ? 1 : 0;
@@ -477,23 +486,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
         } else if (warp == 13) {
             // ------------------------------------------------------------ the walk
             feed_walk(a, a2, fd, ms->walk, lane);
+        } else if constexpr (C8) {
+            feed8_load<DP, S::SLOTS>(a, a2, fd, f8, smem_addr(smem) + S::OFF_RAW + (warp - 14) * (S::SLOTS * kRawTokens * DP), warp - 14, lane);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && fd->dead) feed_drain<S::STAGES>(fd, a.stats);
+    if (tid == 0 && fd->dead) {
+        if constexpr (C8) feed8_drain<S::SLOTS>(fd, f8, a.stats);
+        else feed_drain<S::STAGES>(fd, a.stats);
+    }
     if (warp == 12) tmem_free(tmem, 512);
 }
 
-template <int DP>
+template <int DP, bool C8>
 cudaError_t run_tall(AttendArgs &a, bool negate, cudaStream_t stream) {
-    constexpr size_t bytes = TallShape<DP>::OFF_MISC + sizeof(TallShared);
+    constexpr size_t bytes = TallShape<DP, C8>::OFF_MISC + (C8 ? sizeof(TallShared8) : sizeof(TallShared));
     static_assert(bytes <= 232448, "shared memory of a block");
-    if (prepare_kernel((const void *)k_attend_tall<DP>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
+    if (prepare_kernel((const void *)k_attend_tall<DP, C8>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
+    const uint32_t shape = mma_shape(128, false, false, negate, false);
     static_assert(kTilesTall.TM == kTallRows && kTilesTall.TK == kTcKeys, "the cutting's tiles are the kernel's");
     a.geo.set(kTilesTall);
-    k_attend_tall<DP><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, tc_args(a.c, mma_shape(128, false, false, negate, false)));
+    k_attend_tall<DP, C8><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, C8 ? tc_args8(a.c, DP, shape) : tc_args(a.c, shape));
     return cudaGetLastError();
 }
 
@@ -505,7 +520,9 @@ cudaError_t launch_attend_tall(AttendArgs &a, cudaStream_t stream) {
     // product, and zero becomes the smallest normal number, which tells weights apart only where q.k passes 10^36.
     const bool negate = a.scale_log2 < 0.0f;
     t.scale_log2 = fmaxf(fabsf(a.scale_log2), FLT_MIN);
-    const cudaError_t e = a.c.head_dim <= 64 ? run_tall<64>(t, negate, stream) : run_tall<128>(t, negate, stream);
+    const bool narrow = a.c.head_dim <= 64;
+    const cudaError_t e = a.sc.k ? (narrow ? run_tall<64, true>(t, negate, stream) : run_tall<128, true>(t, negate, stream))
+                                 : (narrow ? run_tall<64, false>(t, negate, stream) : run_tall<128, false>(t, negate, stream));
     a.geo = t.geo;
     return e;
 }
