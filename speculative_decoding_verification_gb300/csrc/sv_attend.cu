@@ -595,7 +595,8 @@ static sv_status attend_call(const KvCache &c, const KvScale &sc, const sv_kv_ba
             a.geo.seg_off = seg + n_groups + 1;
             a.geo.slot0 = attend_slots(batch->rows, q_heads, true, false, prefix.TM, blocks);
         }
-        e = !fma ? launch_attend_few(a, s)
+        e = !fma && sc.k ? launch_attend_few8(a, s)
+            : !fma ? launch_attend_few(a, s)
             : es == 4 && c.head_dim <= 128 && packed <= kFewRows32 && sc.k == nullptr ? launch_attend_few32(a, s)
                                                                          : launch_attend_f32(a, es, true, s);
         own = a.geo;

@@ -456,6 +456,7 @@ cudaError_t launch_attend_f32(AttendArgs &a, int es, bool small, cudaStream_t st
 cudaError_t launch_attend_few32(AttendArgs &a, cudaStream_t stream);
 cudaError_t launch_attend_tall(AttendArgs &a, cudaStream_t stream);
 cudaError_t launch_attend_few(AttendArgs &a, cudaStream_t stream);
+cudaError_t launch_attend_few8(AttendArgs &a, cudaStream_t stream);   // launch_attend_few over a cache held in 8 bits
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");

@@ -26,6 +26,7 @@ struct PieceInfo {
     int box_tiles;                    // tiles before this one load as boxes, the others by rows
     bool own, tree, whole;            // own segment, tree mask, output complete here
     uint8_t par[SV_MAX_TREE];         // a tree's parents (255: invalid)
+    float q_back;                     // what the query tile's numbers are multiplied by (few8 only)
 };
 
 struct Feed {
@@ -58,14 +59,14 @@ __device__ __forceinline__ bool wait_phase(Feed *fd, uint64_t *bar, uint32_t par
     return true;
 }
 
-// `readers`: warps that read a piece description; `fills`: arrivals that make a stage full.
-__device__ __forceinline__ void feed_init(Feed *fd, const AttendArgs &a, int readers, int fills) {
+// `readers`: warps that read a piece description; arrivals that make a stage and a query tile full.
+__device__ __forceinline__ void feed_init(Feed *fd, const AttendArgs &a, int readers, int fills, int q_fills) {
     for (int i = 0; i < 8; ++i) {
         mbar_init(&fd->kv_full[i], i == a.stuck_stage ? fills + 1 : fills);
         mbar_init(&fd->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-        mbar_init(&fd->q_full[i], 128);
+        mbar_init(&fd->q_full[i], q_fills);
         mbar_init(&fd->q_empty[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -320,8 +321,9 @@ __device__ __forceinline__ void feed_produce(const AttendArgs &a, const TcArgs &
     else feed_produce_as<DP, STAGES, QROWS, false>(a, a2, fd, q_base, kv_base, wl, lane);
 }
 
-// The walk's part, one warp: describes the pieces, then that there are no more.
-__device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2, Feed *fd, Walk w, int lane) {
+// The walk's part, one warp: describes the pieces, then that there are no more.  `then` is called with each piece's number once it is described.
+template <class F>
+__device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2, Feed *fd, Walk w, int lane, F then) {
     uint32_t seq = 0;
     for (int it = 0;; ++it) {
         Piece p;
@@ -364,9 +366,13 @@ __device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2,
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&fd->pd_full[it % kRing]);
-        if (more) seq += 2 * (p.k1 - p.k0);
-        else break;
+        if (!more) break;
+        seq += 2 * (p.k1 - p.k0);
+        then(it);
     }
+}
+__device__ __forceinline__ void feed_walk(const AttendArgs &a, const TcArgs &a2, Feed *fd, Walk w, int lane) {
+    feed_walk(a, a2, fd, w, lane, [](int) {});
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,

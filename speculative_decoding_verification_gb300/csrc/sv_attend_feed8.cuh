@@ -1,14 +1,16 @@
 // sv_attend_feed8.cuh — the feed of the tensor-core attention kernels over a cache held in 8 bits: codes come to shared memory as they
 // are, and become the bf16 tiles that the products read.
 //
-// Two warps load, one the keys and one the values: slots of 32 tokens by TMA boxes (by rows where boxes cannot go), with
-// the tokens' scales, into two rings.  The four warps that load bf16 caches turn the slots into tiles instead, two for the keys and
-// two for the values, every other slot each: a code times its scale is a bf16 number, so from there on nothing differs, and the result
-// is to the bit that of a bf16 cache of the same values.
+// Two warps load, one the keys and one the values: slots of 32 tokens by TMA boxes (by rows where boxes cannot go) into two rings.
+// The four warps that load bf16 caches widen the slots to the products' tiles instead.  There are two kinds of tiles:
+//   bf16      a code times its scale, which is a bf16 number: from there on nothing differs, and the result is to the bit that of a
+//             bf16 cache of the same values.  A pair of codes takes five instructions (e4m3 to binary16, two of those to float32, a packed
+//             product, one to bf16).  For the tall kernel, which the products bound; here.
+//   binary16  the code as it is; the scales enter with the scores and the weights.  One instruction a pair.  For few rows, where issue
+//             slots and shared memory are near their bounds; sv_attend_few8.cu.
 //
-// A pair of codes takes five instructions (e4m3 to binary16, two of those to float32, a packed product, one to bf16), 640 a
-// lane and pair of tiles of 128 x 128: as much as the softmax, and both fit under the 1,450 cycles that a pair takes at an SM's
-// share of the measured copy bandwidth.
+// A barrier of a ring is waited for by its phase's parity, so whoever waits for a slot has to wait for each of its fills: with slots that went to
+// two warps in turn, one could take the parity of a fill still to come for that of the one before.
 #pragma once
 
 #include "sv_attend_feed.cuh"
@@ -16,20 +18,25 @@
 namespace sv {
 
 constexpr int kRawTokens = 32;    // tokens of a slot
-constexpr int kMaxSlots8 = 12;
+constexpr int kMaxSlots8 = 8;
 
 struct Feed8 {
     uint64_t full[2][kMaxSlots8], empty[2][kMaxSlots8];   // of the keys' and the values' slots
-    float scale[2][kMaxSlots8][kRawTokens];
+    // Scales of the last four tiles (bf16 tiles only).  A loading warp is at most eight slots, two tiles, ahead of the widening ones.
+    uint64_t scale_full[2][4];
+    uint8_t scale[2][4][kTcKeys];
     uint32_t next[2];                                     // slots a loading warp has begun, left at its end
 };
 
-__device__ __forceinline__ void feed8_init(Feed8 *f8, int slots) {
-    for (int r = 0; r < 2; ++r)
+// `readers`: warps that widen a slot.
+__device__ __forceinline__ void feed8_init(Feed8 *f8, int slots, int readers) {
+    for (int r = 0; r < 2; ++r) {
         for (int i = 0; i < slots; ++i) {
-            mbar_init(&f8->full[r][i], 2 * 32);   // each lane once for its copies and once for its token's scale
-            mbar_init(&f8->empty[r][i], 1);
+            mbar_init(&f8->full[r][i], 32);
+            mbar_init(&f8->empty[r][i], readers);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&f8->scale_full[r][i], 32);
+    }
     f8->next[0] = f8->next[1] = 0;
 }
 
@@ -44,128 +51,171 @@ __device__ __noinline__ void feed8_drain(Feed *fd, Feed8 *f8, sv_stats *stats) {
             }
 }
 
-// One of the loading warps: kv 0 the keys, 1 the values.  Slots at raw_base, DP bytes a token.
-template <int DP, int SLOTS, bool SPLIT>
+// Where chunk ch of 16 codes of a slot's token r lies in it: as the TMA swizzle of 128 (64) bytes puts it for tokens of 128 (64) codes, or
+// in order.
+template <int DP, bool SWIZZLE>
+__device__ __forceinline__ int raw_place(int r, int ch) {
+    return r * DP + ((!SWIZZLE ? ch : DP == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4);
+}
+
+// One of the loading warps: kv 0 the keys, 1 the values.  Slots at raw_base, DP bytes a token.  SCALES: with their scales.  KEYS_SWIZZLED: the
+// keys' slots are swizzled.
+// One warp has to keep up with the others: six cycles an instruction, so a slot's boxes go with as few as can be.  (With the pages of all
+// tokens looked up for every tile, as tiles by rows do, it took 4,000 cycles a tile and set the pace.)
+template <int DP, int SLOTS, bool SCALES, bool KEYS_SWIZZLED, bool SPLIT>
 __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs &a2, Feed *fd, Feed8 *f8, uint32_t raw_base, int kv, int lane) {
+    static_assert(SLOTS <= 8 && SLOTS <= kMaxSlots8, "the scales' ring");
     constexpr int SLOT = kRawTokens * DP, CH = DP / 16, RPI = 32 / CH;   // chunks of a token, tokens of a pass by rows
     const int D = a.c.head_dim;
     const CUtensorMap *map = kv ? &a2.v : &a2.k;
     const char *src = kv ? a.c.v : a.c.k;
     const uint8_t *scales = kv ? a.sc.v : a.sc.k;
+    uint64_t *const fulls = f8->full[kv], *const empties = f8->empty[kv];
     const int ch = lane % CH, rsub = lane / CH;
     const bool real = ch * 16 < D;   // chunks past the head are zero
+    auto raw_at = [&](int r) { return KEYS_SWIZZLED && kv == 0 ? raw_place<DP, true>(r, ch) : raw_place<DP, false>(r, ch); };
     const int psize = a.c.page_size, pshift = a2.page_shift;
     auto page_index = [&](int key) { return pshift >= 0 ? key >> pshift : key / psize; };
-    uint32_t q = 0;                  // slots begun
-    bool on = true;                  // off once a wait gave up
-    // A slot's scales are asked for with its tokens and stored when the next slot is begun, or before a wait.
-    uint32_t held = 0, held_slot = 0;
-    bool holds = false;
-    auto store_scale = [&]() {
-        if (holds) {
-            f8->scale[kv][held_slot][lane] = scale_of(held);
-            mbar_arrive(&f8->full[kv][held_slot]);
-            holds = false;
+    // boxes: a tile's are a lane's each
+    const int box_rows = a2.box_rows > 0 ? a2.box_rows : 8, box_token = lane * box_rows, my_slot = box_token / kRawTokens;
+    const bool boxes = box_token < kTcKeys;
+    uint32_t slot = 0, parity = 1, begun = 0, tiles = 0;   // the next slot, its empty barrier's parity, slots and tiles begun
+    bool on = true;                                        // off once a wait gave up
+    auto take = [&]() {   // waits for the next slot
+        on = __all_sync(0xFFFFFFFFu, wait_phase(fd, &empties[slot], parity));
+        return on;
+    };
+    auto step = [&]() {
+        ++begun;
+        if (++slot == SLOTS) {
+            slot = 0;
+            parity ^= 1;
         }
     };
     for (int it = 0;; ++it) {
         const PieceInfo *pi = &fd->pd[it % kRing];
-        if (!mbar_test_wait(&fd->pd_full[it % kRing], (it / kRing) & 1)) store_scale();
-        __syncwarp();
         if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1))) break;
         const int k0 = pi->k0, k1 = pi->k1;
         if (k0 >= k1) break;
         const int key0 = pi->key0, end = pi->end, h = pi->h, tab = pi->table, box_tiles = pi->box_tiles;
-        const int boxes = box_tiles > 0 ? kRawTokens / a2.box_rows : 0;
         const int32_t *table = a.bt.page_table + tab * a.bt.table_pitch;
         __syncwarp();
         if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
         const uint8_t *my_scales = scales + h * a.sc.head_b;
-        // the pages of this lane's tokens of a tile, asked for a tile ahead
-        int ahead[4];
-        auto ask = [&](int k) {
+        // What is loaded ahead is not looked at before it is needed (a warp stops there until it has come), not even to leave it out: past
+        // the unit's last token stands that one.
+        const int last = end - 1;
+        auto box_index = [&](int k) { return page_index(key0 + k * kTcKeys + box_token); };
+        auto box_page = [&](int k) { return table[page_index(min(key0 + k * kTcKeys + box_token, last))]; };
+        int ahead = box_page(k0);
+        // Scales: of the lane's tokens lane, lane + 32, .. of a tile.  Pages are looked up two tiles ahead and scales one.
+        int spage[4];
+        uint32_t sbyte[4], sgood = 0;   // a bit for each page that is one: the others' scale is 1
+        auto ask_pages = [&](int k) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int key = key0 + k * kTcKeys + s * kRawTokens + lane;
-                ahead[s] = k < k1 && key < end ? table[page_index(key)] : kNoPage;
+                spage[s] = table[page_index(min(key0 + k * kTcKeys + s * kRawTokens + lane, last))];
             }
         };
-        ask(k0);
-        store_scale();   // of the last piece's last slot, while the pages come
-        for (int k = k0; k < k1 && on; ++k) {
-            int id[4];
+        auto ask_scales = [&]() {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) id[s] = ahead[s];
-            ask(k + 1);
-#pragma unroll 1
             for (int s = 0; s < 4; ++s) {
-                const int page = id[0];
-                id[0] = id[1];
-                id[1] = id[2];
-                id[2] = id[3];
-                const uint32_t slot = q % SLOTS;
-                uint64_t *full = &f8->full[kv][slot], *empty = &f8->empty[kv][slot];
-                if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(empty, ((q / SLOTS) & 1) ^ 1))) store_scale();
-                on = __all_sync(0xFFFFFFFFu, wait_phase(fd, empty, ((q / SLOTS) & 1) ^ 1) && !*reinterpret_cast<volatile int *>(&fd->dead));
-                if (!on) break;
-                ++q;
-                const int key = key0 + k * kTcKeys + s * kRawTokens + lane;
-                const int place = key - page_index(key) * psize;
-                const bool good = (unsigned)page < (unsigned)a.c.n_pages;
-                if (!good && page != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
-                const uint32_t scale = good ? my_scales[page * a.sc.page_b] : 127u;
-                const uint32_t to = raw_base + slot * SLOT;
-                bool rows = true;   // every lane has copies by rows on their way
-                if (k < box_tiles) {
-                    const int first = lane * a2.box_rows;   // of the lane's box
-                    const int bpage = __shfl_sync(0xFFFFFFFFu, page, first & 31), bplace = __shfl_sync(0xFFFFFFFFu, place, first & 31);
-                    const uint32_t split = SPLIT ? __ballot_sync(0xFFFFFFFFu, lane < boxes && bplace + 8 > psize) : 0;
-                    if (elect_one()) mbar_expect_arrive_n(full, (kRawTokens - 8 * __popc(split)) * DP, 0);
+                const bool good = (unsigned)spage[s] < (unsigned)a.c.n_pages;
+                sgood = s == 0 ? good : sgood | (uint32_t)good << s;
+                sbyte[s] = my_scales[(good ? spage[s] : 0) * a.sc.page_b];
+            }
+        };
+        if constexpr (SCALES) {
+            ask_pages(k0);
+            ask_scales();
+            ask_pages(k0 + 1);
+        }
+        for (int k = k0; k < k1 && on; ++k, ++tiles) {
+            auto store_scales = [&]() {
+                if constexpr (SCALES) {
+                    uint8_t *to = f8->scale[kv][tiles & 3] + lane;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) to[s * kRawTokens] = (sgood >> s) & 1u ? (uint8_t)sbyte[s] : (uint8_t)127;
+                    mbar_arrive(&f8->scale_full[kv][tiles & 3]);
+                    ask_scales();
+                    ask_pages(k + 2);
+                }
+            };
+            if (k < box_tiles) {
+                const int page = ahead, place = key0 + k * kTcKeys + box_token - box_index(k) * psize;
+                ahead = box_page(k + 1);
+                if (boxes && (unsigned)page >= (unsigned)a.c.n_pages) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                // split: a box that reaches into the next page goes by rows
+                const uint32_t split = SPLIT ? __ballot_sync(0xFFFFFFFFu, boxes && place + 8 > psize) : 0;
+#pragma unroll 1
+                for (int s = 0; s < 4; ++s) {
+                    if (!take()) break;
+                    uint64_t *full = &fulls[slot];
+                    const uint32_t to = raw_base + slot * SLOT;
+                    const uint32_t rows = SPLIT ? (split >> (4 * s)) & 15u : 0;   // boxes of 8 tokens there
+                    if (elect_one()) mbar_expect_arrive_n(full, (kRawTokens - 8 * __popc(rows)) * DP, rows ? 0 : 32);
                     __syncwarp();
                     // a bad page id lies outside the tensor and reads zeros
-                    if (lane < boxes && !((split >> lane) & 1u)) box_load(to + first * DP, map, full, 0, h, bplace, bpage);
+                    if (my_slot == s && !(SPLIT && ((split >> lane) & 1u))) box_load(to + (box_token % kRawTokens) * DP, map, full, 0, h, place, page);
                     __syncwarp();
-                    rows = false;
-                    if (SPLIT && split) {
-                        rows = true;
-                        const int64_t off = good ? page * a.c.page_b + place * a.c.slot_b + h * a.c.head_b : -1;
+                    if (SPLIT && rows) {
+                        const int key = key0 + k * kTcKeys + s * kRawTokens + lane, index = page_index(key), id = table[index];
+                        const bool good = (unsigned)id < (unsigned)a.c.n_pages;
+                        if (!good) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                        const int64_t off = good ? id * a.c.page_b + (key - index * psize) * a.c.slot_b + h * a.c.head_b : -1;
 #pragma unroll 1
                         for (int r0 = 0; r0 < kRawTokens; r0 += RPI) {
                             const int r = r0 + rsub;
                             const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
                             const bool ok = o >= 0 && real;
-                            if ((split >> (r >> 3)) & 1u) cp_async16(to + r * DP + ch * 16, src + (ok ? o + ch * 16 : 0), ok);
+                            if ((rows >> (r >> 3)) & 1u) cp_async16(to + raw_at(r), src + (ok ? o + ch * 16 : 0), ok);
                         }
+                        cp_async_arrive(full);
                     }
-                } else {
-                    const int64_t off = good ? page * a.c.page_b + place * a.c.slot_b + h * a.c.head_b : -1;
+                    step();
+                    if (SCALES && s == 0) store_scales();   // after a piece's first boxes
+                }
+            } else {
+                int id[4];   // all pages are asked for before the first is needed
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int key = key0 + k * kTcKeys + s * kRawTokens + lane;
+                    id[s] = key < end ? table[page_index(key)] : kNoPage;
+                }
+#pragma unroll 1
+                for (int s = 0; s < 4; ++s) {
+                    if (!take()) break;
+                    const int key = key0 + k * kTcKeys + s * kRawTokens + lane, page = id[0];
+                    id[0] = id[1];
+                    id[1] = id[2];
+                    id[2] = id[3];
+                    const bool good = (unsigned)page < (unsigned)a.c.n_pages;
+                    if (!good && page != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                    const int64_t off = good ? page * a.c.page_b + (key - page_index(key) * psize) * a.c.slot_b + h * a.c.head_b : -1;
+                    const uint32_t to = raw_base + slot * SLOT;
 #pragma unroll 2
                     for (int r0 = 0; r0 < kRawTokens; r0 += RPI) {
                         const int r = r0 + rsub;
                         const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
                         const bool ok = o >= 0 && real;
-                        cp_async16(to + r * DP + ch * 16, src + (ok ? o + ch * 16 : 0), ok);
+                        cp_async16(to + raw_at(r), src + (ok ? o + ch * 16 : 0), ok);
                     }
+                    cp_async_arrive(&fulls[slot]);
+                    step();
+                    if (SCALES && s == 0) store_scales();
                 }
-                if (rows) cp_async_arrive(full);
-                else mbar_arrive(full);
-                store_scale();   // of the slot before
-                held = scale;
-                held_slot = slot;
-                holds = true;
             }
         }
     }
-    store_scale();
     cp_async_commit();
     cp_async_wait<0>();   // no row is in flight when the block ends; boxes are when a wait gave up
-    if (lane == 0) f8->next[kv] = q;
+    if (lane == 0) f8->next[kv] = begun;
 }
 
-template <int DP, int SLOTS>
+template <int DP, int SLOTS, bool SCALES, bool KEYS_SWIZZLED>
 __device__ __forceinline__ void feed8_load(const AttendArgs &a, const TcArgs &a2, Feed *fd, Feed8 *f8, uint32_t raw_base, int kv, int lane) {
-    if (a2.split) feed8_load_as<DP, SLOTS, true>(a, a2, fd, f8, raw_base, kv, lane);
-    else feed8_load_as<DP, SLOTS, false>(a, a2, fd, f8, raw_base, kv, lane);
+    if (a2.split) feed8_load_as<DP, SLOTS, SCALES, KEYS_SWIZZLED, true>(a, a2, fd, f8, raw_base, kv, lane);
+    else feed8_load_as<DP, SLOTS, SCALES, KEYS_SWIZZLED, false>(a, a2, fd, f8, raw_base, kv, lane);
 }
 
 // 16 codes times their scale as 16 bf16 numbers, two chunks of 16 bytes.
@@ -183,7 +233,20 @@ __device__ __forceinline__ void widen16(uint4 w, f32x2 scale, uint32_t (&lo)[4],
     }
 }
 
-// One of the four widening warps: it also copies its quarter of the query tiles.  Stages at kv_base as feed_produce fills them; a
+// Which 16 codes a lane of a widening warp takes in a pass.  Eight lanes take two neighbouring tokens, four chunks each, of a token of 128
+// different halves: neither the loads nor the stores to the swizzled tile then meet in a bank.
+template <int DP>
+struct WidenLane {
+    static constexpr int PASS = DP == 128 ? 4 : 8;   // tokens of a pass
+    int row0, ch;                                    // its token of the first pass, its chunk
+    __device__ __forceinline__ explicit WidenLane(int lane) {
+        const int j = lane & 7, p = lane >> 3;
+        row0 = DP == 128 ? (p >> 1) * 2 + (j >> 2) : p * 2 + (j >> 2);
+        ch = DP == 128 ? (j & 3) + 4 * ((j >> 2) ^ (p & 1)) : j & 3;
+    }
+};
+
+// One of the four widening warps, bf16 tiles: it also copies its quarter of the query tiles.  Stages at kv_base as feed_produce fills them; a
 // stage is full when its two warps have arrived.
 template <int DP, int STAGES, int QROWS, int SLOTS>
 __device__ __forceinline__ void feed8_widen(const AttendArgs &a, Feed *fd, Feed8 *f8, uint32_t q_base, uint32_t kv_base, uint32_t raw_base, int wl,
@@ -191,14 +254,11 @@ __device__ __forceinline__ void feed8_widen(const AttendArgs &a, Feed *fd, Feed8
     constexpr int TILE = 128 * DP * 2, HALF = 128 * 128, SLOT = kRawTokens * DP;
     const int D = a.c.head_dim, kv = wl >> 1, sub = wl & 1;
     raw_base += kv * SLOTS * SLOT;
-    // Eight lanes take two neighbouring tokens, four chunks each, of a token of eight different halves: neither the loads nor the
-    // stores to the swizzled tile then meet in a bank.
-    const int j = lane & 7, p = lane >> 3;
-    const int row0 = DP == 128 ? (p >> 1) * 2 + (j >> 2) : p * 2 + (j >> 2);
-    const int ch = DP == 128 ? (j & 3) + 4 * ((j >> 2) ^ (p & 1)) : j & 3;
-    constexpr int PASS = DP == 128 ? 4 : 8;   // tokens of a pass
+    const WidenLane<DP> me(lane);
+    const int row0 = me.row0, ch = me.ch;
+    constexpr int PASS = WidenLane<DP>::PASS;
     const uint32_t from = row0 * DP + ch * 16, to_half = (ch >> 2) * HALF;
-    uint32_t seq = kv, q_phases = 0, slots = sub;   // slots: the next of its ring
+    uint32_t seq = kv, q_phases = 0, slots = 0, tiles = 0;   // slots: the next of its ring
     int qnext = 0;
     bool on = true;
     for (int it = 0;; ++it) {
@@ -237,26 +297,28 @@ __device__ __forceinline__ void feed8_widen(const AttendArgs &a, Feed *fd, Feed8
             cp_async_arrive(&fd->q_full[qs]);
         }
         if (!two) qnext ^= 1;
-        for (int k = k0; k < k1 && on; ++k) {
+        for (int k = k0; k < k1 && on; ++k, ++tiles) {
             const uint32_t stage = seq % STAGES;
-            on = __all_sync(0xFFFFFFFFu, wait_phase(fd, &fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1));
+            on = __all_sync(0xFFFFFFFFu, wait_phase(fd, &fd->kv_empty[stage], ((seq / STAGES) & 1) ^ 1) &&
+                                             wait_phase(fd, &f8->scale_full[kv][tiles & 3], (tiles >> 2) & 1));
             if (!on) break;
             seq += 2;
+            const volatile uint8_t *bytes = f8->scale[kv][tiles & 3];
 #pragma unroll 1
-            for (int s = sub; s < 4 && on; s += 2, slots += 2) {
+            for (int s = 0; s < 4 && on; ++s, ++slots) {   // each warp half of a slot
                 const uint32_t slot = slots % SLOTS;
                 on = __all_sync(0xFFFFFFFFu, wait_phase(fd, &f8->full[kv][slot], (slots / SLOTS) & 1));
                 if (!on) break;
                 const uint32_t raw = raw_base + slot * SLOT + from;
                 const uint32_t tile = kv_base + stage * TILE + s * (kRawTokens * 128) + to_half;
 #pragma unroll 2
-                for (int u = 0; u < kRawTokens / PASS; ++u) {
-                    const int row = u * PASS + row0;
+                for (int v = 0; v < kRawTokens / PASS / 2; ++v) {
+                    const int u = sub * (kRawTokens / PASS / 2) + v, row = u * PASS + row0;
                     uint4 w;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                                  : "r"(raw + u * (PASS * DP)));
-                    const float f = *reinterpret_cast<volatile float *>(&f8->scale[kv][slot][row]);
+                    const float f = scale_of(bytes[s * kRawTokens + row]);
                     uint32_t lo[4], hi[4];
                     widen16(w, f2_pack(f, f), lo, hi);
                     const int c = 2 * (ch & 3);
@@ -290,16 +352,16 @@ __device__ __forceinline__ float cached_value(const AttendArgs &a, int64_t off, 
     }
 }
 
-inline bool cache_map8(CUtensorMap *map, char *base, const KvCache &c, int width, int box_rows) {
+inline bool cache_map8(CUtensorMap *map, char *base, const KvCache &c, int width, int box_rows, CUtensorMapSwizzle swizzle) {
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.kv_heads, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)c.head_b, (cuuint64_t)c.slot_b, (cuuint64_t)c.page_b};
     const cuuint32_t box[4] = {(cuuint32_t)width, 1, (cuuint32_t)box_rows, 1}, one[4] = {1, 1, 1, 1};
     return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // tc_args for codes: boxes of up to a slot's 32 tokens by whole heads.
-inline TcArgs tc_args8(const KvCache &c, int width, uint32_t shape_s) {
+inline TcArgs tc_args8(const KvCache &c, int width, bool keys_swizzled, uint32_t shape_s) {
     TcArgs t{};
     t.shape_s = shape_s;
     const int ps = c.page_size;
@@ -308,7 +370,9 @@ inline TcArgs tc_args8(const KvCache &c, int width, uint32_t shape_s) {
     t.split = rows == 8 && ps % 8 != 0;
     if (rows > 0) {
         t.box_rows = rows;
-        if (encode_tiled() == nullptr || !cache_map8(&t.k, c.k, c, width, rows) || !cache_map8(&t.v, c.v, c, width, rows)) t.box_rows = 0;
+        const CUtensorMapSwizzle none = CU_TENSOR_MAP_SWIZZLE_NONE, own = width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+        if (encode_tiled() == nullptr || !cache_map8(&t.k, c.k, c, width, rows, keys_swizzled ? own : none) || !cache_map8(&t.v, c.v, c, width, rows, none))
+            t.box_rows = 0;
     }
     return t;
 }

@@ -19,88 +19,29 @@
 // What bounds it: memory.  A tile is 64 KB (heads of 128), 2800 cycles of an SM's share of the measured copy bandwidth; its
 // products take about 700 and its softmax about 1300, which the two groups share.  512 sequences x 6 rows, 8 key heads, 1,024 to
 // 2,048 tokens: 525 us, 6.3 TB/s or 0.92 of the measured copy bandwidth (the tall kernel: 1,040 us).
-#include "sv_attend_feed8.cuh"
+#include "sv_attend_few.cuh"
 
 namespace sv {
 
 namespace {
 
-constexpr int NR = kFewRows;
-constexpr int kFewReaders = 13;       // warps that read a piece description
-constexpr float kNoMax = -1e30f;      // maximum of a row that has seen no token yet
-
-// C8: the cache is held in 8 bits.
-template <int DP, bool C8>
+template <int DP>
 struct FewShape {
     static constexpr int TILE = 128 * DP * 2;
-    static constexpr int STAGES = DP == 64 ? 8 : C8 ? 4 : 5;
-    static constexpr int SLOTS = DP == 64 ? 8 : 5;                // of each ring of codes
+    static constexpr int STAGES = DP == 128 ? 5 : 8;
     static constexpr int HALF = 128 * 128;
     static constexpr int OFF_P = 2 * NR * DP * 2;                 // after two query tiles
     static constexpr int PBUF = 128 * 4 * NR;                     // a group's weights: 128 tokens x (32 high + 32 low)
     static constexpr int OFF_KV = OFF_P + 2 * PBUF;
-    static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
-    static constexpr int OFF_MISC = OFF_RAW + (C8 ? 2 * SLOTS * kRawTokens * DP : 0);
+    static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
 };
 
-struct FewShared {
-    Feed fd;
-    uint64_t s_full[2][2], p_full[2], p_done[2], done;
-    Walk walk;
-    long long warp_sum[kTcThreads / 32];
-    // per group
-    float top[2][4][NR];              // the warps' maxima of a row, later their sums
-    alignas(16) float shift[2][NR];   // minus a row's maximum (of scale * log2(e) * q.k)
-    alignas(16) float zero[NR];
-    int64_t to[2][NR];                // where a row's output goes (the first's, where both groups work on the piece)
-    alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end what the group's output is scaled by
-};
-
-struct FewShared8 : FewShared {
-    Feed8 f8;
-};
-
-// Element-wise reduction of x[0..31] over the warp's lanes: lane r gets that of x[r].
-template <class F>
-__device__ __forceinline__ float reduce_rows(float (&x)[NR], int lane, F f) {
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-        const bool up = lane & w;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (i < w) {
-                const float mine = up ? x[i + w] : x[i], other = up ? x[i] : x[i + w];
-                x[i] = f(mine, __shfl_xor_sync(0xFFFFFFFFu, other, w));
-            }
-        }
-    }
-    return x[0];
-}
-
-// The packed rows of a unit that see token `key`, as bits.
-__device__ __forceinline__ uint32_t rows_that_see(const PieceInfo *pi, int key, int G, int n) {
-    if (key >= pi->end) return 0;
-    const int rel = key - pi->ctx;
-    if (rel <= 0) return 0xFFFFFFFFu;
-    if (!pi->tree) return rel * G >= 32 ? 0u : 0xFFFFFFFFu << (rel * G);
-    uint32_t below = 1u << rel, rows = 0;   // the node and what descends from it: parents come before their children
-    for (int i = rel + 1; i < n; ++i) {
-        const int p = pi->par[i - 1];
-        if (p != 255 && ((below >> p) & 1u)) below |= 1u << i;
-    }
-    const uint32_t heads = G >= 32 ? 0xFFFFFFFFu : (1u << G) - 1u;
-    for (int i = rel; i < n; ++i)
-        if ((below >> i) & 1u) rows |= heads << (i * G);
-    return rows;
-}
-
-template <int DP, bool C8>
+template <int DP>
 __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_constant__ AttendArgs a, const __grid_constant__ TcArgs a2) {
-    using S = FewShape<DP, C8>;
+    using S = FewShape<DP>;
     extern __shared__ __align__(1024) char smem[];
     FewShared *ms = reinterpret_cast<FewShared *>(smem + S::OFF_MISC);
     Feed *fd = &ms->fd;
-    Feed8 *f8 = C8 ? &static_cast<FewShared8 *>(ms)->f8 : nullptr;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
 
     if (smem_addr(smem) & 1023) {   // the swizzle goes by address bits
@@ -108,8 +49,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         return;
     }
     if (tid == 0) {
-        feed_init(fd, a, C8 ? kFewReaders + 2 : kFewReaders, C8 ? 2 : 64);
-        if (C8) feed8_init(f8, S::SLOTS);
+        feed_init(fd, a, kFewReaders, 64, 128);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i][0], 1);
             mbar_init(&ms->s_full[i][1], 1);
@@ -274,7 +214,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
                             if (kk >= pi->end) continue;   // flags mean nothing after a wait gave up
                             const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, kk);
                             if (off < 0) continue;
-                            const float v = t < a.c.head_dim ? cached_value<C8>(a, off, a.bt.page_table + pi->table * a.bt.table_pitch, kk, pi->h, t) : 0.0f;
+                            const float v = t < a.c.head_dim
+                                                ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a.c.v + off + pi->h * a.c.head_b)[t] << 16)
+                                                : 0.0f;
                             const char *pj = smem + S::OFF_P + gr * S::PBUF + j * (4 * NR);
                             uint32_t o[32];
                             tmem_ld32(colO, o);
@@ -372,126 +314,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few(const __grid_const
         }
     } else if (warp < 12) {
         regs_dec<kRegsOther>();
-        if constexpr (C8) feed8_widen<DP, S::STAGES, NR, S::SLOTS>(a, fd, f8, sbase, sbase + S::OFF_KV, sbase + S::OFF_RAW, warp - 8, lane);
-        else feed_produce<DP, S::STAGES, NR>(a, a2, fd, sbase, sbase + S::OFF_KV, warp - 8, lane);
+        feed_produce<DP, S::STAGES, NR>(a, a2, fd, sbase, sbase + S::OFF_KV, warp - 8, lane);
     } else {
         regs_dec<kRegsOther>();
-        if (warp == 12) {   // the whole warp runs this, with uniform values
-            // ------------------------------------------------------------ matrix products
-            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-            constexpr uint32_t shape_o = mma_shape(2 * NR, true, true, false, false);
-            uint32_t seq = 0, tiles0 = 0, tiles1 = 0;
-            int rests = 0;   // as in the softmax
-            // O^T += V^T P^T of the tile whose scores were issued before the last
-            int late = 0, late_gr = 0, late_rows = 0;
-            uint32_t late_seq = 0, late_u = 0;
-            auto weigh = [&]() {
-                const uint32_t stage = late_seq % S::STAGES;
-                wait_phase(fd, &fd->kv_full[stage], (late_seq / S::STAGES) & 1);
-                wait_phase(fd, &ms->p_full[late_gr], late_u & 1);
-                __syncwarp();
-                if (late_rows) fence_async_smem();
-                tc_fence_after();
-                const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, DP == 128 ? S::HALF : 0, 1024);
-                const uint64_t p = smem_operand(sbase + S::OFF_P + late_gr * S::PBUF, 0, 1024);
-                const uint32_t o = tm + 128 + late_gr * 64;
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) mma_ss(o, v + kk * (2048 >> 4), p + kk * (2048 >> 4), shape_o, 1u);
-                    mma_commit(&fd->kv_empty[stage]);
-                    mma_commit(&ms->p_done[late_gr]);
-                }
-                __syncwarp();
-            };
-            // Before a wait for what the next scores need: the weighted sum does not wait for it too.
-            auto weigh_first = [&](uint64_t *bar, uint32_t parity) {
-                if (late && !__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) {
-                    weigh();
-                    late = 0;
-                }
-            };
-            auto ready = [&](uint64_t *bar, uint32_t parity) {
-                weigh_first(bar, parity);
-                wait_phase(fd, bar, parity);
-                __syncwarp();
-            };
-            for (int it = 0;; ++it) {
-                const PieceInfo *pi = &fd->pd[it % kRing];
-                weigh_first(&fd->pd_full[it % kRing], (it / kRing) & 1);
-                if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1))) break;
-                const int nk = __shfl_sync(0xFFFFFFFFu, pi->k1 - pi->k0, 0);
-                if (nk <= 0) break;
-                const int rows_from = C8 ? INT32_MAX   // the widening warps fence their tiles
-                                         : __shfl_sync(0xFFFFFFFFu, a2.split ? 0 : pi->box_tiles - pi->k0, 0);   // from this tile on, copied by rows
-                if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
-                if (nk == 1) rests ^= 1;
-                const int first = __shfl_sync(0xFFFFFFFFu, nk == 1 ? rests ^ 1 : 0, 0);   // uniform for the compiler too
-                const int qs = it & 1;
-                const uint64_t q = smem_operand(sbase + qs * (NR * DP * 2), 16, 1024);
-                for (int n = 0; n < nk; ++n) {
-                    const int gr = first ^ (n & 1);
-                    const uint32_t stage = seq % S::STAGES, u = gr ? tiles1 : tiles0;
-                    ready(&fd->kv_full[stage], (seq / S::STAGES) & 1);
-                    if (n == 0) {
-                        ready(&fd->q_full[qs], (it >> 1) & 1);
-                    }
-                    if (n == 0 || n >= rows_from) fence_async_smem();
-                    tc_fence_after();
-                    const uint64_t kt = smem_operand(sbase + S::OFF_KV + stage * S::TILE, 16, 1024);
-                    const uint32_t s = tm + (gr * 2 + (u & 1)) * 32;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < DP / 16; ++kk) {
-                            const uint32_t ka = ((kk >> 2) * S::HALF + (kk & 3) * 32) >> 4, qa = ((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4;
-                            mma_ss(s, kt + ka, q + qa, a2.shape_s, kk > 0);
-                        }
-                        mma_commit(&ms->s_full[gr][u & 1]);
-                        mma_commit(&fd->kv_empty[stage]);
-                        if (n == nk - 1) mma_commit(&fd->q_empty[qs]);
-                    }
-                    __syncwarp();
-                    if (late) weigh();
-                    late = 1;
-                    late_gr = gr;
-                    late_rows = n >= rows_from;
-                    late_seq = seq + 1;
-                    late_u = u;
-                    seq += 2;
-                    if (gr) ++tiles1;
-                    else ++tiles0;
-                }
-            }
-            if (late) weigh();
-            if (elect_one()) mma_commit(&ms->done);
-            wait_phase<true>(fd, &ms->done, 0);   // the products end by themselves
-            __syncwarp();
+        if (warp == 12) {
+            few_products<S, DP, true>(fd, ms, a2, sbase, tmem, mma_shape(2 * NR, true, true, false, false), lane);
         } else if (warp == 13) {
             feed_walk(a, a2, fd, ms->walk, lane);
-        } else if constexpr (C8) {
-            feed8_load<DP, S::SLOTS>(a, a2, fd, f8, sbase + S::OFF_RAW + (warp - 14) * (S::SLOTS * kRawTokens * DP), warp - 14, lane);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && fd->dead) {
-        if constexpr (C8) feed8_drain<S::SLOTS>(fd, f8, a.stats);
-        else feed_drain<S::STAGES>(fd, a.stats);
-    }
+    if (tid == 0 && fd->dead) feed_drain<S::STAGES>(fd, a.stats);
     if (warp == 12) tmem_free(tmem, 256);
     pdl_wait();   // launched beside the prefixes' kernel: done only when that is, for the join waits for this one
 }
 
-template <int DP, bool C8>
+template <int DP>
 cudaError_t run_few(AttendArgs &a, bool negate, cudaStream_t stream) {
-    constexpr size_t bytes = FewShape<DP, C8>::OFF_MISC + (C8 ? sizeof(FewShared8) : sizeof(FewShared));
+    constexpr size_t bytes = FewShape<DP>::OFF_MISC + sizeof(FewShared);
     static_assert(bytes <= 232448, "shared memory of a block");
-    if (prepare_kernel((const void *)k_attend_few<DP, C8>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
-    const uint32_t shape = mma_shape(NR, false, false, false, negate);
-    const TcArgs t = C8 ? tc_args8(a.c, DP, shape) : tc_args(a.c, shape);
+    if (prepare_kernel((const void *)k_attend_few<DP>, kTcThreads, bytes) < 1) return cudaErrorInvalidConfiguration;
+    const TcArgs t = tc_args(a.c, mma_shape(NR, false, false, false, negate));
     // After the prefixes' kernel of the same call, blocks start as that one's end: they need nothing of it.
-    if (a.geo.s0 > 0) return launch_pdl(k_attend_few<DP, C8>, dim3(a.geo.blocks), dim3(kTcThreads), bytes, stream, a, t);
-    k_attend_few<DP, C8><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, t);
+    if (a.geo.s0 > 0) return launch_pdl(k_attend_few<DP>, dim3(a.geo.blocks), dim3(kTcThreads), bytes, stream, a, t);
+    k_attend_few<DP><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, t);
     return cudaGetLastError();
 }
 
@@ -504,8 +352,7 @@ cudaError_t launch_attend_few(AttendArgs &a, cudaStream_t stream) {
     // The maximum is taken after the scale; a negative scale negates the queries in the product, and zero stays zero.
     const bool negate = a.scale_log2 < 0.0f;
     t.scale_log2 = fabsf(a.scale_log2);
-    if (a.sc.k) return a.c.head_dim <= 64 ? run_few<64, true>(t, negate, stream) : run_few<128, true>(t, negate, stream);
-    return a.c.head_dim <= 64 ? run_few<64, false>(t, negate, stream) : run_few<128, false>(t, negate, stream);
+    return a.c.head_dim <= 64 ? run_few<64>(t, negate, stream) : run_few<128>(t, negate, stream);
 }
 
 }  // namespace sv

@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
         return;
     }
     if (tid == 0) {
-        feed_init(fd, a, C8 ? kTallReaders + 2 : kTallReaders, C8 ? 2 : 64);
-        if (C8) feed8_init(f8, S::SLOTS);
+        feed_init(fd, a, C8 ? kTallReaders + 2 : kTallReaders, C8 ? 2 : 64, 128);
+        if (C8) feed8_init(f8, S::SLOTS, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i], 1);
             mbar_init(&ms->p_half[i], 4);
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
             // ------------------------------------------------------------ the walk
             feed_walk(a, a2, fd, ms->walk, lane);
         } else if constexpr (C8) {
-            feed8_load<DP, S::SLOTS>(a, a2, fd, f8, smem_addr(smem) + S::OFF_RAW + (warp - 14) * (S::SLOTS * kRawTokens * DP), warp - 14, lane);
+            feed8_load<DP, S::SLOTS, true, false>(a, a2, fd, f8, smem_addr(smem) + S::OFF_RAW + (warp - 14) * (S::SLOTS * kRawTokens * DP), warp - 14, lane);
         }
     }
     tc_fence_before();
@@ -508,7 +508,7 @@ cudaError_t run_tall(AttendArgs &a, bool negate, cudaStream_t stream) {
     const uint32_t shape = mma_shape(128, false, false, negate, false);
     static_assert(kTilesTall.TM == kTallRows && kTilesTall.TK == kTcKeys, "the cutting's tiles are the kernel's");
     a.geo.set(kTilesTall);
-    k_attend_tall<DP, C8><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, C8 ? tc_args8(a.c, DP, shape) : tc_args(a.c, shape));
+    k_attend_tall<DP, C8><<<a.geo.blocks, kTcThreads, bytes, stream>>>(a, C8 ? tc_args8(a.c, DP, false, shape) : tc_args(a.c, shape));
     return cudaGetLastError();
 }
 

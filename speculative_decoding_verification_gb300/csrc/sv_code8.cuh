@@ -51,6 +51,13 @@ __device__ __forceinline__ float4 codes4(uint32_t four) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// Four codes as two pairs of binary16 numbers.
+__device__ __forceinline__ void codes4_f16(uint32_t four, uint32_t &a, uint32_t &b) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(four));
+}
+
 // Two floats of at most 448 as codes, to nearest, ties to even; NaN stays NaN.
 __device__ __forceinline__ uint32_t to_codes2(float lo, float hi) {
     uint32_t two;

@@ -31,6 +31,11 @@ __host__ __device__ constexpr uint32_t mma_shape(int N, bool a_t, bool b_t, bool
            (b_t ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
 }
 
+// The same with binary16 operands.
+__host__ __device__ constexpr uint32_t mma_shape_f16(int N, bool a_t, bool b_t, bool a_neg, bool b_neg) {
+    return mma_shape(N, a_t, b_t, a_neg, b_neg) & ~(1u << 7 | 1u << 10);
+}
+
 // One thread of the warp, the same one every time.  Products are issued inside `if (elect_one())` in code that the whole
 // warp runs with uniform operands: they then cost 13 (A in tensor memory) to 33 cycles each to issue, against 75 to 100 when
 // the thread is picked by its number, and the tensor cores take 64 for 128 x 128 x 16.
@@ -109,6 +114,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *x) {
 }
 __device__ __forceinline__ void tmem_ld4(uint32_t at, uint32_t (&x)[4]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&x)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : SV_R4(x, 0), SV_R4(x, 4) : "r"(at));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&x)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::SV_W4(x, 0), SV_W4(x, 4), "r"(at) : "memory");
 }
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
     uint32_t x;

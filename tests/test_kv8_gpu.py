@@ -153,16 +153,18 @@ def test_append_ragged_and_in_place(sv):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
-def check_both(sv, c, q, kw, rows_of, par=None, bits=False, okw=None):
-    """sv_kv_attend8 against the oracle over the values, and sv_kv_attend over the values."""
+def check_both(sv, c, q, kw, rows_of, par=None):
+    """sv_kv_attend8 against the oracle over the values; where a block has more rows than the kernel for few takes, in bf16, it is sv_kv_attend
+    over the values to the bit."""
+    bits = q.dtype is BF and q.shape[-1] <= 128 and q.shape[1] * (q.shape[2] // c.k.shape[2]) > 32
     scale = kw.pop("scale", q.shape[-1] ** -0.5)
     stats = sv.new_stats("cuda")
     out, lse = sv.sv_kv_attend8(q, *c.args8, scale=scale, lse=True, stats=stats, **kw)
     assert sv.read_stats(stats)["status"] == 0
     check_attend(c, q.flatten(0, 1) if q.dim() == 4 else q, out.flatten(0, 1) if q.dim() == 4 else out,
                  lse.flatten(0, 1) if q.dim() == 4 else lse, scale, rows_of, par)
-    plain = sv.sv_kv_attend(q, c.k, c.v, *c.args8[4:], scale=scale, lse=True, **kw)
     if bits:
+        plain = sv.sv_kv_attend(q, c.k, c.v, *c.args8[4:], scale=scale, lse=True, **kw)
         assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
     return out, lse
 
@@ -183,7 +185,7 @@ def filled(seed, dtype, contexts, n, H, kv, dim, page, order="psh", groups=None,
                                                    (5, 4, 1, 256, 16, "psh"), (2, 2, 1, 48, 1, "psh"), (300, 2, 1, 128, 64, "phs")])
 def test_attend_over_codes(sv, dtype, n, H, kv, dim, page, order):
     c, q, rows = filled(n + dim, dtype, [0, 1, 127, 128, 700], n, H, kv, dim, page, order, spread=3)
-    check_both(sv, c, q, {}, rows, bits=dtype is BF)
+    check_both(sv, c, q, {}, rows)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -191,7 +193,7 @@ def test_attend_over_codes(sv, dtype, n, H, kv, dim, page, order):
 def test_attend_trees(sv, dtype, n, dim, page):
     c, q, rows = filled(n, dtype, [3, 250, 0], n, 4, 2, dim, page, spread=2)
     par = random_tree(c.rng, 3, n)
-    check_both(sv, c, q, dict(parents=par.cuda()), rows, par, bits=dtype is BF)
+    check_both(sv, c, q, dict(parents=par.cuda()), rows, par)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -210,7 +212,7 @@ def test_attend_shared_prefixes(sv, dtype, n, page, prefixes):
                     s[c.table[b, pre // page].long()] = s[c.table[b0, pre // page].long()]
     c.refresh()
     q = torch.randn((5, n, 8, 128), generator=g).to(dtype).cuda()
-    check_both(sv, c, q, dict(c.group_args), [slice(b * n, b * n + n) for b in range(5)], bits=dtype is BF)
+    check_both(sv, c, q, dict(c.group_args), [slice(b * n, b * n + n) for b in range(5)])
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -221,7 +223,7 @@ def test_attend_scales_of_either_sign_and_scale_bytes_at_the_ends(sv, dtype, sca
     c.vs.copy_(torch.tensor(c.rng.integers(27, 157, tuple(c.vs.shape)).astype(np.uint8)))
     c.ks.copy_(torch.tensor(c.rng.integers(100, 121, tuple(c.ks.shape)).astype(np.uint8)))
     c.refresh()
-    check_both(sv, c, q, dict(scale=scale), rows, bits=dtype is BF)
+    check_both(sv, c, q, dict(scale=scale), rows)
 
 
 @pytest.mark.parametrize("dtype,n,dim", [(BF, 4, 128), (BF, 60, 64), (F32, 4, 64), (BF, 3, 192), (F32, 40, 128)])
@@ -234,7 +236,7 @@ def test_hidden_tokens_cannot_reach_a_row(sv, dtype, n, dim):
     for s in (c.ks, c.vs):
         s[~used.cuda()] = 255
     c.refresh()
-    check_both(sv, c, q, {}, rows, bits=dtype is BF)
+    check_both(sv, c, q, {}, rows)
     # row 1's own value is NaN in one element of head 0: later rows see it, row 0 does not
     t = c.contexts[0] + 1
     c.v8.view(torch.uint8)[c.table[0, t // 16].long(), t % 16, 0, 5] = 0x7F
@@ -259,7 +261,7 @@ def test_rows_of_no_token_and_empty_blocks(sv):
 def test_long_contexts_split_over_blocks(sv):
     """Units that several blocks share, beside short ones; twice the same to the bit."""
     c, q, rows = filled(8, BF, [20000, 3, 9000, 17], 3, 8, 2, 128, 64, spread=4)
-    a = check_both(sv, c, q, {}, rows, bits=True)
+    a = check_both(sv, c, q, {}, rows)
     b = sv.sv_kv_attend8(q, *c.args8, lse=True)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
