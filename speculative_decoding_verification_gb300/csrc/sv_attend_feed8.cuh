@@ -1,7 +1,7 @@
 // sv_attend_feed8.cuh — the feed of the tensor-core attention kernels over a cache held in 8 bits: codes come to shared memory as they
 // are, and become the bf16 tiles that the products read.
 //
-// Two warps load, one the keys and one the values: slots of 32 tokens by TMA boxes (by rows where boxes cannot go) into two rings.
+// Two warps load, one the keys and one the values: slots of 32 or 64 tokens by TMA boxes (by rows where boxes cannot go) into two rings.
 // The four warps that load bf16 caches widen the slots to the products' tiles instead.  There are two kinds of tiles:
 //   bf16      a code times its scale, which is a bf16 number: from there on nothing differs, and the result is to the bit that of a
 //             bf16 cache of the same values.  A pair of codes takes five instructions (e4m3 to binary16, two of those to float32, a packed
@@ -17,7 +17,7 @@
 
 namespace sv {
 
-constexpr int kRawTokens = 32;    // tokens of a slot
+constexpr int kRawTokens = 32;    // tokens of a slot of the tall kernel's
 constexpr int kMaxSlots8 = 8;
 
 struct Feed8 {
@@ -58,14 +58,14 @@ __device__ __forceinline__ int raw_place(int r, int ch) {
     return r * DP + ((!SWIZZLE ? ch : DP == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4);
 }
 
-// One of the loading warps: kv 0 the keys, 1 the values.  Slots at raw_base, DP bytes a token.  SCALES: with their scales.  KEYS_SWIZZLED: the
+// One of the loading warps: kv 0 the keys, 1 the values.  Slots of TOK tokens at raw_base, DP bytes a token.  SCALES: with their scales.  KEYS_SWIZZLED: the
 // keys' slots are swizzled.
 // One warp has to keep up with the others: six cycles an instruction, so a slot's boxes go with as few as can be.  (With the pages of all
 // tokens looked up for every tile, as tiles by rows do, it took 4,000 cycles a tile and set the pace.)
-template <int DP, int SLOTS, bool SCALES, bool KEYS_SWIZZLED, bool SPLIT>
+template <int DP, int TOK, int SLOTS, bool SCALES, bool KEYS_SWIZZLED, bool SPLIT>
 __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs &a2, Feed *fd, Feed8 *f8, uint32_t raw_base, int kv, int lane) {
-    static_assert(SLOTS <= 8 && SLOTS <= kMaxSlots8, "the scales' ring");
-    constexpr int SLOT = kRawTokens * DP, CH = DP / 16, RPI = 32 / CH;   // chunks of a token, tokens of a pass by rows
+    static_assert(TOK * SLOTS <= 2 * kTcKeys && SLOTS <= kMaxSlots8, "the scales' ring");
+    constexpr int SLOT = TOK * DP, NS = kTcKeys / TOK, CH = DP / 16, RPI = 32 / CH;   // slots of a tile; chunks of a token, tokens of a pass by rows
     const int D = a.c.head_dim;
     const CUtensorMap *map = kv ? &a2.v : &a2.k;
     const char *src = kv ? a.c.v : a.c.k;
@@ -77,7 +77,7 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
     const int psize = a.c.page_size, pshift = a2.page_shift;
     auto page_index = [&](int key) { return pshift >= 0 ? key >> pshift : key / psize; };
     // boxes: a tile's are a lane's each
-    const int box_rows = a2.box_rows > 0 ? a2.box_rows : 8, box_token = lane * box_rows, my_slot = box_token / kRawTokens;
+    const int box_rows = a2.box_rows > 0 ? a2.box_rows : 8, box_token = lane * box_rows, my_slot = box_token / TOK;
     const bool boxes = box_token < kTcKeys;
     uint32_t slot = 0, parity = 1, begun = 0, tiles = 0;   // the next slot, its empty barrier's parity, slots and tiles begun
     bool on = true;                                        // off once a wait gave up
@@ -114,7 +114,7 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
         auto ask_pages = [&](int k) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                spage[s] = table[page_index(min(key0 + k * kTcKeys + s * kRawTokens + lane, last))];
+                spage[s] = table[page_index(min(key0 + k * kTcKeys + s * 32 + lane, last))];
             }
         };
         auto ask_scales = [&]() {
@@ -135,7 +135,7 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
                 if constexpr (SCALES) {
                     uint8_t *to = f8->scale[kv][tiles & 3] + lane;
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) to[s * kRawTokens] = (sgood >> s) & 1u ? (uint8_t)sbyte[s] : (uint8_t)127;
+                    for (int s = 0; s < 4; ++s) to[s * 32] = (sgood >> s) & 1u ? (uint8_t)sbyte[s] : (uint8_t)127;
                     mbar_arrive(&f8->scale_full[kv][tiles & 3]);
                     ask_scales();
                     ask_pages(k + 2);
@@ -148,27 +148,30 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
                 // split: a box that reaches into the next page goes by rows
                 const uint32_t split = SPLIT ? __ballot_sync(0xFFFFFFFFu, boxes && place + 8 > psize) : 0;
 #pragma unroll 1
-                for (int s = 0; s < 4; ++s) {
+                for (int s = 0; s < NS; ++s) {
                     if (!take()) break;
                     uint64_t *full = &fulls[slot];
                     const uint32_t to = raw_base + slot * SLOT;
-                    const uint32_t rows = SPLIT ? (split >> (4 * s)) & 15u : 0;   // boxes of 8 tokens there
-                    if (elect_one()) mbar_expect_arrive_n(full, (kRawTokens - 8 * __popc(rows)) * DP, rows ? 0 : 32);
+                    const uint32_t rows = SPLIT ? (split >> (TOK / 8 * s)) & ((1u << (TOK / 8)) - 1u) : 0;   // boxes of 8 tokens there
+                    if (elect_one()) mbar_expect_arrive_n(full, (TOK - 8 * __popc(rows)) * DP, rows ? 0 : 32);
                     __syncwarp();
                     // a bad page id lies outside the tensor and reads zeros
-                    if (my_slot == s && !(SPLIT && ((split >> lane) & 1u))) box_load(to + (box_token % kRawTokens) * DP, map, full, 0, h, place, page);
+                    if (my_slot == s && !(SPLIT && ((split >> lane) & 1u))) box_load(to + (box_token % TOK) * DP, map, full, 0, h, place, page);
                     __syncwarp();
                     if (SPLIT && rows) {
-                        const int key = key0 + k * kTcKeys + s * kRawTokens + lane, index = page_index(key), id = table[index];
-                        const bool good = (unsigned)id < (unsigned)a.c.n_pages;
-                        if (!good) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
-                        const int64_t off = good ? id * a.c.page_b + (key - index * psize) * a.c.slot_b + h * a.c.head_b : -1;
 #pragma unroll 1
-                        for (int r0 = 0; r0 < kRawTokens; r0 += RPI) {
-                            const int r = r0 + rsub;
-                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
-                            const bool ok = o >= 0 && real;
-                            if ((rows >> (r >> 3)) & 1u) cp_async16(to + raw_at(r), src + (ok ? o + ch * 16 : 0), ok);
+                        for (int t0 = 0; t0 < TOK; t0 += 32) {
+                            const int key = key0 + k * kTcKeys + s * TOK + t0 + lane, index = page_index(key), id = table[index];
+                            const bool good = (unsigned)id < (unsigned)a.c.n_pages;
+                            if (!good) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                            const int64_t off = good ? id * a.c.page_b + (key - index * psize) * a.c.slot_b + h * a.c.head_b : -1;
+#pragma unroll 1
+                            for (int r0 = 0; r0 < 32; r0 += RPI) {
+                                const int r = r0 + rsub;
+                                const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+                                const bool ok = o >= 0 && real;
+                                if ((rows >> ((t0 + r) >> 3)) & 1u) cp_async16(to + raw_at(t0 + r), src + (ok ? o + ch * 16 : 0), ok);
+                            }
                         }
                         cp_async_arrive(full);
                     }
@@ -179,26 +182,29 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
                 int id[4];   // all pages are asked for before the first is needed
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    const int key = key0 + k * kTcKeys + s * kRawTokens + lane;
+                    const int key = key0 + k * kTcKeys + s * 32 + lane;
                     id[s] = key < end ? table[page_index(key)] : kNoPage;
                 }
 #pragma unroll 1
-                for (int s = 0; s < 4; ++s) {
+                for (int s = 0; s < NS; ++s) {
                     if (!take()) break;
-                    const int key = key0 + k * kTcKeys + s * kRawTokens + lane, page = id[0];
-                    id[0] = id[1];
-                    id[1] = id[2];
-                    id[2] = id[3];
-                    const bool good = (unsigned)page < (unsigned)a.c.n_pages;
-                    if (!good && page != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
-                    const int64_t off = good ? page * a.c.page_b + (key - page_index(key) * psize) * a.c.slot_b + h * a.c.head_b : -1;
                     const uint32_t to = raw_base + slot * SLOT;
+#pragma unroll 1
+                    for (int t0 = 0; t0 < TOK; t0 += 32) {
+                        const int key = key0 + k * kTcKeys + s * TOK + t0 + lane, page = id[0];
+                        id[0] = id[1];
+                        id[1] = id[2];
+                        id[2] = id[3];
+                        const bool good = (unsigned)page < (unsigned)a.c.n_pages;
+                        if (!good && page != kNoPage) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                        const int64_t off = good ? page * a.c.page_b + (key - page_index(key) * psize) * a.c.slot_b + h * a.c.head_b : -1;
 #pragma unroll 2
-                    for (int r0 = 0; r0 < kRawTokens; r0 += RPI) {
-                        const int r = r0 + rsub;
-                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
-                        const bool ok = o >= 0 && real;
-                        cp_async16(to + raw_at(r), src + (ok ? o + ch * 16 : 0), ok);
+                        for (int r0 = 0; r0 < 32; r0 += RPI) {
+                            const int r = r0 + rsub;
+                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+                            const bool ok = o >= 0 && real;
+                            cp_async16(to + raw_at(t0 + r), src + (ok ? o + ch * 16 : 0), ok);
+                        }
                     }
                     cp_async_arrive(&fulls[slot]);
                     step();
@@ -212,10 +218,10 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
     if (lane == 0) f8->next[kv] = begun;
 }
 
-template <int DP, int SLOTS, bool SCALES, bool KEYS_SWIZZLED>
+template <int DP, int TOK, int SLOTS, bool SCALES, bool KEYS_SWIZZLED>
 __device__ __forceinline__ void feed8_load(const AttendArgs &a, const TcArgs &a2, Feed *fd, Feed8 *f8, uint32_t raw_base, int kv, int lane) {
-    if (a2.split) feed8_load_as<DP, SLOTS, SCALES, KEYS_SWIZZLED, true>(a, a2, fd, f8, raw_base, kv, lane);
-    else feed8_load_as<DP, SLOTS, SCALES, KEYS_SWIZZLED, false>(a, a2, fd, f8, raw_base, kv, lane);
+    if (a2.split) feed8_load_as<DP, TOK, SLOTS, SCALES, KEYS_SWIZZLED, true>(a, a2, fd, f8, raw_base, kv, lane);
+    else feed8_load_as<DP, TOK, SLOTS, SCALES, KEYS_SWIZZLED, false>(a, a2, fd, f8, raw_base, kv, lane);
 }
 
 // 16 codes times their scale as 16 bf16 numbers, two chunks of 16 bytes.

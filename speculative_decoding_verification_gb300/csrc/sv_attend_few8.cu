@@ -30,15 +30,15 @@ template <int DP>
 struct Few8Shape {
     static constexpr int TILE = 128 * DP * 2;
     static constexpr int KST = 3, VST = DP == 128 ? 3 : 4;        // tiles of keys in tensor memory and of values in shared memory
-    static constexpr int SLOTS = 8;                               // of each ring of codes: two of each widening warp
+    static constexpr int TOK = 64, SLOTS = 4;                     // tokens of a slot, slots of each ring of codes: two tiles
     static constexpr int HALF = 128 * 128;
     static constexpr int OFF_P = 2 * NR * DP * 2;                 // after two query tiles
-    static constexpr int PBUF = 128 * 4 * NR;                     // a group's weights: 128 tokens x 32, a row of 128 bytes each
+    static constexpr int PBUF = 128 * 2 * NR;                     // a group's weights: 128 tokens x 32, in the 64-byte swizzle
     static constexpr int OFF_KV = OFF_P + 2 * PBUF;
     static constexpr int OFF_RAW = OFF_KV + VST * TILE;
-    static constexpr int OFF_MISC = OFF_RAW + 2 * SLOTS * kRawTokens * DP;
-    // tensor memory: scores and outputs as in sv_attend_few.cu, then a group's 32 sums of each token's weights, then keys
-    static constexpr uint32_t COL_L = 256, COL_K = 320;
+    static constexpr int OFF_MISC = OFF_RAW + 2 * SLOTS * TOK * DP;
+    // tensor memory: scores as in sv_attend_few.cu, a group's output, its 32 sums of each token's weights twice, then keys
+    static constexpr uint32_t COL_O = 128, COL_L = 192, COL_K = 320;
 };
 // Barriers of the tiles: kv_full, kv_empty [0, KST) are the keys', [KST, KST + VST) the values'.
 
@@ -157,17 +157,17 @@ __device__ __forceinline__ void make_queries(const AttendArgs &a, PieceInfo *pi,
     fence_async_smem();
 }
 
-// One of the four widening warps: slot wl of each tile, tokens 32 wl to 32 wl + 31.  A lane takes one token's keys to tensor memory; of the
+// One of the four widening warps: tokens 32 wl to 32 wl + 31 of each tile, half of a slot.  A lane takes one token's keys to tensor memory; of the
 // values, eight lanes take two neighbouring tokens (WidenLane).
 template <int DP>
 __device__ __forceinline__ void widen_codes(Feed *fd, Feed8 *f8, uint32_t sbase, uint32_t tmem, int wl, int lane) {
     using S = Few8Shape<DP>;
-    constexpr int SLOT = kRawTokens * DP, PASS = WidenLane<DP>::PASS;
+    constexpr int SLOT = S::TOK * DP, PASS = WidenLane<DP>::PASS;
     const WidenLane<DP> me(lane);
-    const uint32_t kraw = sbase + S::OFF_RAW, vraw = kraw + S::SLOTS * SLOT + me.row0 * DP + me.ch * 16;
-    const uint32_t vtile = sbase + S::OFF_KV + (me.ch >> 2) * S::HALF + wl * (kRawTokens * 128);
+    const uint32_t kraw = sbase + S::OFF_RAW + (wl & 1) * 32 * DP, vraw = kraw + S::SLOTS * SLOT + me.row0 * DP + me.ch * 16;
+    const uint32_t vtile = sbase + S::OFF_KV + (me.ch >> 2) * S::HALF + wl * (32 * 128);
     const uint32_t kcol = tmem + S::COL_K + ((uint32_t)(wl * 32) << 16);
-    static_assert(S::SLOTS == 8, "two slots of each warp");
+    static_assert(S::SLOTS == 4 && S::TOK == 64, "a slot goes to the same two warps each time");
     uint32_t n = 0;   // tiles
     bool on = true;
     for (int it = 0;; ++it) {
@@ -178,7 +178,7 @@ __device__ __forceinline__ void widen_codes(Feed *fd, Feed8 *f8, uint32_t sbase,
         __syncwarp();
         if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
         for (int k = 0; k < nk && on; ++k, ++n) {
-            const uint32_t slot = (n & 1) * 4 + wl, parity = (n >> 1) & 1;
+            const uint32_t slot = (n & 1) * 2 + (wl >> 1), parity = (n >> 1) & 1;
             const uint32_t ks = n % S::KST, vs = n % S::VST;
             on = __all_sync(0xFFFFFFFFu, wait_phase(fd, &f8->full[0][slot], parity) &&
                                              wait_phase(fd, &fd->kv_empty[ks], ((n / S::KST) & 1) ^ 1));
@@ -209,7 +209,7 @@ __device__ __forceinline__ void widen_codes(Feed *fd, Feed8 *f8, uint32_t sbase,
                                              wait_phase(fd, &fd->kv_empty[S::KST + vs], ((n / S::VST) & 1) ^ 1));
             if (!on) break;
 #pragma unroll 1
-            for (int u = 0; u < kRawTokens / PASS; u += 4) {
+            for (int u = 0; u < 32 / PASS; u += 4) {
                 uint32_t w[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -267,11 +267,11 @@ __device__ __forceinline__ void issue_products(Feed *fd, FewShared *ms, uint32_t
             __syncwarp();
             tc_fence_after();
             const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, DP == 128 ? S::HALF : 0, 1024);
-            const uint64_t p = smem_operand(sbase + S::OFF_P + gr * S::PBUF, 0, 1024);
-            const uint32_t o = tm + 128 + gr * 64;
+            const uint64_t p = smem_operand64(sbase + S::OFF_P + gr * S::PBUF, 512);
+            const uint32_t o = tm + S::COL_O + gr * NR;
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) mma_ss(o, v + kk * (2048 >> 4), p + kk * (2048 >> 4), shape_o, 1u);
+                for (int kk = 0; kk < 8; ++kk) mma_ss(o, v + kk * (2048 >> 4), p + kk * (1024 >> 4), shape_o, 1u);
                 mma_commit(&fd->kv_empty[S::KST + stage]);
                 mma_commit(&ms->p_done[gr]);
             }
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
     }
     if (tid == 0) {
         feed_init(fd, a, kFewReaders + 2, 4, 1);
-        feed8_init(f8, S::SLOTS, 1);
+        feed8_init(f8, S::SLOTS, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i][0], 1);
             mbar_init(&ms->s_full[i][1], 1);
@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
         // ---------------------------------------------------------------- softmax
         const int gr = warp >> 2, wl = warp & 3, t = wl * 32 + lane;   // group, warp of it, token of the tile (head element at the end)
         const uint32_t base = tmem + ((uint32_t)(wl * 32) << 16);
-        const uint32_t colO = base + 128 + gr * 64, colL = base + S::COL_L + gr * NR;
-        const uint32_t prow = sbase + S::OFF_P + gr * S::PBUF + t * (4 * NR);     // this token's weights
+        const uint32_t colO = base + S::COL_O + gr * NR, colL = base + S::COL_L + gr * (2 * NR);
+        const uint32_t prow = sbase + S::OFF_P + gr * S::PBUF + t * (2 * NR);     // this token's weights; chunk q at q ^ ((t >> 1) & 3)
         uint32_t u = 0;   // tiles this group has worked on
         int rests = 0;    // the group that left the last piece of one tile to the other
         auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + gr) : "memory"); };
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 tc_wait_st();
             }
             float *shift = ms->shift[gr], *alpha = ms->alpha[gr];
-            bool unseen = true;
+            bool unseen = true, flip = false;   // flip: the sums are in the upper half of their columns
             const int begin = solo ? k0 : k0 + gr;
             float cq = 0.0f;   // what scores are multiplied by, but for the key's scale
             const int page0 = page_of(begin, 0);
@@ -460,86 +460,88 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                             if (!((bits >> r) & 1u)) x[r] = -INFINITY;
                     }
                 };
-                // Where a score passes its row's maximum by 2^kGrow, and until every row has seen a token, the group takes the maxima anew.
-                uint32_t grow = unseen;
-                if (!unseen) {
+                // Weights are made from the maxima as they are.  Where a score passes its row's by 2^kGrow the group takes the maxima anew and
+                // makes the tile's weights again, as it does first of all until every row has seen a token.  The sums before the
+                // tile stay where they were: the tile's go to the other half.
+                const uint32_t sums = colL + (flip ? NR : 0), sums_to = colL + (flip ? 0 : NR);
+#pragma unroll 1
+                for (uint32_t grow = unseen;; grow = 1) {
+                    if (grow) {
+#pragma unroll 1
+                        for (int q = 0; q < used; ++q) {
+                            float x[8];
+                            scores(q, ms->zero, x);
+                            const float top = reduce8(x, lane, [](float p, float q) { return fmaxf(p, q); });
+                            if ((lane & 3) == 0) ms->top[gr][wl][8 * q + (lane >> 2)] = top;
+                        }
+                        group_sync();
+                        if (wl == 0) {
+                            const float old = k > begin ? kLift - shift[lane] : kNoMax;
+                            const float now = fmaxf(fmaxf(fmaxf(ms->top[gr][0][lane], ms->top[gr][1][lane]), old),
+                                                    fmaxf(ms->top[gr][2][lane], ms->top[gr][3][lane]));
+                            alpha[lane] = ex2_fast(old - now);
+                            shift[lane] = kLift - now;
+                            const bool none = __any_sync(0xFFFFFFFFu, lane < vr && now == kNoMax);
+                            if (lane == 0) ms->unseen[gr] = none;
+                        }
+                        group_sync();
+                        unseen = *reinterpret_cast<volatile int *>(&ms->unseen[gr]);
+                        if (k > begin) {
+#pragma unroll 1
+                            for (int q = 0; q < used; ++q) {
+                                uint32_t o[8], l[8];
+                                tmem_ld8(colO + 8 * q, o);
+                                tmem_ld8(sums + 8 * q, l);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int r = 0; r < 8; ++r) {
+                                    const float f = alpha[8 * q + r];
+                                    o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
+                                    l[r] = __float_as_uint(__uint_as_float(l[r]) * f);
+                                }
+                                tmem_st8(colO + 8 * q, o);
+                                tmem_st8(sums + 8 * q, l);
+                            }
+                            tc_wait_st();
+                        }
+                    }
                     float over = -INFINITY;
 #pragma unroll 1
-                    for (int q = 0; q < used; ++q) {
+                    for (int q = 0; q < used; ++q) {   // eight rows' weights, a 16-byte chunk
                         float x[8];
+                        uint32_t l[8], w[4];
+                        tmem_ld8(sums + 8 * q, l);
                         scores(q, shift, x);
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) over = fmaxf(over, x[r]);
+                        for (int j = 0; j < 4; ++j) {
+                            over = fmaxf(over, fmaxf(x[2 * j], x[2 * j + 1]));
+                            const f32x2 e = f2_ex2(f2_pack(x[2 * j], x[2 * j + 1]));
+                            float y, z;
+                            f2_unpack(f2_fma(e, back, f2_from_u32x2(l[2 * j], l[2 * j + 1])), y, z);
+                            l[2 * j] = __float_as_uint(y);
+                            l[2 * j + 1] = __float_as_uint(z);
+                            f2_unpack(e, y, z);
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(z), "f"(y));
+                        }
+                        tmem_st8(sums_to + 8 * q, l);
+                        sts128(prow + ((q ^ ((t >> 1) & 3)) << 4), w);
                     }
+                    if (grow) break;
+                    uint32_t again;
                     asm volatile(
                         "{\n\t.reg .pred p, q;\n\tsetp.gt.f32 p, %1, %3;\n\t"
                         "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                        : "=r"(grow)
+                        : "=r"(again)
                         : "f"(over), "r"(1 + gr), "f"(kGrow + kLift)
                         : "memory");
+                    if (!again) break;
+                    tc_wait_st();
                 }
-                if (grow) {
-#pragma unroll 1
-                    for (int q = 0; q < used; ++q) {
-                        float x[8];
-                        scores(q, ms->zero, x);
-                        const float top = reduce8(x, lane, [](float p, float q) { return fmaxf(p, q); });
-                        if ((lane & 3) == 0) ms->top[gr][wl][8 * q + (lane >> 2)] = top;
-                    }
-                    group_sync();
-                    if (wl == 0) {
-                        const float old = k > begin ? kLift - shift[lane] : kNoMax;
-                        const float now = fmaxf(fmaxf(fmaxf(ms->top[gr][0][lane], ms->top[gr][1][lane]), old),
-                                                fmaxf(ms->top[gr][2][lane], ms->top[gr][3][lane]));
-                        alpha[lane] = ex2_fast(old - now);
-                        shift[lane] = kLift - now;
-                        const bool none = __any_sync(0xFFFFFFFFu, lane < vr && now == kNoMax);
-                        if (lane == 0) ms->unseen[gr] = none;
-                    }
-                    group_sync();
-                    unseen = *reinterpret_cast<volatile int *>(&ms->unseen[gr]);
-                    if (k > begin) {
-#pragma unroll 1
-                        for (int q = 0; q < used; ++q) {
-                            uint32_t o[8], l[8];
-                            tmem_ld8(colO + 8 * q, o);
-                            tmem_ld8(colL + 8 * q, l);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) {
-                                const float f = alpha[8 * q + r];
-                                o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
-                                l[r] = __float_as_uint(__uint_as_float(l[r]) * f);
-                            }
-                            tmem_st8(colO + 8 * q, o);
-                            tmem_st8(colL + 8 * q, l);
-                        }
-                        tc_wait_st();
-                    }
-                }
-#pragma unroll 1
-                for (int q = 0; q < used; ++q) {   // eight rows' weights, a 16-byte chunk
-                    float x[8];
-                    uint32_t l[8], w[4];
-                    tmem_ld8(colL + 8 * q, l);
-                    scores(q, shift, x);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const f32x2 e = f2_ex2(f2_pack(x[2 * j], x[2 * j + 1]));
-                        float y, z;
-                        f2_unpack(f2_fma(e, back, f2_from_u32x2(l[2 * j], l[2 * j + 1])), y, z);
-                        l[2 * j] = __float_as_uint(y);
-                        l[2 * j + 1] = __float_as_uint(z);
-                        f2_unpack(e, y, z);
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(z), "f"(y));
-                    }
-                    tmem_st8(colL + 8 * q, l);
-                    sts128(prow + ((q ^ (t & 7)) << 4), w);
-                }
+                flip = !flip;
                 if (down != 1.0f) {   // the rest of this token's scale
 #pragma unroll 1
                     for (int r = 0; r < vr; ++r) {
-                        uint16_t *at = reinterpret_cast<uint16_t *>(smem + S::OFF_P + gr * S::PBUF + t * (4 * NR) + (((r >> 3) ^ (t & 7)) << 4) + (r & 7) * 2);
+                        uint16_t *at = reinterpret_cast<uint16_t *>(smem + S::OFF_P + gr * S::PBUF + t * (2 * NR) + (((r >> 3) ^ ((t >> 1) & 3)) << 4) + (r & 7) * 2);
                         const float w = half_bits(*at);
                         *at = w == 0.0f ? 0 : __half_as_ushort(__float2half_rn(w * down));
                     }
@@ -565,14 +567,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                             const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, kk);
                             if (off < 0) continue;
                             const float v = t < a.c.head_dim ? codes2(reinterpret_cast<const uint8_t *>(a.c.v + off + pi->h * a.c.head_b)[t]).x : 0.0f;
-                            const char *pj = smem + S::OFF_P + gr * S::PBUF + j * (4 * NR);
+                            const char *pj = smem + S::OFF_P + gr * S::PBUF + j * (2 * NR);
                             uint32_t o[32];
                             tmem_ld32(colO, o);
                             tc_wait_ld();
 #pragma unroll
                             for (int r = 0; r < NR; ++r) {
                                 const int at = (r & 7) * 2;
-                                const float w = half_bits(*reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ (j & 7)) << 4) + at));
+                                const float w = half_bits(*reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ ((j >> 1) & 3)) << 4) + at));
                                 if (((see >> r) & 1u) && r < vr) o[r] = __float_as_uint(__uint_as_float(o[r]) + w * v);
                             }
                             tmem_st32(colO, o);
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
             for (int q = 0; q < used; ++q) {
                 uint32_t l[8];
                 float x[8];
-                tmem_ld8(colL + 8 * q, l);
+                tmem_ld8(colL + (flip ? NR : 0) + 8 * q, l);
                 tc_wait_ld();
 #pragma unroll
                 for (int r = 0; r < 8; ++r) x[r] = __uint_as_float(l[r]);
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
 #pragma unroll 1
                 for (int g = ga; g < (solo ? ga + 1 : 2); ++g) {
                     uint32_t o[4];
-                    tmem_ld4(base + 128 + g * 64 + rb, o);
+                    tmem_ld4(base + S::COL_O + g * NR + rb, o);
                     tc_wait_ld();
                     const float4 f = *reinterpret_cast<const float4 *>(ms->alpha[g] + rb);
                     y[0] = fmaf(__uint_as_float(o[0]), f.x, y[0]);
@@ -668,8 +670,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
         widen_codes<DP>(fd, f8, sbase, tmem, warp - 8, lane);
     } else {
         regs_dec<kRegsOther>();
-        if (warp == 12) {
-            issue_products<DP>(fd, ms, a2.shape_s, mma_shape_f16(2 * NR, true, true, false, false), sbase, tmem, lane);
+        if (warp == 12) {   // V transposed times the weights
+            issue_products<DP>(fd, ms, a2.shape_s, mma_shape_f16(NR, true, true, false, false), sbase, tmem, lane);
         } else if (warp == 13) {
             feed_walk(a, a2, fd, ms->walk, lane, [&](int it) {
                 if (__all_sync(0xFFFFFFFFu, wait_phase(fd, &fd->q_empty[it & 1], ((it >> 1) & 1) ^ 1))) {
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 }
             });
         } else {
-            feed8_load<DP, S::SLOTS, false, true>(a, a2, fd, f8, sbase + S::OFF_RAW + (warp - 14) * (S::SLOTS * kRawTokens * DP), warp - 14, lane);
+            feed8_load<DP, S::TOK, S::SLOTS, false, true>(a, a2, fd, f8, sbase + S::OFF_RAW + (warp - 14) * (S::SLOTS * S::TOK * DP), warp - 14, lane);
         }
     }
     tc_fence_before();
