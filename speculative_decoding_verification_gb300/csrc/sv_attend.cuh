@@ -27,6 +27,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 // What the cutting has in common with its test on the host.
 #define SV_HD __host__ __device__ __forceinline__
+// The larger parts of the walk, which a kernel may want out of line (sv_attend_few8.cu): instruction fetches cost it more than calls.
+#ifndef SV_WALK_PART
+#define SV_WALK_PART SV_HD
+#endif
 
 // Row and key tiles of a kernel and what they cost: a key tile, one for more than TM / 2 rows, setting a unit up and writing it out.
 struct AttendTiles {
@@ -119,7 +123,7 @@ SV_HD int group_of(const AttendArgs &a, int b) {
 SV_HD int clamp_int(long long x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : (int)x; }
 
 // Segment s, with every device value clamped to what the arrays hold.  `check` reports what had to be.
-SV_HD Seg seg_of(const AttendArgs &a, const AttendGeo &geo, int s, bool check) {
+SV_WALK_PART Seg seg_of(const AttendArgs &a, const AttendGeo &geo, int s, bool check) {
     Seg g;
     const int cap = a.bt.max_pages * a.c.page_size;
     if (s < a.n_groups) {
@@ -179,13 +183,13 @@ SV_HD int seg_tiles(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int
 SV_HD int tile_cost(const AttendGeo &geo, const Seg &g, int t) {
     return 2 * min(geo.TM, g.packed - t * geo.TM) > geo.TM ? geo.tall_cost : geo.tile_cost;
 }
-SV_HD int unit_span(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+SV_WALK_PART int unit_span(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
     const int kt = seg_tiles(a, geo, g, t);
     return kt > 0 ? geo.unit_cost + kt * tile_cost(geo, g, t) : 0;
 }
 
 // Place of row tile t among a key head's units (t = tiles_m: the cost of all).
-SV_HD int units_before(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
+SV_WALK_PART int units_before(const AttendArgs &a, const AttendGeo &geo, const Seg &g, int t) {
     if (t <= 0) return 0;
     if (!g.chain) return (t - 1) * unit_span(a, geo, g, 0) + unit_span(a, geo, g, t - 1);   // all but the last are full
     int n = 0;

@@ -19,6 +19,8 @@
 // What bounds it: issue slots and memory; a tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth.
 #include <float.h>
 
+#define SV_WALK_PART static __host__ __device__ __noinline__
+
 #include "sv_attend_feed8.cuh"
 #include "sv_attend_few.cuh"
 
@@ -98,26 +100,40 @@ __device__ __forceinline__ void make_queries(const AttendArgs &a, PieceInfo *pi,
     constexpr int CH = DP / 8, RPP = 32 / CH;   // chunks of a row, rows of a pass
     const int r0 = lane / CH, ch = lane % CH, vr = pi->vr, m0 = pi->m0;
     const bool real = ch * 8 < a.c.head_dim;
+    // Copied to where they will be, all at once; a lane then finds the largest of its chunks, and rewrites them.
     const char *q = a.q + (int64_t)pi->r0 * a.q_row + (int64_t)pi->h * a.G * a.q_head + ch * 16;
     const int rows = ((vr + 7) & ~7) / RPP;   // passes: the softmax works on blocks of eight rows
-    // The lane's row of a pass, its head and place; the next pass's is RPP further.
-    const int i0 = (m0 + r0) / a.G, g0 = m0 + r0 - i0 * a.G, di = RPP / a.G, dg = RPP - di * a.G;
-    const int64_t at0 = i0 * a.q_row + g0 * a.q_head, d0 = di * a.q_row + dg * a.q_head, wrap = a.q_row - a.G * a.q_head;
-    auto each = [&](auto use) {
-        int g = g0;
-        int64_t at = at0;
-#pragma unroll 2
+    const uint32_t half = tile + (ch >> 3) * (NR * 128);
+    auto place = [&](int pass) {
+        const int r = pass * RPP + r0;
+        return half + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    };
+    {
+        // the lane's row of a pass, its head and place; the next pass's is RPP further
+        const int i0 = (m0 + r0) / a.G, di = RPP / a.G, dg = RPP - di * a.G;
+        int g = m0 + r0 - i0 * a.G;
+        int64_t at = i0 * a.q_row + g * a.q_head;
+        const int64_t step = di * a.q_row + dg * a.q_head, wrap = a.q_row - a.G * a.q_head;
+#pragma unroll 1
         for (int pass = 0; pass < rows; ++pass) {
-            const int m = pass * RPP + r0;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (m < vr && real) w = *reinterpret_cast<const uint4 *>(q + at);
+            const bool ok = pass * RPP + r0 < vr && real;
+            cp_async16(place(pass), q + (ok ? at : -(int64_t)ch * 16), ok);
             g += dg;
-            at += d0;
+            at += step;
             if (g >= a.G) {
                 g -= a.G;
                 at += wrap;
             }
-            use(m, w);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+    }
+    auto each = [&](auto use) {
+#pragma unroll 2
+        for (int pass = 0; pass < rows; ++pass) {
+            uint4 w;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(place(pass)) : "memory");
+            use(pass, w);
         }
     };
     // The largest finite number: bits of |x| rise as it does, so pairs are compared as whole numbers.  Infinities and NaN, above all others,
@@ -143,7 +159,7 @@ __device__ __forceinline__ void make_queries(const AttendArgs &a, PieceInfo *pi,
     const float f = __uint_as_float((uint32_t)(127 + up) << 23);
     const f32x2 f2 = f2_pack(f, f);
     if (lane == 0) pi->q_back = __uint_as_float((uint32_t)(127 - up) << 23);
-    each([&](int r, uint4 w) {
+    each([&](int pass, uint4 w) {
         const uint32_t in[4] = {w.x, w.y, w.z, w.w};
         uint32_t y[4];
 #pragma unroll
@@ -152,7 +168,7 @@ __device__ __forceinline__ void make_queries(const AttendArgs &a, PieceInfo *pi,
             f2_unpack(f2_mul(f2_from_bf16x2(in[i]), f2), a0, a1);
             asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(a1), "f"(a0));
         }
-        sts128(tile + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), y);
+        sts128(place(pass), y);
     });
     fence_async_smem();
 }
@@ -364,7 +380,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
     const uint32_t sbase = smem_addr(smem);
 
     if (warp < 8) {
-        regs_inc<kRegsSoftmax>();
         // ---------------------------------------------------------------- softmax
         const int gr = warp >> 2, wl = warp & 3, t = wl * 32 + lane;   // group, warp of it, token of the tile (head element at the end)
         const uint32_t base = tmem + ((uint32_t)(wl * 32) << 16);
@@ -373,6 +388,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
         uint32_t u = 0;   // tiles this group has worked on
         int rests = 0;    // the group that left the last piece of one tile to the other
         auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + gr) : "memory"); };
+        auto page_of = [&](const PieceInfo *p, int k, int token) {
+            const int key = min(p->key0 + k * kTcKeys + token, p->end - 1);
+            return a.bt.page_table[p->table * a.bt.table_pitch + (a2.page_shift >= 0 ? key >> a2.page_shift : key / a.c.page_size)];
+        };
+        // Pages of the group's first tile of a piece (this thread's token's, the first token's) and of its second: asked for at the end of
+        // the piece before, where the next one is known by then.
+        int page = 0, page0 = 0, page_next = 0;
+        bool asked = false;
+        auto ask = [&](const PieceInfo *p, int begin) {
+            page = page_of(p, begin, t);
+            page0 = page_of(p, begin, 0);
+            page_next = page_of(p, begin + 2, t);
+        };
         for (int it = 0;; ++it) {
             const PieceInfo *pi = &fd->pd[it % kRing];
             if (!wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1)) break;
@@ -383,6 +411,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
             if (solo) {
                 rests ^= 1;
                 if (rests == gr) {
+                    __syncwarp();
                     if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
                     continue;
                 }
@@ -391,13 +420,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
             // This thread's token's scales: pages are looked up two tiles of the group ahead, scales one.  A warp stops at the first use
             // of a load that is still on its way, so what is loaded ahead is not looked at, not even to leave it out: a token past the
             // unit's last takes the last one's, and a bad page is page 0's until its scales are used.
-            const int32_t *table = a.bt.page_table + pi->table * a.bt.table_pitch;
             const uint8_t *ks = a.sc.k + pi->h * a.sc.head_b, *vs8 = a.sc.v + pi->h * a.sc.head_b;
-            const int last = pi->end - 1;
-            auto page_of = [&](int k, int token) {
-                const int key = min(key0 + k * kTcKeys + token, last);
-                return table[a2.page_shift >= 0 ? key >> a2.page_shift : key / a.c.page_size];
-            };
             auto good = [&](int page) { return (unsigned)page < (unsigned)a.c.n_pages; };
             auto byte_of = [&](const uint8_t *scales, int page) -> uint32_t { return scales[(good(page) ? page : 0) * a.sc.page_b]; };
             {
@@ -412,8 +435,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
             bool unseen = true, flip = false;   // flip: the sums are in the upper half of their columns
             const int begin = solo ? k0 : k0 + gr;
             float cq = 0.0f;   // what scores are multiplied by, but for the key's scale
-            const int page0 = page_of(begin, 0);
-            int page = page_of(begin, t), page_next = page_of(begin + 2, t);
+            if (!asked) ask(pi, begin);
             uint32_t kb_next = byte_of(ks, page), vb_next = byte_of(vs8, page);
             const uint32_t v0 = byte_of(vs8, page0);
             for (int k = begin; k < k1; k += 2, ++u) {
@@ -426,7 +448,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 page = page_next;
                 kb_next = byte_of(ks, page);
                 vb_next = byte_of(vs8, page);
-                page_next = page_of(k + 4, t);
+                page_next = page_of(pi, k + 4, t);
                 const int e0 = min(max((int)v0, 127 - 40), 127 + 40);   // byte that the values' scales are taken from
                 if (k == begin) cq = a.scale_log2 * *reinterpret_cast<const volatile float *>(&pi->q_back);
                 const float cs = fminf(cq, FLT_MAX) * scale_of(kb);
@@ -666,10 +688,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
             end_sync();   // outputs, sums and maxima may be written again
         }
     } else if (warp < 12) {
-        regs_dec<kRegsOther>();
         widen_codes<DP>(fd, f8, sbase, tmem, warp - 8, lane);
     } else {
-        regs_dec<kRegsOther>();
         if (warp == 12) {   // V transposed times the weights
             issue_products<DP>(fd, ms, a2.shape_s, mma_shape_f16(NR, true, true, false, false), sbase, tmem, lane);
         } else if (warp == 13) {
