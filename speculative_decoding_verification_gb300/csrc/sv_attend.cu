@@ -597,7 +597,7 @@ static sv_status attend_call(const KvCache &c, const KvScale &sc, const sv_kv_ba
         }
         e = !fma && sc.k ? launch_attend_few8(a, s)
             : !fma ? launch_attend_few(a, s)
-            : es == 4 && c.head_dim <= 128 && packed <= kFewRows32 && sc.k == nullptr ? launch_attend_few32(a, s)
+            : es == 4 && c.head_dim <= 128 && packed <= kFewRows32 ? launch_attend_few32(a, s)
                                                                          : launch_attend_f32(a, es, true, s);
         own = a.geo;
     }

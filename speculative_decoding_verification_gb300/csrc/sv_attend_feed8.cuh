@@ -317,7 +317,7 @@ __device__ __forceinline__ void feed8_widen(const AttendArgs &a, Feed *fd, Feed8
                 if (!on) break;
                 const uint32_t raw = raw_base + slot * SLOT + from;
                 const uint32_t tile = kv_base + stage * TILE + s * (kRawTokens * 128) + to_half;
-#pragma unroll 2
+#pragma unroll
                 for (int v = 0; v < kRawTokens / PASS / 2; ++v) {
                     const int u = sub * (kRawTokens / PASS / 2) + v, row = u * PASS + row0;
                     uint4 w;

@@ -50,7 +50,8 @@ __device__ __forceinline__ void scale_quad(Quad &o, float f) {
     o.b = f2_fma(o.b, f2, none);
 }
 
-template <int R>
+// C8: the cache is held in 8 bits.  Codes are copied as they are, and become floats, times their scale, as they are read.
+template <int R, bool C8>
 __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs a) {
     constexpr int KB = 32 / R;   // tokens of a batch
     __shared__ Walk s_walk;
@@ -67,13 +68,14 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
     const bool has = lane < D4;                  // the lane holds elements
     float4 *mine = ring + (size_t)wp * 32 * D4;
     const uint32_t mine_at = smem_addr(mine);
-    // A tile's 8 tokens are 8 D4 chunks of 16 bytes of keys and as many of values; lane's chunk i is number lane + 32 i.
-    const int chunks = 8 * D4;
-    int place[8];   // token + 8 * (bytes into the row) of the lane's chunks
+    // A tile's 8 tokens are 8 D4 chunks of 16 bytes of keys (of codes a quarter) and as many of values; lane's chunk i is number lane + 32 i.
+    constexpr int CHUNKS = C8 ? 2 : 8;
+    const int row_chunks = C8 ? D4 / 4 : D4, chunks = 8 * row_chunks;
+    int place[CHUNKS];   // token + 8 * (bytes into the row) of the lane's chunks
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = lane + 32 * i, j = c / D4;
-        place[i] = c < chunks ? j + 8 * 16 * (c - j * D4) : -1;
+    for (int i = 0; i < CHUNKS; ++i) {
+        const int c = lane + 32 * i, j = c / row_chunks;
+        place[i] = c < chunks ? j + 8 * 16 * (c - j * row_chunks) : -1;
     }
     const int step_pages = 64 / psize, step_slots = 64 - step_pages * psize;   // a tile further in the page table
     for (int first = 1;; first = 0) {
@@ -108,8 +110,14 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
         int next_key = p.g.key0 + p.k0 * 64 + wp * 8 + lane;
         int next_pn = next_key / psize, next_slot = next_key - next_pn * psize, next_page = INT32_MIN;
         auto look_up = [&]() { next_page = lane < 8 && next_key < p.end ? table[next_pn] : INT32_MIN; };
+        uint32_t kb = 127, vb = 127, kb_next = 127, vb_next = 127;   // C8: scales of the lane's token of the tile at hand, of the next
         auto copy = [&](int k) {   // tile k, which has been looked up; looks up the next
             int64_t off = -1;
+            if (C8) {
+                const int page = (unsigned)next_page < (unsigned)a.c.n_pages ? next_page : 0;
+                kb_next = a.sc.k[page * a.sc.page_b + h * a.sc.head_b];
+                vb_next = a.sc.v[page * a.sc.page_b + h * a.sc.head_b];
+            }
             if (next_page >= 0 && next_page < a.c.n_pages) off = next_page * a.c.page_b + next_slot * a.c.slot_b + h * a.c.head_b;
             else if (next_page != INT32_MIN) report_error(a.stats, SV_ERR_INVALID_ARG, p.g.table);
             next_key += 64;
@@ -122,7 +130,7 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
             look_up();
             const uint32_t to = mine_at + (uint32_t)((k & 1) * 2 * chunks + lane) * 16;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < CHUNKS; ++i) {
                 if (32 * i >= chunks) break;
                 const int64_t at = __shfl_sync(0xFFFFFFFFu, off, place[i] & 7);
                 if (place[i] >= 0) {
@@ -139,12 +147,24 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
         auto tile = [&](int k, auto hidden) {
             const int key0 = p.g.key0 + k * 64 + wp * 8;
             const float4 *keys = mine + (k & 1) * 2 * chunks + lane, *values = keys + chunks;
+            const uint32_t *kcodes = reinterpret_cast<const uint32_t *>(mine + (k & 1) * 2 * chunks) + lane, *vcodes = kcodes + 4 * chunks;
+            // Four elements of the warp's token j: floats, or codes times their scale.
+            auto four = [&](const float4 *floats, const uint32_t *codes, float scale, int j) {
+                if constexpr (!C8) {
+                    return quad(has ? floats[j * D4] : make_float4(0.f, 0.f, 0.f, 0.f));
+                } else {
+                    Quad x = quad(has ? codes4(codes[j * D4]) : make_float4(0.f, 0.f, 0.f, 0.f));
+                    scale_quad(x, scale);
+                    return x;
+                }
+            };
+            const float ks = C8 ? scale_of(kb) : 1.0f, vs = C8 ? scale_of(vb) : 1.0f;
 #pragma unroll
             for (int b = 0; b < 8 / KB; ++b) {
                 float x[32];
 #pragma unroll
                 for (int j = 0; j < KB; ++j) {
-                    const Quad kk = quad(has ? keys[(b * KB + j) * D4] : make_float4(0.f, 0.f, 0.f, 0.f));
+                    const Quad kk = four(keys, kcodes, C8 ? __shfl_sync(0xFFFFFFFFu, ks, b * KB + j) : 1.0f, b * KB + j);
 #pragma unroll
                     for (int r = 0; r < R; ++r) x[j * R + r] = f2_sum(f2_fma(q[r].a, kk.a, f2_fma(q[r].b, kk.b, 0ull)));
                 }
@@ -172,7 +192,7 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
                 l += e;
 #pragma unroll
                 for (int j = 0; j < KB; ++j) {
-                    const Quad vv = quad(has ? values[(b * KB + j) * D4] : make_float4(0.f, 0.f, 0.f, 0.f));
+                    const Quad vv = four(values, vcodes, C8 ? __shfl_sync(0xFFFFFFFFu, vs, b * KB + j) : 1.0f, b * KB + j);
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const float f = __shfl_sync(0xFFFFFFFFu, e, j * R + r);
@@ -187,6 +207,8 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
         };
         const int seen_by_all = p.seg >= a.n_groups ? p.g.ctx : p.end;
         for (int k = p.k0; k < p.k1; ++k) {
+            kb = kb_next;
+            vb = vb_next;
             if (k + 1 < p.k1) {
                 copy(k + 1);
                 cp_async_wait<1>();
@@ -254,21 +276,22 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
     }
 }
 
-template <int R>
+template <int R, bool C8>
 cudaError_t run_few32(AttendArgs &a, cudaStream_t stream) {
     a.geo.set(tiles_few32(R));
     const size_t bytes = (size_t)kWarps32 * 32 * a.c.head_dim * 4;
-    const int resident = prepare_kernel((const void *)k_attend_few32<R>, kThreads32, bytes);
+    const int resident = prepare_kernel((const void *)k_attend_few32<R, C8>, kThreads32, bytes);
     if (resident < 1) return cudaErrorInvalidConfiguration;
     a.geo.blocks *= resident < 2 ? 1 : 2;
-    k_attend_few32<R><<<a.geo.blocks, kThreads32, bytes, stream>>>(a);
+    k_attend_few32<R, C8><<<a.geo.blocks, kThreads32, bytes, stream>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attend_few32(AttendArgs &a, cudaStream_t stream) {
-    return (int64_t)a.bt.n * a.G <= 4 ? run_few32<4>(a, stream) : run_few32<8>(a, stream);
+    if (a.sc.k) return (int64_t)a.bt.n * a.G <= 4 ? run_few32<4, true>(a, stream) : run_few32<8, true>(a, stream);
+    return (int64_t)a.bt.n * a.G <= 4 ? run_few32<4, false>(a, stream) : run_few32<8, false>(a, stream);
 }
 
 }  // namespace sv

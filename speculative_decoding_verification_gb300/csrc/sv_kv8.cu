@@ -98,16 +98,17 @@ __device__ __forceinline__ float most_finite(const float *x) {
     return m;
 }
 
-// A block takes one row's queries; the first row that a page gets also takes that page's keys and values: the largest element a head, the
-// page's scale from it, then the codes.  Keys are rotated twice, once for each, from the first-level cache the second time.
+// The first row that a page gets takes that page's keys (even blockIdx.y) or values (odd) of eight key heads: the largest element a head, the page's
+// scale from it, then the codes.  Keys are rotated twice, once for each, from the first-level cache the second time.  The blocks for
+// values, which need no angles for them, take every row's queries, an equal part a group of heads.
 template <int ES, bool VEC>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args a) {
     constexpr int E = VEC ? 16 / ES : 1, EV = 16 / ES;
     __shared__ float2 cs[kChunk][SV_KV_MAX_HEAD_DIM / 2];
     __shared__ int32_t par[SV_MAX_TREE];
     __shared__ int s_depth[kChunk];
-    __shared__ uint32_t s_most[2][kHeadGroup];   // bits of floats >= 0 rise as they do
-    __shared__ int s_byte[2][kHeadGroup], s_shift[2][kHeadGroup];
+    __shared__ uint32_t s_most[kHeadGroup];   // bits of floats >= 0 rise as they do
+    __shared__ int s_byte[kHeadGroup], s_shift[kHeadGroup];
     const int tid = threadIdx.x;
     const int row = blockIdx.x, b = row_sequence(a.bt, row);
     const SeqRows sr = seq_rows(a.bt, b);
@@ -120,8 +121,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args
     if (i < 0 || i >= sr.n) return;   // a row of no sequence
     const int psize = a.c.page_size, slot0 = ctx + i, pn = slot0 / psize, place0 = slot0 - pn * psize;
     const bool leads = i == 0 || place0 == 0;
-    if (!leads && a.q == nullptr) return;
-    const int T = leads ? min(sr.n - i, psize - place0) : 1;   // rows whose angles are needed
+    const int which = blockIdx.y & 1;             // keys or values
+    const bool turns = which && a.q != nullptr;   // queries too
+    if (!leads && !turns) return;
+    const int T = leads ? min(sr.n - i, psize - place0) : 1;   // rows of the page
     int page = 0;
     if (leads) {
         page = a.bt.page_table[b * a.bt.table_pitch + pn];
@@ -130,9 +133,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args
             page = -1;
         }
     }
+    const int angled = which ? 1 : T;   // rows whose angles are needed
     if (a.bt.parents != nullptr)
-        for (int j = tid; j < i + T - 1; j += kAppendThreads) par[j] = a.bt.parents[(int64_t)b * (a.bt.n - 1) + j];
-    if (tid < 2 * kHeadGroup) s_most[tid / kHeadGroup][tid % kHeadGroup] = 0;
+        for (int j = tid; j < i + angled - 1; j += kAppendThreads) par[j] = a.bt.parents[(int64_t)b * (a.bt.n - 1) + j];
+    if (tid < kHeadGroup) s_most[tid] = 0;
     __syncthreads();
 
     auto angles = [&](int t0, int n) {   // rows i + t0 .. i + t0 + n - 1
@@ -162,10 +166,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args
     };
 
     const int per = rot_items<ES, VEC>(a.sh);   // items of a rotated head
-    const int h0 = blockIdx.y * kHeadGroup, heads = min(kHeadGroup, a.c.kv_heads - h0);
-    angles(0, min(T, kChunk));
-    if (a.q != nullptr) {   // the row's query heads, an equal part a block
-        const int q0 = (int)((int64_t)a.sh.heads * blockIdx.y / gridDim.y), q1 = (int)((int64_t)a.sh.heads * (blockIdx.y + 1) / gridDim.y);
+    const int group = blockIdx.y >> 1, groups = gridDim.y >> 1, h0 = group * kHeadGroup, heads = min(kHeadGroup, a.c.kv_heads - h0);
+    if (turns || which == 0) angles(0, min(angled, kChunk));
+    if (turns) {
+        const int q0 = (int)((int64_t)a.sh.heads * group / groups), q1 = (int)((int64_t)a.sh.heads * (group + 1) / groups);
         for (int t = tid; t < per * (q1 - q0); t += kAppendThreads) {
             const int h = q0 + t / per;
             rot_item<ES, VEC>(a.sh, a.q + (int64_t)row * a.q_row + h * a.q_head, a.q_out + (int64_t)row * a.qo_row + h * a.qo_head, t % per,
@@ -174,70 +178,70 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args
     }
     if (!leads || page < 0) return;
 
-    const int vper = a.c.head_dim / EV, kitems = heads * per, all = kitems + heads * vper;
-    char *kc = a.c.k + page * a.c.page_b + h0 * a.c.head_b, *vc = a.c.v + page * a.c.page_b + h0 * a.c.head_b;
-    auto each = [&](int t0, int n, auto &&use) {   // use(token, which, head, element, values, count) for all items of a chunk of tokens
+    const int vper = a.c.head_dim / EV, of_head = which ? vper : per, all = heads * of_head;
+    char *codes = (which ? a.c.v : a.c.k) + page * a.c.page_b + h0 * a.c.head_b;
+    uint8_t *scales = (which ? a.v_scale : a.k_scale) + page * a.scale_page + h0 * a.scale_head;
+    const char *src = which ? a.v : a.k;
+    const int64_t src_row = which ? a.v_row : a.k_row, src_head = which ? a.v_head : a.k_head;
+    auto each = [&](int t0, int n, auto &&use) {   // use(token, head, element, values, count) for all items of a chunk of tokens
         for (int u = tid; u < n * all; u += kAppendThreads) {
-            const int t = u / all, w = u - t * all;
-            const int64_t r = row + t0 + t;
-            if (w < kitems) {
-                const int h = w / per;
+            const int t = u / all, w = u - t * all, h = w / of_head, i = w - h * of_head;
+            const char *x0 = src + (int64_t)(row + t0 + t) * src_row + (h0 + h) * src_head;
+            if (which) {
+                float x[EV];
+                unpack<ES>(*reinterpret_cast<const uint4 *>(x0 + (size_t)i * 16), x);
+                use(t0 + t, h, i * EV, x, std::integral_constant<int, EV>{});
+            } else {
                 float x[E], y[E];
                 int e0, e1;
-                rot_values<ES, VEC>(a.sh, a.k + r * a.k_row + (h0 + h) * a.k_head, w - h * per, cs[t], x, y, e0, e1);
-                use(t0 + t, 0, h, e0, x, std::integral_constant<int, E>{});
-                if (e1 >= 0) use(t0 + t, 0, h, e1, y, std::integral_constant<int, E>{});
-            } else {
-                const int h = (w - kitems) / vper, e = (w - kitems - h * vper) * EV;
-                float x[EV];
-                unpack<ES>(*reinterpret_cast<const uint4 *>(a.v + r * a.v_row + (h0 + h) * a.v_head + (size_t)e * ES), x);
-                use(t0 + t, 1, h, e, x, std::integral_constant<int, EV>{});
+                rot_values<ES, VEC>(a.sh, x0, i, cs[t], x, y, e0, e1);
+                use(t0 + t, h, e0, x, std::integral_constant<int, E>{});
+                if (e1 >= 0) use(t0 + t, h, e1, y, std::integral_constant<int, E>{});
             }
         }
     };
-    for (int t0 = 0; t0 < T; t0 += kChunk) {
+    const int chunk = which ? T : kChunk;   // values need no angles: all rows at once
+    for (int t0 = 0; t0 < T; t0 += chunk) {
         if (t0 > 0) {
             __syncthreads();
             angles(t0, min(T - t0, kChunk));
         }
-        each(t0, min(T - t0, kChunk), [&](int, int which, int h, int, const float *x, auto n) {
+        each(t0, min(T - t0, chunk), [&](int, int h, int, const float *x, auto n) {
             const uint32_t m = __float_as_uint(most_finite<n.value>(x));
-            if (m > *reinterpret_cast<volatile uint32_t *>(&s_most[which][h])) atomicMax(&s_most[which][h], m);
+            if (m > *reinterpret_cast<volatile uint32_t *>(&s_most[h])) atomicMax(&s_most[h], m);
         });
     }
     __syncthreads();
     const bool fresh = place0 == 0;   // no cached token in the page
-    if (tid < 2 * heads) {
-        const int which = tid / heads, h = tid - which * heads;
-        uint8_t *at = (which ? a.v_scale : a.k_scale) + page * a.scale_page + (h0 + h) * a.scale_head;
-        int byte = scale_for(__uint_as_float(s_most[which][h])), shift = 0;
+    if (tid < heads) {
+        uint8_t *at = scales + tid * a.scale_head;
+        int byte = scale_for(__uint_as_float(s_most[tid])), shift = 0;
         if (!fresh) {
             const int old = *at;
             byte = max(byte, old);
             shift = byte - old;
         }
         if (fresh || shift > 0) *at = (uint8_t)byte;
-        s_byte[which][h] = byte;
-        s_shift[which][h] = shift;
+        s_byte[tid] = byte;
+        s_shift[tid] = shift;
     }
     __syncthreads();
-    for (int t0 = 0; t0 < T; t0 += kChunk) {
-        if (T > kChunk) {
+    for (int t0 = 0; t0 < T; t0 += chunk) {
+        if (!which && T > kChunk) {
             if (t0 > 0) __syncthreads();
             angles(t0, min(T - t0, kChunk));
         }
-        each(t0, min(T - t0, kChunk), [&](int t, int which, int h, int e, const float *x, auto n) {
-            const float inv = scale_of(s_byte[which][h] == 255 ? 255 : 254 - s_byte[which][h]);
-            store_codes<n.value>((which ? vc : kc) + (place0 + t) * a.c.slot_b + h * a.c.head_b + e, x, inv);
+        each(t0, min(T - t0, chunk), [&](int t, int h, int e, const float *x, auto n) {
+            const float inv = scale_of(s_byte[h] == 255 ? 255 : 254 - s_byte[h]);
+            store_codes<n.value>(codes + (place0 + t) * a.c.slot_b + h * a.c.head_b + e, x, inv);
         });
     }
     if (!fresh) {   // the page's cached tokens, where a scale has grown
-        const int vec = a.c.head_dim / 16, of = 2 * heads * vec;
+        const int vec = a.c.head_dim / 16, of = heads * vec;
         for (int u = tid; u < place0 * of; u += kAppendThreads) {
-            const int t = u / of, w = u - t * of, hh = w / vec, which = hh / heads, h = hh - which * heads;
-            const int shift = s_shift[which][h];
+            const int t = u / of, w = u - t * of, h = w / vec, shift = s_shift[h];
             if (shift == 0) continue;
-            uint4 *at = reinterpret_cast<uint4 *>((which ? vc : kc) + t * a.c.slot_b + h * a.c.head_b + (w - hh * vec) * 16);
+            uint4 *at = reinterpret_cast<uint4 *>(codes + t * a.c.slot_b + h * a.c.head_b + (w - h * vec) * 16);
             *at = rescaled16(*at, shift);
         }
     }
@@ -359,7 +363,7 @@ extern "C" sv_status sv_kv_append8(const sv_kv_cache8 *cache, const sv_kv_batch 
                                    {q_out, q_out_row_stride * es, q_out_head_stride * es, batch->rows, q_heads, width}))
         return SV_ERR_INVALID_ARG;
     const int groups = (cache->kv_heads + kHeadGroup - 1) / kHeadGroup;
-    if (groups > 65535) return SV_ERR_INVALID_ARG;
+    if (2 * groups > 65535) return SV_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (!on_current_device(s, cache->k, k)) return SV_ERR_INVALID_ARG;
     if (stats && cudaMemsetAsync(stats, 0, sizeof(sv_stats), s) != cudaSuccess) return SV_ERR_CUDA;
@@ -369,7 +373,7 @@ extern "C" sv_status sv_kv_append8(const sv_kv_cache8 *cache, const sv_kv_batch 
                   q_row_stride * es, q_head_stride * es, q_out_row_stride * es, q_out_head_stride * es, k_row_stride * es, k_head_stride * es,
                   v_row_stride * es, v_head_stride * es, inv_freq, {q_heads, cache->head_dim, rotary_dim / 2, style}, magnitude, stats};
     const bool vec = rot_vec(rotary_dim / 2, style, es);
-    const dim3 grid((unsigned)batch->rows, (unsigned)groups);
+    const dim3 grid((unsigned)batch->rows, (unsigned)(2 * groups));   // keys and values
     if (es == 4)
         vec ? k_kv_append8<4, true><<<grid, kAppendThreads, 0, s>>>(a) : k_kv_append8<4, false><<<grid, kAppendThreads, 0, s>>>(a);
     else
