@@ -7,8 +7,8 @@ namespace sv {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kHeadGroup = 8;    // key heads of a block
+constexpr int kHeadGroup = 8;    // key heads of a block, a warp each
+constexpr int kAppendThreads = 32 * kHeadGroup;
 constexpr int kChunk = 8;        // tokens whose angles are held at a time
 
 struct Append8Args {
@@ -98,19 +98,32 @@ __device__ __forceinline__ float most_finite(const float *x) {
     return m;
 }
 
-// The first row that a page gets takes that page's keys (even blockIdx.y) or values (odd) of eight key heads: the largest element a head, the page's
-// scale from it, then the codes.  Keys are rotated twice, once for each, from the first-level cache the second time.  The blocks for
-// values, which need no angles for them, take every row's queries, an equal part a group of heads.
+__device__ __forceinline__ void prefetch_l1(const char *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
+// The first row that a page gets takes that page's keys and values, a warp to each of eight key heads: the largest element, the page's
+// scale from it, then the codes.  Keys are rotated twice, once for each, from the first-level cache the second time.  Every row
+// takes its queries, an equal part a group of heads.
+//
+// Bound by latency and instruction issue, not by bytes: a scale needs the page's whole part of the block before its first code, and an
+// element is read, turned, looked at, turned again and rounded.  512 sequences x 6 rows, 32 + 8 + 8 heads of 128, bf16: 36 us, 10.4 us at the
+// memory's rate.  What it reads is asked for before the addresses that hang on the context length are known (42 us without); a
+// block for keys and one for values instead of one for both: 37.6 us; a block's maxima joined in shared memory: 37 us; blocks of 64 threads: 43 us.
 template <int ES, bool VEC>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args a) {
     constexpr int E = VEC ? 16 / ES : 1, EV = 16 / ES;
     __shared__ float2 cs[kChunk][SV_KV_MAX_HEAD_DIM / 2];
     __shared__ int32_t par[SV_MAX_TREE];
     __shared__ int s_depth[kChunk];
-    __shared__ uint32_t s_most[kHeadGroup];   // bits of floats >= 0 rise as they do
-    __shared__ int s_byte[kHeadGroup], s_shift[kHeadGroup];
-    const int tid = threadIdx.x;
-    const int row = blockIdx.x, b = row_sequence(a.bt, row);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = blockIdx.x, group = blockIdx.y, groups = gridDim.y, h = group * kHeadGroup + warp;
+    const int q0 = (int)((int64_t)a.sh.heads * group / groups), q1 = (int)((int64_t)a.sh.heads * (group + 1) / groups);
+    const int lines = (a.c.head_dim * ES + 127) / 128;   // of a head
+    if (a.q != nullptr)
+        for (int t = tid; t < (q1 - q0) * lines; t += kAppendThreads) {
+            const int h = t / lines;
+            prefetch_l1(a.q + (int64_t)row * a.q_row + (q0 + h) * a.q_head + (t - h * lines) * 128);
+        }
+    const int b = row_sequence(a.bt, row);
     const SeqRows sr = seq_rows(a.bt, b);
     const int i = row - sr.r0, ctx = a.bt.context_len[b];
     const int64_t cap = (int64_t)a.bt.max_pages * a.c.page_size;
@@ -121,23 +134,20 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args
     if (i < 0 || i >= sr.n) return;   // a row of no sequence
     const int psize = a.c.page_size, slot0 = ctx + i, pn = slot0 / psize, place0 = slot0 - pn * psize;
     const bool leads = i == 0 || place0 == 0;
-    const int which = blockIdx.y & 1;             // keys or values
-    const bool turns = which && a.q != nullptr;   // queries too
-    if (!leads && !turns) return;
+    if (!leads && a.q == nullptr) return;
     const int T = leads ? min(sr.n - i, psize - place0) : 1;   // rows of the page
-    int page = 0;
-    if (leads) {
-        page = a.bt.page_table[b * a.bt.table_pitch + pn];
-        if (page < 0 || page >= a.c.n_pages) {
-            if (tid == 0) report_error(a.stats, SV_ERR_INVALID_ARG, b);
-            page = -1;
+    if (leads && h < a.c.kv_heads)
+        for (int t = lane; t < 2 * lines * min(T, 16); t += 32) {
+            const int r = t / (2 * lines), l = t - r * 2 * lines;
+            const char *head = l < lines ? a.v + (int64_t)(row + r) * a.v_row + h * a.v_head : a.k + (int64_t)(row + r) * a.k_row + h * a.k_head;
+            prefetch_l1(head + (l < lines ? l : l - lines) * 128);
         }
+    const int page = leads ? a.bt.page_table[b * a.bt.table_pitch + pn] : -1;
+    if (leads && (page < 0 || page >= a.c.n_pages) && tid == 0) report_error(a.stats, SV_ERR_INVALID_ARG, b);
+    if (a.bt.parents != nullptr) {
+        for (int j = tid; j < i + T - 1; j += kAppendThreads) par[j] = a.bt.parents[(int64_t)b * (a.bt.n - 1) + j];
+        __syncthreads();
     }
-    const int angled = which ? 1 : T;   // rows whose angles are needed
-    if (a.bt.parents != nullptr)
-        for (int j = tid; j < i + angled - 1; j += kAppendThreads) par[j] = a.bt.parents[(int64_t)b * (a.bt.n - 1) + j];
-    if (tid < kHeadGroup) s_most[tid] = 0;
-    __syncthreads();
 
     auto angles = [&](int t0, int n) {   // rows i + t0 .. i + t0 + n - 1
         if (tid < n) {
@@ -157,93 +167,114 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args
             s_depth[tid] = depth;
         }
         __syncthreads();
-        for (int j = tid; j < n * a.sh.half; j += kAppendThreads) {
-            const int t = j / a.sh.half, f = j - t * a.sh.half;
-            const float2 c = rope_cos_sin(ctx + s_depth[t], a.inv_freq[f]);
-            cs[t][f] = make_float2(c.x * a.magnitude, c.y * a.magnitude);
+        for (int t = warp; t < n; t += kHeadGroup) {
+            const int at = ctx + s_depth[t];
+            for (int f = lane; f < a.sh.half; f += 32) {
+                const float2 c = rope_cos_sin(at, a.inv_freq[f]);
+                cs[t][f] = make_float2(c.x * a.magnitude, c.y * a.magnitude);
+            }
         }
         __syncthreads();
     };
 
     const int per = rot_items<ES, VEC>(a.sh);   // items of a rotated head
-    const int group = blockIdx.y >> 1, groups = gridDim.y >> 1, h0 = group * kHeadGroup, heads = min(kHeadGroup, a.c.kv_heads - h0);
-    if (turns || which == 0) angles(0, min(angled, kChunk));
-    if (turns) {
-        const int q0 = (int)((int64_t)a.sh.heads * group / groups), q1 = (int)((int64_t)a.sh.heads * (group + 1) / groups);
+    angles(0, min(T, kChunk));
+    if (a.q != nullptr) {
         for (int t = tid; t < per * (q1 - q0); t += kAppendThreads) {
             const int h = q0 + t / per;
             rot_item<ES, VEC>(a.sh, a.q + (int64_t)row * a.q_row + h * a.q_head, a.q_out + (int64_t)row * a.qo_row + h * a.qo_head, t % per,
                               cs[0]);
         }
     }
-    if (!leads || page < 0) return;
+    if (page < 0 || page >= a.c.n_pages) return;
 
-    const int vper = a.c.head_dim / EV, of_head = which ? vper : per, all = heads * of_head;
-    char *codes = (which ? a.c.v : a.c.k) + page * a.c.page_b + h0 * a.c.head_b;
-    uint8_t *scales = (which ? a.v_scale : a.k_scale) + page * a.scale_page + h0 * a.scale_head;
-    const char *src = which ? a.v : a.k;
-    const int64_t src_row = which ? a.v_row : a.k_row, src_head = which ? a.v_head : a.k_head;
-    auto each = [&](int t0, int n, auto &&use) {   // use(token, head, element, values, count) for all items of a chunk of tokens
-        for (int u = tid; u < n * all; u += kAppendThreads) {
-            const int t = u / all, w = u - t * all, h = w / of_head, i = w - h * of_head;
-            const char *x0 = src + (int64_t)(row + t0 + t) * src_row + (h0 + h) * src_head;
-            if (which) {
-                float x[EV];
-                unpack<ES>(*reinterpret_cast<const uint4 *>(x0 + (size_t)i * 16), x);
-                use(t0 + t, h, i * EV, x, std::integral_constant<int, EV>{});
-            } else {
-                float x[E], y[E];
-                int e0, e1;
-                rot_values<ES, VEC>(a.sh, x0, i, cs[t], x, y, e0, e1);
-                use(t0 + t, h, e0, x, std::integral_constant<int, E>{});
-                if (e1 >= 0) use(t0 + t, h, e1, y, std::integral_constant<int, E>{});
+    // use(token, item) for the `of` items a token of n tokens, each by one lane.
+    auto each = [&](int n, int of, auto &&use) {
+        const int dt = 32 / of, di = 32 - dt * of;
+        int t = lane / of, w = lane - t * of;
+#pragma unroll 2
+        while (t < n) {
+            use(t, w);
+            t += dt;
+            w += di;
+            if (w >= of) {
+                w -= of;
+                ++t;
             }
         }
     };
-    const int chunk = which ? T : kChunk;   // values need no angles: all rows at once
-    for (int t0 = 0; t0 < T; t0 += chunk) {
-        if (t0 > 0) {
-            __syncthreads();
-            angles(t0, min(T - t0, kChunk));
-        }
-        each(t0, min(T - t0, chunk), [&](int, int h, int, const float *x, auto n) {
-            const uint32_t m = __float_as_uint(most_finite<n.value>(x));
-            if (m > *reinterpret_cast<volatile uint32_t *>(&s_most[h])) atomicMax(&s_most[h], m);
-        });
-    }
-    __syncthreads();
-    const bool fresh = place0 == 0;   // no cached token in the page
-    if (tid < heads) {
-        uint8_t *at = scales + tid * a.scale_head;
-        int byte = scale_for(__uint_as_float(s_most[tid])), shift = 0;
-        if (!fresh) {
-            const int old = *at;
-            byte = max(byte, old);
-            shift = byte - old;
-        }
-        if (fresh || shift > 0) *at = (uint8_t)byte;
-        s_byte[tid] = byte;
-        s_shift[tid] = shift;
-    }
-    __syncthreads();
-    for (int t0 = 0; t0 < T; t0 += chunk) {
-        if (!which && T > kChunk) {
-            if (t0 > 0) __syncthreads();
-            angles(t0, min(T - t0, kChunk));
-        }
-        each(t0, min(T - t0, chunk), [&](int t, int h, int e, const float *x, auto n) {
-            const float inv = scale_of(s_byte[h] == 255 ? 255 : 254 - s_byte[h]);
-            store_codes<n.value>(codes + (place0 + t) * a.c.slot_b + h * a.c.head_b + e, x, inv);
-        });
-    }
-    if (!fresh) {   // the page's cached tokens, where a scale has grown
-        const int vec = a.c.head_dim / 16, of = heads * vec;
-        for (int u = tid; u < place0 * of; u += kAppendThreads) {
-            const int t = u / of, w = u - t * of, h = w / vec, shift = s_shift[h];
-            if (shift == 0) continue;
-            uint4 *at = reinterpret_cast<uint4 *>(codes + t * a.c.slot_b + h * a.c.head_b + (w - h * vec) * 16);
+    const bool fresh = place0 == 0, mine = h < a.c.kv_heads;   // no cached token in the page; a warp with a head
+    auto scale_at = [&](uint8_t *scales) { return scales + page * a.scale_page + h * a.scale_head; };
+    // The page's scale from the largest element that a lane has seen; `shift`: by how much the cached tokens' codes go down.
+    auto settle = [&](uint8_t *at, float most, int old, int &shift) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        const int byte = max(scale_for(most), old);
+        shift = fresh ? 0 : byte - old;
+        if (lane == 0 && (fresh || shift > 0)) *at = (uint8_t)byte;
+        return byte;
+    };
+    auto inverse = [](int byte) { return scale_of(byte == 255 ? 255 : 254 - byte); };
+    auto cached = [&](char *codes, int shift) {   // the page's cached tokens, where the scale has grown
+        if (shift <= 0) return;
+        each(place0, a.c.head_dim / 16, [&](int t, int w) {
+            uint4 *at = reinterpret_cast<uint4 *>(codes + t * a.c.slot_b + w * 16);
             *at = rescaled16(*at, shift);
-        }
+        });
+    };
+    const int64_t to = page * a.c.page_b + h * a.c.head_b;
+    if (mine) {
+        const char *src = a.v + (int64_t)row * a.v_row + h * a.v_head;
+        uint8_t *at = scale_at(a.v_scale);
+        const int old = fresh ? 0 : *at;
+        float most = 0.0f;
+        auto load = [&](int t, int w, float (&x)[EV]) { unpack<ES>(*reinterpret_cast<const uint4 *>(src + t * a.v_row + w * 16), x); };
+        each(T, a.c.head_dim / EV, [&](int t, int w) {
+            float x[EV];
+            load(t, w, x);
+            most = fmaxf(most, most_finite<EV>(x));
+        });
+        int shift;
+        const float inv = inverse(settle(at, most, old, shift));
+        each(T, a.c.head_dim / EV, [&](int t, int w) {
+            float x[EV];
+            load(t, w, x);
+            store_codes<EV>(a.c.v + to + (place0 + t) * a.c.slot_b + w * EV, x, inv);
+        });
+        cached(a.c.v + to, shift);
+    }
+    {
+        const char *src = a.k + (int64_t)row * a.k_row + h * a.k_head;
+        uint8_t *at = scale_at(a.k_scale);
+        const int old = mine && !fresh ? *at : 0;
+        float most = 0.0f, x[E], y[E];
+        int e0, e1, shift = 0;
+        auto chunks = [&](bool again, auto &&use) {   // use(token): the element of x, y at e0, e1
+            for (int t0 = 0; t0 < T; t0 += kChunk) {
+                const int n = min(T - t0, kChunk);
+                if (t0 > 0 || (again && T > kChunk)) {
+                    __syncthreads();
+                    angles(t0, n);
+                }
+                if (mine)
+                    each(n, per, [&](int t, int w) {
+                        rot_values<ES, VEC>(a.sh, src + (t0 + t) * a.k_row, w, cs[t], x, y, e0, e1);
+                        use(t0 + t);
+                    });
+            }
+        };
+        chunks(false, [&](int) {
+            most = fmaxf(most, most_finite<E>(x));
+            if (e1 >= 0) most = fmaxf(most, most_finite<E>(y));
+        });
+        float inv = 0.0f;
+        if (mine) inv = inverse(settle(at, most, old, shift));
+        chunks(true, [&](int t) {
+            char *codes = a.c.k + to + (place0 + t) * a.c.slot_b;
+            store_codes<E>(codes + e0, x, inv);
+            if (e1 >= 0) store_codes<E>(codes + e1, y, inv);
+        });
+        cached(a.c.k + to, shift);
     }
 }
 
@@ -363,7 +394,7 @@ extern "C" sv_status sv_kv_append8(const sv_kv_cache8 *cache, const sv_kv_batch 
                                    {q_out, q_out_row_stride * es, q_out_head_stride * es, batch->rows, q_heads, width}))
         return SV_ERR_INVALID_ARG;
     const int groups = (cache->kv_heads + kHeadGroup - 1) / kHeadGroup;
-    if (2 * groups > 65535) return SV_ERR_INVALID_ARG;
+    if (groups > 65535) return SV_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (!on_current_device(s, cache->k, k)) return SV_ERR_INVALID_ARG;
     if (stats && cudaMemsetAsync(stats, 0, sizeof(sv_stats), s) != cudaSuccess) return SV_ERR_CUDA;
@@ -373,7 +404,7 @@ extern "C" sv_status sv_kv_append8(const sv_kv_cache8 *cache, const sv_kv_batch 
                   q_row_stride * es, q_head_stride * es, q_out_row_stride * es, q_out_head_stride * es, k_row_stride * es, k_head_stride * es,
                   v_row_stride * es, v_head_stride * es, inv_freq, {q_heads, cache->head_dim, rotary_dim / 2, style}, magnitude, stats};
     const bool vec = rot_vec(rotary_dim / 2, style, es);
-    const dim3 grid((unsigned)batch->rows, (unsigned)(2 * groups));   // keys and values
+    const dim3 grid((unsigned)batch->rows, (unsigned)groups);
     if (es == 4)
         vec ? k_kv_append8<4, true><<<grid, kAppendThreads, 0, s>>>(a) : k_kv_append8<4, false><<<grid, kAppendThreads, 0, s>>>(a);
     else
