@@ -227,6 +227,47 @@ def test_in_a_graph_beside_another_stream(sv):
         p.check_bytes(want[3])
 
 
+def test_graphs_that_share_a_workspace(sv):
+    """A captured fork and a captured compaction with one workspace, replayed in turn; results in arrays with a pitch and in the inputs' place."""
+    p = Pool(8, 2, 8, 2, 64, E4M3, 20, 90, extra=300, shared=3)
+    src = p.rng.integers(-1, 20, 50)
+    rows, wctx, wrefs, copies = okv.fork(p.refs, p.ctx, p.table, src, 4, 8)
+    to, wafter, n = okv.compact(wrefs)
+    ws = sv.Workspace()
+    inputs = [p.dev(x) for x in (p.refs, p.ctx, p.table, src)]
+    refs = inputs[0].clone()
+    wide = torch.full((50, p.width + 5), -9, dtype=torch.int32).cuda()
+    first = [c.clone() for c in (*p.caches, *p.scales)]
+
+    def fork():
+        return sv.sv_kv_fork(*p.caches, refs, *inputs[1:], reserve=4, refs_out=refs, table_out=wide[:, :p.width], workspace=ws, **p.kw)
+
+    def compact():
+        return sv.sv_kv_compact(*p.caches, refs, wide[:, :p.width], refs_out=refs, table_out=wide[:, :p.width], workspace=ws, **p.kw)
+    fork(), compact()
+    graphs = []
+    for f in (fork, compact):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            out = f()
+    for _ in range(4):
+        for c, f in zip((*p.caches, *p.scales, refs), (*first, inputs[0])):
+            c.copy_(f)
+        graphs[0].replay()
+        middle = refs.clone(), wide.clone()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert middle[0].tolist() == wrefs and middle[1][:, :p.width].tolist() == rows and bool((wide[:, p.width:] == -9).all())
+        assert refs.tolist() == wafter and int(out[2]) == n
+        assert wide[:, :p.width].tolist() == [[to[e] if e >= 0 else int(e) for e in row] for row in rows]
+    # a sequence's bytes after both are those of the tokens it continues
+    for j, b in enumerate(src):
+        for e in range(-(-int(p.ctx[b]) // 8) if b >= 0 else 0):
+            t = min(8, int(p.ctx[b]) - 8 * e)
+            for c, was in zip(p.caches, p.bytes):
+                assert torch.equal(c.view(torch.uint8)[:, wide[j, e].long(), :t].cpu(), was[:, p.table[b, e], :t])
+
+
 def test_beams_as_they_are_used(sv):
     """Beams over a cache held in 8 bits: append, attend, reorder, now and then compact; each beam's attention is that of a cache of its own that
     was never shared."""
