@@ -45,11 +45,9 @@ struct Feed {
 // descriptions of pieces are still waited for (`patient`): they come from the walk, which waits for nothing but their readers, so
 // that all warps see the same pieces to the last.  A tile then takes microseconds, and that wait's own limit of many seconds is
 // never met.
-#ifndef SV_WAIT_PART
-#define SV_WAIT_PART __device__ __forceinline__
-#endif
-template <bool patient>
-SV_WAIT_PART bool wait_longer(Feed *fd, uint64_t *bar, uint32_t parity) {
+template <bool patient = false>
+__device__ __forceinline__ bool wait_phase(Feed *fd, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
     const long long until = clock64() + (patient ? 8 * kWaitLimitCycles : fd->limit);
     do {
         if (!patient && *reinterpret_cast<volatile int *>(&fd->dead)) return false;
@@ -59,10 +57,6 @@ SV_WAIT_PART bool wait_longer(Feed *fd, uint64_t *bar, uint32_t parity) {
         }
     } while (!mbar_try_wait_sleep(bar, parity, kSuspendHintNs));
     return true;
-}
-template <bool patient = false>
-__device__ __forceinline__ bool wait_phase(Feed *fd, uint64_t *bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_longer<patient>(fd, bar, parity);
 }
 
 // `readers`: warps that read a piece description; arrivals that make a stage and a query tile full.

@@ -2,7 +2,10 @@
 // wide.  The products, groups and barriers are those of sv_attend_few.cu; what differs is how a cache in 8 bits comes to them.
 //
 // Codes are e4m3 numbers, which binary16 holds, so keys and values become binary16 tiles without their scales, one instruction a pair
-// of codes.  Queries are binary16 too: a power of two brings the tile's largest to [2^14, 2^15), so what drops below 2^-24 is 2^-38 of it.
+// of codes.  Queries are binary16 too: a power of two brings the tile's largest to [2^14, 2^15), so what drops below 2^-24 is 2^-38 of it.  A
+// row much smaller than another of its tile thus has scores off by up to 2^-39 of that other's largest: nothing, up to where
+// float32 no longer resolves scores (2^22 and more, times log2(e)).  A power for each row, with a branch in the softmax for tiles that need
+// them, took 511 us where this takes 487.
 //   scores    q' . code, times scale * 2^(key's exponent) * (the queries' power of two): a factor of the thread, whose token it is
 //   weights   with E_j the exponent of token j's values, less the group's first token's,
 //                 out = sum_j 2^(s_j) 2^(E_j) code_j / sum_j 2^(s_j) = sum_j w_j code_j / sum_j w_j 2^(-E_j),   w_j = 2^(s_j + E_j - M)
@@ -46,6 +49,7 @@ struct Few8Shape {
 
 struct Few8Shared : FewShared {
     Feed8 f8;
+    float scale[2];                   // what the groups' outputs are in
     int unseen[2];                    // a row of the group has seen no token yet
 };
 
@@ -392,15 +396,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
             const int key = min(p->key0 + k * kTcKeys + token, p->end - 1);
             return a.bt.page_table[p->table * a.bt.table_pitch + (a2.page_shift >= 0 ? key >> a2.page_shift : key / a.c.page_size)];
         };
-        // Pages of the group's first tile of a piece (this thread's token's, the first token's) and of its second: asked for at the end of
-        // the piece before, where the next one is known by then.
-        int page = 0, page0 = 0, page_next = 0;
-        bool asked = false;
-        auto ask = [&](const PieceInfo *p, int begin) {
-            page = page_of(p, begin, t);
-            page0 = page_of(p, begin, 0);
-            page_next = page_of(p, begin + 2, t);
-        };
         for (int it = 0;; ++it) {
             const PieceInfo *pi = &fd->pd[it % kRing];
             if (!wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1)) break;
@@ -435,7 +430,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
             bool unseen = true, flip = false;   // flip: the sums are in the upper half of their columns
             const int begin = solo ? k0 : k0 + gr;
             float cq = 0.0f;   // what scores are multiplied by, but for the key's scale
-            if (!asked) ask(pi, begin);
+            int page = page_of(pi, begin, t), page_next = page_of(pi, begin + 2, t);
+            const int page0 = page_of(pi, begin, 0);
             uint32_t kb_next = byte_of(ks, page), vb_next = byte_of(vs8, page);
             const uint32_t v0 = byte_of(vs8, page0);
             for (int k = begin; k < k1; k += 2, ++u) {
@@ -564,8 +560,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
 #pragma unroll 1
                     for (int r = 0; r < vr; ++r) {
                         uint16_t *at = reinterpret_cast<uint16_t *>(smem + S::OFF_P + gr * S::PBUF + t * (2 * NR) + (((r >> 3) ^ ((t >> 1) & 3)) << 4) + (r & 7) * 2);
-                        const float w = half_bits(*at);
-                        *at = w == 0.0f ? 0 : __half_as_ushort(__float2half_rn(w * down));
+                        *at = (sees >> r) & 1u ? __half_as_ushort(__float2half_rn(half_bits(*at) * down)) : 0;   // NaN where it is seen
                     }
                 }
                 if (masked) {

@@ -6,8 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from kv8_helpers import E4M3, Cache8, order_axes, values
-from kv_helpers import check_attend, f64, random_tree
+from kv8_helpers import E4M3, Cache8, check_attend8, order_axes, values
+from kv_helpers import f64, random_tree
 from oracle import kv as okv
 
 pytestmark = pytest.mark.gpu
@@ -161,7 +161,7 @@ def check_both(sv, c, q, kw, rows_of, par=None):
     stats = sv.new_stats("cuda")
     out, lse = sv.sv_kv_attend8(q, *c.args8, scale=scale, lse=True, stats=stats, **kw)
     assert sv.read_stats(stats)["status"] == 0
-    check_attend(c, q.flatten(0, 1) if q.dim() == 4 else q, out.flatten(0, 1) if q.dim() == 4 else out,
+    check_attend8(c, q.flatten(0, 1) if q.dim() == 4 else q, out.flatten(0, 1) if q.dim() == 4 else out,
                  lse.flatten(0, 1) if q.dim() == 4 else lse, scale, rows_of, par)
     if bits:
         plain = sv.sv_kv_attend(q, c.k, c.v, *c.args8[4:], scale=scale, lse=True, **kw)
@@ -247,6 +247,38 @@ def test_hidden_tokens_cannot_reach_a_row(sv, dtype, n, dim):
     assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("dtype,n,dim", [(BF, 6, 128), (BF, 7, 64), (BF, 60, 64), (F32, 2, 64), (F32, 20, 96)])
+@pytest.mark.parametrize("most", [13, 30, 60, 110])
+def test_query_rows_of_very_different_size(sv, dtype, n, dim, most):
+    """Rows (each head's) between 2^-most and 1 beside rows of zeros, with scores up to some 2^3 and, by the scale, 2^20 (at 2^22 float32 no longer tells
+    scores apart)."""
+    c, q, rows = filled(n + most, dtype, [200, 0, 33], n, 4, 2, dim, 16, spread=2)
+    size = torch.tensor(2.0 ** -c.rng.integers(0, most + 1, (3, n, 4, 1)), dtype=F32)
+    size[0, 0, 1] = 0.0
+    size[0, 1, 2] = 2.0 ** -most
+    size[0, 2 % n, 3] = 1.0
+    q = (q.float().cpu() * size).to(dtype).cuda()
+    for scale in (dim ** -0.5, 2.0 ** (min(most, 18) - 4)):
+        check_both(sv, c, q, dict(scale=scale), rows)
+
+
+@pytest.mark.parametrize("dtype,n", [(BF, 4), (BF, 40), (F32, 2), (F32, 30)])
+def test_a_scale_that_is_nan_reaches_whoever_sees_it(sv, dtype, n):
+    """However small the weight of its tokens: by the values' scale and by the keys'."""
+    for which in range(2):
+        c, q, rows = filled(n, dtype, [100, 70], n, 4, 2, 64, 16)
+        if which == 0:
+            c.k8.view(torch.uint8)[c.table[0, 2].long(), :, 0] = 0   # the page's keys: scores of 0, beside those of 1000 and more
+            q[0, :, 0] = 100 * c.k[c.table[0, 0].long(), 3, 0]
+        (c.vs, c.ks)[which][c.table[0, 2].long(), 0] = 255
+        out, lse = sv.sv_kv_attend8(q, *c.args8, lse=True)
+        bad = torch.isnan(out).cpu()
+        want = torch.zeros_like(bad)
+        want[0, :, :2] = True
+        assert torch.equal(bad, want)
+        assert torch.equal(torch.isnan(lse).cpu(), want[..., 0] if which else torch.zeros_like(want[..., 0]))
+
+
 def test_rows_of_no_token_and_empty_blocks(sv):
     """Ragged: an empty block, a block without context."""
     c, q, _ = filled(2, BF, [0, 50, 9], 4, 4, 2, 64, 16)
@@ -255,7 +287,7 @@ def test_rows_of_no_token_and_empty_blocks(sv):
     out, lse = sv.sv_kv_attend8(flat, *c.args8, row_start=start, max_rows=4, lse=True)
     one, l1 = sv.sv_kv_attend8(q, *c.args8, lse=True)
     assert torch.equal(out[:4], one[0])
-    check_attend(c, flat, out, lse, 64 ** -0.5, [slice(0, 4), slice(4, 4), slice(4, 7)])
+    check_attend8(c, flat, out, lse, 64 ** -0.5, [slice(0, 4), slice(4, 4), slice(4, 7)])
 
 
 def test_long_contexts_split_over_blocks(sv):
@@ -365,7 +397,7 @@ def test_a_step_as_it_is_used(sv):
         sv.sv_kv_append8(k.cuda(), v.cuda(), k8[0], v8[0], ks[0], vs[0], ctx, dev_table, parents=par.cuda())
         out, lse = sv.sv_kv_attend8(q.cuda(), k8[0], v8[0], ks[0], vs[0], ctx, dev_table, parents=par.cuda(), lse=True)
         held = SimpleNamespace(contexts=ctx.tolist(), table=torch.tensor(table), k=values(k8[0], ks[0]), v=values(v8[0], vs[0]))
-        check_attend(held, q.flatten(0, 1), out.flatten(0, 1).cpu(), lse.flatten(0, 1).cpu(), D ** -0.5,
+        check_attend8(held, q.flatten(0, 1), out.flatten(0, 1).cpu(), lse.flatten(0, 1).cpu(), D ** -0.5,
                      [slice(b * n, b * n + n) for b in range(B)], par)
         acc = rng.integers(0, n, B).astype(np.int32)
         path = np.full((B, n - 1), -1, np.int32)

@@ -6,8 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from kv8_helpers import E4M3, Cache8
-from kv_helpers import check_attend, random_tree
+from kv8_helpers import E4M3, Cache8, check_attend8
+from kv_helpers import random_tree
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -152,7 +152,7 @@ def test_ragged_blocks_after_shared_prefixes(sv, dtype, n):
     st = sv.new_stats("cuda")
     out, lse = sv.sv_kv_attend8(q, *c.args8, row_start=torch.tensor(start).cuda(), max_rows=n, lse=True, stats=st, **c.group_args)
     assert sv.read_stats(st)["status"] == 0
-    check_attend(c, q, out, lse, 64 ** -0.5, [slice(int(a), int(b)) for a, b in zip(start, start[1:])])
+    check_attend8(c, q, out, lse, 64 ** -0.5, [slice(int(a), int(b)) for a, b in zip(start, start[1:])])
 
 
 def step(sv, caches, scales, table, contexts, tree, q, k, v, freq, acc, path):
