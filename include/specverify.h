@@ -667,8 +667,14 @@ sv_status sv_kv_append8(const sv_kv_cache8 *cache, const sv_kv_batch *batch, sv_
 /* ----------------------------------------------------------------------------------------
  * sv_kv_attend8 — sv_kv_attend over a cache held in 8 bits (no counterpart on the pages).  q and out have type dtype; the other
  * arguments, shared prefixes, masks, limits and the workspace (sv_kv_attend_workspace_size) are sv_kv_attend's.
- * The result is that of sv_kv_attend over a cache of type dtype that holds the elements' values (rounded to bf16 with dtype SV_BF16,
- * which is exact for scales of 2^-124 and above).
+ * The result is that of sv_kv_attend over a cache of type dtype that holds the elements' values: in float32 up to the order of its sums, and
+ * with dtype SV_BF16, head_dim up to 128 and more than 32 rows times query heads a key head, to the bit (values are rounded
+ * to bf16, which is exact for scales of 2^-124 and above).  With SV_BF16 and fewer rows, or wider heads, values are not rounded.
+ * The few rows' scores take queries exact down to 2^-24 of the block's largest and within 2^-39 of it below that; a weight
+ * of the sum over the values is rounded to binary16, within 2^-12 of it (below 2^-18 of the largest, within 2^-30 of that), and what it
+ * is divided by is not rounded.  Each such weight carries its page's scale of the values.  Where pages' scales lie more than 2^40 below
+ * that of a key head's first page in the part of the context that a block works on, what they hold is off by up to 2^-64 of that scale.
+ * Scores, times log2(e), are resolved up to 2^22.  A NaN code or scale reaches the rows that see its token, and no other.
  * -------------------------------------------------------------------------------------- */
 sv_status sv_kv_attend8(const sv_kv_cache8 *cache, const sv_kv_batch *batch, sv_dtype dtype, const void *q, int64_t q_row_stride,
                         int64_t q_head_stride, int q_heads, float scale, const int32_t *group_start,
@@ -729,8 +735,8 @@ typedef struct sv_kv_pool {
  * reserve, passes max_pages * page_size (both treated as -1), a page id >= n_pages, or a token's entry that names no page; with the page for
  * refs below its holders.  SV_ERR_NO_PAGE with the new sequence where no page is free: its entry is then -1, and what it would have
  * held is lost with it.  Nothing is read or written out of range for any of these.
- * Returns SV_ERR_INVALID_ARG for null pointers, sizes below 1, reserve < 0, misaligned bases or strides, B * max_pages or
- * N * max_pages or N * n_layers above 2^31 - 1, or outputs that overlap inputs.
+ * Returns SV_ERR_INVALID_ARG for null pointers, sizes below 1, reserve < 0, misaligned bases or strides, n_pages or N above 2^30,
+ * B * max_pages or N * max_pages or N * n_layers above 2^31 - 1, or outputs that overlap inputs.
  * -------------------------------------------------------------------------------------- */
 size_t sv_kv_fork_workspace_size(int n_pages, int N);
 
@@ -784,7 +790,7 @@ void sv_set_profile_events(void *begin, void *end);
  * shows that the library's bounded waits return an error instead of hanging; no copy is in
  * flight and nothing faults.
  *
- * sv_selftest_attend_stall: while limit_cycles > 0, sv_kv_attend called from this host thread runs its tensor-core
+ * sv_selftest_attend_stall: while limit_cycles > 0, sv_kv_attend and sv_kv_attend8 called from this host thread runs its tensor-core
  * kernels with one barrier that nothing completes, and their waits give up after limit_cycles SM clock cycles.  A block that
  * meets it reports SV_ERR_TIMEOUT, waits for its copies and products in flight and ends with meaningless output; the
  * context stays usable.  0 ends it.

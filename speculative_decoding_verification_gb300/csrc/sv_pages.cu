@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024, kPlanBlocks = 8;
 constexpr int kNobody = INT32_MAX;
+constexpr int kPlanMost = 1 << 30;   // pages, and sequences of a new batch: loops step past their ends by less than that
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(256) k_compact_copy(const PageRuns r, const in
 
 bool pool_ok(const sv_kv_pool *p) {
     if (p == nullptr || p->k == nullptr || p->v == nullptr || (p->k_scale == nullptr) != (p->v_scale == nullptr)) return false;
-    if (p->n_layers < 1 || p->n_pages < 1 || p->page_size < 1 || p->kv_heads < 1 || p->head_bytes < 1 || p->head_bytes > 4 * SV_KV_MAX_HEAD_DIM)
+    if (p->n_layers < 1 || p->n_pages < 1 || p->n_pages > kPlanMost || p->page_size < 1 || p->kv_heads < 1 || p->head_bytes < 1 || p->head_bytes > 4 * SV_KV_MAX_HEAD_DIM)
         return false;
     // offsets of a page's vectors are formed in 32 bits
     if ((int64_t)p->page_size * p->kv_heads > INT32_MAX || (int64_t)p->page_size * p->kv_heads * (p->head_bytes / 16) > INT32_MAX / 8) return false;
@@ -439,7 +440,7 @@ extern "C" sv_status sv_kv_fork(const sv_kv_pool *pool, const int32_t *refs, con
         table_out_pitch < max_pages)
         return SV_ERR_INVALID_ARG;
     if ((int64_t)max_pages * pool->page_size > kMaxSlots || (int64_t)B * max_pages > INT32_MAX || (int64_t)N * max_pages > INT32_MAX ||
-        (int64_t)N * pool->n_layers > INT32_MAX)
+        (int64_t)N * pool->n_layers > INT32_MAX || N > kPlanMost)
         return SV_ERR_INVALID_ARG;
     const int n_pages = pool->n_pages;
     const int64_t in = table_extent(B, table_pitch, max_pages), out = table_extent(N, table_out_pitch, max_pages);

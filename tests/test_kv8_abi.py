@@ -118,7 +118,7 @@ def pool(**kw):
 
 
 BAD_POOL = [dict(k=None), dict(v=None), dict(ks=FAKE), dict(vs=FAKE), dict(k=FAKE + 4), dict(ls=8), dict(ps=24), dict(ss=4), dict(hs=2), dict(hb=0),
-            dict(hb=24), dict(hb=2048), dict(layers=0), dict(pages=0), dict(size=0), dict(kv=0), dict(size=2**20, kv=2**12)]
+            dict(hb=24), dict(hb=2048), dict(layers=0), dict(pages=0), dict(size=0), dict(kv=0), dict(size=2**20, kv=2**12), dict(pages=2**30 + 1)]
 
 
 def test_fork_rejects_bad_arguments(sv):
@@ -126,12 +126,12 @@ def test_fork_rejects_bad_arguments(sv):
     R, C, T, S, RO, TO, CO = (FAKE * i for i in range(1, 8))
 
     def call(refs=R, ctx=C, table=T, pitch=5, mp=5, B=3, src=S, N=4, reserve=2, ro=RO, to=TO, top=5, co=CO, w=FAKE, wb=None, **kw):
-        wb = lib.sv_kv_fork_workspace_size(10, max(N, 1)) if wb is None else wb
+        wb = lib.sv_kv_fork_workspace_size(10, min(max(N, 1), 2**30)) if wb is None else wb
         return lib.sv_kv_fork(pool(**kw), refs, ctx, table, pitch, mp, B, src, N, reserve, ro, to, top, co, None, w, wb, None)
     for kw in BAD_POOL + [dict(refs=None), dict(ctx=None), dict(table=None), dict(src=None), dict(ro=None), dict(to=None), dict(co=None), dict(B=0),
                           dict(N=0), dict(mp=0), dict(pitch=4), dict(top=4), dict(reserve=-1), dict(mp=2**29, pitch=2**29, top=2**29),
                           dict(to=T), dict(to=T + 8), dict(co=C), dict(co=S + 4), dict(ro=R + 4), dict(to=RO), dict(ro=T), dict(co=TO + 16),
-                          dict(N=2**30), dict(to=R)]:
+                          dict(N=2**30), dict(to=R), dict(N=2**30 + 1, mp=1, B=1, layers=1)]:
         assert call(**kw) == 1, kw
     assert call(w=None) == 5 and call(w=FAKE + 16) == 5 and call(wb=100) == 5
     assert lib.sv_kv_fork_workspace_size(0, 4) == 0 and lib.sv_kv_fork_workspace_size(4, 0) == 0
