@@ -59,10 +59,11 @@ __device__ __forceinline__ int raw_place(int r, int ch) {
 }
 
 // One of the loading warps: kv 0 the keys, 1 the values.  Slots of TOK tokens at raw_base, DP bytes a token.  SCALES: with their scales.  KEYS_SWIZZLED: the
-// keys' slots are swizzled.
+// keys' slots are swizzled.  ALL_BOXES: the last tiles go as boxes too, with what their pages hold past the last token and zeros for pages past it,
+// for a softmax that leaves out what a row does not see.
 // One warp has to keep up with the others: six cycles an instruction, so a slot's boxes go with as few as can be.  (With the pages of all
 // tokens looked up for every tile, as tiles by rows do, it took 4,000 cycles a tile and set the pace.)
-template <int DP, int TOK, int SLOTS, bool SCALES, bool KEYS_SWIZZLED, bool SPLIT>
+template <int DP, int TOK, int SLOTS, bool SCALES, bool KEYS_SWIZZLED, bool ALL_BOXES, bool SPLIT>
 __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs &a2, Feed *fd, Feed8 *f8, uint32_t raw_base, int kv, int lane) {
     static_assert(TOK * SLOTS <= 2 * kTcKeys && SLOTS <= kMaxSlots8, "the scales' ring");
     constexpr int SLOT = TOK * DP, NS = kTcKeys / TOK, CH = DP / 16, RPI = 32 / CH;   // slots of a tile; chunks of a token, tokens of a pass by rows
@@ -97,7 +98,8 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
         if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(fd, &fd->pd_full[it % kRing], (it / kRing) & 1))) break;
         const int k0 = pi->k0, k1 = pi->k1;
         if (k0 >= k1) break;
-        const int key0 = pi->key0, end = pi->end, h = pi->h, tab = pi->table, box_tiles = pi->box_tiles;
+        const int key0 = pi->key0, end = pi->end, h = pi->h, tab = pi->table;
+        const int box_tiles = !ALL_BOXES ? pi->box_tiles : a2.box_rows > 0 && (a2.split || key0 % a2.box_rows == 0) ? INT32_MAX : 0;
         const int32_t *table = a.bt.page_table + tab * a.bt.table_pitch;
         __syncwarp();
         if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
@@ -142,9 +144,11 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
                 }
             };
             if (k < box_tiles) {
-                const int page = ahead, place = key0 + k * kTcKeys + box_token - box_index(k) * psize;
+                int page = ahead;
+                const int place = key0 + k * kTcKeys + box_token - box_index(k) * psize;
                 ahead = box_page(k + 1);
-                if (boxes && (unsigned)page >= (unsigned)a.c.n_pages) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                if (ALL_BOXES && key0 + k * kTcKeys + box_token > last) page = a.c.n_pages;   // past the last token: outside the tensor, zeros
+                else if (boxes && (unsigned)page >= (unsigned)a.c.n_pages) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
                 // split: a box that reaches into the next page goes by rows
                 const uint32_t split = SPLIT ? __ballot_sync(0xFFFFFFFFu, boxes && place + 8 > psize) : 0;
 #pragma unroll 1
@@ -161,9 +165,9 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
                     if (SPLIT && rows) {
 #pragma unroll 1
                         for (int t0 = 0; t0 < TOK; t0 += 32) {
-                            const int key = key0 + k * kTcKeys + s * TOK + t0 + lane, index = page_index(key), id = table[index];
-                            const bool good = (unsigned)id < (unsigned)a.c.n_pages;
-                            if (!good) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
+                            const int key = key0 + k * kTcKeys + s * TOK + t0 + lane, index = page_index(key), id = table[min(index, page_index(last))];
+                            const bool good = (unsigned)id < (unsigned)a.c.n_pages && (!ALL_BOXES || key <= last);
+                            if (!good && key <= last) report_error(a.stats, SV_ERR_INVALID_ARG, tab);
                             const int64_t off = good ? id * a.c.page_b + (key - index * psize) * a.c.slot_b + h * a.c.head_b : -1;
 #pragma unroll 1
                             for (int r0 = 0; r0 < 32; r0 += RPI) {
@@ -218,10 +222,10 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
     if (lane == 0) f8->next[kv] = begun;
 }
 
-template <int DP, int TOK, int SLOTS, bool SCALES, bool KEYS_SWIZZLED>
+template <int DP, int TOK, int SLOTS, bool SCALES, bool KEYS_SWIZZLED, bool ALL_BOXES>
 __device__ __forceinline__ void feed8_load(const AttendArgs &a, const TcArgs &a2, Feed *fd, Feed8 *f8, uint32_t raw_base, int kv, int lane) {
-    if (a2.split) feed8_load_as<DP, TOK, SLOTS, SCALES, KEYS_SWIZZLED, true>(a, a2, fd, f8, raw_base, kv, lane);
-    else feed8_load_as<DP, TOK, SLOTS, SCALES, KEYS_SWIZZLED, false>(a, a2, fd, f8, raw_base, kv, lane);
+    if (a2.split) feed8_load_as<DP, TOK, SLOTS, SCALES, KEYS_SWIZZLED, ALL_BOXES, true>(a, a2, fd, f8, raw_base, kv, lane);
+    else feed8_load_as<DP, TOK, SLOTS, SCALES, KEYS_SWIZZLED, ALL_BOXES, false>(a, a2, fd, f8, raw_base, kv, lane);
 }
 
 // 16 codes times their scale as 16 bf16 numbers, two chunks of 16 bytes.

@@ -5,7 +5,7 @@
 // of codes.  Queries are binary16 too: a power of two brings the tile's largest to [2^14, 2^15), so what drops below 2^-24 is 2^-38 of it.  A
 // row much smaller than another of its tile thus has scores off by up to 2^-39 of that other's largest: nothing, up to where
 // float32 no longer resolves scores (2^22 and more, times log2(e)).  A power for each row, with a branch in the softmax for tiles that need
-// them, took 511 us where this takes 487.
+// them, took 511 us where this took 487.
 //   scores    q' . code, times scale * 2^(key's exponent) * (the queries' power of two): a factor of the thread, whose token it is
 //   weights   with E_j the exponent of token j's values, less the group's first token's,
 //                 out = sum_j 2^(s_j) 2^(E_j) code_j / sum_j 2^(s_j) = sum_j w_j code_j / sum_j w_j 2^(-E_j),   w_j = 2^(s_j + E_j - M)
@@ -19,7 +19,11 @@
 // written, read, written wide and read by the products) would else be the bound.
 // The walk's warp makes the query tiles, ahead of the products.  Blocks of eight columns without rows are left out of the softmax.
 //
-// What bounds it: issue slots and memory; a tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth.
+// A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 1,970, and a piece's beginning
+// and end some 9,000 on top.  What bounds it: latency, of the softmax's steps and of instruction fetches (the block's kinds of warps run
+// more code than the caches next to them hold; the same instructions in another order are 3 to 10% slower or faster).  512 sequences x 6
+// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 475 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
+// 8,192 to 16,384 tokens: 335 us.  Heads of 64 halve the bytes and not the steps: 490 us, where the bf16 cache takes 366.
 #include <float.h>
 
 #define SV_WALK_PART static __host__ __device__ __noinline__
@@ -696,7 +700,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 }
             });
         } else {
-            feed8_load<DP, S::TOK, S::SLOTS, false, true>(a, a2, fd, f8, sbase + S::OFF_RAW + (warp - 14) * (S::SLOTS * S::TOK * DP), warp - 14, lane);
+            feed8_load<DP, S::TOK, S::SLOTS, false, true, true>(a, a2, fd, f8, sbase + S::OFF_RAW + (warp - 14) * (S::SLOTS * S::TOK * DP), warp - 14, lane);
         }
     }
     tc_fence_before();

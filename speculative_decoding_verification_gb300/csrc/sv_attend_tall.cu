@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_tall(const __grid_cons
             // ------------------------------------------------------------ the walk
             feed_walk(a, a2, fd, ms->walk, lane);
         } else if constexpr (C8) {
-            feed8_load<DP, kRawTokens, S::SLOTS, true, false>(a, a2, fd, f8, smem_addr(smem) + S::OFF_RAW + (warp - 14) * (S::SLOTS * kRawTokens * DP), warp - 14, lane);
+            feed8_load<DP, kRawTokens, S::SLOTS, true, false, false>(a, a2, fd, f8, smem_addr(smem) + S::OFF_RAW + (warp - 14) * (S::SLOTS * kRawTokens * DP), warp - 14, lane);
         }
     }
     tc_fence_before();
