@@ -50,7 +50,8 @@ __device__ __forceinline__ void scale_quad(Quad &o, float f) {
     o.b = f2_fma(o.b, f2, none);
 }
 
-// C8: the cache is held in 8 bits.  Codes are copied as they are, and become floats, times their scale, as they are read.
+// C8: the cache is held in 8 bits.  Codes are copied as they are, and become floats, times their scale, as they are read.  Issue slots bound that: the
+// single tokens above take 128 us (112 over floats, of whose bytes the codes are a quarter; in tiles of 16 rows 403).
 template <int R, bool C8>
 __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs a) {
     constexpr int KB = 32 / R;   // tokens of a batch

@@ -28,7 +28,9 @@ constexpr int kTallRows = 256;
 constexpr int kTallReaders = 13;      // warps that read a piece description
 constexpr uint32_t kColS = 0, kColO = 256;
 
-// C8: the cache is held in 8 bits.
+// C8: the cache is held in 8 bits.  Codes become the bf16 tiles of before (sv_attend_feed8.cuh), so results are those of a bf16 cache of the same values
+// to the bit; what they cost is the widening, four warps' five instructions a pair of codes, once for each row tile: 2 sequences x
+// 1,300 rows over 3,000 tokens 298 us (241 over bf16), the prompt above 316 us for the whole call (284), 16 trees of 57 rows 70 us (60).
 template <int DP, bool C8>
 struct TallShape {
     static constexpr int TILE = 128 * DP * 2;              // bytes of 128 rows

@@ -292,6 +292,8 @@ struct Commit8Args {
 // One block a (layer, sequence), as in k_kv_commit; thread t holds one 16-byte column of a head's codes.  Destinations rise and no source lies before
 // its destination, so pages are finished one after the other, and a page's own scale is needed by nothing that comes later.  All
 // threads read the scales as they were; the new ones are written at the end.
+// Bound by latency: table, scales and codes are loads that follow one another, for a few moves a block.  32 layers x 64 sequences, trees of
+// 57: 12.1 us in a graph, 4.4 us at the memory's rate (k_kv_commit: 12 us for twice the bytes).
 __global__ void __launch_bounds__(256) k_kv_commit8(const Commit8Args a) {
     __shared__ int64_t src[SV_MAX_TREE], dst[SV_MAX_TREE];
     __shared__ int32_t src_page[SV_MAX_TREE], dst_page[SV_MAX_TREE];
