@@ -20,10 +20,10 @@
 // The walk's warp makes the query tiles, ahead of the products.  Blocks of eight columns without rows are left out of the softmax.
 //
 // A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 1,970, and a piece's beginning
-// and end some 9,000 on top.  What bounds it: latency, of the softmax's steps and of instruction fetches (the block's kinds of warps run
-// more code than the caches next to them hold; the same instructions in another order are 3 to 10% slower or faster).  512 sequences x 6
-// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 475 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
-// 8,192 to 16,384 tokens: 335 us.  Heads of 64 halve the bytes and not the steps: 490 us, where the bf16 cache takes 366.
+// and end some 8,000 on top.  What bounds it: latency, of the softmax's steps and of instruction fetches (the block's kinds of warps run
+// more code than the caches next to them hold; the same instructions in another order are 3 to 20% slower or faster).  512 sequences x 6
+// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 458 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
+// 8,192 to 16,384 tokens: 335 us.  Heads of 64 halve the bytes and not the steps: 447 us, where the bf16 cache takes 366.
 #include <float.h>
 
 #define SV_WALK_PART static __host__ __device__ __noinline__
@@ -81,6 +81,41 @@ __device__ __forceinline__ void scan_codes(uint32_t tile, int t, uint32_t *flags
     const uint32_t all = __ballot_sync(0xFFFFFFFFu, bad);
     if ((t & 31) == 0) flags[t >> 5] = all;
     fence_async_smem();
+}
+
+// Adds to the group's output what the products left out: of each flagged token the values, NaN among them, times the weights that the product
+// would have used, for the rows that see it.  t: the thread's head element.  Rare, and out of line for the sake of the loop that calls it (512 x 6 rows
+// 475 us with it in line, 458 without).
+template <int DP>
+__device__ __noinline__ void add_unseen(const AttendArgs &a, const PieceInfo *pi, uint32_t *flags, int first, uint32_t colO, const char *weights, int t) {
+#pragma unroll 1
+    for (int j = 0; j < 128; ++j) {
+        if (!((*reinterpret_cast<volatile uint32_t *>(&flags[j >> 5]) >> (j & 31)) & 1u)) continue;
+        const int kk = first + j;
+        const uint32_t see = rows_that_see(pi, kk, a.G, a.bt.n);
+        if (kk >= pi->end) continue;   // flags mean nothing after a wait gave up
+        const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, kk);
+        if (off < 0) continue;
+        const float v = t < a.c.head_dim ? codes2(reinterpret_cast<const uint8_t *>(a.c.v + off + pi->h * a.c.head_b)[t]).x : 0.0f;
+        const char *pj = weights + j * (2 * NR);
+        uint32_t o[32];
+        tmem_ld32(colO, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int at = (r & 7) * 2;
+            const float w = half_bits(*reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ ((j >> 1) & 3)) << 4) + at));
+            if (((see >> r) & 1u) && r < pi->vr) o[r] = __float_as_uint(__uint_as_float(o[r]) + w * v);
+        }
+        tmem_st32(colO, o);
+        tc_wait_st();
+    }
+}
+
+// The same out of line, where that leaves the loop's instructions better placed: 512 x 6 rows with heads of 64 447 us (557 in line), of 128 483 (458).
+template <int DP>
+__device__ __noinline__ void scan_called(uint32_t tile, int t, uint32_t *flags) {
+    scan_codes<DP>(tile, t, flags);
 }
 
 // Reduction of x[0..7] over the warp's lanes: lane i gets that of x[i / 4].
@@ -573,34 +608,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                     const uint32_t n = pi->seq / 2 + (k - k0), stage = n % S::VST;
                     wait_phase(fd, &fd->kv_full[S::KST + stage], (n / S::VST) & 1);
                     __syncwarp();
-                    scan_codes<DP>(sbase + S::OFF_KV + stage * S::TILE, t, fd->vflag[stage]);
+                    if constexpr (DP == 64) scan_called<DP>(sbase + S::OFF_KV + stage * S::TILE, t, fd->vflag[stage]);
+                    else scan_codes<DP>(sbase + S::OFF_KV + stage * S::TILE, t, fd->vflag[stage]);
                     group_sync();   // the flags and every token's weights are written
                     uint32_t any = 0;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) any |= *reinterpret_cast<volatile uint32_t *>(&fd->vflag[stage][q]);
                     if (any) {
-#pragma unroll 1
-                        for (int j = 0; j < 128; ++j) {
-                            if (!((*reinterpret_cast<volatile uint32_t *>(&fd->vflag[stage][j >> 5]) >> (j & 31)) & 1u)) continue;
-                            const int kk = key0 + k * kTcKeys + j;
-                            const uint32_t see = rows_that_see(pi, kk, a.G, a.bt.n);
-                            if (kk >= pi->end) continue;   // flags mean nothing after a wait gave up
-                            const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, kk);
-                            if (off < 0) continue;
-                            const float v = t < a.c.head_dim ? codes2(reinterpret_cast<const uint8_t *>(a.c.v + off + pi->h * a.c.head_b)[t]).x : 0.0f;
-                            const char *pj = smem + S::OFF_P + gr * S::PBUF + j * (2 * NR);
-                            uint32_t o[32];
-                            tmem_ld32(colO, o);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int r = 0; r < NR; ++r) {
-                                const int at = (r & 7) * 2;
-                                const float w = half_bits(*reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ ((j >> 1) & 3)) << 4) + at));
-                                if (((see >> r) & 1u) && r < vr) o[r] = __float_as_uint(__uint_as_float(o[r]) + w * v);
-                            }
-                            tmem_st32(colO, o);
-                            tc_wait_st();
-                        }
+                        add_unseen<DP>(a, pi, fd->vflag[stage], key0 + k * kTcKeys, colO, smem + S::OFF_P + gr * S::PBUF, t);
                     }
                 }
                 tc_wait_st();

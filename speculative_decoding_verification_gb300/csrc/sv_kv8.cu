@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append8(const Append8Args
         for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
         const int byte = max(scale_for(most), old);
         shift = fresh ? 0 : byte - old;
+        __syncwarp();   // every lane has read the scale
         if (lane == 0 && (fresh || shift > 0)) *at = (uint8_t)byte;
         return byte;
     };
