@@ -14,7 +14,7 @@
 //             largest, within 2^-30 of that): a 256th of what a code may be off what it was made from.  Two parts took half as long again
 //             in the softmax, which has to keep up with memory here.
 //             An E_j below -40 is taken as -40 and the rest multiplies the weight, so that pages of zeros (whose scale is the least) count
-//             in the sum.
+//             in the sum.  E_j up to 64 leave every weight there that is within 2^-26 of its row's largest; above, the least may drop out.
 // Keys are widened to tensor memory, from where the products take them, values to shared memory: its bandwidth (a tile of values is
 // written, read, written wide and read by the products) would else be the bound.
 // The walk's warp makes the query tiles, ahead of the products.  Blocks of eight columns without rows are left out of the softmax.
@@ -22,7 +22,7 @@
 // A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 1,970, and a piece's beginning
 // and end some 8,000 on top.  What bounds it: latency, of the softmax's steps and of instruction fetches (the block's kinds of warps run
 // more code than the caches next to them hold; the same instructions in another order are 3 to 20% slower or faster).  512 sequences x 6
-// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 458 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
+// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 460 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
 // 8,192 to 16,384 tokens: 335 us.  Heads of 64 halve the bytes and not the steps: 447 us, where the bf16 cache takes 366.
 #include <float.h>
 
@@ -59,6 +59,8 @@ struct Few8Shared : FewShared {
 
 // Weights are up to 2^(kGrow + kLift), where binary16 ends at 2^16: kGrow is how far a score may pass its maximum before that is taken anew.
 constexpr float kLift = 4.0f, kGrow = 11.0f;
+// Sums of weights are kept times 2^kSums: 2^(kSums - E_j) stays a normal number for every scale beside a first page of the least (E_j up to 167).
+constexpr int kSums = 41;
 
 __device__ __forceinline__ float half_bits(uint16_t x) { return __half2float(*reinterpret_cast<const __half *>(&x)); }
 
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 const int ev = (int)vb - e0, up = vb == 255 ? 0 : max(ev, -40);
                 const float lift = (float)up;
                 const float down = vb == 255 ? NAN : ev < -40 ? pow2i(ev + 40) : 1.0f;   // the rest of the scale
-                const f32x2 lift2 = f2_pack(lift, lift), back = f2_pack(pow2i(-up), pow2i(-up));
+                const f32x2 lift2 = f2_pack(lift, lift), back = f2_pack(pow2i(kSums - up), pow2i(kSums - up));
                 const bool masked = key0 + (k + 1) * kTcKeys > ctx;
                 const uint32_t sees = masked ? rows_that_see(pi, key0 + k * kTcKeys + t, a.G, a.bt.n) : 0xFFFFFFFFu;
                 // the group's previous product has read the weights and written the output
@@ -642,15 +644,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 const float sum = reduce8(x, lane, [](float p, float q) { return p + q; });
                 if ((lane & 3) == 0) ms->top[gr][wl][8 * q + (lane >> 2)] = sum;
             }
-            if (t == 0) ms->scale[gr] = scale_of(min(max((int)v0, 127 - 40), 127 + 40));
+            if (t == 0) ms->scale[gr] = scale_of(min(max((int)v0, 127 - 40), 127 + 40) + kSums);
             __syncwarp();
             if (lane == 0) mbar_arrive(&fd->pd_empty[it % kRing]);
             end_sync();
             if (warp == ga * 4) {
                 auto sum_of = [&](int g) { return (ms->top[g][0][lane] + ms->top[g][1][lane]) + (ms->top[g][2][lane] + ms->top[g][3][lane]); };
-                float m = -ms->shift[ga][lane], f0 = 1.0f, f1 = 0.0f, all = sum_of(ga);
+                float m = -ms->shift[ga][lane] - kSums, f0 = 1.0f, f1 = 0.0f, all = sum_of(ga);
                 if (!solo) {
-                    const float top0 = m, top1 = -ms->shift[1][lane];
+                    const float top0 = m, top1 = -ms->shift[1][lane] - kSums;
                     m = fmaxf(top0, top1);
                     f0 = ex2_fast(top0 - m);
                     f1 = ex2_fast(top1 - m);

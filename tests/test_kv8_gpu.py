@@ -226,6 +226,24 @@ def test_attend_scales_of_either_sign_and_scale_bytes_at_the_ends(sv, dtype, sca
     check_both(sv, c, q, dict(scale=scale), rows)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("large", [100, 127, 150])
+def test_a_first_page_of_zeros_before_the_largest_values(sv, dtype, n, large):
+    """Keys and values of zeros (their scale is the least, and counts as 2^-40) before pages of values up to 2^31, whose scales are at most 2^64 above
+    that, as far as the sum of the weights holds those of the zeros: a weight times its scale is 2^(4 - 40 - 64 - d) there or more, d bits below its
+    row's largest, and float32 ends at 2^-126, so what is lost is below 2^-26.  A context that is split over blocks beside short ones."""
+    c, q, rows = filled(n + large, dtype, [9000, 40, 300], n, 4, 2, 64, 16)
+    for b in range(3):
+        first = c.table[b, 0].long()
+        for codes, scale in ((c.k8, c.ks), (c.v8, c.vs)):
+            codes.view(torch.uint8)[first] = 0
+            scale[first] = 7
+        c.vs[c.table[b, 1:].long()] = torch.tensor(c.rng.integers(large - 30, large + 1, (c.table.shape[1] - 1, 2)).astype(np.uint8)).cuda()
+    c.refresh()
+    check_both(sv, c, q, {}, rows)
+
+
 @pytest.mark.parametrize("dtype,n,dim", [(BF, 4, 128), (BF, 60, 64), (F32, 4, 64), (BF, 3, 192), (F32, 40, 128)])
 def test_hidden_tokens_cannot_reach_a_row(sv, dtype, n, dim):
     """NaN codes, NaN scales, pages that nobody sees: slots past the block and a tree's other branches.  A value of NaN that a row sees makes it NaN and no other."""
