@@ -23,6 +23,15 @@ struct FewShared {
     alignas(16) float alpha[2][NR];   // what a new maximum scales the row by; at the end what the group's output is scaled by
 };
 
+// Whether a weighted sum has to be issued before anything else, by a warp that issues scores up to three tiles ahead of them.  `waiting` tiles have
+// scores and no sum yet; `groups` has their groups, a bit each; `next` is the group whose scores come next, or -1.  A group has two score
+// buffers, and the softmax has read one for good when it has written the tile's weights, which the tile's sum waits for: with two tiles of the
+// group waiting, the next tile's scores would go over ones that are still read.  Groups take turns within a piece, but a piece of one tile goes to either: an
+// odd number of tiles, a piece of one and the next piece's first can be three of one group in a row.
+SV_HD bool sum_is_due(uint32_t waiting, uint32_t groups, int next) {
+    return waiting == 3 || (waiting == 2 && next >= 0 && groups == (next ? 3u : 0u));
+}
+
 // The packed rows of a unit that see token `key`, as bits.
 __device__ __forceinline__ uint32_t rows_that_see(const PieceInfo *pi, int key, int G, int n) {
     if (key >= pi->end) return 0;

@@ -317,24 +317,25 @@ __device__ __forceinline__ void issue_products(Feed *fd, FewShared *ms, uint32_t
     for (;;) {
         // What comes next, a piece or a tile, waits for two barriers.  While they are not complete the weighted sums go ahead.
         const bool piece = i == nk;
+        const int gr = first ^ (i & 1);   // of the tile
         const int next = piece ? it + 1 : it;
         uint64_t *b0 = piece ? &fd->pd_full[next % kRing] : &fd->kv_full[n % S::KST], *b1 = !piece && i == 0 ? &fd->q_full[it & 1] : b0;
         const uint32_t p0 = piece ? next / kRing & 1 : n / S::KST & 1, p1 = !piece && i == 0 ? it >> 1 & 1 : p0;
 #pragma unroll 1
-        while (weighed < n && (n - weighed == 3 || ends || !__all_sync(0xFFFFFFFFu, mbar_test_wait(b0, p0) && mbar_test_wait(b1, p1)))) {
-            const uint32_t stage = weighed % S::VST, gr = groups & 1;
+        while (weighed < n && (sum_is_due(n - weighed, groups, piece ? -1 : gr) || ends || !__all_sync(0xFFFFFFFFu, mbar_test_wait(b0, p0) && mbar_test_wait(b1, p1)))) {
+            const uint32_t stage = weighed % S::VST, of = groups & 1;
             wait_phase(fd, &fd->kv_full[S::KST + stage], (weighed / S::VST) & 1);
-            wait_phase(fd, &ms->p_full[gr], parities & 1);
+            wait_phase(fd, &ms->p_full[of], parities & 1);
             __syncwarp();
             tc_fence_after();
             const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, DP == 128 ? S::HALF : 0, 1024);
-            const uint64_t p = smem_operand64(sbase + S::OFF_P + gr * S::PBUF, 512);
-            const uint32_t o = tm + S::COL_O + gr * NR;
+            const uint64_t p = smem_operand64(sbase + S::OFF_P + of * S::PBUF, 512);
+            const uint32_t o = tm + S::COL_O + of * NR;
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) mma_ss(o, v + kk * (2048 >> 4), p + kk * (1024 >> 4), shape_o, 1u);
                 mma_commit(&fd->kv_empty[S::KST + stage]);
-                mma_commit(&ms->p_done[gr]);
+                mma_commit(&ms->p_done[of]);
             }
             __syncwarp();
             ++weighed;
@@ -363,7 +364,6 @@ __device__ __forceinline__ void issue_products(Feed *fd, FewShared *ms, uint32_t
         wait_phase(fd, b1, p1);
         __syncwarp();
         tc_fence_after();
-        const int gr = first ^ (i & 1);
         const uint32_t stage = n % S::KST, u = gr ? tiles1 : tiles0;
         const uint32_t sc = tm + (gr * 2 + (u & 1)) * 32, kt = tm + S::COL_K + stage * (DP / 2);
         const uint64_t q = smem_operand(sbase + (it & 1) * (NR * DP * 2), 16, 1024);
