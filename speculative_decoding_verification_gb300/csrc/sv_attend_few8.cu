@@ -5,25 +5,25 @@
 // of codes.  Queries are binary16 too: a power of two brings the tile's largest to [2^14, 2^15), so what drops below 2^-24 is 2^-38 of it.  A
 // row much smaller than another of its tile thus has scores off by up to 2^-39 of that other's largest: nothing, up to where
 // float32 no longer resolves scores (2^22 and more, times log2(e)).  A power for each row, with a branch in the softmax for tiles that need
-// them, took 511 us where this took 487.
+// them, took 511 us where this took 487 (both before weights had two parts).
 //   scores    q' . code, times scale * 2^(key's exponent) * (the queries' power of two): a factor of the thread, whose token it is
 //   weights   with E_j the exponent of token j's values, less the group's first token's,
 //                 out = sum_j 2^(s_j) 2^(E_j) code_j / sum_j 2^(s_j) = sum_j w_j code_j / sum_j w_j 2^(-E_j),   w_j = 2^(s_j + E_j - M)
 //             where M follows the largest s_j + E_j as a maximum does: weights are as exact as those of an unscaled cache whatever the
-//             scales are.  A weight enters its product with the codes as one binary16 number, within 2^-12 of it (below 2^-18 of the
-//             largest, within 2^-30 of that): a 256th of what a code may be off what it was made from.  Two parts took half as long again
-//             in the softmax, which has to keep up with memory here.
+//             scales are.  A weight enters its product with the codes as two binary16 numbers, itself rounded and what that leaves, rounded: within
+//             2^-22 of it, or of the largest 2^-29 where that is more (half of binary16's last step, 2^-25, beside 2^kLift).  One number alone, off by up to
+//             2^-11, would take 462 us where this takes 491, and outputs would differ with how many rows a block has.
 //             An E_j below -40 is taken as -40 and the rest multiplies the weight, so that pages of zeros (whose scale is the least) count
 //             in the sum.  E_j up to 64 leave every weight there that is within 2^-26 of its row's largest; above, the least may drop out.
 // Keys are widened to tensor memory, from where the products take them, values to shared memory: its bandwidth (a tile of values is
 // written, read, written wide and read by the products) would else be the bound.
 // The walk's warp makes the query tiles, ahead of the products.  Blocks of eight columns without rows are left out of the softmax.
 //
-// A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 1,970, and a piece's beginning
-// and end some 8,000 on top.  What bounds it: latency, of the softmax's steps and of instruction fetches (the block's kinds of warps run
+// A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 2,110, and a piece's beginning
+// and end some 7,000 on top.  What bounds it: latency, of the softmax's steps and of instruction fetches (the block's kinds of warps run
 // more code than the caches next to them hold; the same instructions in another order are 3 to 20% slower or faster).  512 sequences x 6
-// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 460 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
-// 8,192 to 16,384 tokens: 335 us.  Heads of 64 halve the bytes and not the steps: 447 us, where the bf16 cache takes 366.
+// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 491 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
+// 8,192 to 16,384 tokens: 359 us.  Heads of 64 halve the bytes and not the steps: 494 us, where the bf16 cache takes 366.
 #include <float.h>
 
 #define SV_WALK_PART static __host__ __device__ __noinline__
@@ -38,16 +38,17 @@ namespace {
 template <int DP>
 struct Few8Shape {
     static constexpr int TILE = 128 * DP * 2;
-    static constexpr int KST = 3, VST = DP == 128 ? 3 : 4;        // tiles of keys in tensor memory and of values in shared memory
+    static constexpr int KST = DP == 128 ? 2 : 3, VST = DP == 128 ? 3 : 4;   // tiles of keys in tensor memory and of values in shared memory
     static constexpr int TOK = 64, SLOTS = 4;                     // tokens of a slot, slots of each ring of codes: two tiles
     static constexpr int HALF = 128 * 128;
     static constexpr int OFF_P = 2 * NR * DP * 2;                 // after two query tiles
-    static constexpr int PBUF = 128 * 2 * NR;                     // a group's weights: 128 tokens x 32, in the 64-byte swizzle
+    static constexpr int PBUF = 128 * 4 * NR;                     // a group's weights: 128 tokens x 32 rounded ones, 32 rests
     static constexpr int OFF_KV = OFF_P + 2 * PBUF;
     static constexpr int OFF_RAW = OFF_KV + VST * TILE;
     static constexpr int OFF_MISC = OFF_RAW + 2 * SLOTS * TOK * DP;
-    // tensor memory: scores as in sv_attend_few.cu, a group's output, its 32 sums of each token's weights twice, then keys
-    static constexpr uint32_t COL_O = 128, COL_L = 192, COL_K = 320;
+    // tensor memory: scores as in sv_attend_few.cu, a group's output (of the weights and of their rests), its 32 sums of each token's weights
+    // twice, then keys
+    static constexpr uint32_t COL_O = 128, COL_L = 256, COL_K = 384;
 };
 // Barriers of the tiles: kv_full, kv_empty [0, KST) are the keys', [KST, KST + VST) the values'.
 
@@ -61,6 +62,19 @@ struct Few8Shared : FewShared {
 constexpr float kLift = 4.0f, kGrow = 11.0f;
 // Sums of weights are kept times 2^kSums: 2^(kSums - E_j) stays a normal number for every scale beside a first page of the least (E_j up to 167).
 constexpr int kSums = 41;
+
+// Two weights as pairs of binary16 numbers: each rounded, and what that leaves, rounded.
+__device__ __forceinline__ void weight_halves(f32x2 e, uint32_t &hi, uint32_t &lo) {
+    float x, y;
+    f2_unpack(e, x, y);
+    asm("{\n\t.reg .b16 a, b, m;\n\t.reg .f32 p, q;\n\t"
+        "cvt.rn.f16x2.f32 %0, %3, %2;\n\t"
+        "mov.b32 {a, b}, %0;\n\tmov.b16 m, 0xBC00;\n\t"
+        "fma.rn.f32.f16 p, a, m, %2;\n\tfma.rn.f32.f16 q, b, m, %3;\n\t"
+        "cvt.rn.f16x2.f32 %1, q, p;\n\t}"
+        : "=&r"(hi), "=r"(lo)
+        : "f"(x), "f"(y));
+}
 
 __device__ __forceinline__ float half_bits(uint16_t x) { return __half2float(*reinterpret_cast<const __half *>(&x)); }
 
@@ -87,7 +101,7 @@ __device__ __forceinline__ void scan_codes(uint32_t tile, int t, uint32_t *flags
 
 // Adds to the group's output what the products left out: of each flagged token the values, NaN among them, times the weights that the product
 // would have used, for the rows that see it.  t: the thread's head element.  Rare, and out of line for the sake of the loop that calls it (512 x 6 rows
-// 475 us with it in line, 458 without).
+// 475 us with it in line, 458 without, before weights had two parts).
 template <int DP>
 __device__ __noinline__ void add_unseen(const AttendArgs &a, const PieceInfo *pi, uint32_t *flags, int first, uint32_t colO, const char *weights, int t) {
 #pragma unroll 1
@@ -99,14 +113,15 @@ __device__ __noinline__ void add_unseen(const AttendArgs &a, const PieceInfo *pi
         const int64_t off = slot_offset(a.c, a.bt.page_table + pi->table * a.bt.table_pitch, kk);
         if (off < 0) continue;
         const float v = t < a.c.head_dim ? codes2(reinterpret_cast<const uint8_t *>(a.c.v + off + pi->h * a.c.head_b)[t]).x : 0.0f;
-        const char *pj = weights + j * (2 * NR);
+        const char *pj = weights + j * (4 * NR);
         uint32_t o[32];
         tmem_ld32(colO, o);
         tc_wait_ld();
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int at = (r & 7) * 2;
-            const float w = half_bits(*reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ ((j >> 1) & 3)) << 4) + at));
+            const float w = half_bits(*reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ (j & 7)) << 4) + at)) +
+                            half_bits(*reinterpret_cast<const uint16_t *>(pj + ((((r >> 3) + 4) ^ (j & 7)) << 4) + at));
             if (((see >> r) & 1u) && r < pi->vr) o[r] = __float_as_uint(__uint_as_float(o[r]) + w * v);
         }
         tmem_st32(colO, o);
@@ -114,7 +129,8 @@ __device__ __noinline__ void add_unseen(const AttendArgs &a, const PieceInfo *pi
     }
 }
 
-// The same out of line, where that leaves the loop's instructions better placed: 512 x 6 rows with heads of 64 447 us (557 in line), of 128 483 (458).
+// The same out of line, for the kernel of heads up to 64, where that leaves the loop's instructions better placed: 512 x 6 rows with heads of 48 and 64 497 and
+// 494 us (550 in line), but of 80, 96 and 128 570 in the other kernel (491 to 494 in line).
 template <int DP>
 __device__ __noinline__ void scan_called(uint32_t tile, int t, uint32_t *flags) {
     scan_codes<DP>(tile, t, flags);
@@ -329,11 +345,11 @@ __device__ __forceinline__ void issue_products(Feed *fd, FewShared *ms, uint32_t
             __syncwarp();
             tc_fence_after();
             const uint64_t v = smem_operand(sbase + S::OFF_KV + stage * S::TILE, DP == 128 ? S::HALF : 0, 1024);
-            const uint64_t p = smem_operand64(sbase + S::OFF_P + of * S::PBUF, 512);
-            const uint32_t o = tm + S::COL_O + of * NR;
+            const uint64_t p = smem_operand(sbase + S::OFF_P + of * S::PBUF, 0, 1024);
+            const uint32_t o = tm + S::COL_O + of * (2 * NR);
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) mma_ss(o, v + kk * (2048 >> 4), p + kk * (1024 >> 4), shape_o, 1u);
+                for (int kk = 0; kk < 8; ++kk) mma_ss(o, v + kk * (2048 >> 4), p + kk * (2048 >> 4), shape_o, 1u);
                 mma_commit(&fd->kv_empty[S::KST + stage]);
                 mma_commit(&ms->p_done[of]);
             }
@@ -428,8 +444,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
         // ---------------------------------------------------------------- softmax
         const int gr = warp >> 2, wl = warp & 3, t = wl * 32 + lane;   // group, warp of it, token of the tile (head element at the end)
         const uint32_t base = tmem + ((uint32_t)(wl * 32) << 16);
-        const uint32_t colO = base + S::COL_O + gr * NR, colL = base + S::COL_L + gr * (2 * NR);
-        const uint32_t prow = sbase + S::OFF_P + gr * S::PBUF + t * (2 * NR);     // this token's weights; chunk q at q ^ ((t >> 1) & 3)
+        const uint32_t colO = base + S::COL_O + gr * (2 * NR), colL = base + S::COL_L + gr * (2 * NR);
+        const uint32_t prow = sbase + S::OFF_P + gr * S::PBUF + t * (4 * NR);     // this token's weights; chunk q at q ^ (t & 7)
         uint32_t u = 0;   // tiles this group has worked on
         int rests = 0;    // the group that left the last piece of one tile to the other
         auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + gr) : "memory"); };
@@ -464,6 +480,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
 #pragma unroll
                 for (int j = 0; j < 32; ++j) zero[j] = 0;
                 tmem_st32(colO, zero);
+                tmem_st32(colO + NR, zero);
                 tmem_st32(colL, zero);
                 tc_wait_st();
             }
@@ -501,7 +518,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 __syncwarp();
                 tc_fence_after();
                 // Everything goes by blocks of eight rows, in rolled loops that read the scores anew: what the softmax would hold
-                // unrolled in registers costs more in instruction fetches (736 us for 512 x 6 rows over 1-2k tokens).
+                // unrolled in registers costs more in instruction fetches (736 us for 512 x 6 rows over 1-2k tokens, where this took 487).
                 auto scores = [&](int q, const float *less, float (&x)[8]) {
                     uint32_t raw[8];
                     tmem_ld8(colS + 8 * q, raw);
@@ -548,17 +565,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                         if (k > begin) {
 #pragma unroll 1
                             for (int q = 0; q < used; ++q) {
-                                uint32_t o[8], l[8];
+                                uint32_t o[8], o2[8], l[8];
                                 tmem_ld8(colO + 8 * q, o);
+                                tmem_ld8(colO + NR + 8 * q, o2);
                                 tmem_ld8(sums + 8 * q, l);
                                 tc_wait_ld();
 #pragma unroll
                                 for (int r = 0; r < 8; ++r) {
                                     const float f = alpha[8 * q + r];
                                     o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
+                                    o2[r] = __float_as_uint(__uint_as_float(o2[r]) * f);
                                     l[r] = __float_as_uint(__uint_as_float(l[r]) * f);
                                 }
                                 tmem_st8(colO + 8 * q, o);
+                                tmem_st8(colO + NR + 8 * q, o2);
                                 tmem_st8(sums + 8 * q, l);
                             }
                             tc_wait_st();
@@ -568,7 +588,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
 #pragma unroll 1
                     for (int q = 0; q < used; ++q) {   // eight rows' weights, a 16-byte chunk
                         float x[8];
-                        uint32_t l[8], w[4];
+                        uint32_t l[8], w[4], rest[4];
                         tmem_ld8(sums + 8 * q, l);
                         scores(q, shift, x);
 #pragma unroll
@@ -579,11 +599,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                             f2_unpack(f2_fma(e, back, f2_from_u32x2(l[2 * j], l[2 * j + 1])), y, z);
                             l[2 * j] = __float_as_uint(y);
                             l[2 * j + 1] = __float_as_uint(z);
-                            f2_unpack(e, y, z);
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(z), "f"(y));
+                            weight_halves(e, w[j], rest[j]);
                         }
                         tmem_st8(sums_to + 8 * q, l);
-                        sts128(prow + ((q ^ ((t >> 1) & 3)) << 4), w);
+                        sts128(prow + ((q ^ (t & 7)) << 4), w);
+                        sts128(prow + (((q + 4) ^ (t & 7)) << 4), rest);
                     }
                     if (grow) break;
                     uint32_t again;
@@ -600,8 +620,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 if (down != 1.0f) {   // the rest of this token's scale
 #pragma unroll 1
                     for (int r = 0; r < vr; ++r) {
-                        uint16_t *at = reinterpret_cast<uint16_t *>(smem + S::OFF_P + gr * S::PBUF + t * (2 * NR) + (((r >> 3) ^ ((t >> 1) & 3)) << 4) + (r & 7) * 2);
-                        *at = (sees >> r) & 1u ? __half_as_ushort(__float2half_rn(half_bits(*at) * down)) : 0;   // NaN where it is seen
+                        char *row = smem + S::OFF_P + gr * S::PBUF + t * (4 * NR) + (r & 7) * 2;
+                        uint16_t *at = reinterpret_cast<uint16_t *>(row + (((r >> 3) ^ (t & 7)) << 4));
+                        uint16_t *rest = reinterpret_cast<uint16_t *>(row + ((((r >> 3) + 4) ^ (t & 7)) << 4));
+                        const float w = (sees >> r) & 1u ? (half_bits(*at) + half_bits(*rest)) * down : 0.0f;   // NaN where it is seen
+                        *at = __half_as_ushort(__float2half_rn(w));
+                        *rest = __half_as_ushort(__float2half_rn(w - half_bits(*at)));
                     }
                 }
                 if (masked) {
@@ -682,14 +706,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                 float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
                 for (int g = ga; g < (solo ? ga + 1 : 2); ++g) {
-                    uint32_t o[4];
-                    tmem_ld4(base + S::COL_O + g * NR + rb, o);
+                    uint32_t o[4], o2[4];   // the products with the weights and with their rests
+                    tmem_ld4(base + S::COL_O + g * (2 * NR) + rb, o);
+                    tmem_ld4(base + S::COL_O + g * (2 * NR) + NR + rb, o2);
                     tc_wait_ld();
                     const float4 f = *reinterpret_cast<const float4 *>(ms->alpha[g] + rb);
-                    y[0] = fmaf(__uint_as_float(o[0]), f.x, y[0]);
-                    y[1] = fmaf(__uint_as_float(o[1]), f.y, y[1]);
-                    y[2] = fmaf(__uint_as_float(o[2]), f.z, y[2]);
-                    y[3] = fmaf(__uint_as_float(o[3]), f.w, y[3]);
+                    y[0] = fmaf(__uint_as_float(o[0]) + __uint_as_float(o2[0]), f.x, y[0]);
+                    y[1] = fmaf(__uint_as_float(o[1]) + __uint_as_float(o2[1]), f.y, y[1]);
+                    y[2] = fmaf(__uint_as_float(o[2]) + __uint_as_float(o2[2]), f.z, y[2]);
+                    y[3] = fmaf(__uint_as_float(o[3]) + __uint_as_float(o2[3]), f.w, y[3]);
                 }
                 if (t < D) {
 #pragma unroll
@@ -707,7 +732,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
         widen_codes<DP>(fd, f8, sbase, tmem, warp - 8, lane);
     } else {
         if (warp == 12) {   // V transposed times the weights
-            issue_products<DP>(fd, ms, a2.shape_s, mma_shape_f16(NR, true, true, false, false), sbase, tmem, lane);
+            issue_products<DP>(fd, ms, a2.shape_s, mma_shape_f16(2 * NR, true, true, false, false), sbase, tmem, lane);
         } else if (warp == 13) {
             feed_walk(a, a2, fd, ms->walk, lane, [&](int it) {
                 if (__all_sync(0xFFFFFFFFu, wait_phase(fd, &fd->q_empty[it & 1], ((it >> 1) & 1) ^ 1))) {

@@ -24,12 +24,6 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, u
            1ull << 46 | 2ull << 61;
 }
 
-// The same in the 64-byte swizzle, with a contiguous axis of 32 elements that is not summed over: rows of 64 bytes, 16-byte chunk c of row r at
-// chunk c ^ ((r >> 1) & 3).
-__device__ __forceinline__ uint64_t smem_operand64(uint32_t addr, uint32_t stride) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((stride >> 4) & 0x3FFF) << 32 | 1ull << 46 | 4ull << 61;
-}
-
 // bf16 operands, float32 accumulation, M = 128 rows by N columns.  a_t, b_t: the operand's contiguous axis in shared memory is not
 // the one summed over; a_neg, b_neg: the operand enters negated.
 __host__ __device__ constexpr uint32_t mma_shape(int N, bool a_t, bool b_t, bool a_neg, bool b_neg) {
