@@ -111,11 +111,15 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
         int next_key = p.g.key0 + p.k0 * 64 + wp * 8 + lane;
         int next_pn = next_key / psize, next_slot = next_key - next_pn * psize, next_page = INT32_MIN;
         auto look_up = [&]() { next_page = lane < 8 && next_key < p.end ? table[next_pn] : INT32_MIN; };
-        uint32_t kb = 127, vb = 127, kb_next = 127, vb_next = 127;   // C8: scales of the lane's token of the tile at hand, of the next
+        // C8: scales of the lane's token of the tile at hand, of the next; 1 where that one's page is none of the pool's (not looked at before they are used: a
+        // warp stops there until they have come)
+        uint32_t kb = 127, vb = 127, kb_next = 127, vb_next = 127;
+        bool paged = false;
         auto copy = [&](int k) {   // tile k, which has been looked up; looks up the next
             int64_t off = -1;
             if (C8) {
-                const int page = (unsigned)next_page < (unsigned)a.c.n_pages ? next_page : 0;
+                paged = (unsigned)next_page < (unsigned)a.c.n_pages;
+                const int page = paged ? next_page : 0;
                 kb_next = a.sc.k[page * a.sc.page_b + h * a.sc.head_b];
                 vb_next = a.sc.v[page * a.sc.page_b + h * a.sc.head_b];
             }
@@ -208,8 +212,8 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
         };
         const int seen_by_all = p.seg >= a.n_groups ? p.g.ctx : p.end;
         for (int k = p.k0; k < p.k1; ++k) {
-            kb = kb_next;
-            vb = vb_next;
+            kb = paged ? kb_next : 127u;
+            vb = paged ? vb_next : 127u;
             if (k + 1 < p.k1) {
                 copy(k + 1);
                 cp_async_wait<1>();

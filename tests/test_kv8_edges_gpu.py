@@ -1,0 +1,56 @@
+"""GPU tests of attention over codes where it can go wrong: the same calls in every kernel, against the oracle."""
+import pytest
+import torch
+
+from kv8_helpers import Cache8, check_attend8
+from test_kv8_gpu import filled
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+# type, rows, query heads, width: the kernel for few rows of either type, that for more, and that of wide heads
+KERNELS = [(BF, 4, 4, 64), (BF, 5, 8, 128), (BF, 40, 4, 128), (BF, 3, 4, 192), (F32, 1, 4, 64), (F32, 3, 4, 128), (F32, 30, 4, 64)]
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import speculative_decoding_verification_gb300 as sv
+    sv.load()
+    return sv
+
+
+def spare_first_page(c):
+    """Moves what page 0 holds elsewhere: (cache, numbers of two pages that no table names)."""
+    free = sorted(set(range(c.k8.shape[0])) - set(c.table.flatten().tolist()))
+    if 0 not in free:
+        to = free.pop()
+        for x in (c.k8, c.v8, c.ks, c.vs):
+            x.view(torch.uint8)[to] = x.view(torch.uint8)[0]
+        c.table[c.table == 0] = to
+        c.args["page_table"] = c.table.cuda()
+        free = [0] + free
+    return free[0], free[1]
+
+
+@pytest.mark.parametrize("dtype,n,H,dim", KERNELS)
+@pytest.mark.parametrize("bad", [-1, -7, 1 << 20, 2 ** 31 - 1])
+def test_a_page_outside_the_pool_reads_zeros_whatever_the_first_page_holds(sv, dtype, n, H, dim, bad):
+    """It is reported; its tokens have keys and values of 0, and no other page's scale has to do with them."""
+    from speculative_decoding_verification_gb300 import _abi
+    c, q, rows = filled(n + dim, dtype, [300, 70, 130], n, H, 2, dim, 16, spread=2)
+    first, zeros = spare_first_page(c)
+    for s in (c.ks, c.vs):
+        s[first] = 255
+        s[zeros] = 127
+    for x in (c.k8, c.v8):
+        x.view(torch.uint8)[first] = 0x7F
+        x.view(torch.uint8)[zeros] = 0
+    table = c.table.clone()
+    for b, entry in ((0, 3), (0, 17), (1, 0), (2, 4)):
+        table[b, entry] = bad
+        c.table[b, entry] = zeros
+    c.refresh()
+    stats = sv.new_stats("cuda")
+    out, lse = sv.sv_kv_attend8(q, *c.args8[:5], table.cuda(), lse=True, stats=stats)
+    assert sv.read_stats(stats)["status"] == _abi.SV_ERR_INVALID_ARG
+    check_attend8(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), dim ** -0.5, rows)
