@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
 constexpr size_t kNoSlot = ~(size_t)0;   // a block whose range holds no tile of the unit
 
 // Adds the pieces of one row, a warp: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over n blocks, in order; slot_of(p) is
-// the p-th one's slot.  Lanes take the pieces' maxima and sums, then the row's elements.
+// the p-th one's slot.  Lanes take the pieces' maxima and sums, then the row's elements.  Pieces whose tokens the row did not see are left out, by a
+// weight of -0, and so are those whose weight underflows to 0, but not over codes: a NaN there reaches the row all the same.
 template <int ES, class F>
 __device__ __forceinline__ void join_row(const AttendArgs &a, int row, int qh, int n, int lane, F slot_of) {
     const int D = a.c.head_dim, D4 = D / 4;
@@ -338,7 +339,7 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, int row, int qh, i
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         top = fmaxf(top, m);
         const float ref = top == -INFINITY ? 0.0f : top;
-        const float w = ml.y == 0.0f ? 0.0f : exp2f(ml.x - ref), before = exp2f(m - ref);
+        const float w = ml.y == 0.0f ? -0.0f : exp2f(ml.x - ref), before = exp2f(m - ref);
         float sum = w * ml.y;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
@@ -351,7 +352,7 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, int row, int qh, i
         for (int q = 0; q < many; ++q) {
             const float f = __shfl_sync(0xFFFFFFFFu, w, q);
             const size_t at = __shfl_sync(0xFFFFFFFFu, slot, q) * D;
-            if (f != 0.0f) {
+            if (a.sc.k ? __float_as_uint(f) != 0x80000000u : f != 0.0f) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int col = lane + 32 * j;

@@ -54,3 +54,32 @@ def test_a_page_outside_the_pool_reads_zeros_whatever_the_first_page_holds(sv, d
     out, lse = sv.sv_kv_attend8(q, *c.args8[:5], table.cuda(), lse=True, stats=stats)
     assert sv.read_stats(stats)["status"] == _abi.SV_ERR_INVALID_ARG
     check_attend8(c, q.flatten(0, 1), out.flatten(0, 1), lse.flatten(0, 1), dim ** -0.5, rows)
+
+
+@pytest.mark.parametrize("dtype,n,H,dim", KERNELS)
+@pytest.mark.parametrize("prefix", [0, 1024])
+def test_nan_reaches_every_row_from_a_part_of_the_context_without_weight(sv, dtype, n, H, dim, prefix):
+    """A value of NaN, by its code and by its scale, among tokens that another block works on, or that the prefix holds, and whose weights underflow
+    beside the largest."""
+    ctx = [prefix + 2500, prefix + 40]
+    for by_scale in (False, True):
+        c = Cache8(n + dim, dtype, ctx, n, 2, dim, 16, groups=[(0, prefix)] if prefix else None)
+        g = torch.Generator().manual_seed(7)
+        for b in range(2):
+            c.put(b, ctx[b], torch.randn((n, 2, dim), generator=g), torch.randn((n, 2, dim), generator=g))
+        c.refresh()
+        q = torch.randn((2, n, H, dim), generator=g).to(dtype).cuda()
+        k8, v8 = c.k8.view(torch.uint8), c.v8.view(torch.uint8)
+        for b, at, best in ((0, 100, ctx[0] - 200), (1, 100 if prefix else 3, ctx[1] - 3)):
+            page, place = c.table[b, at // 16].long(), at % 16
+            k8[page, :, 0] = 0   # scores of 0 beside those of 1000 and more
+            q[b, :, : H // 2] = 1000.0 * c.k[c.table[b, best // 16].long(), best % 16, 0]
+            if by_scale:
+                c.vs[page, 0] = 255
+            else:
+                v8[page, place, 0, 3] = 0x7F
+        out, lse = sv.sv_kv_attend8(q, *c.args8, lse=True, **c.group_args)
+        want = torch.zeros(out.shape, dtype=torch.bool)
+        want[:, :, : H // 2, slice(None) if by_scale else slice(3, 4)] = True
+        assert (torch.isnan(out).cpu() == want).all(), by_scale
+        assert not torch.isnan(lse).any()
