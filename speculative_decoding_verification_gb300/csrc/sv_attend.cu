@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
             for (int m = wp; m < TM; m += 8) {
                 const int lim = row_lim[m];
                 float x[TK / 32], top = -INFINITY;
+                uint32_t hidden = 0;   // the lane's tokens that the row does not see
 #pragma unroll
                 for (int j = 0; j < TK / 32; ++j) {
                     const int key = first + lane + j * 32;
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
                         sees = (row_anc[m * S::ANC + (rel >> 5)] >> (rel & 31)) & 1u;
                     }
                     x[j] = sees ? ss[m * S::SP + lane + j * 32] : -INFINITY;
+                    if (C8 && !sees) hidden |= 1u << j;
                     top = fmaxf(top, x[j]);
                 }
 #pragma unroll
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < TK / 32; ++j) {
-                    const float e = exp2f(x[j] - base);
+                    const float e = C8 && ((hidden >> j) & 1u) ? -0.0f : exp2f(x[j] - base);
                     ss[m * S::SP + lane + j * 32] = e;
                     sum += e;
                 }
@@ -212,7 +214,8 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
             }
             __syncthreads();
             // A tile in which some row does not see some key multiplies only where the weight is not zero: 0 * inf
-            // of a token that is not seen must not reach the sum.
+            // of a token that is not seen must not reach the sum.  Over codes, where the weight is not -0, that of a token that is not seen: a NaN reaches
+            // every row that sees it, however small the weight.
             const bool masked = first + TK > p.end || (p.seg >= a.n_groups && first + TK > p.g.ctx);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) 
 #pragma unroll
                             for (int r = 0; r < 4; ++r) {
                                 const float e = u == 0 ? pw[r].x : u == 1 ? pw[r].y : u == 2 ? pw[r].z : pw[r].w;
-                                if (!guard.value || e != 0.0f) {
+                                if (!guard.value || (C8 ? __float_as_uint(e) != 0x80000000u : e != 0.0f)) {
                                     acc[r][c].x = fmaf(e, v.x, acc[r][c].x);
                                     acc[r][c].y = fmaf(e, v.y, acc[r][c].y);
                                     acc[r][c].z = fmaf(e, v.z, acc[r][c].z);

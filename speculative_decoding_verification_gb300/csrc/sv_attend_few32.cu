@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
         };
         look_up();
         copy(p.k0);
-        // Where a tile holds hidden tokens, a weight of zero multiplies nothing: their values may not be finite.
+        // Where a tile holds hidden tokens, a weight of zero multiplies nothing: their values may not be finite.  Over codes the weights of hidden tokens
+        // are -0 and multiply nothing: a NaN reaches every row that sees it, however small the weight.
         auto tile = [&](int k, auto hidden) {
             const int key0 = p.g.key0 + k * 64 + wp * 8;
             const float4 *keys = mine + (k & 1) * 2 * chunks + lane, *values = keys + chunks;
@@ -175,8 +176,9 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
                 }
                 float s = sum_lanes(x, lane) * a.scale_log2;
                 const int key = key0 + b * KB + slot;
+                bool sees = true;
                 if (hidden.value) {
-                    bool sees = key < lim;
+                    sees = key < lim;
                     if (tree && key >= p.g.ctx && key < p.end) sees = (anc >> (key - p.g.ctx)) & 1u;
                     if (!sees) s = -INFINITY;
                 } else if (row >= p.vr) {
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
                     for (int r = 0; r < R; ++r) scale_quad(o[r], __shfl_sync(0xFFFFFFFFu, alpha, r));
                     m = now;
                 }
-                const float e = exp2f(s - ref);
+                const float e = C8 && hidden.value && !sees ? -0.0f : exp2f(s - ref);
                 l += e;
 #pragma unroll
                 for (int j = 0; j < KB; ++j) {
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads32, 2) k_attend_few32(const AttendArgs
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const float f = __shfl_sync(0xFFFFFFFFu, e, j * R + r);
-                        if (!hidden.value || f != 0.0f) {
+                        if (!hidden.value || (C8 ? __float_as_uint(f) != 0x80000000u : f != 0.0f)) {
                             const f32x2 f2 = f2_pack(f, f);
                             o[r].a = f2_fma(f2, vv.a, o[r].a);
                             o[r].b = f2_fma(f2, vv.b, o[r].b);

@@ -83,3 +83,33 @@ def test_nan_reaches_every_row_from_a_part_of_the_context_without_weight(sv, dty
         want[:, :, : H // 2, slice(None) if by_scale else slice(3, 4)] = True
         assert (torch.isnan(out).cpu() == want).all(), by_scale
         assert not torch.isnan(lse).any()
+
+
+@pytest.mark.parametrize("dtype,n,H,dim", KERNELS)
+@pytest.mark.parametrize("ctx", [37, 133, 6, 200])
+@pytest.mark.parametrize("tree", [False, True])
+def test_nan_reaches_whoever_sees_it_however_small_its_weight(sv, dtype, n, H, dim, ctx, tree):
+    """A value's NaN code or NaN scale at a token whose weight underflows to 0, among tokens that not all rows see: a cached one near the block, and
+    one of the block's own."""
+    if tree and n < 3:
+        pytest.skip("no tree")
+    for at, by_scale in ((ctx - 1, False), (ctx - 1, True), (ctx + n // 2, False)):
+        c, q, _ = filled(n + dim, dtype, [ctx, 20], n, H, 2, dim, 8)
+        k8, v8 = c.k8.view(torch.uint8), c.v8.view(torch.uint8)
+        page, place = c.table[0, at // 8].long(), at % 8
+        k8[page, place, 0] = 0                               # a score of 0 beside those of 1000 and more
+        q[0, :, : H // 2] = 1000.0 * c.k[c.table[0, 0].long(), 1, 0]
+        if by_scale:
+            c.vs[page, 0] = 255
+            seen_from, elements = at - at % 8, slice(None)
+        else:
+            v8[page, place, 0, 3] = 0x7F
+            seen_from, elements = at, slice(3, 4)
+        par = torch.tensor([[0] * (n - 1)] * 2, dtype=torch.int32) if tree else None   # all of them children of row 0
+        out, lse = sv.sv_kv_attend8(q, *c.args8, lse=True, parents=None if par is None else par.cuda())
+        want = torch.zeros(out.shape, dtype=torch.bool)
+        for i in range(n):
+            seen = seen_from <= ctx or i == seen_from - ctx if tree else seen_from <= ctx + i
+            want[0, i, : H // 2, elements] = seen
+        assert (torch.isnan(out).cpu() == want).all(), (at, by_scale)
+        assert not torch.isnan(lse).any()
