@@ -58,6 +58,10 @@ __device__ __forceinline__ int raw_place(int r, int ch) {
     return r * DP + ((!SWIZZLE ? ch : DP == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4);
 }
 
+// The first token of a lane's box in a tile.  Lanes without a box stay within the tile too: all look pages up tiles ahead, and kMaxSlots leaves room for
+// tiles past the last slot, not for 31 boxes of 32 tokens.
+SV_HD int box_offset(int lane, int box_rows) { return min(lane * box_rows, kTcKeys - 1); }
+
 // One of the loading warps: kv 0 the keys, 1 the values.  Slots of TOK tokens at raw_base, DP bytes a token.  SCALES: with their scales.  KEYS_SWIZZLED: the
 // keys' slots are swizzled.  ALL_BOXES: the last tiles go as boxes too, with what their pages hold past the last token and zeros for pages past it,
 // for a softmax that leaves out what a row does not see.
@@ -78,8 +82,8 @@ __device__ __forceinline__ void feed8_load_as(const AttendArgs &a, const TcArgs 
     const int psize = a.c.page_size, pshift = a2.page_shift;
     auto page_index = [&](int key) { return pshift >= 0 ? key >> pshift : key / psize; };
     // boxes: a tile's are a lane's each
-    const int box_rows = a2.box_rows > 0 ? a2.box_rows : 8, box_token = lane * box_rows, my_slot = box_token / TOK;
-    const bool boxes = box_token < kTcKeys;
+    const int box_rows = a2.box_rows > 0 ? a2.box_rows : 8, box_token = box_offset(lane, box_rows), my_slot = lane * box_rows / TOK;
+    const bool boxes = lane * box_rows < kTcKeys;
     uint32_t slot = 0, parity = 1, begun = 0, tiles = 0;   // the next slot, its empty barrier's parity, slots and tiles begun
     bool on = true;                                        // off once a wait gave up
     auto take = [&]() {   // waits for the next slot
