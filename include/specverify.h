@@ -735,8 +735,8 @@ typedef struct sv_kv_pool {
  *  workspace    dev, >= sv_kv_fork_workspace_size(n_pages, N) bytes, 256-byte aligned, as other calls'.
  * Device-side checks, in stats: SV_ERR_INVALID_ARG with the sequence for a src outside [-1, B), a context_len that is negative or, with
  * reserve, passes max_pages * page_size (both treated as -1), a page id >= n_pages, or a token's entry that names no page; with the page for
- * refs below its holders.  SV_ERR_NO_PAGE with the new sequence where no page is free: its entry is then -1, and what it would have
- * held is lost with it.  Nothing is read or written out of range for any of these.
+ * refs below its holders in the old table (others then count as 0).  SV_ERR_NO_PAGE with the new sequence where no page is free: its
+ * entry is then -1, and what it would have held is lost with it.  Nothing is read or written out of range for any of these.
  * Returns SV_ERR_INVALID_ARG for null pointers, sizes below 1, reserve < 0, misaligned bases or strides, n_pages or N above 2^30,
  * B * max_pages or N * max_pages or N * n_layers above 2^31 - 1, or outputs that overlap inputs.
  * -------------------------------------------------------------------------------------- */
