@@ -919,14 +919,14 @@ def sv_kv_commit8(k_cache, v_cache, k_scale, v_scale, context_len, page_table, a
 def _kv_pool(k_cache, v_cache, k_scale, v_scale):
     """(device, pages, packed sv_kv_pool) of caches [layers, pages, page_size, kv_heads, dim] of any element type."""
     dev, shape, st = _paged(k_cache, v_cache, 5)
-    es = k_cache.element_size()
+    es = k_cache.element_size()   # other one-byte caches (with one scale a tensor, say) have no scales of their pages
     scale_at, sst = (0, 0), (0, 0, 0)
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale come together")
     if k_scale is not None:
         sst = _scales(k_scale, v_scale, shape, dev)
         scale_at = k_scale.data_ptr(), v_scale.data_ptr()
-    elif es == 1:
+    elif k_cache.dtype is torch.float8_e4m3fn:
         raise ValueError("a cache held in 8 bits has scales: pass k_scale and v_scale")
     return dev, shape[1], _abi.KV_POOL.pack(k_cache.data_ptr(), v_cache.data_ptr(), *scale_at, st[0] * es, st[1] * es, st[2] * es, st[3] * es,
                                             shape[4] * es, *sst, shape[0], shape[1], shape[2], shape[3])
@@ -958,7 +958,7 @@ def sv_kv_fork(k_cache, v_cache, page_refs, context_len, page_table, src, reserv
     """sv_kv_fork: a new batch whose sequence j continues sequence src[j] of the old one (-1: an empty sequence).
 
     k_cache, v_cache [layers, pages, page_size, kv_heads, dim] of any type (with k_scale, v_scale [layers, pages, kv_heads] where
-    they are held in 8 bits); page_refs int32 [pages]: holders of each page, 0 free; context_len int32 [B]; page_table int32 [B,
+    they are held in 8 bits, float8_e4m3fn); page_refs int32 [pages]: holders of each page, 0 free; context_len int32 [B]; page_table int32 [B,
     max_pages], -1 where an entry names no page; src int32 [N].  Full pages are shared, a partly filled one is copied for all but its
     first new sequence, entries up to slot context + reserve are given free pages.  refs_out may be page_refs.
     Returns (table_out [N, max_pages], context_out [N], refs_out [pages])."""

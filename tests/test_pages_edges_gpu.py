@@ -47,3 +47,21 @@ def test_counts_below_the_holders_are_reported_and_give_no_page_away(sv, src, la
         assert (refs[new] == 1).all()
     named = np.bincount(table[table >= 0], minlength=p.pages)
     assert (refs >= named).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.int8, torch.float8_e5m2])
+def test_one_byte_caches_without_scales_of_their_pages(sv, dtype):
+    """Their bytes move as those of a cache held in 8 bits do; that one is refused without its scales."""
+    p = Pool(5, 2, 4, 2, 32, E4M3, 6, 40)
+    src = np.array([0, 0, 1, 3, 3, 5])
+    plain = [c.clone().view(dtype) for c in p.caches]
+    table, ctx, refs = p.fork(sv, src, 3)
+    got = sv.sv_kv_fork(*plain, p.dev(p.refs), p.dev(p.ctx), p.dev(p.table), p.dev(src), reserve=3)
+    assert all(torch.equal(a, b) for a, b in zip(got, (table, ctx, refs)))
+    want = sv.sv_kv_compact(*p.caches, refs, table, **p.kw)
+    got = sv.sv_kv_compact(*plain, refs, table)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for a, b in zip(plain, p.caches):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    with pytest.raises(ValueError, match="scales"):
+        sv.sv_kv_fork(*p.caches, p.dev(p.refs), p.dev(p.ctx), p.dev(p.table), p.dev(src))
