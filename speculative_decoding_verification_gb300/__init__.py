@@ -960,7 +960,7 @@ def sv_kv_fork(k_cache, v_cache, page_refs, context_len, page_table, src, reserv
     k_cache, v_cache [layers, pages, page_size, kv_heads, dim] of any type (with k_scale, v_scale [layers, pages, kv_heads] where
     they are held in 8 bits, float8_e4m3fn); page_refs int32 [pages]: holders of each page, 0 free; context_len int32 [B]; page_table int32 [B,
     max_pages], -1 where an entry names no page; src int32 [N].  Full pages are shared, a partly filled one is copied for all but its
-    first new sequence, entries up to slot context + reserve are given free pages.  refs_out may be page_refs.
+    first new sequence, entries up to slot context + reserve are given free pages.  With N 0 the whole batch ends.  refs_out may be page_refs.
     Returns (table_out [N, max_pages], context_out [N], refs_out [pages])."""
     lib = _abi.load_packed()
     dev, pages, pool = _kv_pool(k_cache, v_cache, k_scale, v_scale)
@@ -970,12 +970,15 @@ def sv_kv_fork(k_cache, v_cache, page_refs, context_len, page_table, src, reserv
     N = src.numel()
     of = _ints(src, "src", torch.int32, N, dev)
     table_out, to, to_pitch = _table_out(table_out, (N, width), dev)
-    context_out = _out(context_out, "context_out", torch.int32, (N,), dev)
+    context_out = ctx_out = _out(context_out, "context_out", torch.int32, (N,), dev)
+    if N == 0:   # the whole batch ends: a new one of a single empty sequence, which nobody sees
+        none = torch.full((width + 2,), -1, dtype=torch.int32, device=dev)
+        N, of, to, to_pitch, ctx_out = 1, none.data_ptr(), none[1:].data_ptr(), width, none[width + 1:]
     refs_out = _out(refs_out, "refs_out", torch.int32, (pages,), dev)
     st = _stats(stats, dev).data_ptr() if stats is not None else 0
     ws = (workspace or _default_ws).get(_fork_ws_bytes(pages, N), dev)
     code = _call(dev, stream, lib.sv_kv_fork, pool, refs, ctx, table, pitch, width, B, of, N, int(reserve), refs_out.data_ptr(), to, to_pitch,
-                 context_out.data_ptr(), st, ws.data_ptr(), ws.numel())
+                 ctx_out.data_ptr(), st, ws.data_ptr(), ws.numel())
     if code:
         _abi.check("sv_kv_fork", code)
     return table_out, context_out, refs_out

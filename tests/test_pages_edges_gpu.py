@@ -65,3 +65,15 @@ def test_one_byte_caches_without_scales_of_their_pages(sv, dtype):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     with pytest.raises(ValueError, match="scales"):
         sv.sv_kv_fork(*p.caches, p.dev(p.refs), p.dev(p.ctx), p.dev(p.table), p.dev(src))
+
+
+def test_a_batch_that_ends_whole(sv):
+    """No new sequences: every page goes that nobody else holds."""
+    p = Pool(6, 2, 4, 2, 16, BF, 5, 30)
+    for refs_out in (None, p.dev(p.refs)):
+        table, ctx, refs = p.fork(sv, np.zeros(0), 4, refs_out=refs_out)
+        left = p.refs.copy()
+        np.subtract.at(left, p.table[p.table >= 0], 1)
+        assert table.shape == (0, p.width) and ctx.shape == (0,) and refs.tolist() == left.tolist()
+        assert refs_out is None or refs is refs_out
+    p.check_bytes([])
