@@ -12,18 +12,18 @@
 //             where M follows the largest s_j + E_j as a maximum does: weights are as exact as those of an unscaled cache whatever the
 //             scales are.  A weight enters its product with the codes as two binary16 numbers, itself rounded and what that leaves, rounded: within
 //             2^-22 of it, or of the largest 2^-29 where that is more (half of binary16's last step, 2^-25, beside 2^kLift).  One number alone, off by up to
-//             2^-11, would take 462 us where this takes 491, and outputs would differ with how many rows a block has.
+//             2^-11, took 462 us where this takes 484, and outputs would differ with how many rows a block has.
 //             An E_j below -40 is taken as -40 and the rest multiplies the weight, so that pages of zeros (whose scale is the least) count
 //             in the sum.  E_j up to 64 leave every weight there that is within 2^-26 of its row's largest; above, the least may drop out.
 // Keys are widened to tensor memory, from where the products take them, values to shared memory: its bandwidth (a tile of values is
 // written, read, written wide and read by the products) would else be the bound.
 // The walk's warp makes the query tiles, ahead of the products.  Blocks of eight columns without rows are left out of the softmax.
 //
-// A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 2,110, and a piece's beginning
+// A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 2,100, and a piece's beginning
 // and end some 7,000 on top.  What bounds it: latency, of the softmax's steps and of instruction fetches (the block's kinds of warps run
 // more code than the caches next to them hold; the same instructions in another order are 3 to 20% slower or faster).  512 sequences x 6
-// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 491 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
-// 8,192 to 16,384 tokens: 359 us.  Heads of 64 halve the bytes and not the steps: 494 us, where the bf16 cache takes 366.
+// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 484 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
+// 8,192 to 16,384 tokens: 356 us.  Heads of 64 halve the bytes and not the steps: 477 us, where the bf16 cache takes 366.
 #include <float.h>
 
 #define SV_WALK_PART static __host__ __device__ __noinline__
@@ -129,11 +129,23 @@ __device__ __noinline__ void add_unseen(const AttendArgs &a, const PieceInfo *pi
     }
 }
 
-// The same out of line, for the kernel of heads up to 64, where that leaves the loop's instructions better placed: 512 x 6 rows with heads of 48 and 64 497 and
-// 494 us (550 in line), but of 80, 96 and 128 570 in the other kernel (491 to 494 in line).
+// The same out of line, for the kernel of heads up to 64, where that leaves the loop's instructions better placed: 512 x 6 rows with heads of 48 and 64 479 and
+// 477 us (550 in line), but of 80, 96 and 128 537 to 540 in the other kernel (484 to 487 in line).
 template <int DP>
 __device__ __noinline__ void scan_called(uint32_t tile, int t, uint32_t *flags) {
     scan_codes<DP>(tile, t, flags);
+}
+
+// The rest of token t's scale on its weights, as two numbers again.  Out of line as the above: 484 us (492 in line).
+__device__ __noinline__ void scale_weights(char *row, int t, uint32_t sees, float down, int vr) {
+#pragma unroll 1
+    for (int r = 0; r < vr; ++r) {
+        uint16_t *at = reinterpret_cast<uint16_t *>(row + (r & 7) * 2 + (((r >> 3) ^ (t & 7)) << 4));
+        uint16_t *rest = reinterpret_cast<uint16_t *>(row + (r & 7) * 2 + ((((r >> 3) + 4) ^ (t & 7)) << 4));
+        const float w = (sees >> r) & 1u ? (half_bits(*at) + half_bits(*rest)) * down : 0.0f;   // NaN where it is seen
+        *at = __half_as_ushort(__float2half_rn(w));
+        *rest = __half_as_ushort(__float2half_rn(w - half_bits(*at)));
+    }
 }
 
 // Reduction of x[0..7] over the warp's lanes: lane i gets that of x[i / 4].
@@ -617,17 +629,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                     tc_wait_st();
                 }
                 flip = !flip;
-                if (down != 1.0f) {   // the rest of this token's scale
-#pragma unroll 1
-                    for (int r = 0; r < vr; ++r) {
-                        char *row = smem + S::OFF_P + gr * S::PBUF + t * (4 * NR) + (r & 7) * 2;
-                        uint16_t *at = reinterpret_cast<uint16_t *>(row + (((r >> 3) ^ (t & 7)) << 4));
-                        uint16_t *rest = reinterpret_cast<uint16_t *>(row + ((((r >> 3) + 4) ^ (t & 7)) << 4));
-                        const float w = (sees >> r) & 1u ? (half_bits(*at) + half_bits(*rest)) * down : 0.0f;   // NaN where it is seen
-                        *at = __half_as_ushort(__float2half_rn(w));
-                        *rest = __half_as_ushort(__float2half_rn(w - half_bits(*at)));
-                    }
-                }
+                if (down != 1.0f) scale_weights(smem + S::OFF_P + gr * S::PBUF + t * (4 * NR), t, sees, down, vr);
                 if (masked) {
                     // Codes that are NaN are replaced by zeros; they are added here for the rows that see them, with the weights that the
                     // product would have used.
