@@ -59,8 +59,7 @@ struct ForkArgs {
     int32_t *refs_out, *table_out, *context_out;
     sv_stats *stats;
     // workspace
-    int32_t *gone;       // [n_pages] holders of the old table
-    int32_t *come;       // [n_pages] of its tokens' full pages in the new one
+    int2 *holders;       // [n_pages] those of the old table (x), and new sequences that share the page (y)
     int32_t *owner;      // [n_pages] first new sequence whose last tokens fill the page in part
     int32_t *free_list;  // [n_pages] free pages, rising
     int32_t *counts;     // [2][kPlanBlocks] free pages and wanted pages of a block's part
@@ -100,7 +99,7 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     const int first = me * kPlanThreads + tid;
     pdl_trigger();
     for (int p = first; p < a.n_pages; p += all) {
-        a.gone[p] = a.come[p] = 0;
+        a.holders[p] = make_int2(0, 0);
         a.owner[p] = kNobody;
     }
     cluster_sync();
@@ -108,7 +107,7 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     for (int64_t e = first; e < (int64_t)a.B * a.max_pages; e += all) {
         const int b = (int)(e / a.max_pages), p = a.table[b * a.pitch + (e - (int64_t)b * a.max_pages)];
         if (p >= a.n_pages) report_error(a.stats, SV_ERR_INVALID_ARG, b);
-        else if (p >= 0) atomicAdd(&a.gone[p], 1);
+        else if (p >= 0) atomicAdd(&a.holders[p].x, 1);
     }
     const int warp = first >> 5, warps = all >> 5, lane = tid & 31;
     for (int j = warp; j < a.N; j += warps) {
@@ -117,7 +116,7 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         for (int e = lane; e < named; e += 32) {
             const int p = c.row[e];
             if ((unsigned)p >= (unsigned)a.n_pages) report_error(a.stats, SV_ERR_INVALID_ARG, j);
-            else if (e < c.full) atomicAdd(&a.come[p], 1);
+            else if (e < c.full) atomicAdd(&a.holders[p].y, 1);
             else atomicMin(&a.owner[p], j);
         }
     }
@@ -128,9 +127,10 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     int free_here = 0;
     for (int p = p0; p < p1; ++p) {
         // counted apart: a page whose count lacks holders is reported, and is not free while a sequence comes to it
-        const int others = a.refs[p] - a.gone[p];
+        const int2 held = a.holders[p];
+        const int others = a.refs[p] - held.x;
         if (others < 0) report_error(a.stats, SV_ERR_INVALID_ARG, p);
-        int r = max(others, 0) + a.come[p];
+        int r = max(others, 0) + held.y;
         if (a.owner[p] != kNobody) {
             if (r == 0) r = 1;   // the first new sequence keeps it
             else a.owner[p] = kNobody;
@@ -400,13 +400,12 @@ bool share(const int32_t *a, int64_t n, const int32_t *b, int64_t m) {
 int64_t table_extent(int rows, int64_t pitch, int width) { return rows > 0 ? (rows - 1) * pitch + width : 0; }
 
 struct ForkPlan {
-    size_t gone, come, owner, list, counts, copies, bytes;
+    size_t holders, owner, list, counts, copies, bytes;
 };
 ForkPlan plan_fork(int n_pages, int N) {
     Carver cv;
     ForkPlan p{};
-    p.gone = cv.take<int32_t>(n_pages);
-    p.come = cv.take<int32_t>(n_pages);
+    p.holders = cv.take<int2>(n_pages);
     p.owner = cv.take<int32_t>(n_pages);
     p.list = cv.take<int32_t>(n_pages);
     p.counts = cv.take<int32_t>(2 * kPlanBlocks);
@@ -469,8 +468,7 @@ extern "C" sv_status sv_kv_fork(const sv_kv_pool *pool, const int32_t *refs, con
     char *w = static_cast<char *>(workspace);
     ForkArgs a{refs, context_len, page_table, src, table_pitch, table_out_pitch, max_pages, B, N, reserve, n_pages, pool->page_size,
                refs_out, table_out, context_out, stats};
-    a.gone = reinterpret_cast<int32_t *>(w + pl.gone);
-    a.come = reinterpret_cast<int32_t *>(w + pl.come);
+    a.holders = reinterpret_cast<int2 *>(w + pl.holders);
     a.owner = reinterpret_cast<int32_t *>(w + pl.owner);
     a.free_list = reinterpret_cast<int32_t *>(w + pl.list);
     a.counts = reinterpret_cast<int32_t *>(w + pl.counts);
