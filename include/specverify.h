@@ -671,10 +671,10 @@ sv_status sv_kv_append8(const sv_kv_cache8 *cache, const sv_kv_batch *batch, sv_
  * with dtype SV_BF16, head_dim up to 128 and more than 32 rows times query heads a key head, to the bit (values are rounded
  * to bf16, which is exact for scales of 2^-124 and above).  With SV_BF16 and fewer rows, or wider heads, values are not rounded.
  * The few rows' scores take queries exact down to 2^-24 of the block's largest and within 2^-39 of it below that; a weight
- * of the sum over the values is held in two binary16 numbers, within 2^-22 of it or, where that is more, 2^-29 of the row's largest, and
+ * of the sum over the values is held in two binary16 numbers, within 2^-22 of it or, where that is more, 2^-40 of the row's largest, and
  * what it is divided by is not rounded (with more rows: in two bf16 numbers, within 2^-16).  Each such weight carries its page's
  * scale of the values, taken from that of a key head's first page in the part of the context that a block works on (from 2^-40 or
- * 2^40 where that lies below or above).  What pages hold whose scales are more than 2^40 below it is off by up to 2^-60 of it; beside
+ * 2^40 where that lies below or above).  What pages hold whose scales are more than 2^40 below it is off by up to 2^-70 of it; beside
  * pages whose scales are more than 2^64 above it (values of 2^33 and more beside pages of zeros), tokens of the least may drop out of the sum.
  * Scores, times log2(e), are resolved up to 2^22.  A NaN code or scale reaches the rows that see its token, and no other.
  * -------------------------------------------------------------------------------------- */

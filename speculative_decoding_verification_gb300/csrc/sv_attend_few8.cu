@@ -10,20 +10,21 @@
 //   weights   with E_j the exponent of token j's values, less the group's first token's,
 //                 out = sum_j 2^(s_j) 2^(E_j) code_j / sum_j 2^(s_j) = sum_j w_j code_j / sum_j w_j 2^(-E_j),   w_j = 2^(s_j + E_j - M)
 //             where M follows the largest s_j + E_j as a maximum does: weights are as exact as those of an unscaled cache whatever the
-//             scales are.  A weight enters its product with the codes as two binary16 numbers, itself rounded and what that leaves, rounded: within
-//             2^-22 of it, or of the largest 2^-29 where that is more (half of binary16's last step, 2^-25, beside 2^kLift).  One number alone, off by up to
-//             2^-11, took 462 us where this takes 484, and outputs would differ with how many rows a block has.
+//             scales are.  A weight enters its product with the codes as two binary16 numbers, itself rounded and 2^11 times what that leaves,
+//             rounded: within 2^-22 of it, or of the largest 2^-40 where that is more (half of binary16's last step, 2^-25, of 2^-11, beside 2^kLift).  One
+//             number alone, off by up to 2^-11, took 462 us where this takes 491, and outputs would differ with how many rows a block has; without the 2^11
+//             tokens beside one with nearly all the weight would have a number that is not much better.
 //             An E_j below -40 is taken as -40 and the rest multiplies the weight, so that pages of zeros (whose scale is the least) count
 //             in the sum.  E_j up to 64 leave every weight there that is within 2^-26 of its row's largest; above, the least may drop out.
 // Keys are widened to tensor memory, from where the products take them, values to shared memory: its bandwidth (a tile of values is
 // written, read, written wide and read by the products) would else be the bound.
 // The walk's warp makes the query tiles, ahead of the products.  Blocks of eight columns without rows are left out of the softmax.
 //
-// A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 2,100, and a piece's beginning
+// A tile is 32 KB (heads of 128), 1,450 cycles of an SM's share of the measured copy bandwidth; long contexts take 2,120, and a piece's beginning
 // and end some 7,000 on top.  What bounds it: latency, of the softmax's steps and of instruction fetches (the block's kinds of warps run
 // more code than the caches next to them hold; the same instructions in another order are 3 to 20% slower or faster).  512 sequences x 6
-// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 484 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
-// 8,192 to 16,384 tokens: 356 us.  Heads of 64 halve the bytes and not the steps: 477 us, where the bf16 cache takes 366.
+// rows, 8 key heads of 128, 1,024 to 2,048 tokens: 491 us (the kernel of a bf16 cache: 525), 251 at the memory's rate.  64 sequences over
+// 8,192 to 16,384 tokens: 360 us.  Heads of 64 halve the bytes and not the steps: 481 us, where the bf16 cache takes 366.
 #include <float.h>
 
 #define SV_WALK_PART static __host__ __device__ __noinline__
@@ -63,20 +64,24 @@ constexpr float kLift = 4.0f, kGrow = 11.0f;
 // Sums of weights are kept times 2^kSums: 2^(kSums - E_j) stays a normal number for every scale beside a first page of the least (E_j up to 167).
 constexpr int kSums = 41;
 
-// Two weights as pairs of binary16 numbers: each rounded, and what that leaves, rounded.
+// Two weights as pairs of binary16 numbers: each rounded, and 2^11 times what that leaves (at most half a step, 2^-11 of the weight, so no larger
+// than that), rounded.
+constexpr float kRestBack = 1.0f / 2048.0f;
 __device__ __forceinline__ void weight_halves(f32x2 e, uint32_t &hi, uint32_t &lo) {
-    float x, y;
+    float x, y, x11, y11;
     f2_unpack(e, x, y);
+    f2_unpack(f2_mul(e, f2_pack(2048.0f, 2048.0f)), x11, y11);
     asm("{\n\t.reg .b16 a, b, m;\n\t.reg .f32 p, q;\n\t"
         "cvt.rn.f16x2.f32 %0, %3, %2;\n\t"
-        "mov.b32 {a, b}, %0;\n\tmov.b16 m, 0xBC00;\n\t"
-        "fma.rn.f32.f16 p, a, m, %2;\n\tfma.rn.f32.f16 q, b, m, %3;\n\t"
+        "mov.b32 {a, b}, %0;\n\tmov.b16 m, 0xE800;\n\t"   // -2048
+        "fma.rn.f32.f16 p, a, m, %4;\n\tfma.rn.f32.f16 q, b, m, %5;\n\t"
         "cvt.rn.f16x2.f32 %1, q, p;\n\t}"
         : "=&r"(hi), "=r"(lo)
-        : "f"(x), "f"(y));
+        : "f"(x), "f"(y), "f"(x11), "f"(y11));
 }
 
 __device__ __forceinline__ float half_bits(uint16_t x) { return __half2float(*reinterpret_cast<const __half *>(&x)); }
+__device__ __forceinline__ float weight_of(uint16_t hi, uint16_t lo) { return fmaf(half_bits(lo), kRestBack, half_bits(hi)); }
 
 // scan_values for binary16 tiles of codes, where only NaN is not finite.
 template <int DP>
@@ -120,8 +125,8 @@ __device__ __noinline__ void add_unseen(const AttendArgs &a, const PieceInfo *pi
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int at = (r & 7) * 2;
-            const float w = half_bits(*reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ (j & 7)) << 4) + at)) +
-                            half_bits(*reinterpret_cast<const uint16_t *>(pj + ((((r >> 3) + 4) ^ (j & 7)) << 4) + at));
+            const float w = weight_of(*reinterpret_cast<const uint16_t *>(pj + (((r >> 3) ^ (j & 7)) << 4) + at),
+                                      *reinterpret_cast<const uint16_t *>(pj + ((((r >> 3) + 4) ^ (j & 7)) << 4) + at));
             if (((see >> r) & 1u) && r < pi->vr) o[r] = __float_as_uint(__uint_as_float(o[r]) + w * v);
         }
         tmem_st32(colO, o);
@@ -129,22 +134,22 @@ __device__ __noinline__ void add_unseen(const AttendArgs &a, const PieceInfo *pi
     }
 }
 
-// The same out of line, for the kernel of heads up to 64, where that leaves the loop's instructions better placed: 512 x 6 rows with heads of 48 and 64 479 and
-// 477 us (550 in line), but of 80, 96 and 128 537 to 540 in the other kernel (484 to 487 in line).
+// The same out of line, for the kernel of heads up to 64, where that leaves the loop's instructions better placed: 512 x 6 rows with heads of 48 and 64 482 and
+// 481 us (556 in line), but of 80, 96 and 128 554 in the other kernel (491 to 494 in line).
 template <int DP>
 __device__ __noinline__ void scan_called(uint32_t tile, int t, uint32_t *flags) {
     scan_codes<DP>(tile, t, flags);
 }
 
-// The rest of token t's scale on its weights, as two numbers again.  Out of line as the above: 484 us (492 in line).
+// The rest of token t's scale on its weights, as two numbers again.  Out of line as the above: heads of 64 481 us (493 in line).
 __device__ __noinline__ void scale_weights(char *row, int t, uint32_t sees, float down, int vr) {
 #pragma unroll 1
     for (int r = 0; r < vr; ++r) {
         uint16_t *at = reinterpret_cast<uint16_t *>(row + (r & 7) * 2 + (((r >> 3) ^ (t & 7)) << 4));
         uint16_t *rest = reinterpret_cast<uint16_t *>(row + (r & 7) * 2 + ((((r >> 3) + 4) ^ (t & 7)) << 4));
-        const float w = (sees >> r) & 1u ? (half_bits(*at) + half_bits(*rest)) * down : 0.0f;   // NaN where it is seen
+        const float w = (sees >> r) & 1u ? weight_of(*at, *rest) * down : 0.0f;   // NaN where it is seen
         *at = __half_as_ushort(__float2half_rn(w));
-        *rest = __half_as_ushort(__float2half_rn(w - half_bits(*at)));
+        *rest = __half_as_ushort(__float2half_rn((w - half_bits(*at)) * (1.0f / kRestBack)));
     }
 }
 
@@ -713,10 +718,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attend_few8(const __grid_cons
                     tmem_ld4(base + S::COL_O + g * (2 * NR) + NR + rb, o2);
                     tc_wait_ld();
                     const float4 f = *reinterpret_cast<const float4 *>(ms->alpha[g] + rb);
-                    y[0] = fmaf(__uint_as_float(o[0]) + __uint_as_float(o2[0]), f.x, y[0]);
-                    y[1] = fmaf(__uint_as_float(o[1]) + __uint_as_float(o2[1]), f.y, y[1]);
-                    y[2] = fmaf(__uint_as_float(o[2]) + __uint_as_float(o2[2]), f.z, y[2]);
-                    y[3] = fmaf(__uint_as_float(o[3]) + __uint_as_float(o2[3]), f.w, y[3]);
+                    y[0] = fmaf(fmaf(__uint_as_float(o2[0]), kRestBack, __uint_as_float(o[0])), f.x, y[0]);
+                    y[1] = fmaf(fmaf(__uint_as_float(o2[1]), kRestBack, __uint_as_float(o[1])), f.y, y[1]);
+                    y[2] = fmaf(fmaf(__uint_as_float(o2[2]), kRestBack, __uint_as_float(o[2])), f.z, y[2]);
+                    y[3] = fmaf(fmaf(__uint_as_float(o2[3]), kRestBack, __uint_as_float(o[3])), f.w, y[3]);
                 }
                 if (t < D) {
 #pragma unroll
