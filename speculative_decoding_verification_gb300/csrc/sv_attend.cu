@@ -47,7 +47,7 @@ struct F32Shape {
 // double buffered with asynchronous copies.  For float32 with more rows than few32 takes and for bf16 heads wider than 128: the
 // FMA rate and, with few rows, the four block barriers a tile bound it.
 // C8: the cache is held in 8 bits.  Codes are copied as they are and become floats as they are read; a key's scale multiplies its
-// score, a value's its elements.  16 sequences x 24 packed rows over 700 to 2,048 tokens: 282 us (236 over floats: widening comes on top of
+// score, a value's its elements.  16 sequences x 24 packed rows over 700 to 2,048 tokens: 286 us (236 over floats: widening comes on top of
 // the FMA rate).
 template <int ES, int DP, int TM, bool C8>
 __global__ void __launch_bounds__(kAttThreads) k_attend_f32(const AttendArgs a) {

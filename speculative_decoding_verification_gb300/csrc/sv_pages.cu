@@ -3,8 +3,8 @@
 // Each call is two kernels.  The plan, one cluster of blocks that meet at hardware barriers, works on the tables and counts: they are
 // small (a few entries a thread), so its time is that of its dependent passes (each a load, an atomic or two, a barrier), and one launch takes
 // less than one for each pass.  The copy moves whole runs of bytes and is bound by memory; it is launched beside the plan, so that
-// its blocks wait where they will run.  In a graph: 256 beams that continue one another, eight layers, 19.5 us (16.5 MB of copies, 2.5 us);
-// eight branches of one request 13.2 us; 642 MB moved in eight layers 112 us, 5.7 TB/s, 0.86 of the measured copy bandwidth; a small pool 10.6 us.
+// its blocks wait where they will run.  In a graph: 256 beams that continue one another, eight layers, 19.3 us (16.5 MB of copies, 2.5 us);
+// eight branches of one request 13.6 us; 642 MB moved in eight layers 112 us, 5.7 TB/s, 0.86 of the measured copy bandwidth; a small pool 10.4 us.
 #include "sv_kv.cuh"
 
 namespace sv {
